@@ -58,7 +58,7 @@ class kvq_layout(C.Structure):
 EXPORTS = ["kvq_layout_query", "kvq_append", "kvq_decode_attn", "kvq_decode_plan",
            "kvq_decode_path", "kvq_status_string", "kvq_decode_attn_noalloc", "kvq_context_shard",
            "kvq_merge_attn", "kvq_fit_nuq_lut", "kvq_measure_distortion", "kvq_rate_allocate",
-           "kvq_append_ragged", "kvq_decode_attn_ragged"]
+           "kvq_append_ragged", "kvq_decode_attn_ragged", "kvq_tree_attn", "kvq_tree_workspace"]
 NUQ_FIT_WORKSPACE_BYTES = 3 * 65538 * 8
 
 _lib = None
@@ -111,6 +111,11 @@ def lib():
         L.kvq_append_ragged.restype = C.c_int
         L.kvq_decode_attn_ragged.argtypes = [C.POINTER(kvq_config), vp, i32p, u16p, u16p, vp, vp, C.c_uint64, vp]
         L.kvq_decode_attn_ragged.restype = C.c_int
+        L.kvq_tree_attn.argtypes = [C.POINTER(kvq_config), vp, i32p, u16p, u16p, u16p, vp, C.c_int32, i32p, u16p, vp,
+                                    vp, C.c_uint64, vp]
+        L.kvq_tree_attn.restype = C.c_int
+        L.kvq_tree_workspace.argtypes = [C.POINTER(kvq_config), C.c_int32, C.POINTER(C.c_uint64)]
+        L.kvq_tree_workspace.restype = C.c_int
         L.kvq_status_string.argtypes = [C.c_int]
         L.kvq_status_string.restype = C.c_char_p
         _lib = L
@@ -394,6 +399,61 @@ def kvq_merge_attn(outs, lses, out, lse_out=None, stream=None):
     _check("kvq_merge_attn", st)
 
 
+def tree_mask(parents):
+    """Mask words for kvq_tree_attn, int32 [B, n, ceil(n / 32)] on the CPU, of
+    the trees whose node i follows parents[b][i] (an earlier node, or -1 for
+    a child of the last cached token): every node sees its ancestors and
+    itself."""
+    import numpy as np
+    import torch
+    p = np.asarray(parents, np.int64)
+    if p.ndim != 2 or p.shape[1] < 1:
+        raise ValueError("parents: one row of nodes per sequence")
+    B, n = p.shape
+    if ((p < -1) | (p >= np.arange(n))).any():
+        raise ValueError("parents: a node follows an earlier one, or -1")
+    sees = np.zeros((B, n, (n + 31) // 32 * 32), bool)
+    for i in range(n):
+        sees[:, i] = sees[np.arange(B), np.maximum(p[:, i], 0)] & (p[:, i] >= 0)[:, None]
+        sees[:, i, i] = True
+    words = np.packbits(sees.reshape(B, n, -1, 32), axis=-1, bitorder="little")
+    return torch.from_numpy(np.ascontiguousarray(words).view("<i4")[..., 0].copy())
+
+
+def kvq_tree_attn(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse=None, workspace=None, nodes=None,
+                  stream=None):
+    """Attention of n drafted tokens per sequence, q [B, Hq, n, d], over batch
+    row b's tokens[b] cached tokens and the drafted tokens k_draft, v_draft
+    [B, Hkv, n, d] that mask (int32 words, see tree_mask) lets each see; mask
+    None: the cache alone.  nodes: how many of the n slots each row uses."""
+    import torch
+    c = _cfg(cfg)
+    lay = kvq_layout_query(c)
+    hkv, hq = _totals(c)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, n, d]")
+    n = int(q.shape[2])
+    nq, nk = c.batch * hq * n * c.head_dim * 2, c.batch * hkv * n * c.head_dim * 2
+    st = lib().kvq_tree_attn(
+        C.byref(c), _ptr(layer_buf, "layer_buf", numel=lay.layer_bytes), _rows(tokens, c.batch, "tokens"),
+        _ptr(q, "q", torch.float16, nq),
+        _ptr(k_draft, "k_draft", torch.float16, nk, allow_none=mask is None),
+        _ptr(v_draft, "v_draft", torch.float16, nk, allow_none=mask is None),
+        _ptr(mask, "mask", torch.int32, c.batch * n * ((n + 31) // 32) * 4, allow_none=True), n,
+        None if nodes is None else _rows(nodes, c.batch, "nodes"), _ptr(out, "out", torch.float16, nq),
+        _ptr(lse, "lse", torch.float32, c.batch * hq * n * 4, allow_none=True),
+        _ptr(workspace, "workspace", allow_none=True),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("kvq_tree_attn", st)
+
+
+def kvq_tree_workspace(cfg, n_nodes: int) -> int:
+    """Bytes of scratch that kvq_tree_attn needs for up to n_nodes per sequence."""
+    out = C.c_uint64()
+    _check("kvq_tree_workspace", lib().kvq_tree_workspace(C.byref(_cfg(cfg)), int(n_nodes), C.byref(out)))
+    return out.value
+
+
 # ------------------------------------------------------------ conveniences
 
 class Layer:
@@ -422,6 +482,15 @@ class Layer:
 
     def decode_ragged(self, tokens, q, out, lse=None, workspace=None, stream=None):
         kvq_decode_attn_ragged(self.cfg, self.buf, tokens, q, out, lse, workspace, None, stream)
+
+    def tree_attn(self, tokens, q, k_draft, v_draft, mask, out, lse=None, workspace=None, nodes=None, stream=None):
+        kvq_tree_attn(self.cfg, self.buf, tokens, q, k_draft, v_draft, mask, out, lse, workspace, nodes, stream)
+
+
+def new_tree_workspace(cfg, n_nodes: int, device="cuda"):
+    """Scratch for kvq_tree_attn calls of up to n_nodes per sequence."""
+    import torch
+    return torch.empty(kvq_tree_workspace(cfg, n_nodes), dtype=torch.uint8, device=device)
 
 
 def new_workspace(cfg, device="cuda"):

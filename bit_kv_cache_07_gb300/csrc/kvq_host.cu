@@ -4,7 +4,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "kvq_internal.cuh"
+#include "kvq_tree.cuh"
 
 using namespace kvq;
 
@@ -625,6 +625,116 @@ kvq_status kvq_decode_attn(const kvq_config* cfg, const void* layer_buf, int32_t
   if (st != KVQ_OK) return st;
   if (need > 0 && (!workspace || ws_bytes < need || ((uintptr_t)workspace % 16))) return KVQ_ERR_WORKSPACE;
   return decode_launch(&p, persistent, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------- many rows per KV head
+
+// Rows per block of the tile kernels: the smallest of 16, 32, 64, 128 that
+// holds a KV head's rows (fewer rows leave more of a CTA's warps to the keys).
+static int spec_row_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+static kvq_status tree_rows(const kvq_config* cfg, const Geometry& g, const int32_t* tokens, const int32_t* nodes,
+                            int32_t n_nodes) {
+  if (n_nodes < 1) return KVQ_ERR_INVALID_ARG;
+  if (n_nodes > kMaxTreeNodes || g.B > kMaxRaggedRows || cfg->max_tokens > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  if (!tokens) return KVQ_OK;  // workspace query
+  for (int b = 0; b < g.B; ++b) {
+    if (tokens[b] < 0 || (nodes && (nodes[b] < 0 || nodes[b] > n_nodes))) return KVQ_ERR_INVALID_ARG;
+    if (tokens[b] > cfg->max_tokens) return KVQ_ERR_CAPACITY;
+  }
+  return KVQ_OK;
+}
+
+// Slots for partial results of a call whose KV heads have up to g * n_nodes rows.
+static uint64_t tree_scratch(const Geometry& g, int32_t n_nodes, uint64_t* ml, uint64_t* flags) {
+  const int64_t rows = (int64_t)g.g * n_nodes;
+  const int rblk = spec_row_block(rows);
+  const uint64_t slots = kMaxSpecCtas + 2ull * g.NS * ((rows + rblk - 1) / rblk), sub = kTile / rblk;
+  *ml = align_up(slots * sub * rblk * 8);
+  *flags = align_up(slots * (kTile / 16) * 4);  // the most sub: sizes do not fall as nodes grow
+  return *ml + *flags + slots * sub * rblk * kHeadDim * 4;
+}
+
+kvq_status kvq_tree_workspace(const kvq_config* cfg, int32_t n_nodes, uint64_t* bytes) {
+  Geometry g;
+  kvq_status st = make_geometry(cfg, &g);
+  if (st != KVQ_OK) return st;
+  if (!bytes) return KVQ_ERR_INVALID_ARG;
+  st = tree_rows(cfg, g, nullptr, nullptr, n_nodes);
+  if (st != KVQ_OK) return st;
+  uint64_t ml, fl;
+  *bytes = tree_scratch(g, n_nodes, &ml, &fl);
+  return KVQ_OK;
+}
+
+kvq_status kvq_tree_attn(const kvq_config* cfg, const void* layer_buf, const int32_t* tokens, const uint16_t* q,
+                         const uint16_t* k_draft, const uint16_t* v_draft, const uint32_t* mask, int32_t n_nodes,
+                         const int32_t* nodes, uint16_t* out, float* lse, void* workspace, uint64_t ws_bytes,
+                         kvq_stream_t stream) {
+  Geometry g;
+  kvq_status st = make_geometry(cfg, &g);
+  if (st != KVQ_OK) return st;
+  if (!layer_buf || !tokens || !q || !out || (mask && (!k_draft || !v_draft))) return KVQ_ERR_INVALID_ARG;
+  st = tree_rows(cfg, g, tokens, nodes, n_nodes);
+  if (st != KVQ_OK) return st;
+  if (((uintptr_t)layer_buf | (uintptr_t)q | (uintptr_t)out) % 16) return KVQ_ERR_INVALID_ARG;
+  if (mask && (((uintptr_t)k_draft | (uintptr_t)v_draft) % 16 || (uintptr_t)mask % 4)) return KVQ_ERR_INVALID_ARG;
+  if ((uintptr_t)lse % 4) return KVQ_ERR_INVALID_ARG;
+  uint64_t ml, fl;
+  if (!workspace || ws_bytes < tree_scratch(g, n_nodes, &ml, &fl) || (uintptr_t)workspace % 16) return KVQ_ERR_WORKSPACE;
+  kvq_layout L;
+  build_layout(cfg, g, &L);
+  TreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.geo = g;
+  layer_ptrs(L, const_cast<void*>(layer_buf), &p.L);
+  p.q = q;
+  p.kd = k_draft;
+  p.vd = v_draft;
+  p.mask = mask;
+  p.out = out;
+  p.lse = lse;
+  p.n = n_nodes;
+  p.words = (n_nodes + 31) / 32;
+  p.rblk = spec_row_block((int64_t)g.g * n_nodes);
+  p.sub = kTile / p.rblk;
+  p.part_ml = reinterpret_cast<float2*>(workspace);
+  p.part_flag = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + ml);
+  p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml + fl);
+  const double sm = cfg->softmax_scale > 0.0f ? (double)cfg->softmax_scale : 1.0 / std::sqrt((double)kHeadDim);
+  p.q_scale = (float)(sm * 1.4426950408889634);
+  p.hadamard_c = (float)(1.0 / std::sqrt((double)kHeadDim));
+  for (int i = 0; i < 8; ++i) {
+    p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
+    p.v_lut_off[i] = cfg->v_lut[i] - cfg->v_lut[0];
+  }
+  if (g.pre_rope)
+    for (int i = 0; i < kHeadDim / 2; ++i) p.theta[i] = std::pow((double)cfg->rope_theta, -2.0 * i / (double)kHeadDim);
+  int64_t total = 0, pairs = 0;
+  bool any = false;
+  for (int b = 0; b < g.B; ++b) {
+    const int nb = nodes ? nodes[b] : n_nodes;
+    const TileCounts tc = tile_counts(g, tokens[b], mask ? nb : 0);
+    const int64_t heads = (int64_t)g.Hkv * (((int64_t)g.g * nb + p.rblk - 1) / p.rblk);
+    p.rows.tokens[b] = tokens[b];
+    p.rows.nodes[b] = nb;
+    p.rows.tile0[b] = (int)total;
+    p.rows.pair0[b] = (int)pairs;
+    pairs += heads;
+    total += heads * (tc.qt + tc.ft);
+    any = any || nb > 0;
+    if (total > (1ll << 30)) return KVQ_ERR_UNSUPPORTED;
+  }
+  if (!any) return KVQ_OK;  // no row holds a node
+  p.rows.tile0[g.B] = (int)total;
+  p.rows.pair0[g.B] = (int)pairs;
+  int sms = 0;
+  if (device_sm_count(&sms) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (g.sm_budget > 0 && g.sm_budget < sms) sms = g.sm_budget;
+  int64_t ctas = sms < kMaxSpecCtas ? sms : kMaxSpecCtas;
+  p.total = (int)total;
+  p.ncta = (int)(ctas < total ? ctas : total);
+  return launch_tree_attn(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -463,6 +463,53 @@ KVQ_API kvq_status kvq_context_shard(const kvq_config *cfg, int32_t tokens, int3
 KVQ_API kvq_status kvq_merge_attn(int32_t n_parts, int64_t rows, int32_t head_dim, const uint16_t *outs,
                           const float *lses, uint16_t *out, float *lse_out, kvq_stream_t stream);
 
+/* Speculative decoding: a draft model proposes a tree of n_nodes tokens per
+ * sequence and one call verifies them all.
+ *
+ * kvq_tree_attn -- attention of the drafted tokens over the cache and over
+ * those drafted tokens that each of them follows from.  Node i of batch row b
+ * attends every one of the row's tokens[b] cached tokens, and drafted token j
+ * where bit j % 32 of mask word [b][i][j / 32] is set (its ancestors and
+ * itself, or any other pattern).  Nothing is written to the cache: the caller
+ * appends the accepted path with kvq_append / kvq_append_ragged.
+ *   layer_buf  device, as written by kvq_append
+ *   tokens     host int32 [batch], 0 <= tokens[b] <= max_tokens
+ *   q          device fp16 [B][Hq][n_nodes][d], rotated for its positions
+ *   k_draft, v_draft  device fp16 [B][Hkv][n_nodes][d]: the drafted tokens' keys
+ *              as attention uses them (with k_pre_rope too: already rotated)
+ *              and values (never Hadamard-rotated); heads as kvq_append's
+ *   mask       device u32 [B][n_nodes][ceil(n_nodes / 32)], or NULL: no drafted
+ *              token is attended, k_draft and v_draft are not read (queries
+ *              over the cache alone: a context shard that does not hold the
+ *              newest tokens).  Bits past nodes[b] are ignored, and a key or
+ *              value that a node does not see never reaches its result,
+ *              whatever it holds
+ *   n_nodes    1..256, the inputs' node dimension
+ *   nodes      host int32 [batch], 0 <= nodes[b] <= n_nodes, or NULL (n_nodes
+ *              everywhere): row b has the first nodes[b] of its slots; the
+ *              others are not read, and their out and lse stay as they are
+ *   out        device fp16 [B][Hq][n_nodes][d]
+ *   lse        device f32 [B][Hq][n_nodes] natural-log log-sum-exp, or NULL;
+ *              a node that sees nothing gets out = 0 and lse = -inf
+ *   workspace  device scratch of >= kvq_tree_workspace bytes, 16-byte aligned;
+ *              its contents need not be zero and mean nothing afterwards.
+ *              Calls that share it must not overlap on the GPU.
+ * Keys are dequantized to 22 bits (hi + lo fp16 parts), values and attention
+ * weights to fp16; logits, maxima and sums are fp32.  The result does not
+ * depend on timing.  Two launches.
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (n_nodes > 256, batch >
+ * 256, max_tokens > 2^30, more than 2^30 tiles of 128 keys), KVQ_ERR_CAPACITY,
+ * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA. */
+KVQ_API kvq_status kvq_tree_attn(const kvq_config *cfg, const void *layer_buf, const int32_t *tokens, const uint16_t *q,
+                         const uint16_t *k_draft, const uint16_t *v_draft, const uint32_t *mask, int32_t n_nodes,
+                         const int32_t *nodes, uint16_t *out, float *lse, void *workspace, uint64_t ws_bytes,
+                         kvq_stream_t stream);
+
+/* kvq_tree_workspace -- host only: bytes of scratch that kvq_tree_attn needs
+ * for up to n_nodes nodes per sequence.  Errors: those of kvq_layout_query,
+ * KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (n_nodes > 256, batch > 256). */
+KVQ_API kvq_status kvq_tree_workspace(const kvq_config *cfg, int32_t n_nodes, uint64_t *bytes);
+
 /* Static string naming a status code. */
 KVQ_API const char *kvq_status_string(kvq_status status);
 
