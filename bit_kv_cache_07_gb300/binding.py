@@ -58,7 +58,8 @@ class kvq_layout(C.Structure):
 EXPORTS = ["kvq_layout_query", "kvq_append", "kvq_decode_attn", "kvq_decode_plan",
            "kvq_decode_path", "kvq_status_string", "kvq_decode_attn_noalloc", "kvq_context_shard",
            "kvq_merge_attn", "kvq_fit_nuq_lut", "kvq_measure_distortion", "kvq_rate_allocate",
-           "kvq_append_ragged", "kvq_decode_attn_ragged", "kvq_tree_attn", "kvq_tree_workspace"]
+           "kvq_append_ragged", "kvq_decode_attn_ragged", "kvq_tree_attn", "kvq_tree_workspace",
+           "kvq_attn_mass", "kvq_evict", "kvq_evict_workspace"]
 NUQ_FIT_WORKSPACE_BYTES = 3 * 65538 * 8
 
 _lib = None
@@ -116,6 +117,12 @@ def lib():
         L.kvq_tree_attn.restype = C.c_int
         L.kvq_tree_workspace.argtypes = [C.POINTER(kvq_config), C.c_int32, C.POINTER(C.c_uint64)]
         L.kvq_tree_workspace.restype = C.c_int
+        L.kvq_attn_mass.argtypes = [C.POINTER(kvq_config), vp, i32p, u16p, vp, vp, C.c_int32, C.c_float, vp, vp]
+        L.kvq_attn_mass.restype = C.c_int
+        L.kvq_evict.argtypes = [C.POINTER(kvq_config), vp, i32p, i32p, vp, vp, vp, vp, C.c_uint64, vp]
+        L.kvq_evict.restype = C.c_int
+        L.kvq_evict_workspace.argtypes = [C.POINTER(kvq_config), C.POINTER(C.c_uint64)]
+        L.kvq_evict_workspace.restype = C.c_int
         L.kvq_status_string.argtypes = [C.c_int]
         L.kvq_status_string.restype = C.c_char_p
         _lib = L
@@ -454,6 +461,54 @@ def kvq_tree_workspace(cfg, n_nodes: int) -> int:
     return out.value
 
 
+def kvq_attn_mass(cfg, layer_buf, tokens, q, lse, mass, weight=None, decay: float = 1.0, stream=None):
+    """Add the attention weights of the rows q [B, Hq, n, d] (or [B, Hq, d]),
+    whose log-sum-exp the attention returned as lse, to the record mass
+    [B, Hkv, max_tokens] f32 of the cache's tokens; weight [B, n] f32."""
+    import torch
+    c = _cfg(cfg)
+    lay = kvq_layout_query(c)
+    hq = _totals(c)[1]
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, n, d] or [B, Hq, d]")
+    n = int(q.shape[2]) if q.dim() == 4 else 1
+    st = lib().kvq_attn_mass(
+        C.byref(c), _ptr(layer_buf, "layer_buf", numel=lay.layer_bytes), _rows(tokens, c.batch, "tokens"),
+        _ptr(q, "q", torch.float16, c.batch * hq * n * c.head_dim * 2), _ptr(lse, "lse", torch.float32, c.batch * hq * n * 4),
+        _ptr(weight, "weight", torch.float32, c.batch * n * 4, allow_none=True), n, float(decay),
+        _ptr(mass, "mass", torch.float32, c.batch * c.n_kv_heads * c.max_tokens * 4), _stream(stream))
+    _check("kvq_attn_mass", st)
+
+
+def kvq_evict(cfg, layer_buf, tokens, n_groups, mass, mass_out, source=None, workspace=None, stream=None):
+    """Drop n_groups[b] 32-token groups of the least recorded weight from every
+    stream of batch row b, in place.  mass_out (mass itself, or another
+    tensor) becomes the compacted cache's record; source int32 [B, Hkv, group
+    slots] tells where each slot's group came from.  Returns the rows' tokens
+    afterwards."""
+    import torch
+    c = _cfg(cfg)
+    lay = kvq_layout_query(c)
+    rows, drop = _rows(tokens, c.batch, "tokens"), _rows(n_groups, c.batch, "n_groups")
+    record = c.batch * c.n_kv_heads * c.max_tokens * 4
+    slots = max(0, c.max_tokens - c.n_sink - c.n_recent) // 32
+    st = lib().kvq_evict(
+        C.byref(c), _ptr(layer_buf, "layer_buf", numel=lay.layer_bytes), rows, drop,
+        _ptr(mass, "mass", torch.float32, record), _ptr(mass_out, "mass_out", torch.float32, record),
+        _ptr(source, "source", torch.int32, c.batch * c.n_kv_heads * slots * 4, allow_none=True),
+        _ptr(workspace, "workspace", allow_none=True),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("kvq_evict", st)
+    return [t - 32 * e for t, e in zip(rows, drop)]
+
+
+def kvq_evict_workspace(cfg) -> int:
+    """Bytes of scratch that kvq_evict needs."""
+    out = C.c_uint64()
+    _check("kvq_evict_workspace", lib().kvq_evict_workspace(C.byref(_cfg(cfg)), C.byref(out)))
+    return out.value
+
+
 # ------------------------------------------------------------ conveniences
 
 class Layer:
@@ -485,6 +540,25 @@ class Layer:
 
     def tree_attn(self, tokens, q, k_draft, v_draft, mask, out, lse=None, workspace=None, nodes=None, stream=None):
         kvq_tree_attn(self.cfg, self.buf, tokens, q, k_draft, v_draft, mask, out, lse, workspace, nodes, stream)
+
+    def attn_mass(self, tokens, q, lse, mass, weight=None, decay: float = 1.0, stream=None):
+        kvq_attn_mass(self.cfg, self.buf, tokens, q, lse, mass, weight, decay, stream)
+
+    def evict(self, tokens, n_groups, mass, mass_out, source=None, workspace=None, stream=None):
+        return kvq_evict(self.cfg, self.buf, tokens, n_groups, mass, mass_out, source, workspace, stream)
+
+
+def new_mass(cfg, device="cuda"):
+    """A zeroed record for kvq_attn_mass: f32 [B, n_kv_heads, max_tokens]."""
+    import torch
+    c = _cfg(cfg)
+    return torch.zeros((c.batch, c.n_kv_heads, c.max_tokens), dtype=torch.float32, device=device)
+
+
+def new_evict_workspace(cfg, device="cuda"):
+    """Scratch for kvq_evict."""
+    import torch
+    return torch.empty(max(16, kvq_evict_workspace(cfg)), dtype=torch.uint8, device=device)
 
 
 def new_tree_workspace(cfg, n_nodes: int, device="cuda"):

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "kvq_evict.cuh"
 #include "kvq_tree.cuh"
 
 using namespace kvq;
@@ -735,6 +736,129 @@ kvq_status kvq_tree_attn(const kvq_config* cfg, const void* layer_buf, const int
   p.total = (int)total;
   p.ncta = (int)(ctas < total ? ctas : total);
   return launch_tree_attn(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_attn_mass(const kvq_config* cfg, const void* layer_buf, const int32_t* tokens, const uint16_t* q,
+                         const float* lse, const float* weight, int32_t n_rows, float decay, float* mass,
+                         kvq_stream_t stream) {
+  Geometry g;
+  kvq_status st = make_geometry(cfg, &g);
+  if (st != KVQ_OK) return st;
+  if (!layer_buf || !tokens || !q || !lse || !mass || n_rows < 1 || !std::isfinite(decay)) return KVQ_ERR_INVALID_ARG;
+  if (g.B > kMaxRaggedRows || cfg->max_tokens > (1 << 30) || n_rows > (1 << 20)) return KVQ_ERR_UNSUPPORTED;
+  if (((uintptr_t)layer_buf | (uintptr_t)q) % 16 || ((uintptr_t)lse | (uintptr_t)weight | (uintptr_t)mass) % 4)
+    return KVQ_ERR_INVALID_ARG;
+  kvq_layout L;
+  build_layout(cfg, g, &L);
+  MassParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.geo = g;
+  layer_ptrs(L, const_cast<void*>(layer_buf), &p.L);
+  p.q = q;
+  p.lse = lse;
+  p.weight = weight;
+  p.mass = mass;
+  p.n = n_rows;
+  p.cap = cfg->max_tokens;
+  p.decay = decay;
+  p.q_scale = cfg->softmax_scale > 0.0f ? cfg->softmax_scale : (float)(1.0 / std::sqrt((double)kHeadDim));
+  for (int i = 0; i < 8; ++i) p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
+  if (g.pre_rope)
+    for (int i = 0; i < kHeadDim / 2; ++i) p.theta[i] = std::pow((double)cfg->rope_theta, -2.0 * i / (double)kHeadDim);
+  int64_t total = 0;
+  for (int b = 0; b < g.B; ++b) {
+    if (tokens[b] < 0) return KVQ_ERR_INVALID_ARG;
+    if (tokens[b] > cfg->max_tokens) return KVQ_ERR_CAPACITY;
+    const TileCounts tc = tile_counts(g, tokens[b], 0);
+    p.rows.tokens[b] = tokens[b];
+    p.rows.tile0[b] = (int)total;
+    total += (int64_t)g.Hkv * (tc.qt + tc.ft);
+    if (total > (1ll << 30)) return KVQ_ERR_UNSUPPORTED;
+  }
+  if (total == 0) return KVQ_OK;  // every row is empty
+  p.rows.tile0[g.B] = (int)total;
+  int sms = 0;
+  if (device_sm_count(&sms) != cudaSuccess) return KVQ_ERR_CUDA;
+  if (g.sm_budget > 0 && g.sm_budget < sms) sms = g.sm_budget;
+  p.total = (int)total;
+  p.ncta = (int)(sms < total ? sms : total);
+  return launch_attn_mass(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+// Scratch of an eviction: order keys, the two slot lists, the streams' move
+// counts, copies of the window (all of the ring; the unquantized cache's
+// window tokens).
+static uint64_t evict_scratch(const kvq_config* cfg, const Geometry& g, EvictParams* p, char* base) {
+  const int64_t rest = (int64_t)cfg->max_tokens - cfg->n_sink - cfg->n_recent;
+  p->S = cfg->n_sink;
+  p->R = cfg->n_recent;
+  p->cap = rest > 0 ? (int)(rest / kGroupTokens) : 0;
+  p->max_tokens = cfg->max_tokens;
+  p->save_rows = p->cap == 0 ? 0 : g.fp16_mode ? cfg->n_recent + kGroupTokens - 1 : g.ring;
+  uint64_t off = 0;
+  auto put = [&](uint64_t bytes) {
+    char* at = base + off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  const uint64_t slots = (uint64_t)g.NS * p->cap;
+  p->keys = reinterpret_cast<unsigned long long*>(put(slots * 8));
+  p->hole = reinterpret_cast<int*>(put(slots * 4));
+  p->mover = reinterpret_cast<int*>(put(slots * 4));
+  p->moves = reinterpret_cast<int*>(put((uint64_t)g.NS * 4));
+  p->saved = put((uint64_t)g.NS * 2 * p->save_rows * kHeadDim * 2);
+  return off;
+}
+
+static kvq_status evict_config(const kvq_config* cfg, Geometry* g) {
+  const kvq_status st = make_geometry(cfg, g);
+  if (st != KVQ_OK) return st;
+  // a key cached before RoPE has its slot as its position: its group cannot move
+  if (g->pre_rope || g->B > kMaxRaggedRows || cfg->max_tokens > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+kvq_status kvq_evict_workspace(const kvq_config* cfg, uint64_t* bytes) {
+  Geometry g;
+  const kvq_status st = evict_config(cfg, &g);
+  if (st != KVQ_OK) return st;
+  if (!bytes) return KVQ_ERR_INVALID_ARG;
+  EvictParams p;
+  *bytes = evict_scratch(cfg, g, &p, nullptr);
+  return KVQ_OK;
+}
+
+kvq_status kvq_evict(const kvq_config* cfg, void* layer_buf, const int32_t* tokens, const int32_t* n_groups,
+                     const float* mass, float* mass_out, int32_t* source, void* workspace, uint64_t ws_bytes,
+                     kvq_stream_t stream) {
+  Geometry g;
+  const kvq_status st = evict_config(cfg, &g);
+  if (st != KVQ_OK) return st;
+  if (!layer_buf || !tokens || !n_groups || !mass || !mass_out) return KVQ_ERR_INVALID_ARG;
+  if ((uintptr_t)layer_buf % 16 || ((uintptr_t)mass | (uintptr_t)mass_out | (uintptr_t)source) % 4) return KVQ_ERR_INVALID_ARG;
+  const uint64_t record = (uint64_t)g.NS * cfg->max_tokens * 4;
+  if (mass != mass_out && (uintptr_t)mass < (uintptr_t)mass_out + record && (uintptr_t)mass_out < (uintptr_t)mass + record)
+    return KVQ_ERR_INVALID_ARG;  // neither the same record nor another
+  EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (!workspace || (uintptr_t)workspace % 16 || ws_bytes < evict_scratch(cfg, g, &p, static_cast<char*>(workspace)))
+    return KVQ_ERR_WORKSPACE;
+  kvq_layout L;
+  build_layout(cfg, g, &L);
+  p.geo = g;
+  layer_ptrs(L, layer_buf, &p.L);
+  p.mass = mass;
+  p.mass_out = mass_out;
+  p.source = source;
+  for (int b = 0; b < g.B; ++b) {
+    if (tokens[b] < 0 || n_groups[b] < 0) return KVQ_ERR_INVALID_ARG;
+    if (tokens[b] > cfg->max_tokens) return KVQ_ERR_CAPACITY;
+    if (n_groups[b] > group_count(p, tokens[b])) return KVQ_ERR_INVALID_ARG;
+    p.tokens[b] = tokens[b];
+    p.evict[b] = n_groups[b];
+    p.most = n_groups[b] > p.most ? n_groups[b] : p.most;
+  }
+  return launch_evict(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // extern "C"

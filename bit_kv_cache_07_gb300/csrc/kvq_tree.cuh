@@ -52,6 +52,21 @@ struct TreeParams {
   SpecRows rows;
 };
 
+struct MassParams {
+  Geometry geo;
+  LayerPtrs L;
+  const uint16_t* q;     // [B][Hq][n][d]
+  const float* lse;      // [B][Hq][n]
+  const float* weight;   // [B][n] or null
+  float* mass;           // [NS][cap]
+  int n, cap;            // query rows per sequence, tokens per stream of the record
+  int ncta, total;       // CTAs, tiles
+  float decay, q_scale;  // q_scale: the softmax scale
+  float k_lut_off[8];
+  double theta[kHeadDim / 2];
+  SpecRows rows;
+};
+
 // Tiles of a (b, h, row block): quantized, fp16.
 struct TileCounts {
   int S_eff, Nq, W, k1;  // sinks present, quantized tokens, window tokens, fp16 tokens (sinks + window)
@@ -234,5 +249,6 @@ __device__ __forceinline__ bool finite8(const uint4& u) {
 #endif  // __CUDACC__
 
 cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st);
+cudaError_t launch_attn_mass(const MassParams& p, cudaStream_t st);
 
 }  // namespace kvq

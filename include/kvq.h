@@ -510,6 +510,78 @@ KVQ_API kvq_status kvq_tree_attn(const kvq_config *cfg, const void *layer_buf, c
  * KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (n_nodes > 256, batch > 256). */
 KVQ_API kvq_status kvq_tree_workspace(const kvq_config *cfg, int32_t n_nodes, uint64_t *bytes);
 
+/* A cache that stays within a bound: the attention that every cached token
+ * received is recorded (kvq_attn_mass, after a decode or a tree's
+ * verification), and when room is needed the groups that received the least
+ * leave (kvq_evict).
+ *
+ * kvq_attn_mass -- add query rows' attention weights to the record:
+ *   mass[s][t] = decay * mass[s][t]
+ *       + sum over the query heads j of stream s's KV head and rows i of
+ *         weight[b][i] * exp(scale * q[b][j][i] . k[s][t] - lse[b][j][i])
+ * for every t < tokens[b].
+ *   layer_buf  device, as written by kvq_append
+ *   tokens     host int32 [batch], 0 <= tokens[b] <= max_tokens: the tokens the
+ *              rows attended in the cache
+ *   q          device fp16 [B][Hq][n_rows][d] (n_rows 1: kvq_decode_attn's q)
+ *   lse        device f32 [B][Hq][n_rows]: the rows' natural-log log-sum-exp as
+ *              kvq_decode_attn or kvq_tree_attn returned it; a row of -inf adds
+ *              nothing
+ *   weight     device f32 [B][n_rows], or NULL (all 1): 0 leaves a row out (a
+ *              node that was not accepted, a slot that is not used), whatever
+ *              its q and lse hold
+ *   n_rows     1..2^20
+ *   decay      finite; 1 accumulates, less forgets
+ *   mass       device f32 [B][n_kv_heads][max_tokens], in the cache's own
+ *              stream order; the caller zero-fills it once.  Entries from
+ *              tokens[b] on are left as they are
+ * One pass over the keys, one launch, no workspace; every entry is summed by
+ * one thread in a fixed order.
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (batch > 256, max_tokens >
+ * 2^30, n_rows > 2^20, more than 2^30 tiles of 128 keys), KVQ_ERR_CAPACITY,
+ * KVQ_ERR_CUDA. */
+KVQ_API kvq_status kvq_attn_mass(const kvq_config *cfg, const void *layer_buf, const int32_t *tokens, const uint16_t *q,
+                         const float *lse, const float *weight, int32_t n_rows, float decay, float *mass,
+                         kvq_stream_t stream);
+
+/* kvq_evict -- drop n_groups[b] whole 32-token groups from every stream of
+ * batch row b and compact the cache in place; the row then holds
+ * tokens[b] - 32 * n_groups[b] tokens, in a state that every other call
+ * accepts.  Each KV head drops its own groups.
+ *   Candidates are the window rule's G = floor((tokens - n_sink - n_recent) /
+ *   32) groups (positions [n_sink + 32 j, + 32)), in the unquantized cache too;
+ *   sinks and the window stay.  The groups with the least total record leave,
+ *   on equal totals the lower group first (a NaN total counts as the largest).
+ *   Groups behind the new end, left = G - n_groups, move into the freed slots:
+ *   the k-th free slot < left takes the k-th kept group >= left.  The window
+ *   keeps its order (its ring is rotated by 32 * n_groups slots).  Slots from
+ *   the new end on are left as they were.
+ *   tokens     host int32 [batch], 0 <= tokens[b] <= max_tokens
+ *   n_groups   host int32 [batch], 0 <= n_groups[b] <= G
+ *   mass       device f32 [B][n_kv_heads][max_tokens], see kvq_attn_mass
+ *   mass_out   device, same shape, mass itself or a record apart from it: the
+ *              record of the compacted cache; entries in [new tokens, tokens)
+ *              become 0, those from tokens[b] on are left as they are
+ *   source     device int32 [B][n_kv_heads][floor((max_tokens - n_sink -
+ *              n_recent) / 32)] or NULL: the group slot that slot j's group came
+ *              from, for j < left (the others are left as they are), for data
+ *              that the caller keeps per token
+ *   workspace  device scratch of >= kvq_evict_workspace bytes, 16-byte aligned;
+ *              its contents need not be zero and mean nothing afterwards.
+ *              Calls that share it must not overlap on the GPU.
+ * Keys cached before RoPE (k_pre_rope) are refused: their position is their
+ * slot.  Three launches (four for the unquantized cache).
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (k_pre_rope, batch > 256,
+ * max_tokens > 2^30), KVQ_ERR_CAPACITY, KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA. */
+KVQ_API kvq_status kvq_evict(const kvq_config *cfg, void *layer_buf, const int32_t *tokens, const int32_t *n_groups,
+                     const float *mass, float *mass_out, int32_t *source, void *workspace, uint64_t ws_bytes,
+                     kvq_stream_t stream);
+
+/* kvq_evict_workspace -- host only: bytes of scratch that kvq_evict needs.
+ * Errors: those of kvq_layout_query, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED
+ * as kvq_evict. */
+KVQ_API kvq_status kvq_evict_workspace(const kvq_config *cfg, uint64_t *bytes);
+
 /* Static string naming a status code. */
 KVQ_API const char *kvq_status_string(kvq_status status);
 
