@@ -1,0 +1,430 @@
+// kvq_fill.cuh -- dequantization of 128-key tiles into the shared-memory
+// operands of the matrix instructions (kvq_tree_tc.cu, kvq_mass.cu): keys as
+// hi + lo fp16 parts (22 bits), values as fp16, rows of 128 bytes with the
+// 128-byte swizzle (tile_off).
+//
+// 256 threads fill a tile.  The raw codes and scales of a tile are read into
+// registers first (load) and converted later (keys, values), so that a tile's
+// loads are in flight while the one before it is waited for.
+//
+// Two mappings.  Uniform codes without RoPE: a thread owns 8 channels of 8
+// consecutive keys (of one group: a channel's scale is read once for 8
+// codes).  Non-uniform codes and keys cached before RoPE: a thread owns 8
+// channel pairs (c, c + 64) of 4 consecutive keys.
+#pragma once
+
+#include "kvq_tree.cuh"
+
+namespace kvq {
+
+#ifdef __CUDACC__
+
+// 1024 + x by the fp16 exponent, then the offset leaves: exact integers.
+__device__ __forceinline__ uint32_t lop_and_or(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
+  return r;
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ __half2 h2_const(uint16_t bits) {
+  return __halves2half2(__ushort_as_half(bits), __ushort_as_half(bits));
+}
+
+// The 8 codes of a chunk as fp16 pairs.  Pair i holds channels (2 i, 2 i + 1)
+// for 8-bit codes and (i, i + 4) for 4- and 2-bit codes (one mask takes both
+// out of a word): the operands' channel order within a chunk (chunk_order).
+template <int BITS>
+__device__ __forceinline__ void code_pairs(uint2 w, __half2 (&c)[4]) {
+  if constexpr (BITS == 8) {
+    const __half2 k1024 = h2_const(0x6400);
+    c[0] = __hsub2(as_h2(__byte_perm(w.x, 0x64646464u, 0x4140u)), k1024);
+    c[1] = __hsub2(as_h2(__byte_perm(w.x, 0x64646464u, 0x4342u)), k1024);
+    c[2] = __hsub2(as_h2(__byte_perm(w.y, 0x64646464u, 0x4140u)), k1024);
+    c[3] = __hsub2(as_h2(__byte_perm(w.y, 0x64646464u, 0x4342u)), k1024);
+  } else if constexpr (BITS == 4) {
+    const __half2 k1024 = h2_const(0x6400), k16th = h2_const(0x2C00), km64 = h2_const(0xD400);
+    c[0] = __hsub2(as_h2(lop_and_or(w.x, 0x000F000Fu, 0x64006400u)), k1024);
+    c[1] = __hfma2(as_h2(lop_and_or(w.x, 0x00F000F0u, 0x64006400u)), k16th, km64);
+    c[2] = __hsub2(as_h2(lop_and_or(w.x >> 8, 0x000F000Fu, 0x64006400u)), k1024);
+    c[3] = __hfma2(as_h2(lop_and_or(w.x >> 8, 0x00F000F0u, 0x64006400u)), k16th, km64);
+  } else {
+    // 16 bits: channels 0..3 to the low half, 4..7 to the high half
+    const uint32_t x = __byte_perm(w.x, 0, 0x4140u);
+    c[0] = __hsub2(as_h2(lop_and_or(x, 0x00030003u, 0x64006400u)), h2_const(0x6400));
+    c[1] = __hfma2(as_h2(lop_and_or(x, 0x000C000Cu, 0x64006400u)), h2_const(0x3400), h2_const(0xDC00));  // /4 - 256
+    c[2] = __hfma2(as_h2(lop_and_or(x, 0x00300030u, 0x64006400u)), h2_const(0x2C00), h2_const(0xD400));  // /16 - 64
+    c[3] = __hfma2(as_h2(lop_and_or(x, 0x00C000C0u, 0x64006400u)), h2_const(0x2400), h2_const(0xCC00));  // /64 - 16
+  }
+}
+// Whether a chunk's channels are stored in the order 0 4 1 5 2 6 3 7.
+__host__ __device__ inline bool paired_order(int bits) { return bits == 4 || bits == 2; }
+__device__ __forceinline__ uint4 pair_chunk(const uint4& u) {
+  return make_uint4(__byte_perm(u.x, u.z, 0x5410), __byte_perm(u.x, u.z, 0x7632), __byte_perm(u.y, u.w, 0x5410),
+                    __byte_perm(u.y, u.w, 0x7632));
+}
+
+// a * b + c with fp16 factors and an fp32 sum, rounded once.
+__device__ __forceinline__ float fma_h(__half a, __half b, float c) {
+  float d;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;\n" : "=f"(d) : "h"(__half_as_ushort(a)), "h"(__half_as_ushort(b)), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float sub_h(__half a, float c) {  // a - c
+  float d;
+  asm("sub.rn.f32.f16 %0, %1, %2;\n" : "=f"(d) : "h"(__half_as_ushort(a)), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_sat(float lo, float hi) {  // to fp16, saturating at its range (NaN stays)
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// x as its fp16 value and minus what is left of it: x = hi - neg.
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t* hi, uint32_t* neg) {
+  *hi = pack_sat(x0, x1);
+  const __half2 h = as_h2(*hi);
+  *neg = as_u32(__floats2half2_rn(sub_h(__low2half(h), x0), sub_h(__high2half(h), x1)));
+}
+
+// Turns of position pos at frequency f (turns per position as a 64-bit
+// fraction): the product's wrap is the reduction, so the angle is exact to
+// 2^-32 turns at every position below 2^31.
+__device__ __forceinline__ float2 phasor(uint32_t pos, unsigned long long f) {
+  const uint32_t turns = pos * (uint32_t)(f >> 32) + __umulhi(pos, (uint32_t)f);
+  float sn, cs;
+  sincospif((float)(int)turns * 4.656612873077393e-10f /* 2^-31: half turns */, &sn, &cs);
+  return make_float2(cs, sn);
+}
+
+struct TileSrc {
+  TileCounts tc;
+  int s, b, n_b;      // stream, batch row, drafted tokens
+  bool quant;
+  size_t draft0;      // first row of the stream in k_draft / v_draft
+};
+
+// Raw codes and scales of a thread's share of a tile.
+struct RawTile {
+  uint2 k[8], v[8];
+  uint32_t ks[8], vs[8];
+};
+
+__device__ __forceinline__ uint2 load_codes(const uint8_t* row, int bits, int chunk) {
+  uint2 r = make_uint2(0, 0);
+  if (bits == 8) r = __ldg(reinterpret_cast<const uint2*>(row) + chunk);
+  else if (bits == 4) r.x = __ldg(reinterpret_cast<const uint32_t*>(row) + chunk);
+  else r.x = __ldg(reinterpret_cast<const uint16_t*>(row) + chunk);
+  return r;
+}
+
+// Uniform codes: the thread's loads of quantized tile kt.  Keys past the end
+// are not read (Nq is a whole number of groups, so a thread's 8 keys are all
+// there or none).
+template <bool V>
+__device__ __forceinline__ void load_uniform(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid, RawTile& r) {
+  const int cb = tid & 15, f = kt * kTile + (tid >> 4) * 8;
+  if (f >= src.tc.Nq) return;
+  const size_t tok = (size_t)src.s * G.qcap + f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) r.k[u] = load_codes(L.k_codes + (tok + u) * G.krow, G.kb, cb);
+  if (G.gkc) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) r.ks[u] = __ldg(L.k_scales + (tok + u) * G.nkg + 8 * cb / G.gkc);
+  } else {
+    const uint4* sc = reinterpret_cast<const uint4*>(L.k_scales + ((size_t)src.s * G.gcap + f / kGroupTokens) * kHeadDim + 8 * cb);
+    const uint4 a = __ldg(sc), b = __ldg(sc + 1);
+    r.ks[0] = a.x, r.ks[1] = a.y, r.ks[2] = a.z, r.ks[3] = a.w;
+    r.ks[4] = b.x, r.ks[5] = b.y, r.ks[6] = b.z, r.ks[7] = b.w;
+  }
+  if constexpr (V) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      r.v[u] = load_codes(L.v_codes + (tok + u) * G.vrow, G.vb, cb);
+      r.vs[u] = __ldg(L.v_scales + (tok + u) * G.nvg + 8 * cb / G.gv);
+    }
+  }
+}
+
+// Channel pair i of a chunk in the operands' order: the index of its first
+// and second channel.
+template <int BITS>
+__device__ __forceinline__ constexpr int pair_a(int i) { return BITS == 8 ? 2 * i : i; }
+template <int BITS>
+__device__ __forceinline__ constexpr int pair_b(int i) { return BITS == 8 ? 2 * i + 1 : i + 4; }
+
+// Keys of a uniform tile: K^ = min + code * scale in fp32 (the product of an
+// integer code and an fp16 scale is exact, so the sum rounds once), then
+// times the channel norm, then split into two fp16 parts.
+template <int BITS, bool IQ>
+__device__ __forceinline__ void keys_uniform(const Geometry& G, const LayerPtrs& L, int s, bool have, int tid, const RawTile& r,
+                                             uint8_t* sK, uint8_t* sN) {
+  const int cb = tid & 15, t0 = (tid >> 4) * 8;
+  float norm[8];
+  if (IQ && G.knorm) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) norm[i] = __ldg(L.k_norm + (size_t)s * kHeadDim + 8 * cb + i);
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    uint32_t hi[4] = {0, 0, 0, 0}, neg[4] = {0, 0, 0, 0};
+    if (have) {
+      __half2 c[4];
+      code_pairs<BITS>(r.k[u], c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int a = pair_a<BITS>(i), b = pair_b<BITS>(i);
+        const __half2 ma = as_h2(r.ks[IQ ? u : a]), mb = as_h2(r.ks[IQ ? u : b]);
+        float x0 = fma_h(__low2half(c[i]), __high2half(ma), __low2float(ma));
+        float x1 = fma_h(__high2half(c[i]), __high2half(mb), __low2float(mb));
+        if (IQ && G.knorm) x0 *= norm[a], x1 *= norm[b];
+        split2(x0, x1, &hi[i], &neg[i]);
+      }
+    }
+    const uint32_t o = tile_off(t0 + u, cb);
+    *reinterpret_cast<uint4*>(sK + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(sN + o) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+  }
+}
+
+// Values of a uniform tile, rounded to fp16 once.
+template <int BITS>
+__device__ __forceinline__ void values_uniform(bool have, int tid, const RawTile& r, uint8_t* sV) {
+  const int cb = tid & 15, t0 = (tid >> 4) * 8;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    uint32_t v[4] = {0, 0, 0, 0};
+    if (have) {
+      __half2 c[4];
+      code_pairs<BITS>(r.v[u], c);
+      const __half2 ms = as_h2(r.vs[u]), mn = __low2half2(ms), sc = __high2half2(ms);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = as_u32(__hfma2(c[i], sc, mn));
+      // the largest code's value may pass the fp16 range by the scale's rounding
+      if (fabsf(__low2float(ms)) + (float)((1 << BITS) - 1) * fabsf(__high2float(ms)) > 65504.0f) {
+        const __half2 top = h2_const(0x7BFF), bottom = h2_const(0xFBFF);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(v[i]), top), bottom));
+      }
+    }
+    *reinterpret_cast<uint4*>(sV + tile_off(t0 + u, cb)) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+template <bool V>
+__device__ __forceinline__ void fill_uniform(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid,
+                                             const RawTile& r, uint8_t* sK, uint8_t* sN, uint8_t* sV) {
+  const bool have = kt * kTile + (tid >> 4) * 8 < src.tc.Nq;
+  if (sK) {
+    if (G.gkc) {
+      if (G.kb == 8) keys_uniform<8, true>(G, L, src.s, have, tid, r, sK, sN);
+      else if (G.kb == 4) keys_uniform<4, true>(G, L, src.s, have, tid, r, sK, sN);
+      else keys_uniform<2, true>(G, L, src.s, have, tid, r, sK, sN);
+    } else {
+      if (G.kb == 8) keys_uniform<8, false>(G, L, src.s, have, tid, r, sK, sN);
+      else if (G.kb == 4) keys_uniform<4, false>(G, L, src.s, have, tid, r, sK, sN);
+      else keys_uniform<2, false>(G, L, src.s, have, tid, r, sK, sN);
+    }
+  }
+  if constexpr (V) {
+    if (sV) {
+      if (G.vb == 8) values_uniform<8>(have, tid, r, sV);
+      else if (G.vb == 4) values_uniform<4>(have, tid, r, sV);
+      else values_uniform<2>(have, tid, r, sV);
+    }
+  }
+}
+
+// ------------------------------------------- non-uniform codes, RoPE, fp16
+
+// Channels [8 chunk, + 8) of a non-uniform row: 24 bits at bit 24 chunk.
+__device__ __forceinline__ uint32_t codes3(const uint8_t* row, int chunk) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
+  const int bit = 24 * chunk, i = bit >> 5;
+  return __funnelshift_r(__ldg(w + i), __ldg(w + min(i + 1, 11)), bit & 31) & 0xFFFFFFu;
+}
+__device__ __forceinline__ void values3(uint32_t w, float2 ms, const float* lut, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaf(ms.y, lut[(w >> (3 * i)) & 7], ms.x);
+}
+
+// Dequantized channels of quantized key / value f for the two chunks cb and
+// cb + 8 (lut: the level offsets in shared memory).
+__device__ __forceinline__ void general_keys(const Geometry& G, const LayerPtrs& L, const float* lut, int s, int f, int cb,
+                                             float (&x)[2][8]) {
+  if (G.kb == 3) {
+    const size_t tok = (size_t)s * G.qcap + f;
+    const float2 ms = unpack_min_scale(__ldg(L.k_scales + tok));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      values3(codes3(L.k_codes + tok * G.krow, cb + 8 * h), ms, lut, x[h]);
+      chunk_outliers(L.k_col + tok * G.nout, L.k_val + tok * G.nout, G.nout, cb + 8 * h, x[h]);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) k_chunk(G, L, lut, s, f, cb + 8 * h, x[h]);
+  }
+}
+__device__ __forceinline__ void general_values(const Geometry& G, const LayerPtrs& L, const float* lut, int s, int f, int cb,
+                                               float (&y)[2][8]) {
+  if (G.vb == 3) {
+    const size_t tok = (size_t)s * G.qcap + f;
+    const float2 ms = unpack_min_scale(__ldg(L.v_scales + tok));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      values3(codes3(L.v_codes + tok * G.vrow, cb + 8 * h), ms, lut, y[h]);
+      chunk_outliers(L.v_col + tok * G.nout, L.v_val + tok * G.nout, G.nout, cb + 8 * h, y[h]);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) v_chunk(G, L, lut, s, f, cb + 8 * h, y[h]);
+  }
+}
+
+__device__ __forceinline__ void store_keys(const float (&x)[8], int t, int chunk, uint8_t* sK, uint8_t* sN) {
+  uint32_t hi[4], neg[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], &hi[i], &neg[i]);
+  const uint32_t o = tile_off(t, chunk);
+  *reinterpret_cast<uint4*>(sK + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(sN + o) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+}
+__device__ __forceinline__ void zero_chunk(uint8_t* s, int t, int chunk) {
+  *reinterpret_cast<uint4*>(s + tile_off(t, chunk)) = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void rotate_pairs(float (&x)[2][8], const float2 (&e)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = x[0][i], c = x[1][i];
+    x[0][i] = a * e[i].x - c * e[i].y;
+    x[1][i] = c * e[i].x + a * e[i].y;
+  }
+}
+
+// Keys of a quantized tile with non-uniform codes or RoPE.  The first of the
+// thread's 4 consecutive positions has its angles computed, the others
+// follow by one complex product each (step: e^{i theta}).
+__device__ __forceinline__ void fill_general_keys(const Geometry& G, const LayerPtrs& L, const unsigned long long* freq,
+                                                  const float* lut, const TileSrc& src, int kt, int tid, uint8_t* sK, uint8_t* sN) {
+  const int cb = tid & 7, t0 = (tid >> 3) * 4, f0 = kt * kTile + t0;
+  if (f0 >= src.tc.Nq) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) zero_chunk(sK, t0 + u, cb + 8 * h), zero_chunk(sN, t0 + u, cb + 8 * h);
+    return;
+  }
+  float2 e[8], step[8];
+  if (G.pre_rope) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = phasor((uint32_t)(G.pos_offset + G.S + f0), freq[8 * cb + i]);
+      step[i] = phasor(1, freq[8 * cb + i]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    float x[2][8];
+    general_keys(G, L, lut, src.s, f0 + u, cb, x);
+    if (G.pre_rope) {
+      rotate_pairs(x, e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = spec_cmul(e[i], step[i]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) store_keys(x[h], t0 + u, cb + 8 * h, sK, sN);
+  }
+}
+__device__ __forceinline__ void fill_general_values(const Geometry& G, const LayerPtrs& L, const float* lut, const TileSrc& src,
+                                                    int kt, int tid, uint8_t* sV) {
+  const int cb = tid & 7, t0 = (tid >> 3) * 4, f0 = kt * kTile + t0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (f0 >= src.tc.Nq) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) zero_chunk(sV, t0 + u, cb + 8 * h);
+      continue;
+    }
+    float y[2][8];
+    general_values(G, L, lut, src.s, f0 + u, cb, y);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint4*>(sV + tile_off(t0 + u, cb + 8 * h)) =
+          make_uint4(pack_sat(y[h][0], y[h][1]), pack_sat(y[h][2], y[h][3]), pack_sat(y[h][4], y[h][5]), pack_sat(y[h][6], y[h][7]));
+  }
+}
+
+// fp16 tile: cached keys (rotated when they were cached before RoPE; then in
+// two parts), drafted keys as they are, zeros behind them.
+__device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtrs& L, const unsigned long long* freq,
+                                               const uint16_t* kd, const TileSrc& src, int kt, int tid, uint8_t* sK, uint8_t* sN) {
+  if (!G.pre_rope) {
+    const int cb = tid & 15;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = (tid >> 4) + 16 * u, f = kt * kTile + t;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      int pos;
+      if (f < src.tc.k1) v = __ldg(reinterpret_cast<const uint4*>(fp16_row(G, L.k_sink, L.k_ring, src.s, src.tc, f, &pos)) + cb);
+      else if (f < src.tc.k1 + src.n_b) v = __ldg(reinterpret_cast<const uint4*>(kd + (src.draft0 + f - src.tc.k1) * kHeadDim) + cb);
+      *reinterpret_cast<uint4*>(sK + tile_off(t, cb)) = v;
+    }
+    return;
+  }
+  const int cb = tid & 7;
+#pragma unroll 1
+  for (int u = 0; u < 4; ++u) {
+    const int t = (tid >> 3) * 4 + u, f = kt * kTile + t;
+    float x[2][8] = {};
+    int pos = 0;
+    const uint16_t* row = nullptr;
+    if (f < src.tc.k1) row = fp16_row(G, L.k_sink, L.k_ring, src.s, src.tc, f, &pos);
+    else if (f < src.tc.k1 + src.n_b) row = kd + (src.draft0 + f - src.tc.k1) * kHeadDim;
+    if (row) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) unpack8(__ldg(reinterpret_cast<const uint4*>(row) + cb + 8 * h), x[h]);
+      if (f < src.tc.k1) {
+        float2 e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = phasor((uint32_t)(G.pos_offset + pos), freq[8 * cb + i]);
+        rotate_pairs(x, e);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) store_keys(x[h], t, cb + 8 * h, sK, sN);
+  }
+}
+
+// Values of an fp16 tile.  A drafted value that is not finite enters as zero
+// (a weight of zero must not meet it); true is returned then, and the merge
+// adds it to the rows that see it.
+__device__ __forceinline__ bool fill_fp16_values(const Geometry& G, const LayerPtrs& L, const uint16_t* vd, const TileSrc& src,
+                                                 int kt, int tid, uint8_t* sV) {
+  const int cb = tid & 15;
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int t = (tid >> 4) + 16 * u, f = kt * kTile + t;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    int pos;
+    if (f < src.tc.k1) {
+      v = __ldg(reinterpret_cast<const uint4*>(fp16_row(G, L.v_sink, L.v_ring, src.s, src.tc, f, &pos)) + cb);
+    } else if (f < src.tc.k1 + src.n_b) {
+      v = __ldg(reinterpret_cast<const uint4*>(vd + (src.draft0 + f - src.tc.k1) * kHeadDim) + cb);
+      if (!finite8(v)) {
+        bad = true;
+        float y[8];
+        unpack8(v, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = isfinite(y[i]) ? y[i] : 0.0f;
+        v = pack8(y);
+      }
+    }
+    *reinterpret_cast<uint4*>(sV + tile_off(t, cb)) = v;
+  }
+  return bad;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace kvq

@@ -630,9 +630,23 @@ kvq_status kvq_decode_attn(const kvq_config* cfg, const void* layer_buf, int32_t
 
 // ---------------------------------------------------- many rows per KV head
 
-// Rows per block of the tile kernels: the smallest of 16, 32, 64, 128 that
-// holds a KV head's rows (fewer rows leave more of a CTA's warps to the keys).
-static int spec_row_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Rows per block of the tile kernels, partial results per piece and rows of
+// each: 16 rows leave all of a CTA's warps to the keys (8 partial results),
+// more go to the tensor-core kernel (128 rows).
+static void spec_blocks(int64_t rows, int* rblk, int* sub, int* rstride) {
+  *rblk = rows <= 16 ? 16 : 128;
+  *sub = rows <= 16 ? 8 : 1;
+  *rstride = (int)(rows <= 16 ? 16 : rows < 128 ? (rows + 15) / 16 * 16 : 128);
+}
+
+// RoPE frequencies: radians per position, and turns as 64-bit fractions.
+static void spec_rope(float base, double* theta, unsigned long long* freq) {
+  for (int i = 0; i < kHeadDim / 2; ++i) {
+    theta[i] = std::pow((double)base, -2.0 * i / (double)kHeadDim);
+    const double turns = theta[i] * 0.15915494309189533576888376337251, whole = std::floor(turns);
+    freq[i] = (unsigned long long)std::ldexp(turns - whole, 64);  // (1 - 2^-53) 2^64 at most
+  }
+}
 
 static kvq_status tree_rows(const kvq_config* cfg, const Geometry& g, const int32_t* tokens, const int32_t* nodes,
                             int32_t n_nodes) {
@@ -646,14 +660,16 @@ static kvq_status tree_rows(const kvq_config* cfg, const Geometry& g, const int3
   return KVQ_OK;
 }
 
-// Slots for partial results of a call whose KV heads have up to g * n_nodes rows.
+// Partial results of a call whose KV heads have up to g * n_nodes rows.
 static uint64_t tree_scratch(const Geometry& g, int32_t n_nodes, uint64_t* ml, uint64_t* flags) {
   const int64_t rows = (int64_t)g.g * n_nodes;
-  const int rblk = spec_row_block(rows);
-  const uint64_t slots = kMaxSpecCtas + 2ull * g.NS * ((rows + rblk - 1) / rblk), sub = kTile / rblk;
-  *ml = align_up(slots * sub * rblk * 8);
-  *flags = align_up(slots * (kTile / 16) * 4);  // the most sub: sizes do not fall as nodes grow
-  return *ml + *flags + slots * sub * rblk * kHeadDim * 4;
+  int rblk, sub, rstride;
+  spec_blocks(rows, &rblk, &sub, &rstride);
+  const uint64_t slots = kMaxSpecCtas + 2ull * g.NS * ((rows + rblk - 1) / rblk);
+  const uint64_t part = 128;  // sub * rstride at most; the same for all, so that sizes do not fall as nodes grow
+  *ml = align_up(slots * part * 8);
+  *flags = align_up(slots * 8 * 4);
+  return *ml + *flags + slots * part * kHeadDim * 4;
 }
 
 kvq_status kvq_tree_workspace(const kvq_config* cfg, int32_t n_nodes, uint64_t* bytes) {
@@ -697,8 +713,7 @@ kvq_status kvq_tree_attn(const kvq_config* cfg, const void* layer_buf, const int
   p.lse = lse;
   p.n = n_nodes;
   p.words = (n_nodes + 31) / 32;
-  p.rblk = spec_row_block((int64_t)g.g * n_nodes);
-  p.sub = kTile / p.rblk;
+  spec_blocks((int64_t)g.g * n_nodes, &p.rblk, &p.sub, &p.rstride);
   p.part_ml = reinterpret_cast<float2*>(workspace);
   p.part_flag = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + ml);
   p.part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml + fl);
@@ -709,8 +724,7 @@ kvq_status kvq_tree_attn(const kvq_config* cfg, const void* layer_buf, const int
     p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
     p.v_lut_off[i] = cfg->v_lut[i] - cfg->v_lut[0];
   }
-  if (g.pre_rope)
-    for (int i = 0; i < kHeadDim / 2; ++i) p.theta[i] = std::pow((double)cfg->rope_theta, -2.0 * i / (double)kHeadDim);
+  if (g.pre_rope) spec_rope(cfg->rope_theta, p.theta, p.freq);
   int64_t total = 0, pairs = 0;
   bool any = false;
   for (int b = 0; b < g.B; ++b) {
@@ -763,8 +777,7 @@ kvq_status kvq_attn_mass(const kvq_config* cfg, const void* layer_buf, const int
   p.decay = decay;
   p.q_scale = cfg->softmax_scale > 0.0f ? cfg->softmax_scale : (float)(1.0 / std::sqrt((double)kHeadDim));
   for (int i = 0; i < 8; ++i) p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
-  if (g.pre_rope)
-    for (int i = 0; i < kHeadDim / 2; ++i) p.theta[i] = std::pow((double)cfg->rope_theta, -2.0 * i / (double)kHeadDim);
+  if (g.pre_rope) spec_rope(cfg->rope_theta, p.theta, p.freq);
   int64_t total = 0;
   for (int b = 0; b < g.B; ++b) {
     if (tokens[b] < 0) return KVQ_ERR_INVALID_ARG;

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
       const int r = 16 * wr + g + 8 * e;
       if (r < nr) {
-        const size_t at = ((size_t)slot * p.sub + wk) * p.rblk + r;
+        const size_t at = ((size_t)slot * p.sub + wk) * p.rstride + r;
         if (tq == 0) p.part_ml[at] = make_float2(m[e], l[e]);
         float* acc = p.part_acc + at * kHeadDim;
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
     const int c0 = tile_owner(p.ncta, p.total, first), c1 = tile_owner(p.ncta, p.total, first + tiles - 1);
     const int np = (c1 - c0 + 1) * p.sub;
     for (int i = w; i < np; i += 4) {
-      const size_t sl = (size_t)(c0 + item) * p.sub + i, at = sl * p.rblk + rr;
+      const size_t sl = (size_t)(c0 + item) * p.sub + i, at = sl * p.rstride + rr;
       const float2 ml = p.part_ml[at];
       if (kind && p.part_flag[sl]) sFlag = 1;
       if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // nothing seen
@@ -388,7 +388,7 @@ cudaError_t launch_t(const TreeParams& p, cudaStream_t st) {
 
 cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-  if (p.total > 0) e = p.rblk == 16 ? launch_t<1>(p, st) : p.rblk == 32 ? launch_t<2>(p, st) : p.rblk == 64 ? launch_t<4>(p, st) : launch_t<8>(p, st);
+  if (p.total > 0) e = p.rblk == 16 ? launch_t<1>(p, st) : launch_tree_tc(p, st);
   if (e != cudaSuccess) return e;
   return launch_dependent(tree_merge_kernel, dim3(p.geo.g * p.n, p.geo.Hkv, p.geo.B), dim3(128), 0, st, p);
 }

@@ -14,7 +14,7 @@ namespace kvq {
 
 constexpr int kTile = 128;          // keys per tile
 constexpr int kMaxTreeNodes = 256;  // drafted tokens per sequence
-constexpr int kMaxSpecCtas = 152 * 2;  // CTAs of the tile kernels (bounds the workspace)
+constexpr int kMaxSpecCtas = 160;   // CTAs of the tile kernels, one per SM at most (bounds the workspace)
 
 // Work of one call, planned on the host.  Rows of KV head h, batch row b:
 // r = j * nodes[b] + i for query head j of the group and node i; they are cut
@@ -39,16 +39,18 @@ struct TreeParams {
   const uint32_t* mask;  // [B][n][words] or null (no drafted keys)
   uint16_t* out;
   float* lse;
-  float2* part_ml;    // [slots][sub][rblk] (maximum in log2 units, sum)
-  float* part_acc;    // [slots][sub][rblk][d]
+  float2* part_ml;    // [slots][sub][rstride] (maximum in log2 units, sum)
+  float* part_acc;    // [slots][sub][rstride][d]
   uint32_t* part_flag;  // [slots][sub] a drafted value of the piece is not finite
   int n, words;       // nodes per sequence (the inputs' stride), mask words per node
   int rblk, sub;      // rows per block; partial results per piece
+  int rstride;        // rows of a partial result
   int ncta, total;    // CTAs, tiles
   float q_scale;      // softmax scale * log2(e)
   float hadamard_c;
   float k_lut_off[8], v_lut_off[8];
-  double theta[kHeadDim / 2];
+  double theta[kHeadDim / 2];               // RoPE radians per position
+  unsigned long long freq[kHeadDim / 2];    // RoPE turns per position, 64-bit fractions
   SpecRows rows;
 };
 
@@ -64,6 +66,7 @@ struct MassParams {
   float decay, q_scale;  // q_scale: the softmax scale
   float k_lut_off[8];
   double theta[kHeadDim / 2];
+  unsigned long long freq[kHeadDim / 2];
   SpecRows rows;
 };
 
@@ -249,6 +252,7 @@ __device__ __forceinline__ bool finite8(const uint4& u) {
 #endif  // __CUDACC__
 
 cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st);
+cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t st);
 cudaError_t launch_attn_mass(const MassParams& p, cudaStream_t st);
 
 }  // namespace kvq

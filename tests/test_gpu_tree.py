@@ -107,9 +107,11 @@ def check(B, cfg, lengths, n, nodes=None, seed=0, mask="tree", poison=False):
 LENGTHS = [0, 1, 35, 36, 67, 68, 300, 997]
 
 
+@pytest.mark.parametrize("n", [5, 9])
 @pytest.mark.parametrize("form", sorted(FORMS))
-def test_forms(B, form):
-    check(B, config(form, 8, 4, 2, 1024), LENGTHS, 5, seed=1)
+def test_forms(B, form, n):
+    """10 and 18 rows per KV head: the two kernels."""
+    check(B, config(form, 8, 4, 2, 1024), LENGTHS, n, seed=1)
 
 
 @pytest.mark.parametrize("g,n", [(1, 1), (1, 16), (1, 17), (3, 11), (4, 16), (7, 9), (8, 16), (8, 33), (2, 65), (1, 130), (8, 256)])
@@ -136,8 +138,9 @@ def test_no_drafted_tokens(B, form):
 
 
 @pytest.mark.parametrize("form", ["kv4", "fp16"])
-def test_not_finite_behind_the_mask(B, form):
-    check(B, config(form, 3, 4, 2, 400), [0, 200, 399], 9, seed=6, poison=True)
+@pytest.mark.parametrize("n", [7, 40])
+def test_not_finite_behind_the_mask(B, form, n):
+    check(B, config(form, 3, 4, 2, 400), [0, 200, 399], n, seed=6, poison=True)
 
 
 def test_many_rows_of_a_batch(B):
