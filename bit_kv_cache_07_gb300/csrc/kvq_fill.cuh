@@ -100,7 +100,7 @@ __device__ __forceinline__ float2 phasor(uint32_t pos, unsigned long long f) {
 struct TileSrc {
   TileCounts tc;
   int s, b, n_b;      // stream, batch row, drafted tokens
-  bool quant;
+  int slot0;          // ring slot of the window's first token
   size_t draft0;      // first row of the stream in k_draft / v_draft
 };
 
@@ -110,12 +110,22 @@ struct RawTile {
   uint32_t ks[8], vs[8];
 };
 
-__device__ __forceinline__ uint2 load_codes(const uint8_t* row, int bits, int chunk) {
-  uint2 r = make_uint2(0, 0);
-  if (bits == 8) r = __ldg(reinterpret_cast<const uint2*>(row) + chunk);
-  else if (bits == 4) r.x = __ldg(reinterpret_cast<const uint32_t*>(row) + chunk);
-  else r.x = __ldg(reinterpret_cast<const uint16_t*>(row) + chunk);
-  return r;
+// One load per key, without a branch between them: they are all in flight at
+// once (a branch per load made each wait for the one before).
+template <int BITS>
+__device__ __forceinline__ void load_codes(const uint8_t* rows, int pitch, int chunk, uint2 (&c)[8]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const uint8_t* row = rows + u * pitch;
+    if constexpr (BITS == 8) c[u] = __ldg(reinterpret_cast<const uint2*>(row) + chunk);
+    else if constexpr (BITS == 4) c[u].x = __ldg(reinterpret_cast<const uint32_t*>(row) + chunk);
+    else c[u].x = __ldg(reinterpret_cast<const uint16_t*>(row) + chunk);
+  }
+}
+__device__ __forceinline__ void load_codes(const uint8_t* rows, int bits, int chunk, uint2 (&c)[8]) {
+  if (bits == 8) load_codes<8>(rows, 128, chunk, c);
+  else if (bits == 4) load_codes<4>(rows, 64, chunk, c);
+  else load_codes<2>(rows, 32, chunk, c);
 }
 
 // Uniform codes: the thread's loads of quantized tile kt.  Keys past the end
@@ -126,11 +136,11 @@ __device__ __forceinline__ void load_uniform(const Geometry& G, const LayerPtrs&
   const int cb = tid & 15, f = kt * kTile + (tid >> 4) * 8;
   if (f >= src.tc.Nq) return;
   const size_t tok = (size_t)src.s * G.qcap + f;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) r.k[u] = load_codes(L.k_codes + (tok + u) * G.krow, G.kb, cb);
+  load_codes(L.k_codes + tok * G.krow, G.kb, cb, r.k);
   if (G.gkc) {
+    const uint32_t* sc = L.k_scales + tok * 2 + (cb >> 3);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) r.ks[u] = __ldg(L.k_scales + (tok + u) * G.nkg + 8 * cb / G.gkc);
+    for (int u = 0; u < 8; ++u) r.ks[u] = __ldg(sc + 2 * u);
   } else {
     const uint4* sc = reinterpret_cast<const uint4*>(L.k_scales + ((size_t)src.s * G.gcap + f / kGroupTokens) * kHeadDim + 8 * cb);
     const uint4 a = __ldg(sc), b = __ldg(sc + 1);
@@ -138,11 +148,10 @@ __device__ __forceinline__ void load_uniform(const Geometry& G, const LayerPtrs&
     r.ks[4] = b.x, r.ks[5] = b.y, r.ks[6] = b.z, r.ks[7] = b.w;
   }
   if constexpr (V) {
+    load_codes(L.v_codes + tok * G.vrow, G.vb, cb, r.v);
+    const uint32_t* sc = L.v_scales + tok * G.nvg + 8 * cb / G.gv;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      r.v[u] = load_codes(L.v_codes + (tok + u) * G.vrow, G.vb, cb);
-      r.vs[u] = __ldg(L.v_scales + (tok + u) * G.nvg + 8 * cb / G.gv);
-    }
+    for (int u = 0; u < 8; ++u) r.vs[u] = __ldg(sc + u * G.nvg);
   }
 }
 
@@ -248,36 +257,44 @@ __device__ __forceinline__ void values3(uint32_t w, float2 ms, const float* lut,
   for (int i = 0; i < 8; ++i) x[i] = fmaf(ms.y, lut[(w >> (3 * i)) & 7], ms.x);
 }
 
-// Dequantized channels of quantized key / value f for the two chunks cb and
-// cb + 8 (lut: the level offsets in shared memory).
-__device__ __forceinline__ void general_keys(const Geometry& G, const LayerPtrs& L, const float* lut, int s, int f, int cb,
-                                             float (&x)[2][8]) {
-  if (G.kb == 3) {
-    const size_t tok = (size_t)s * G.qcap + f;
-    const float2 ms = unpack_min_scale(__ldg(L.k_scales + tok));
+// A thread's share of a general tile: 4 consecutive tokens, the chunks cb and
+// cb + 8.  Non-uniform rows: the codes, {min, scale} and (one per lane of the
+// 8 that share the tokens) the outliers.  Uniform rows go through k_chunk.
+struct RawGeneral {
+  uint32_t w[4][2];   // 24 bits each
+  uint32_t ms[4];
+  uint32_t out[4];    // outlier (tid & 7): column << 16 | value
+};
+__device__ __forceinline__ void load_general(const uint8_t* codes, const uint32_t* scales, const uint8_t* col, const uint16_t* val,
+                                             int nout, size_t tok, int cb, RawGeneral& r) {
+  const uint8_t* row = codes + tok * 48;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      values3(codes3(L.k_codes + tok * G.krow, cb + 8 * h), ms, lut, x[h]);
-      chunk_outliers(L.k_col + tok * G.nout, L.k_val + tok * G.nout, G.nout, cb + 8 * h, x[h]);
+  for (int u = 0; u < 4; ++u) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) r.w[u][h] = codes3(row + 48 * u, cb + 8 * h);
+    r.ms[u] = __ldg(scales + tok + u);
+    r.out[u] = 0xFFFF0000u;  // no channel
+    if (cb < nout) {
+      const size_t o = (tok + u) * nout + cb;
+      r.out[u] = (uint32_t)__ldg(col + o) << 16 | __ldg(val + o);
     }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) k_chunk(G, L, lut, s, f, cb + 8 * h, x[h]);
   }
 }
-__device__ __forceinline__ void general_values(const Geometry& G, const LayerPtrs& L, const float* lut, int s, int f, int cb,
-                                               float (&y)[2][8]) {
-  if (G.vb == 3) {
-    const size_t tok = (size_t)s * G.qcap + f;
-    const float2 ms = unpack_min_scale(__ldg(L.v_scales + tok));
+__device__ __forceinline__ void general_values(const RawGeneral& r, int u, const float* lut, int nout, int cb, float (&x)[2][8]) {
+  const float2 ms = unpack_min_scale(r.ms[u]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      values3(codes3(L.v_codes + tok * G.vrow, cb + 8 * h), ms, lut, y[h]);
-      chunk_outliers(L.v_col + tok * G.nout, L.v_val + tok * G.nout, G.nout, cb + 8 * h, y[h]);
+  for (int h = 0; h < 2; ++h) values3(r.w[u][h], ms, lut, x[h]);
+  for (int j = 0; j < nout; ++j) {
+    const uint32_t o = __shfl_sync(0xffffffffu, r.out[u], j, 8);
+    const int c = o >> 16;
+    if (((c >> 3) & 7) == cb) {
+      const float v = half_bits_to_float((uint16_t)o);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c == 64 * h + 8 * cb + i) x[h][i] = v;
     }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) v_chunk(G, L, lut, s, f, cb + 8 * h, y[h]);
   }
 }
 
@@ -307,13 +324,16 @@ __device__ __forceinline__ void rotate_pairs(float (&x)[2][8], const float2 (&e)
 __device__ __forceinline__ void fill_general_keys(const Geometry& G, const LayerPtrs& L, const unsigned long long* freq,
                                                   const float* lut, const TileSrc& src, int kt, int tid, uint8_t* sK, uint8_t* sN) {
   const int cb = tid & 7, t0 = (tid >> 3) * 4, f0 = kt * kTile + t0;
-  if (f0 >= src.tc.Nq) {
+  if (kt * kTile + (t0 & ~31) >= src.tc.Nq) {  // a whole group (and so a whole warp's 16 keys)
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) zero_chunk(sK, t0 + u, cb + 8 * h), zero_chunk(sN, t0 + u, cb + 8 * h);
     return;
   }
+  RawGeneral raw;
+  if (G.kb == 3)
+    load_general(L.k_codes, L.k_scales, L.k_col, L.k_val, G.nout, (size_t)src.s * G.qcap + f0, cb, raw);
   float2 e[8], step[8];
   if (G.pre_rope) {
 #pragma unroll
@@ -325,7 +345,12 @@ __device__ __forceinline__ void fill_general_keys(const Geometry& G, const Layer
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     float x[2][8];
-    general_keys(G, L, lut, src.s, f0 + u, cb, x);
+    if (G.kb == 3) {
+      general_values(raw, u, lut, G.nout, cb, x);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) k_chunk(G, L, lut, src.s, f0 + u, cb + 8 * h, x[h]);
+    }
     if (G.pre_rope) {
       rotate_pairs(x, e);
 #pragma unroll
@@ -338,20 +363,54 @@ __device__ __forceinline__ void fill_general_keys(const Geometry& G, const Layer
 __device__ __forceinline__ void fill_general_values(const Geometry& G, const LayerPtrs& L, const float* lut, const TileSrc& src,
                                                     int kt, int tid, uint8_t* sV) {
   const int cb = tid & 7, t0 = (tid >> 3) * 4, f0 = kt * kTile + t0;
+  if (kt * kTile + (t0 & ~31) >= src.tc.Nq) {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (f0 >= src.tc.Nq) {
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) zero_chunk(sV, t0 + u, cb + 8 * h);
-      continue;
-    }
+    return;
+  }
+  RawGeneral raw;
+  if (G.vb == 3)
+    load_general(L.v_codes, L.v_scales, L.v_col, L.v_val, G.nout, (size_t)src.s * G.qcap + f0, cb, raw);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
     float y[2][8];
-    general_values(G, L, lut, src.s, f0 + u, cb, y);
+    if (G.vb == 3) {
+      general_values(raw, u, lut, G.nout, cb, y);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v_chunk(G, L, lut, src.s, f0 + u, cb + 8 * h, y[h]);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       *reinterpret_cast<uint4*>(sV + tile_off(t0 + u, cb + 8 * h)) =
           make_uint4(pack_sat(y[h][0], y[h][1]), pack_sat(y[h][2], y[h][3]), pack_sat(y[h][4], y[h][5]), pack_sat(y[h][6], y[h][7]));
   }
+}
+
+// Row of fp16 key f: sinks, then the window ring (slot0: the slot of its first
+// token), then the drafted tokens; null behind them.
+__device__ __forceinline__ const uint16_t* fp16_key(const Geometry& G, const uint16_t* sink, const uint16_t* ring,
+                                                    const uint16_t* draft, const TileSrc& src, int f) {
+  if (f >= src.tc.k1) return f < src.tc.k1 + src.n_b ? draft + (src.draft0 + f - src.tc.k1) * kHeadDim : nullptr;
+  if (f < src.tc.S_eff) return sink + ((size_t)src.s * G.S + f) * kHeadDim;
+  int slot = src.slot0 + f - src.tc.S_eff;
+  if (slot >= G.ring) slot -= G.ring;  // the window is at most one turn of the ring
+  return ring + ((size_t)src.s * G.ring + slot) * kHeadDim;
+}
+__device__ __forceinline__ int fp16_pos(const TileSrc& src, int S, int f) {  // position of cached fp16 key f
+  return f < src.tc.S_eff ? f : S + src.tc.Nq + (f - src.tc.S_eff);
+}
+// 16 bytes at p (zeros where p is null), as one predicated load.
+__device__ __forceinline__ uint4 load16_if(const uint16_t* p, int chunk) {
+  uint4 v;
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u64 p, %4, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\nmov.u32 %2, 0;\nmov.u32 %3, 0;\n"
+      "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%5];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "l"(p + 8 * chunk));
+  return v;
 }
 
 // fp16 tile: cached keys (rotated when they were cached before RoPE; then in
@@ -360,35 +419,26 @@ __device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtr
                                                const uint16_t* kd, const TileSrc& src, int kt, int tid, uint8_t* sK, uint8_t* sN) {
   if (!G.pre_rope) {
     const int cb = tid & 15;
+    uint4 v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int t = (tid >> 4) + 16 * u, f = kt * kTile + t;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      int pos;
-      if (f < src.tc.k1) v = __ldg(reinterpret_cast<const uint4*>(fp16_row(G, L.k_sink, L.k_ring, src.s, src.tc, f, &pos)) + cb);
-      else if (f < src.tc.k1 + src.n_b) v = __ldg(reinterpret_cast<const uint4*>(kd + (src.draft0 + f - src.tc.k1) * kHeadDim) + cb);
-      *reinterpret_cast<uint4*>(sK + tile_off(t, cb)) = v;
-    }
+    for (int u = 0; u < 8; ++u) v[u] = load16_if(fp16_key(G, L.k_sink, L.k_ring, kd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(sK + tile_off((tid >> 4) + 16 * u, cb)) = v[u];
     return;
   }
   const int cb = tid & 7;
 #pragma unroll 1
   for (int u = 0; u < 4; ++u) {
     const int t = (tid >> 3) * 4 + u, f = kt * kTile + t;
-    float x[2][8] = {};
-    int pos = 0;
-    const uint16_t* row = nullptr;
-    if (f < src.tc.k1) row = fp16_row(G, L.k_sink, L.k_ring, src.s, src.tc, f, &pos);
-    else if (f < src.tc.k1 + src.n_b) row = kd + (src.draft0 + f - src.tc.k1) * kHeadDim;
-    if (row) {
+    const uint16_t* row = fp16_key(G, L.k_sink, L.k_ring, kd, src, f);
+    float x[2][8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) unpack8(__ldg(reinterpret_cast<const uint4*>(row) + cb + 8 * h), x[h]);
-      if (f < src.tc.k1) {
-        float2 e[8];
+    for (int h = 0; h < 2; ++h) unpack8(load16_if(row, cb + 8 * h), x[h]);
+    if (f < src.tc.k1) {
+      float2 e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = phasor((uint32_t)(G.pos_offset + pos), freq[8 * cb + i]);
-        rotate_pairs(x, e);
-      }
+      for (int i = 0; i < 8; ++i) e[i] = phasor((uint32_t)(G.pos_offset + fp16_pos(src, G.S, f)), freq[8 * cb + i]);
+      rotate_pairs(x, e);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) store_keys(x[h], t, cb + 8 * h, sK, sN);
@@ -402,25 +452,21 @@ __device__ __forceinline__ bool fill_fp16_values(const Geometry& G, const LayerP
                                                  int kt, int tid, uint8_t* sV) {
   const int cb = tid & 15;
   bool bad = false;
+  uint4 v[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) v[u] = load16_if(fp16_key(G, L.v_sink, L.v_ring, vd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const int t = (tid >> 4) + 16 * u, f = kt * kTile + t;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    int pos;
-    if (f < src.tc.k1) {
-      v = __ldg(reinterpret_cast<const uint4*>(fp16_row(G, L.v_sink, L.v_ring, src.s, src.tc, f, &pos)) + cb);
-    } else if (f < src.tc.k1 + src.n_b) {
-      v = __ldg(reinterpret_cast<const uint4*>(vd + (src.draft0 + f - src.tc.k1) * kHeadDim) + cb);
-      if (!finite8(v)) {
-        bad = true;
-        float y[8];
-        unpack8(v, y);
+    const int t = (tid >> 4) + 16 * u;
+    if (kt * kTile + t >= src.tc.k1 && !finite8(v[u])) {
+      bad = true;
+      float y[8];
+      unpack8(v[u], y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = isfinite(y[i]) ? y[i] : 0.0f;
-        v = pack8(y);
-      }
+      for (int i = 0; i < 8; ++i) y[i] = isfinite(y[i]) ? y[i] : 0.0f;
+      v[u] = pack8(y);
     }
-    *reinterpret_cast<uint4*>(sV + tile_off(t, cb)) = v;
+    *reinterpret_cast<uint4*>(sV + tile_off(t, cb)) = v[u];
   }
   return bad;
 }

@@ -631,11 +631,11 @@ kvq_status kvq_decode_attn(const kvq_config* cfg, const void* layer_buf, int32_t
 // ---------------------------------------------------- many rows per KV head
 
 // Rows per block of the tile kernels, partial results per piece and rows of
-// each: 16 rows leave all of a CTA's warps to the keys (8 partial results),
+// each: 16 rows leave the consumer warps to the keys (4 partial results),
 // more go to the tensor-core kernel (128 rows).
 static void spec_blocks(int64_t rows, int* rblk, int* sub, int* rstride) {
   *rblk = rows <= 16 ? 16 : 128;
-  *sub = rows <= 16 ? 8 : 1;
+  *sub = rows <= 16 ? 4 : 1;
   *rstride = (int)(rows <= 16 ? 16 : rows < 128 ? (rows + 15) / 16 * 16 : 128);
 }
 

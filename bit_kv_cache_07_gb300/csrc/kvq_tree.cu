@@ -7,13 +7,16 @@
 //   out_r = sum_t exp(z_rt - m_r) v_t / l_r,  l_r = sum_t exp(z_rt - m_r),
 // with the quantized part of the sum rotated back once when V is stored
 // Hadamard-rotated.  A row that sees nothing gives 0 and lse = -inf.
-#include "kvq_tree.cuh"
+#include "kvq_pipe.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kTreeThreads = 256;
-constexpr uint32_t kTileBytes = kTile * kHeadDim * 2;  // 32 KB
+constexpr int kSmallRows = 16;
+constexpr int kConsumers = 128;
+constexpr int kThreadsSmall = kConsumers + kProducers;
+constexpr uint32_t kSmemSmall = 1024 + kSmallRows * kHeadDim * 2 + 2 * kStageBytes + 256;
+static_assert(kSmemSmall <= 227 * 1024, "shared memory of one CTA");
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -24,256 +27,182 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Tile kt of one kind of stream s (batch row b) into shared memory: K as
-// hi + lo fp16 parts, V as fp16.  Thread (tid >> 3) takes 4 consecutive keys,
-// tid & 7 the channels [8 cb, 8 cb + 8) and the same of the second half (a
-// RoPE pair's two channels).  Keys past the end become zeros.
-__device__ __forceinline__ void fill_tile(const TreeParams& p, const TileCounts& tc, int s, int b, bool quant, int kt, int n_b,
-                                          uint8_t* sK, uint8_t* sKlo, uint8_t* sV, uint32_t* flag, int tid) {
-  const Geometry& G = p.geo;
-  const int cb = tid & 7;
-  for (int u = 0; u < 4; ++u) {
-    const int t = (tid >> 3) * 4 + u, f = kt * kTile + t;
-    float x[2][8], y[2][8];
-    uint4 vraw[2];
-    bool have = false, direct = false;
-    int pos = 0;
-    if (quant) {
-      if (f < tc.Nq) {
-        have = true;
-        pos = G.S + f;
+// Up to 16 query rows per KV head: a 128-row tensor-core tile would be mostly
+// padding, and the dequantization of a tile costs more than its products.
+// The same producers fill the tiles; 4 warps take 32 keys of each with
+// mma.sync (m16n8k16), every warp with its own softmax state and partial
+// result.
+__device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, const uint8_t* sQ, const uint8_t* stage0,
+                                        volatile int* bad_piece, int x, int x_end, int tid, volatile int* gave_up) {
+  auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
+  const int lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3;
+  const uint32_t aQ = (uint32_t)__cvta_generic_to_shared(sQ), a0 = (uint32_t)__cvta_generic_to_shared(stage0);
+  int i = 0;
+  for (int piece = 0; x < x_end; ++piece) {
+    const Piece c = piece_at(p, x, x_end);
+    const bool two = c.quant || p.geo.pre_rope;
+    const uint32_t* mask_row[2] = {nullptr, nullptr};
+    if (p.mask && !c.quant)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          k_chunk(G, p.L, p.k_lut_off, s, f, cb + 8 * h, x[h]);
-          v_chunk(G, p.L, p.v_lut_off, s, f, cb + 8 * h, y[h]);
-        }
-      }
-    } else if (f < tc.k1 + n_b) {
-      have = direct = true;
-      const uint16_t *kr, *vr;
-      if (f < tc.k1) {
-        kr = fp16_row(G, p.L.k_sink, p.L.k_ring, s, tc, f, &pos);
-        vr = fp16_row(G, p.L.v_sink, p.L.v_ring, s, tc, f, &pos);
-      } else {
-        const size_t row = in_stream(G, s) * p.n + (f - tc.k1);
-        kr = p.kd + row * kHeadDim;
-        vr = p.vd + row * kHeadDim;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        unpack8(*reinterpret_cast<const uint4*>(kr + 8 * cb + 64 * h), x[h]);
-        vraw[h] = *reinterpret_cast<const uint4*>(vr + 8 * cb + 64 * h);
-        if (f >= tc.k1 && !finite8(vraw[h])) {
-          // a drafted value that some rows must not see: it enters as zero
-          // here and the merge adds it to the rows that do
-          *flag = 1;
-          unpack8(vraw[h], y[h]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[h][i] = isfinite(y[h][i]) ? y[h][i] : 0.0f;
-          vraw[h] = pack8(y[h]);
-        }
-      }
-    }
-    if (have && G.pre_rope && f < (quant ? tc.Nq : tc.k1)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 e = spec_expi(((double)G.pos_offset + pos) * p.theta[8 * cb + i]);
-        const float a = x[0][i], c = x[1][i];
-        x[0][i] = a * e.x - c * e.y;
-        x[1][i] = c * e.x + a * e.y;
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 hi = make_uint4(0, 0, 0, 0), lo = hi, v = hi;
-      if (have) {
-        split8(x[h], &hi, &lo);
-        if (direct) {
-          v = vraw[h];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[h][i] = fminf(fmaxf(y[h][i], -65504.0f), 65504.0f);
-          v = pack8(y[h]);
-        }
-      }
-      const uint32_t o = tile_off(t, cb + 8 * h);
-      *reinterpret_cast<uint4*>(sK + o) = hi;
-      *reinterpret_cast<uint4*>(sKlo + o) = lo;
-      *reinterpret_cast<uint4*>(sV + o) = v;
-    }
-  }
-}
-
-// One CTA walks its range of tiles.  WR warps along the rows (16 each), WK
-// along the keys of a tile; each (row, key) warp keeps its own softmax state
-// and writes its own partial result.
-template <int WR>
-__global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid_constant__ TreeParams p) {
-  constexpr int WK = 8 / WR, KW = kTile / WK, KC = KW < 32 ? KW : 32;  // keys per warp of a tile, per step
-  constexpr int NT = KC / 8;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sK = smem, *sKlo = smem + kTileBytes, *sV = smem + 2 * kTileBytes, *sQ = smem + 3 * kTileBytes;
-  uint32_t* sMask = reinterpret_cast<uint32_t*>(sQ + 16 * WR * kHeadDim * 2);  // [16 WR][8]
-  __shared__ uint32_t flag;
-  const Geometry& G = p.geo;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, wr = w % WR, wk = w / WR;
-  const int g = lane >> 2, tq = lane & 3;
-  const uint32_t aK = (uint32_t)__cvta_generic_to_shared(sK), aKlo = (uint32_t)__cvta_generic_to_shared(sKlo),
-                 aV = (uint32_t)__cvta_generic_to_shared(sV), aQ = (uint32_t)__cvta_generic_to_shared(sQ);
-  int x = cta_first_tile(p.ncta, p.total, blockIdx.x);
-  const int x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
-  while (x < x_end) {
-    // the piece that starts at tile x
-    const int b = row_of(p.rows.tile0, G.B, x);
-    const int n_b = p.rows.nodes[b], M = G.g * n_b, nrb = (M + p.rblk - 1) / p.rblk;
-    const TileCounts tc = tile_counts(G, p.rows.tokens[b], p.mask ? n_b : 0);
-    const int per = tc.qt + tc.ft, off = x - p.rows.tile0[b], pair = off / per, k = off - pair * per;
-    const int h = pair / nrb, rb = pair - h * nrb, s = b * G.Hkv + h;
-    const bool quant = k < tc.qt;
-    const int k0 = quant ? k : k - tc.qt, kind_tiles = quant ? tc.qt : tc.ft;
-    const int cnt = min(kind_tiles - k0, x_end - x);
-    const int slot = blockIdx.x + 2 * (p.rows.pair0[b] + pair) + (quant ? 0 : 1);
-    const int r0 = rb * p.rblk, nr = min(p.rblk, M - r0);
-    const uint16_t* qb = p.q + ((size_t)b * G.Hq_tot + (size_t)layer_head(G, h) * G.g) * p.n * kHeadDim;
-    __syncthreads();  // the previous piece is done with shared memory
-    if (tid == 0) flag = 0;
-    for (int i = tid; i < 16 * WR * 16; i += kTreeThreads) {
-      const int r = i >> 4, ch = i & 15;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < nr) {
-        const int j = (r0 + r) / n_b, node = (r0 + r) - j * n_b;
-        v = *reinterpret_cast<const uint4*>(qb + ((size_t)j * p.n + node) * kHeadDim + 8 * ch);
-      }
-      *reinterpret_cast<uint4*>(sQ + r * 256 + ((ch ^ (r & 7)) << 4)) = v;
-    }
-    if (!quant && p.mask)
-      for (int i = tid; i < 16 * WR * p.words; i += kTreeThreads) {
-        const int r = i / p.words, wd = i - r * p.words;
-        sMask[r * 8 + wd] = r < nr ? p.mask[((size_t)b * p.n + (r0 + r) % n_b) * p.words + wd] : 0;
-      }
-    __syncthreads();
+      for (int e = 0; e < 2; ++e)
+        if (g + 8 * e < c.nr) mask_row[e] = p.mask + ((size_t)c.b * p.n + (g + 8 * e) % c.n_b) * p.words;
     uint32_t qa[8][4];
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const int r = 16 * wr + (lane & 15), ch = 2 * ks + (lane >> 4);
-      ldsm4(qa[ks], aQ + r * 256 + ((ch ^ (r & 7)) << 4));
-    }
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-
-    for (int kt = k0; kt < k0 + cnt; ++kt) {
-      __syncthreads();  // every warp is done with the previous tile
-      fill_tile(p, tc, s, b, quant, kt, p.mask ? n_b : 0, sK, sKlo, sV, &flag, tid);
-      __syncthreads();
-#pragma unroll 1
-      for (int c0 = wk * KW; c0 < wk * KW + KW; c0 += KC) {
-        float z[NT][4];
+    for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+    for (int t = 0; t < c.cnt; ++t, ++i) {
+      const int st = i & 1;
+      const uint32_t aK = a0 + st * kStageBytes, aN = aK + kTileBytes, aV = aN + kTileBytes;
+      if (!wait(B.full_k + 8 * st, i >> 1)) return;
+      if (t == 0) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.0f;
+        for (int ks = 0; ks < 8; ++ks) ldsm4(qa[ks], aQ + q_off<kSmallRows>(lane & 15, 2 * ks + (lane >> 4)));
+      }
+      // logits of keys 32 w + 8 n + 2 tq + {0, 1}, rows g and g + 8
+      float z[4][4] = {}, zn[4][4] = {};
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
+      for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-          for (int i = 0; i < NT; i += 2) {
-            // keys c0 + 8 i .. + 16, channels 16 ks .. + 16
-            const int t = c0 + 8 * i + (lane & 7) + ((lane >> 4) << 3), ch = 2 * ks + ((lane >> 3) & 1);
-            const uint32_t off = tile_off(t, ch);
-            uint32_t kb[4];
-            ldsm4(kb, aK + off);
-            mma16816(z[i], qa[ks], kb[0], kb[1]);
-            mma16816(z[i + 1], qa[ks], kb[2], kb[3]);
-            ldsm4(kb, aKlo + off);
-            mma16816(z[i], qa[ks], kb[0], kb[1]);
-            mma16816(z[i + 1], qa[ks], kb[2], kb[3]);
+        for (int n = 0; n < 4; n += 2) {
+          const uint32_t off = tile_off(32 * w + 8 * n + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
+          uint32_t kb[4];
+          ldsm4(kb, aK + off);
+          mma16816(z[n], qa[ks], kb[0], kb[1]);
+          mma16816(z[n + 1], qa[ks], kb[2], kb[3]);
+          if (two) {
+            ldsm4(kb, aN + off);
+            mma16816(zn[n], qa[ks], kb[0], kb[1]);
+            mma16816(zn[n + 1], qa[ks], kb[2], kb[3]);
           }
         }
-        // scale and mask; this thread holds rows g, g + 8 and keys c0 + 8 i + 2 tq + {0, 1}
-        const int base = kt * kTile + c0;
-        float mx[2] = {-INFINITY, -INFINITY};
+      mbar_arrive(B.empty_k + 8 * st);
+      const int f0 = (c.k0 + t) * kTile + 32 * w;
+      uint32_t ok[2];
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+      for (int e = 0; e < 2; ++e) ok[e] = seen(p, c, mask_row[e], f0);
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int f = base + 8 * i + 2 * tq + (e & 1), r = 16 * wr + g + 8 * (e >> 1);
-            bool ok;
-            if (quant) {
-              ok = f < tc.Nq;
-            } else {
-              const int d = f - tc.k1;
-              ok = d < 0 || (p.mask && d < n_b && ((sMask[r * 8 + (d >> 5)] >> (d & 31)) & 1));
-            }
-            z[i][e] = ok ? z[i][e] * p.q_scale : -INFINITY;
-            mx[e >> 1] = fmaxf(mx[e >> 1], z[i][e]);
-          }
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[n][e] = (ok[e >> 1] >> (8 * n + 2 * tq + (e & 1))) & 1 ? (z[n][e] - zn[n][e]) * p.q_scale : -INFINITY;
+          mx[e >> 1] = fmaxf(mx[e >> 1], z[n][e]);
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+      }
+      // the maximum moves when a logit passes it by 2^8 (see the tensor-core kernel)
+      const bool move[2] = {mx[0] > m[0] + 8.0f, mx[1] > m[1] + 8.0f};
+      if (__any_sync(0xffffffffu, move[0] || move[1])) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-          const float mn = fmaxf(m[e], mx[e]);
-          const float al = mn == -INFINITY ? 1.0f : ex2(m[e] - mn);
-          m[e] = mn;
+          const float al = move[e] ? ex2(m[e] - mx[e]) : 1.0f;
+          if (move[e]) m[e] = mx[e];
           l[e] *= al;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i][2 * e] *= al, o[i][2 * e + 1] *= al;
-        }
-        const float mu[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            z[i][e] = ex2(z[i][e] - mu[e >> 1]);
-            l[e >> 1] += z[i][e];
-          }
-        // O += P V; P rounds to fp16 (relative 2^-11 of each weight, as the output does)
-#pragma unroll
-        for (int ks = 0; ks < KC / 16; ++ks) {
-          const uint32_t pa[4] = {pack2(z[2 * ks][0], z[2 * ks][1]), pack2(z[2 * ks][2], z[2 * ks][3]),
-                                  pack2(z[2 * ks + 1][0], z[2 * ks + 1][1]), pack2(z[2 * ks + 1][2], z[2 * ks + 1][3])};
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const int t = c0 + 16 * ks + (lane & 15), ch = i + (lane >> 4);
-            uint32_t vb[4];
-            ldsm4t(vb, aV + tile_off(t, ch));
-            mma16816(o[i], pa, vb[0], vb[1]);
-            mma16816(o[i + 1], pa, vb[2], vb[3]);
-          }
+          for (int n = 0; n < 16; ++n) o[n][2 * e] *= al, o[n][2 * e + 1] *= al;
         }
       }
+      const float mu[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          z[n][e] = ex2(z[n][e] - mu[e >> 1]);
+          l[e >> 1] += z[n][e];
+        }
+      if (!wait(B.full_v + 8 * st, i >> 1)) return;
+      // O += P V; P rounds to fp16 (relative 2^-11 of each weight, as the output does)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const uint32_t pa[4] = {pack2(z[2 * ks][0], z[2 * ks][1]), pack2(z[2 * ks][2], z[2 * ks][3]),
+                                pack2(z[2 * ks + 1][0], z[2 * ks + 1][1]), pack2(z[2 * ks + 1][2], z[2 * ks + 1][3])};
+#pragma unroll
+        for (int n = 0; n < 16; n += 2) {
+          uint32_t vb[4];
+          ldsm4t(vb, aV + tile_off(32 * w + 16 * ks + (lane & 15), n + (lane >> 4)));
+          mma16816(o[n], pa, vb[0], vb[1]);
+          mma16816(o[n + 1], pa, vb[2], vb[3]);
+        }
+      }
+      mbar_arrive(B.empty_v + 8 * st);
     }
-    // the piece's partial result
+    // the piece's partial result; this thread holds slots 8 n + 2 tq + {0, 1} of the values' channel order
+    const bool paired = c.quant && !p.geo.pre_rope && p.geo.kb != 3 && paired_order(p.geo.vb);
+    if (tid == 0 && !c.quant) {
+      const uint32_t bad = bad_piece[piece & 3] == piece + 1;
+      for (int e = 0; e < p.sub; ++e) p.part_flag[(size_t)c.slot * p.sub + e] = bad;
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      const int r = 16 * wr + g + 8 * e;
-      if (r < nr) {
-        const size_t at = ((size_t)slot * p.sub + wk) * p.rstride + r;
+      const int r = g + 8 * e;
+      if (r < c.nr) {
+        const size_t at = ((size_t)c.slot * p.sub + w) * p.rstride + r;
         if (tq == 0) p.part_ml[at] = make_float2(m[e], l[e]);
         float* acc = p.part_acc + at * kHeadDim;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          *reinterpret_cast<float2*>(acc + 8 * i + 2 * tq) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+        for (int n = 0; n < 16; ++n) {
+          if (paired) acc[8 * n + tq] = o[n][2 * e], acc[8 * n + tq + 4] = o[n][2 * e + 1];
+          else *reinterpret_cast<float2*>(acc + 8 * n + 2 * tq) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
+        }
       }
     }
-    if (tid < p.sub) p.part_flag[(size_t)slot * p.sub + tid] = flag;
-    x += cnt;
+    x += c.cnt;
+  }
+}
+
+__global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __grid_constant__ TreeParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (1024 - ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
+  uint8_t *stage0 = smem, *sQ = stage0 + 2 * kStageBytes, *tail = sQ + kSmallRows * kHeadDim * 2;
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 132);
+  volatile int* bad_piece = reinterpret_cast<volatile int*>(tail + 208);
+  float* lut = reinterpret_cast<float*>(tail + 144);
+  const int tid = threadIdx.x;
+  const uint32_t b0 = (uint32_t)__cvta_generic_to_shared(tail);
+  const Bars B{b0, b0 + 16, b0 + 32, b0 + 48, 0, 0, 0, 0};
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B.full_k + 8 * i, kProducers);
+      mbar_init(B.full_v + 8 * i, kProducers);
+      mbar_init(B.empty_k + 8 * i, kConsumers);
+      mbar_init(B.empty_v + 8 * i, kConsumers);
+    }
+    *gave_up = 0;
+    for (int i = 0; i < 4; ++i) bad_piece[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (tid < 16) lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
+  __syncthreads();
+  const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
+  if (tid < kConsumers) consume(p, B, sQ, stage0, bad_piece, x, x_end, tid, gave_up);
+  else produce<kSmallRows>(p, B, sQ, stage0, lut, bad_piece, x, x_end, tid - kConsumers, gave_up);
+  __syncthreads();
+  if (*gave_up) {  // a wait ran out: every row of the range becomes NaN
+    for (int y = x; y < x_end;) {
+      const Piece c = piece_at(p, y, x_end);
+      for (int r = tid; r < c.nr * p.sub; r += kThreadsSmall)
+        p.part_ml[((size_t)c.slot * p.sub + r / c.nr) * p.rstride + r % c.nr] = make_float2(NAN, NAN);
+      y += c.cnt;
+    }
   }
 }
 
@@ -374,13 +303,11 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   if (p.lse && lane == 0) p.lse[orow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-template <int WR>
-cudaError_t launch_t(const TreeParams& p, cudaStream_t st) {
+cudaError_t launch_small(const TreeParams& p, cudaStream_t st) {
   static std::atomic<long long> memo[kMemoDevices];
-  const int smem = (int)(3 * kTileBytes) + 16 * WR * (kHeadDim * 2 + 32);
-  cudaError_t e = ensure_smem_limit(tree_attn_kernel<WR>, memo, smem);
+  const cudaError_t e = ensure_smem_limit(tree_small_kernel, memo, (int)kSmemSmall);
   if (e != cudaSuccess) return e;
-  tree_attn_kernel<WR><<<p.ncta, kTreeThreads, smem, st>>>(p);
+  tree_small_kernel<<<p.ncta, kThreadsSmall, kSmemSmall, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -388,7 +315,7 @@ cudaError_t launch_t(const TreeParams& p, cudaStream_t st) {
 
 cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-  if (p.total > 0) e = p.rblk == 16 ? launch_t<1>(p, st) : launch_tree_tc(p, st);
+  if (p.total > 0) e = p.rblk == kSmallRows ? launch_small(p, st) : launch_tree_tc(p, st);
   if (e != cudaSuccess) return e;
   return launch_dependent(tree_merge_kernel, dim3(p.geo.g * p.n, p.geo.Hkv, p.geo.B), dim3(128), 0, st, p);
 }

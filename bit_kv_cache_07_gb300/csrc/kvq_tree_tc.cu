@@ -13,49 +13,16 @@
 // The maximum moves only when a logit passes it by 2^8 (weights then stay
 // below fp16's range), so O is rarely rescaled.
 // 13 warps leave every thread 128 registers (17 would leave 96, and spills).
-#include "kvq_fill.cuh"
+#include "kvq_pipe.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr int kSoftThreads = 128;
-constexpr int kProducers = 256;
 constexpr int kThreadsTc = kSoftThreads + kProducers + 32;
-constexpr uint32_t kTileBytes = kTile * kHeadDim * 2;
-constexpr uint32_t kStageBytes = 3 * kTileBytes;  // K hi, K neg, V
 constexpr uint32_t kSmemTc = 1024 + kTileBytes + 2 * kStageBytes + 256;
 static_assert(kSmemTc <= 227 * 1024, "shared memory of one CTA");
 constexpr float kLazy = 8.0f;  // log2 units
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// ------------------------------------------------------------- barriers
-__device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-// Wait for a phase, with a limit (well over any wait of a running kernel);
-// past it the CTA gives up: every role leaves its loop.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, volatile int* gave_up) {
-  for (int it = 0; it < (1 << 24); ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(phase)
-        : "memory");
-    if (ok) return true;
-    if ((it & 255) == 255 && *gave_up) return false;
-  }
-  *gave_up = 1;
-  return false;
-}
 
 // ------------------------------------------------- tensor-core operands
 // Shared-memory operand with the 128-byte swizzle: start, leading and stride
@@ -129,87 +96,6 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// A piece of the CTA's range: consecutive tiles of one kind of one (b, h, row
-// block).
-struct Piece {
-  TileCounts tc;
-  int b, h, s, n_b, r0, nr, k0, cnt, slot;
-  bool quant;
-};
-__device__ __forceinline__ Piece piece_at(const TreeParams& p, int x, int x_end) {
-  const Geometry& G = p.geo;
-  Piece c;
-  c.b = row_of(p.rows.tile0, G.B, x);
-  c.n_b = p.rows.nodes[c.b];
-  c.tc = tile_counts(G, p.rows.tokens[c.b], p.mask ? c.n_b : 0);
-  const int M = G.g * c.n_b, nrb = (M + p.rblk - 1) / p.rblk;
-  const int per = c.tc.qt + c.tc.ft, off = x - p.rows.tile0[c.b], pair = off / per, k = off - pair * per;
-  c.h = pair / nrb;
-  const int rb = pair - c.h * nrb;
-  c.s = c.b * G.Hkv + c.h;
-  c.quant = k < c.tc.qt;
-  c.k0 = c.quant ? k : k - c.tc.qt;
-  c.cnt = min((c.quant ? c.tc.qt : c.tc.ft) - c.k0, x_end - x);
-  c.slot = blockIdx.x + 2 * (p.rows.pair0[c.b] + pair) + (c.quant ? 0 : 1);
-  c.r0 = rb * p.rblk;
-  c.nr = min(p.rblk, M - c.r0);
-  return c;
-}
-
-struct Bars {  // shared-memory addresses; by stage (o_done, done: one)
-  uint32_t full_k, full_v, empty_k, empty_v, s_full, p_full, o_done, done;
-};
-
-// ------------------------------------------------------------- producers
-__device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint8_t* sQ, uint8_t* stage0, const float* lut,
-                                        volatile int* bad_piece, int x, int x_end, int tid, volatile int* gave_up) {
-  const Geometry& G = p.geo;
-  const bool general = G.pre_rope || G.kb == 3;
-  int i = 0;  // tiles so far
-  for (int piece = 0; x < x_end; ++piece) {
-    const Piece c = piece_at(p, x, x_end);
-    TileSrc src{c.tc, c.s, c.b, p.mask ? c.n_b : 0, c.quant, in_stream(G, c.s) * p.n};
-    RawTile raw;
-    if (c.quant && !general) load_uniform<true>(G, p.L, src, c.k0, tid, raw);
-    // the previous piece's last product has read Q
-    if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
-    const uint16_t* qb = p.q + ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n * kHeadDim;
-    const bool paired = c.quant && !general && paired_order(G.kb);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int r = (tid >> 4) + 16 * u, ch = tid & 15;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < c.nr) {
-        const int j = (c.r0 + r) / c.n_b, node = c.r0 + r - j * c.n_b;
-        v = __ldg(reinterpret_cast<const uint4*>(qb + ((size_t)j * p.n + node) * kHeadDim) + ch);
-        if (paired) v = pair_chunk(v);
-      }
-      *reinterpret_cast<uint4*>(sQ + tile_off(r, ch)) = v;
-    }
-    bool bad = false;
-    for (int k = c.k0; k < c.k0 + c.cnt; ++k, ++i) {
-      const int st = i & 1;
-      const uint32_t again = ((i >> 1) - 1) & 1;
-      uint8_t *sK = stage0 + st * kStageBytes, *sN = sK + kTileBytes, *sV = sN + kTileBytes;
-      if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
-      if (!c.quant) fill_fp16_keys(G, p.L, p.freq, p.kd, src, k, tid, sK, sN);
-      else if (general) fill_general_keys(G, p.L, p.freq, lut, src, k, tid, sK, sN);
-      else fill_uniform<true>(G, p.L, src, k, tid, raw, sK, sN, nullptr);
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(B.full_k + 8 * st);
-      if (i >= 2 && !mbar_wait(B.empty_v + 8 * st, again, gave_up)) return;
-      if (!c.quant) bad |= fill_fp16_values(G, p.L, p.vd, src, k, tid, sV);
-      else if (general) fill_general_values(G, p.L, lut + 8, src, k, tid, sV);
-      else fill_uniform<true>(G, p.L, src, k, tid, raw, nullptr, nullptr, sV);
-      if (bad) bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(B.full_v + 8 * st);
-      if (c.quant && !general && k + 1 < c.k0 + c.cnt) load_uniform<true>(G, p.L, src, k + 1, tid, raw);
-    }
-    x += c.cnt;
-  }
-}
-
 // ---------------------------------------------------------------- issuer
 __device__ __forceinline__ bool issue_pv(const Bars& B, uint32_t tmem, uint32_t stage0, int i, bool first, volatile int* gave_up) {
   const int st = i & 1, ph = (i >> 1) & 1;
@@ -256,23 +142,6 @@ __device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32
 }
 
 // --------------------------------------------------------------- softmax
-// Bit e: the row sees key f0 + e.
-__device__ __forceinline__ uint32_t seen(const TreeParams& p, const Piece& c, const uint32_t* mask_row, int f0) {
-  if (c.quant) return f0 < c.tc.Nq ? 0xFFFFFFFFu : 0;  // whole groups of 32
-  const int d0 = f0 - c.tc.k1;                          // drafted index of key f0
-  if (d0 + 32 <= 0) return 0xFFFFFFFFu;
-  if (!mask_row || d0 >= c.n_b) return d0 < 0 ? (1u << -d0) - 1 : 0;
-  uint32_t m;
-  if (d0 <= 0) {
-    m = mask_row[0] << -d0;
-  } else {
-    const int w = d0 >> 5;
-    m = __funnelshift_r(mask_row[w], w + 1 < p.words ? mask_row[w + 1] : 0u, d0 & 31);
-  }
-  if (c.n_b - d0 < 32) m &= (1u << (c.n_b - d0)) - 1;
-  return d0 < 0 ? m | ((1u << -d0) - 1) : m;
-}
-
 __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint32_t tmem, volatile int* bad_piece, int x,
                                         int x_end, int tid, volatile int* gave_up) {
   // warp-uniform: the TMEM loads are for whole warps
@@ -402,8 +271,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
       mbar_init(B.empty_v + 8 * i, 1);
       mbar_init(B.s_full + 8 * i, 1);
       mbar_init(B.p_full + 8 * i, kSoftThreads);
-      mbar_init(B.o_done + 8 * i, 1);
     }
+    mbar_init(B.o_done, 1);
     mbar_init(B.done, 1);
     *gave_up = 0;
     for (int i = 0; i < 4; ++i) bad_piece[i] = 0;
@@ -425,7 +294,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
   if (w < kSoftThreads / 32) {
     softmax(p, B, tmem, bad_piece, x, x_end, tid, gave_up);
   } else if (w < issuer) {
-    produce(p, B, sQ, stage0, lut, bad_piece, x, x_end, tid - kSoftThreads, gave_up);
+    produce<kTile>(p, B, sQ, stage0, lut, bad_piece, x, x_end, tid - kSoftThreads, gave_up);
   } else {
     if ((tid & 31) == 0) {
       issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(sQ), (uint32_t)__cvta_generic_to_shared(stage0), x, x_end, gave_up);
