@@ -31,30 +31,32 @@ __device__ __forceinline__ __half2 h2_const(uint16_t bits) {
   return __halves2half2(__ushort_as_half(bits), __ushort_as_half(bits));
 }
 
-// The 8 codes of a chunk as fp16 pairs.  Pair i holds channels (2 i, 2 i + 1)
-// for 8-bit codes and (i, i + 4) for 4- and 2-bit codes (one mask takes both
-// out of a word): the operands' channel order within a chunk (chunk_order).
-template <int BITS>
+// The 8 codes of a chunk as fp16 pairs, less 2^(BITS - 1) when CENTRED.  Pair
+// i holds channels (2 i, 2 i + 1) for 8-bit codes and (i, i + 4) for 4- and
+// 2-bit codes (one mask takes both out of a word): the operands' channel
+// order within a chunk.
+template <int BITS, bool CENTRED = false>
 __device__ __forceinline__ void code_pairs(uint2 w, __half2 (&c)[4]) {
   if constexpr (BITS == 8) {
-    const __half2 k1024 = h2_const(0x6400);
-    c[0] = __hsub2(as_h2(__byte_perm(w.x, 0x64646464u, 0x4140u)), k1024);
-    c[1] = __hsub2(as_h2(__byte_perm(w.x, 0x64646464u, 0x4342u)), k1024);
-    c[2] = __hsub2(as_h2(__byte_perm(w.y, 0x64646464u, 0x4140u)), k1024);
-    c[3] = __hsub2(as_h2(__byte_perm(w.y, 0x64646464u, 0x4342u)), k1024);
+    const __half2 off = h2_const(CENTRED ? 0x6480 : 0x6400);  // 1024 (+ 128)
+    c[0] = __hsub2(as_h2(__byte_perm(w.x, 0x64646464u, 0x4140u)), off);
+    c[1] = __hsub2(as_h2(__byte_perm(w.x, 0x64646464u, 0x4342u)), off);
+    c[2] = __hsub2(as_h2(__byte_perm(w.y, 0x64646464u, 0x4140u)), off);
+    c[3] = __hsub2(as_h2(__byte_perm(w.y, 0x64646464u, 0x4342u)), off);
   } else if constexpr (BITS == 4) {
-    const __half2 k1024 = h2_const(0x6400), k16th = h2_const(0x2C00), km64 = h2_const(0xD400);
-    c[0] = __hsub2(as_h2(lop_and_or(w.x, 0x000F000Fu, 0x64006400u)), k1024);
-    c[1] = __hfma2(as_h2(lop_and_or(w.x, 0x00F000F0u, 0x64006400u)), k16th, km64);
-    c[2] = __hsub2(as_h2(lop_and_or(w.x >> 8, 0x000F000Fu, 0x64006400u)), k1024);
-    c[3] = __hfma2(as_h2(lop_and_or(w.x >> 8, 0x00F000F0u, 0x64006400u)), k16th, km64);
+    const __half2 off = h2_const(CENTRED ? 0x6408 : 0x6400), k16th = h2_const(0x2C00);  // 1024 (+ 8)
+    const __half2 off16 = h2_const(CENTRED ? 0xD480 : 0xD400);                            // -64 (- 8)
+    c[0] = __hsub2(as_h2(lop_and_or(w.x, 0x000F000Fu, 0x64006400u)), off);
+    c[1] = __hfma2(as_h2(lop_and_or(w.x, 0x00F000F0u, 0x64006400u)), k16th, off16);
+    c[2] = __hsub2(as_h2(lop_and_or(w.x >> 8, 0x000F000Fu, 0x64006400u)), off);
+    c[3] = __hfma2(as_h2(lop_and_or(w.x >> 8, 0x00F000F0u, 0x64006400u)), k16th, off16);
   } else {
     // 16 bits: channels 0..3 to the low half, 4..7 to the high half
     const uint32_t x = __byte_perm(w.x, 0, 0x4140u);
-    c[0] = __hsub2(as_h2(lop_and_or(x, 0x00030003u, 0x64006400u)), h2_const(0x6400));
-    c[1] = __hfma2(as_h2(lop_and_or(x, 0x000C000Cu, 0x64006400u)), h2_const(0x3400), h2_const(0xDC00));  // /4 - 256
-    c[2] = __hfma2(as_h2(lop_and_or(x, 0x00300030u, 0x64006400u)), h2_const(0x2C00), h2_const(0xD400));  // /16 - 64
-    c[3] = __hfma2(as_h2(lop_and_or(x, 0x00C000C0u, 0x64006400u)), h2_const(0x2400), h2_const(0xCC00));  // /64 - 16
+    c[0] = __hsub2(as_h2(lop_and_or(x, 0x00030003u, 0x64006400u)), h2_const(CENTRED ? 0x6402 : 0x6400));
+    c[1] = __hfma2(as_h2(lop_and_or(x, 0x000C000Cu, 0x64006400u)), h2_const(0x3400), h2_const(CENTRED ? 0xDC08 : 0xDC00));  // /4 - 256 (- 2)
+    c[2] = __hfma2(as_h2(lop_and_or(x, 0x00300030u, 0x64006400u)), h2_const(0x2C00), h2_const(CENTRED ? 0xD420 : 0xD400));  // /16 - 64 (- 2)
+    c[3] = __hfma2(as_h2(lop_and_or(x, 0x00C000C0u, 0x64006400u)), h2_const(0x2400), h2_const(CENTRED ? 0xCC80 : 0xCC00));  // /64 - 16 (- 2)
   }
 }
 // Whether a chunk's channels are stored in the order 0 4 1 5 2 6 3 7.
@@ -64,17 +66,6 @@ __device__ __forceinline__ uint4 pair_chunk(const uint4& u) {
                     __byte_perm(u.y, u.w, 0x7632));
 }
 
-// a * b + c with fp16 factors and an fp32 sum, rounded once.
-__device__ __forceinline__ float fma_h(__half a, __half b, float c) {
-  float d;
-  asm("fma.rn.f32.f16 %0, %1, %2, %3;\n" : "=f"(d) : "h"(__half_as_ushort(a)), "h"(__half_as_ushort(b)), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float sub_h(__half a, float c) {  // a - c
-  float d;
-  asm("sub.rn.f32.f16 %0, %1, %2;\n" : "=f"(d) : "h"(__half_as_ushort(a)), "f"(c));
-  return d;
-}
 __device__ __forceinline__ uint32_t pack_sat(float lo, float hi) {  // to fp16, saturating at its range (NaN stays)
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
@@ -83,8 +74,8 @@ __device__ __forceinline__ uint32_t pack_sat(float lo, float hi) {  // to fp16, 
 // x as its fp16 value and minus what is left of it: x = hi - neg.
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t* hi, uint32_t* neg) {
   *hi = pack_sat(x0, x1);
-  const __half2 h = as_h2(*hi);
-  *neg = as_u32(__floats2half2_rn(sub_h(__low2half(h), x0), sub_h(__high2half(h), x1)));
+  const float2 h = __half22float2(as_h2(*hi));
+  *neg = as_u32(__floats2half2_rn(h.x - x0, h.y - x1));
 }
 
 // Turns of position pos at frequency f (turns per position as a 64-bit
@@ -95,6 +86,13 @@ __device__ __forceinline__ float2 phasor(uint32_t pos, unsigned long long f) {
   float sn, cs;
   sincospif((float)(int)turns * 4.656612873077393e-10f /* 2^-31: half turns */, &sn, &cs);
   return make_float2(cs, sn);
+}
+
+// Byte offset of a 16-byte chunk of row r among ROWS rows of 128 channels
+// (two halves of 64 channels, swizzled like the tiles).
+template <int ROWS>
+__device__ __forceinline__ uint32_t q_off(int r, int chunk) {
+  return (uint32_t)((chunk >> 3) * (ROWS * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
 }
 
 struct TileSrc {
@@ -131,8 +129,7 @@ __device__ __forceinline__ void load_codes(const uint8_t* rows, int bits, int ch
 // Uniform codes: the thread's loads of quantized tile kt.  Keys past the end
 // are not read (Nq is a whole number of groups, so a thread's 8 keys are all
 // there or none).
-template <bool V>
-__device__ __forceinline__ void load_uniform(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid, RawTile& r) {
+__device__ __forceinline__ void load_keys(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid, RawTile& r) {
   const int cb = tid & 15, f = kt * kTile + (tid >> 4) * 8;
   if (f >= src.tc.Nq) return;
   const size_t tok = (size_t)src.s * G.qcap + f;
@@ -147,11 +144,43 @@ __device__ __forceinline__ void load_uniform(const Geometry& G, const LayerPtrs&
     r.ks[0] = a.x, r.ks[1] = a.y, r.ks[2] = a.z, r.ks[3] = a.w;
     r.ks[4] = b.x, r.ks[5] = b.y, r.ks[6] = b.z, r.ks[7] = b.w;
   }
-  if constexpr (V) {
-    load_codes(L.v_codes + tok * G.vrow, G.vb, cb, r.v);
-    const uint32_t* sc = L.v_scales + tok * G.nvg + 8 * cb / G.gv;
+}
+__device__ __forceinline__ void load_values(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid, RawTile& r) {
+  const int cb = tid & 15, f = kt * kTile + (tid >> 4) * 8;
+  if (f >= src.tc.Nq) return;
+  const size_t tok = (size_t)src.s * G.qcap + f;
+  load_codes(L.v_codes + tok * G.vrow, G.vb, cb, r.v);
+  const uint32_t* sc = L.v_scales + tok * G.nvg + 8 * cb / G.gv;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) r.vs[u] = __ldg(sc + u * G.nvg);
+  for (int u = 0; u < 8; ++u) r.vs[u] = __ldg(sc + u * G.nvg);
+}
+
+// Ask for quantized tile kt in L2 (one thread): codes and scales of its keys
+// are contiguous, whole multiples of 16 bytes.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  if (bytes)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
+}
+template <bool V>
+__device__ __forceinline__ void prefetch_tile(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt) {
+  const int f = kt * kTile, n = min(kTile, src.tc.Nq - f);  // whole groups
+  if (n <= 0) return;
+  const size_t tok = (size_t)src.s * G.qcap + f;
+  prefetch_l2(L.k_codes + tok * G.krow, n * G.krow);
+  if (G.kb == 3) prefetch_l2(L.k_scales + tok, n * 4);
+  else if (G.gkc) prefetch_l2(L.k_scales + tok * G.nkg, n * G.nkg * 4);
+  else prefetch_l2(L.k_scales + tok * (kHeadDim / kGroupTokens), n * (kHeadDim / kGroupTokens) * 4);
+  if constexpr (V) {
+    prefetch_l2(L.v_codes + tok * G.vrow, n * G.vrow);
+    prefetch_l2(L.v_scales + tok * (G.vb == 3 ? 1 : G.nvg), n * (G.vb == 3 ? 1 : G.nvg) * 4);
+  }
+  if (G.kb == 3 && G.nout) {
+    prefetch_l2(L.k_col + tok * G.nout, n * G.nout);
+    prefetch_l2(L.k_val + tok * G.nout, n * G.nout * 2);
+    if constexpr (V) {
+      prefetch_l2(L.v_col + tok * G.nout, n * G.nout);
+      prefetch_l2(L.v_val + tok * G.nout, n * G.nout * 2);
+    }
   }
 }
 
@@ -162,32 +191,85 @@ __device__ __forceinline__ constexpr int pair_a(int i) { return BITS == 8 ? 2 * 
 template <int BITS>
 __device__ __forceinline__ constexpr int pair_b(int i) { return BITS == 8 ? 2 * i + 1 : i + 4; }
 
-// Keys of a uniform tile: K^ = min + code * scale in fp32 (the product of an
-// integer code and an fp16 scale is exact, so the sum rounds once), then
-// times the channel norm, then split into two fp16 parts.
-template <int BITS, bool IQ>
-__device__ __forceinline__ void keys_uniform(const Geometry& G, const LayerPtrs& L, int s, bool have, int tid, const RawTile& r,
-                                             uint8_t* sK, uint8_t* sN) {
+// Keys of a uniform tile with a scale per channel and group of 32 tokens:
+//   k = c' s + (m + 2^(b-1) s),  c' = code - 2^(b-1).
+// The product c' s has 19 bits: its fp16 value hi and the rest neg = hi - c' s
+// are exact.  The other part is the same for the 32 keys of a group, so it
+// reaches the logits as one number per row and group, q . m + 2^(b-1) q . s:
+// rows 0..3 of sM hold the tile's groups' m, rows 4..7 their s (8 rows of 128
+// channels, q_off<8>).  Half the instructions of an fp32 k split in two.
+template <int BITS>
+__device__ __forceinline__ void keys_channel(bool have, int tid, const RawTile& r, uint8_t* sK, uint8_t* sN) {
   const int cb = tid & 15, t0 = (tid >> 4) * 8;
-  float norm[8];
-  if (IQ && G.knorm) {
+  __half2 sc[4];
+  bool big = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) norm[i] = __ldg(L.k_norm + (size_t)s * kHeadDim + 8 * cb + i);
+  for (int i = 0; i < 4; ++i) {
+    sc[i] = as_h2(__byte_perm(r.ks[pair_a<BITS>(i)], r.ks[pair_b<BITS>(i)], 0x7632));
+    const float2 f = __half22float2(sc[i]);
+    big = big || fmaxf(fabsf(f.x), fabsf(f.y)) * (1 << (BITS - 1)) > 65504.0f;  // c' s may pass the fp16 range
   }
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     uint32_t hi[4] = {0, 0, 0, 0}, neg[4] = {0, 0, 0, 0};
     if (have) {
       __half2 c[4];
+      code_pairs<BITS, true>(r.k[u], c);
+      if (!big) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 h = __hmul2(c[i], sc[i]);
+          hi[i] = as_u32(h);
+          neg[i] = as_u32(__hfma2(__hneg2(c[i]), sc[i], h));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = __half22float2(c[i]), b = __half22float2(sc[i]);
+          split2(a.x * b.x, a.y * b.y, &hi[i], &neg[i]);
+        }
+      }
+    }
+    const uint32_t o = tile_off(t0 + u, cb);
+    *reinterpret_cast<uint4*>(sK + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(sN + o) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+  }
+}
+template <int BITS>
+__device__ __forceinline__ void group_rows(bool have, int tid, const RawTile& r, uint8_t* sM) {
+  const int cb = tid & 15, tg = tid >> 4;
+  if (tg & 3) return;  // the first of the group's four threads of a channel chunk
+  uint32_t m[4] = {0, 0, 0, 0}, sc[4] = {0, 0, 0, 0};
+  if (have)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = __byte_perm(r.ks[pair_a<BITS>(i)], r.ks[pair_b<BITS>(i)], 0x5410);
+      sc[i] = __byte_perm(r.ks[pair_a<BITS>(i)], r.ks[pair_b<BITS>(i)], 0x7632);
+    }
+  *reinterpret_cast<uint4*>(sM + q_off<8>(tg >> 2, cb)) = make_uint4(m[0], m[1], m[2], m[3]);
+  *reinterpret_cast<uint4*>(sM + q_off<8>(4 + (tg >> 2), cb)) = make_uint4(sc[0], sc[1], sc[2], sc[3]);
+}
+
+// Keys of a uniform tile with a scale per token and 64 channels (InnerQ):
+// k = (min + code * scale) * norm in fp32, split into two fp16 parts.
+template <int BITS>
+__device__ __forceinline__ void keys_token(const Geometry& G, const LayerPtrs& L, int s, bool have, int tid, const RawTile& r,
+                                           uint8_t* sK, uint8_t* sN) {
+  const int cb = tid & 15, t0 = (tid >> 4) * 8;
+  float norm[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) norm[i] = G.knorm ? __ldg(L.k_norm + (size_t)s * kHeadDim + 8 * cb + i) : 1.0f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    uint32_t hi[4] = {0, 0, 0, 0}, neg[4] = {0, 0, 0, 0};
+    if (have) {
+      __half2 c[4];
       code_pairs<BITS>(r.k[u], c);
+      const float2 ms = unpack_min_scale(r.ks[u]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int a = pair_a<BITS>(i), b = pair_b<BITS>(i);
-        const __half2 ma = as_h2(r.ks[IQ ? u : a]), mb = as_h2(r.ks[IQ ? u : b]);
-        float x0 = fma_h(__low2half(c[i]), __high2half(ma), __low2float(ma));
-        float x1 = fma_h(__high2half(c[i]), __high2half(mb), __low2float(mb));
-        if (IQ && G.knorm) x0 *= norm[a], x1 *= norm[b];
-        split2(x0, x1, &hi[i], &neg[i]);
+        const float2 f = __half22float2(c[i]);
+        split2(fmaf(f.x, ms.y, ms.x) * norm[pair_a<BITS>(i)], fmaf(f.y, ms.y, ms.x) * norm[pair_b<BITS>(i)], &hi[i], &neg[i]);
       }
     }
     const uint32_t o = tile_off(t0 + u, cb);
@@ -220,28 +302,31 @@ __device__ __forceinline__ void values_uniform(bool have, int tid, const RawTile
   }
 }
 
-template <bool V>
-__device__ __forceinline__ void fill_uniform(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid,
-                                             const RawTile& r, uint8_t* sK, uint8_t* sN, uint8_t* sV) {
+__device__ __forceinline__ void fill_uniform_keys(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid,
+                                                  const RawTile& r, uint8_t* sK, uint8_t* sN) {
   const bool have = kt * kTile + (tid >> 4) * 8 < src.tc.Nq;
-  if (sK) {
-    if (G.gkc) {
-      if (G.kb == 8) keys_uniform<8, true>(G, L, src.s, have, tid, r, sK, sN);
-      else if (G.kb == 4) keys_uniform<4, true>(G, L, src.s, have, tid, r, sK, sN);
-      else keys_uniform<2, true>(G, L, src.s, have, tid, r, sK, sN);
-    } else {
-      if (G.kb == 8) keys_uniform<8, false>(G, L, src.s, have, tid, r, sK, sN);
-      else if (G.kb == 4) keys_uniform<4, false>(G, L, src.s, have, tid, r, sK, sN);
-      else keys_uniform<2, false>(G, L, src.s, have, tid, r, sK, sN);
-    }
+  if (G.gkc) {
+    if (G.kb == 8) keys_token<8>(G, L, src.s, have, tid, r, sK, sN);
+    else if (G.kb == 4) keys_token<4>(G, L, src.s, have, tid, r, sK, sN);
+    else keys_token<2>(G, L, src.s, have, tid, r, sK, sN);
+  } else {
+    if (G.kb == 8) keys_channel<8>(have, tid, r, sK, sN);
+    else if (G.kb == 4) keys_channel<4>(have, tid, r, sK, sN);
+    else keys_channel<2>(have, tid, r, sK, sN);
   }
-  if constexpr (V) {
-    if (sV) {
-      if (G.vb == 8) values_uniform<8>(have, tid, r, sV);
-      else if (G.vb == 4) values_uniform<4>(have, tid, r, sV);
-      else values_uniform<2>(have, tid, r, sV);
-    }
-  }
+}
+__device__ __forceinline__ void fill_group_rows(const Geometry& G, const TileSrc& src, int kt, int tid, const RawTile& r, uint8_t* sM) {
+  const bool have = kt * kTile + (tid >> 4) * 8 < src.tc.Nq;
+  if (G.kb == 8) group_rows<8>(have, tid, r, sM);
+  else if (G.kb == 4) group_rows<4>(have, tid, r, sM);
+  else group_rows<2>(have, tid, r, sM);
+}
+__device__ __forceinline__ void fill_uniform_values(const Geometry& G, const TileSrc& src, int kt, int tid, const RawTile& r,
+                                                    uint8_t* sV) {
+  const bool have = kt * kTile + (tid >> 4) * 8 < src.tc.Nq;
+  if (G.vb == 8) values_uniform<8>(have, tid, r, sV);
+  else if (G.vb == 4) values_uniform<4>(have, tid, r, sV);
+  else values_uniform<2>(have, tid, r, sV);
 }
 
 // ------------------------------------------- non-uniform codes, RoPE, fp16

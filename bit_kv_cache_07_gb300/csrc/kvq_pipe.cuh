@@ -12,6 +12,8 @@ namespace kvq {
 constexpr int kProducers = 256;
 constexpr uint32_t kTileBytes = kTile * kHeadDim * 2;  // 32 KB
 constexpr uint32_t kStageBytes = 3 * kTileBytes;       // K hi, K neg, V
+constexpr uint32_t kGroupRowBytes = 8 * kHeadDim * 2;  // the groups' min and scale rows
+constexpr int kAhead = 3;                              // tiles asked for in L2 ahead of their loads
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -41,13 +43,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, volatile
   }
   *gave_up = 1;
   return false;
-}
-
-// Byte offset of a 16-byte chunk of query row r among ROWS rows (two halves
-// of 64 channels, swizzled like the tiles).
-template <int ROWS>
-__device__ __forceinline__ uint32_t q_off(int r, int chunk) {
-  return (uint32_t)((chunk >> 3) * (ROWS * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
 }
 
 // A piece of the CTA's range: consecutive tiles of one kind of one (b, h, row
@@ -83,7 +78,7 @@ struct Bars {  // shared-memory addresses; by stage (o_done, done: one)
 
 // ------------------------------------------------------------- producers
 template <int ROWS>
-__device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint8_t* sQ, uint8_t* stage0, const float* lut,
+__device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint8_t* sQ, uint8_t* stage0, uint8_t* sM, const float* lut,
                                         volatile int* bad_piece, int x, int x_end, int tid, volatile int* gave_up) {
   const Geometry& G = p.geo;
   const bool general = G.pre_rope || G.kb == 3;
@@ -92,11 +87,14 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
     const Piece c = piece_at(p, x, x_end);
     const TileSrc src{c.tc, c.s, c.b, p.mask ? c.n_b : 0, c.tc.Nq % G.ring, in_stream(G, c.s) * p.n};
     RawTile raw;
-    if (c.quant && !general) load_uniform<true>(G, p.L, src, c.k0, tid, raw);
+    const bool uniform = c.quant && !general;
+    if (c.quant && tid == 0)
+      for (int k = c.k0 + (uniform ? 1 : 0); k < min(c.k0 + kAhead, c.k0 + c.cnt); ++k) prefetch_tile<true>(G, p.L, src, k);
+    if (uniform) load_keys(G, p.L, src, c.k0, tid, raw), load_values(G, p.L, src, c.k0, tid, raw);
     // the previous piece's last product has read Q
     if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
     const uint16_t* qb = p.q + ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n * kHeadDim;
-    const bool paired = c.quant && !general && paired_order(G.kb);
+    const bool paired = uniform && paired_order(G.kb);
 #pragma unroll
     for (int u = 0; u < ROWS / 16; ++u) {
       const int r = (tid >> 4) + 16 * u, ch = tid & 15;
@@ -116,17 +114,24 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
       if (!c.quant) fill_fp16_keys(G, p.L, p.freq, p.kd, src, k, tid, sK, sN);
       else if (general) fill_general_keys(G, p.L, p.freq, lut, src, k, tid, sK, sN);
-      else fill_uniform<true>(G, p.L, src, k, tid, raw, sK, sN, nullptr);
+      else fill_uniform_keys(G, p.L, src, k, tid, raw, sK, sN);
+      if (uniform && !G.gkc) {  // (one buffer: the tile before must have been read)
+        if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
+        fill_group_rows(G, src, k, tid, raw, sM);
+      }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       mbar_arrive(B.full_k + 8 * st);
+      const bool more = k + 1 < c.k0 + c.cnt;
+      if (uniform && more) load_keys(G, p.L, src, k + 1, tid, raw);  // in flight under the values' conversion
+      if (c.quant && tid == 0 && k + kAhead < c.k0 + c.cnt) prefetch_tile<true>(G, p.L, src, k + kAhead);
       if (i >= 2 && !mbar_wait(B.empty_v + 8 * st, again, gave_up)) return;
       if (!c.quant) bad |= fill_fp16_values(G, p.L, p.vd, src, k, tid, sV);
       else if (general) fill_general_values(G, p.L, lut + 8, src, k, tid, sV);
-      else fill_uniform<true>(G, p.L, src, k, tid, raw, nullptr, nullptr, sV);
+      else fill_uniform_values(G, src, k, tid, raw, sV);
       if (bad) bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       mbar_arrive(B.full_v + 8 * st);
-      if (c.quant && !general && k + 1 < c.k0 + c.cnt) load_uniform<true>(G, p.L, src, k + 1, tid, raw);
+      if (uniform && more) load_values(G, p.L, src, k + 1, tid, raw);
     }
     x += c.cnt;
   }

@@ -15,7 +15,7 @@ namespace {
 constexpr int kSmallRows = 16;
 constexpr int kConsumers = 128;
 constexpr int kThreadsSmall = kConsumers + kProducers;
-constexpr uint32_t kSmemSmall = 1024 + kSmallRows * kHeadDim * 2 + 2 * kStageBytes + 256;
+constexpr uint32_t kSmemSmall = 1024 + kSmallRows * kHeadDim * 2 + 2 * kStageBytes + kGroupRowBytes + 256;
 static_assert(kSmemSmall <= 227 * 1024, "shared memory of one CTA");
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -46,15 +46,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // The same producers fill the tiles; 4 warps take 32 keys of each with
 // mma.sync (m16n8k16), every warp with its own softmax state and partial
 // result.
-__device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, const uint8_t* sQ, const uint8_t* stage0,
+__device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, const uint8_t* sQ, const uint8_t* stage0, const uint8_t* sM,
                                         volatile int* bad_piece, int x, int x_end, int tid, volatile int* gave_up) {
   auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
   const int lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3;
-  const uint32_t aQ = (uint32_t)__cvta_generic_to_shared(sQ), a0 = (uint32_t)__cvta_generic_to_shared(stage0);
+  const uint32_t aQ = (uint32_t)__cvta_generic_to_shared(sQ), a0 = (uint32_t)__cvta_generic_to_shared(stage0),
+                 aM = (uint32_t)__cvta_generic_to_shared(sM);
   int i = 0;
   for (int piece = 0; x < x_end; ++piece) {
     const Piece c = piece_at(p, x, x_end);
-    const bool two = c.quant || p.geo.pre_rope;
+    const bool two = c.quant || p.geo.pre_rope, grouped = channel_scales(p.geo) && c.quant;
     const uint32_t* mask_row[2] = {nullptr, nullptr};
     if (p.mask && !c.quant)
 #pragma unroll
@@ -89,6 +90,24 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
             mma16816(zn[n + 1], qa[ks], kb[2], kb[3]);
           }
         }
+      float base[2] = {0.0f, 0.0f};  // rows g, g + 8: what the warp's 32 keys, one group, share
+      if (grouped) {
+        float zg[4] = {};
+#pragma unroll
+        for (int ks = 0; ks < 8; ks += 2) {
+          uint32_t kb[4];
+          ldsm4(kb, aM + q_off<8>(lane & 7, 2 * ks + (lane >> 3)));
+          mma16816(zg, qa[ks], kb[0], kb[1]);
+          mma16816(zg, qa[ks + 1], kb[2], kb[3]);
+        }
+        // column n (min of group n), 4 + n (its scale): lane 4 g + n / 2, element n & 1
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float a = (w & 1) ? zg[2 * e + 1] : zg[2 * e];
+          const float mn = __shfl_sync(0xffffffffu, a, (lane & ~3) + (w >> 1)), sc = __shfl_sync(0xffffffffu, a, (lane & ~3) + 2 + (w >> 1));
+          base[e] = fmaf((float)(1 << (p.geo.kb - 1)), sc, mn);
+        }
+      }
       mbar_arrive(B.empty_k + 8 * st);
       const int f0 = (c.k0 + t) * kTile + 32 * w;
       uint32_t ok[2];
@@ -99,7 +118,7 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          z[n][e] = (ok[e >> 1] >> (8 * n + 2 * tq + (e & 1))) & 1 ? (z[n][e] - zn[n][e]) * p.q_scale : -INFINITY;
+          z[n][e] = (ok[e >> 1] >> (8 * n + 2 * tq + (e & 1))) & 1 ? (z[n][e] - zn[n][e] + base[e >> 1]) * p.q_scale : -INFINITY;
           mx[e >> 1] = fmaxf(mx[e >> 1], z[n][e]);
         }
 #pragma unroll
@@ -172,7 +191,7 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
 __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (1024 - ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
-  uint8_t *stage0 = smem, *sQ = stage0 + 2 * kStageBytes, *tail = sQ + kSmallRows * kHeadDim * 2;
+  uint8_t *stage0 = smem, *sQ = stage0 + 2 * kStageBytes, *sM = sQ + kSmallRows * kHeadDim * 2, *tail = sM + kGroupRowBytes;
   volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 132);
   volatile int* bad_piece = reinterpret_cast<volatile int*>(tail + 208);
   float* lut = reinterpret_cast<float*>(tail + 144);
@@ -193,8 +212,8 @@ __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __gr
   if (tid < 16) lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
   __syncthreads();
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
-  if (tid < kConsumers) consume(p, B, sQ, stage0, bad_piece, x, x_end, tid, gave_up);
-  else produce<kSmallRows>(p, B, sQ, stage0, lut, bad_piece, x, x_end, tid - kConsumers, gave_up);
+  if (tid < kConsumers) consume(p, B, sQ, stage0, sM, bad_piece, x, x_end, tid, gave_up);
+  else produce<kSmallRows>(p, B, sQ, stage0, sM, lut, bad_piece, x, x_end, tid - kConsumers, gave_up);
   __syncthreads();
   if (*gave_up) {  // a wait ran out: every row of the range becomes NaN
     for (int y = x; y < x_end;) {

@@ -100,6 +100,10 @@ __host__ __device__ inline int row_of(const int* tab, int rows, int v) {
   return lo;
 }
 
+// Keys with a scale per channel and group that the tile kernels take apart
+// (kvq_fill.cuh: keys_channel).
+__host__ __device__ inline bool channel_scales(const Geometry& G) { return !G.pre_rope && G.kb != 3 && !G.gkc && !G.fp16_mode; }
+
 #ifdef __CUDACC__
 
 // Byte offset of channel c of key t in a tile: two halves of 64 channels,

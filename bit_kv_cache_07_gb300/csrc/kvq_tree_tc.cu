@@ -8,8 +8,10 @@
 // S = Q K^T accumulates in TMEM (two buffers of 128 columns: the next tile's
 // logits are computed under this tile's exponentials), the weights return
 // there as fp16 over the logits they came from, and O += P V reads them from
-// TMEM (O in columns 256..383).  Keys enter as hi - neg (22 bits): two passes
-// of the 128-channel product for quantized keys, one for fp16 ones.
+// TMEM (O in columns 256..383).  Quantized keys enter in two exact fp16 parts
+// (two passes of the 128-channel product), fp16 keys in one; what the 32 keys
+// of a per-channel group share comes from a 16-column product with the groups'
+// min and scale rows (columns 384 + 16 st).
 // The maximum moves only when a logit passes it by 2^8 (weights then stay
 // below fp16's range), so O is rarely rescaled.
 // 13 warps leave every thread 128 registers (17 would leave 96, and spills).
@@ -20,7 +22,9 @@ namespace {
 
 constexpr int kSoftThreads = 128;
 constexpr int kThreadsTc = kSoftThreads + kProducers + 32;
-constexpr uint32_t kSmemTc = 1024 + kTileBytes + 2 * kStageBytes + 256;
+// The 16-column product reads 8 rows behind the group rows as its columns
+// 8..15 (of no use): the kilobyte that holds the barriers.
+constexpr uint32_t kSmemTc = kTileBytes + 2 * kStageBytes + kGroupRowBytes + 1024;
 static_assert(kSmemTc <= 227 * 1024, "shared memory of one CTA");
 constexpr float kLazy = 8.0f;  // log2 units
 
@@ -33,6 +37,7 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
 }
 // fp32 accumulator, fp16 operands, M = N = 128.
 constexpr uint32_t kIdesc = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);
+constexpr uint32_t kIdesc16 = (1u << 4) | ((16u / 8) << 17) | ((128u / 16) << 24);  // N = 16
 constexpr uint32_t kNegB = 1u << 14, kRowsB = 1u << 16;  // B negated; B's keys along its rows
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -77,6 +82,14 @@ __device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
                  "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                  "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
+__device__ __forceinline__ void tm_load8(uint32_t (&r)[8], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
@@ -110,13 +123,14 @@ __device__ __forceinline__ bool issue_pv(const Bars& B, uint32_t tmem, uint32_t 
   mma_commit(B.o_done);
   return true;
 }
-__device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t q, uint32_t stage0, int x,
-                                      int x_end, volatile int* gave_up) {
+__device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t q, uint32_t stage0, uint32_t rows,
+                                      int x, int x_end, volatile int* gave_up) {
   int i = 0;
   bool first_prev = false;
   while (x < x_end) {
     const Piece c = piece_at(p, x, x_end);
     const int parts = c.quant || p.geo.pre_rope ? 2 : 1;
+    const bool grouped = channel_scales(p.geo) && c.quant;
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
       if (!mbar_wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
@@ -129,6 +143,12 @@ __device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32
           mma_ss(tmem + 128 * st, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), kIdesc | (part ? kNegB : 0),
                  part + ks > 0);
         }
+      }
+      if (grouped) {  // q . m and q . s of the tile's four groups (columns 8..15 are of no use)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(tmem + 384 + 16 * st, smem_desc(q + (ks >> 2) * (kTile * 128) + (ks & 3) * 32, 16, 1024),
+                 smem_desc(rows + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 1024), kIdesc16, ks > 0);
       }
       mma_commit(B.s_full + 8 * st);
       mma_commit(B.empty_k + 8 * st);
@@ -154,6 +174,8 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
     const bool work = (r & ~31) < c.nr;  // the warp holds rows
     const uint32_t* mask_row =
         p.mask && !c.quant && r < c.nr ? p.mask + ((size_t)c.b * p.n + (c.r0 + r) % c.n_b) * p.words : nullptr;
+    const bool grouped = channel_scales(p.geo) && c.quant;
+    const float centre = (float)(1 << (p.geo.kb - 1));
     float m = -INFINITY, l = 0.0f;
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
@@ -163,22 +185,30 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
       if (work) {
         const int f0 = (c.k0 + t) * kTile;
         uint32_t ok[4], v[32];
-        float top = -INFINITY;
+        float top = -INFINITY, base[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // the groups' share of the logits
+        if (grouped) {
+          uint32_t y[8];
+          tm_load8(y, tmem + 384 + 16 * st + lane0);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch)
+            base[ch] = fmaf(centre, __uint_as_float(y[4 + ch]), __uint_as_float(y[ch])) * p.q_scale;
+        }
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           ok[ch] = seen(p, c, mask_row, f0 + 32 * ch);
           tm_load32(v, S + 32 * ch);
           tm_wait_ld(v);
+          float mx = -INFINITY;
           if (ok[ch] == 0xFFFFFFFFu) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if ((ok[ch] >> e) & 1) top = fmaxf(top, __uint_as_float(v[e]));
+              if ((ok[ch] >> e) & 1) mx = fmaxf(mx, __uint_as_float(v[e]));
           }
+          top = fmaxf(top, fmaf(mx, p.q_scale, base[ch]));
         }
-        top *= p.q_scale;
         const bool move = top > m + kLazy;
         if (__any_sync(0xffffffffu, move)) {
           const float al = move ? ex2(m - top) : 1.0f;
@@ -203,14 +233,15 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
           tm_load32(v, S + 32 * ch);
           tm_wait_ld(v);
           uint32_t h[16];
+          const float off = base[ch] - mu;
           if (ok[ch] != 0xFFFFFFFFu) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = (ok[ch] >> e) & 1 ? v[e] : 0xFF800000u;  // -inf
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float a = ex2(fmaf(__uint_as_float(v[2 * e]), p.q_scale, -mu));
-            const float b = ex2(fmaf(__uint_as_float(v[2 * e + 1]), p.q_scale, -mu));
+            const float a = ex2(fmaf(__uint_as_float(v[2 * e]), p.q_scale, off));
+            const float b = ex2(fmaf(__uint_as_float(v[2 * e + 1]), p.q_scale, off));
             l += a + b;
             h[e] = as_u32(__floats2half2_rn(a, b));
           }
@@ -253,8 +284,7 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
 
 __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + (1024 - ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
-  uint8_t *sQ = smem, *stage0 = smem + kTileBytes, *tail = stage0 + 2 * kStageBytes;
+  uint8_t *sQ = smem_raw, *stage0 = sQ + kTileBytes, *sM = stage0 + 2 * kStageBytes, *tail = sM + kGroupRowBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 128);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 132);
@@ -274,7 +304,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
     }
     mbar_init(B.o_done, 1);
     mbar_init(B.done, 1);
-    *gave_up = 0;
+    // (the swizzle's 1024-byte alignment: there is no other shared memory to shift the start)
+    *gave_up = ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023) != 0;
     for (int i = 0; i < 4; ++i) bad_piece[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -291,13 +322,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
   tc_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
-  if (w < kSoftThreads / 32) {
+  if (*gave_up) {
+  } else if (w < kSoftThreads / 32) {
     softmax(p, B, tmem, bad_piece, x, x_end, tid, gave_up);
   } else if (w < issuer) {
-    produce<kTile>(p, B, sQ, stage0, lut, bad_piece, x, x_end, tid - kSoftThreads, gave_up);
+    produce<kTile>(p, B, sQ, stage0, sM, lut, bad_piece, x, x_end, tid - kSoftThreads, gave_up);
   } else {
     if ((tid & 31) == 0) {
-      issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(sQ), (uint32_t)__cvta_generic_to_shared(stage0), x, x_end, gave_up);
+      issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(sQ), (uint32_t)__cvta_generic_to_shared(stage0),
+            (uint32_t)__cvta_generic_to_shared(sM), x, x_end, gave_up);
       mma_commit(B.done);  // whatever is in flight ends before TMEM is freed
       mbar_wait(B.done, 0, gave_up);
     }
