@@ -1,16 +1,14 @@
-// kvq_fill.cuh -- dequantization of 128-key tiles into the shared-memory
-// operands of the matrix instructions (kvq_tree_tc.cu, kvq_mass.cu): keys as
-// hi + lo fp16 parts (22 bits), values as fp16, rows of 128 bytes with the
-// 128-byte swizzle (tile_off).
+// kvq_fill.cuh -- dequantization of 96-key tiles into the shared-memory
+// operands of the matrix instructions: keys in two fp16 parts (22 bits),
+// values as fp16, rows of 128 bytes with the 128-byte swizzle (tile_off).
 //
-// 256 threads fill a tile.  The raw codes and scales of a tile are read into
-// registers first (load) and converted later (keys, values), so that a tile's
-// loads are in flight while the one before it is waited for.
-//
-// Two mappings.  Uniform codes without RoPE: a thread owns 8 channels of 8
-// consecutive keys (of one group: a channel's scale is read once for 8
-// codes).  Non-uniform codes and keys cached before RoPE: a thread owns 8
-// channel pairs (c, c + 64) of 4 consecutive keys.
+// A tile's stored bytes come to shared memory by asynchronous bulk copies,
+// several tiles ahead (load_tile); 256 threads convert them in short loops,
+// whose code stays in the instruction caches (unrolled over registers, the
+// fetches cost as much as the work).  Thread (tid & 15) owns 8 channels,
+// tid >> 4 the keys 32 j + (tid >> 4) and + 16 of group j; with RoPE or
+// non-uniform codes, tid & 7 owns the channel pairs (c, c + 64) of key
+// 32 j + (tid >> 3).
 #pragma once
 
 #include "kvq_tree.cuh"
@@ -102,86 +100,45 @@ struct TileSrc {
   size_t draft0;      // first row of the stream in k_draft / v_draft
 };
 
-// Raw codes and scales of a thread's share of a tile.
-struct RawTile {
-  uint2 k[8], v[8];
-  uint32_t ks[8], vs[8];
-};
-
-// One load per key, without a branch between them: they are all in flight at
-// once (a branch per load made each wait for the one before).
-template <int BITS>
-__device__ __forceinline__ void load_codes(const uint8_t* rows, int pitch, int chunk, uint2 (&c)[8]) {
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const uint8_t* row = rows + u * pitch;
-    if constexpr (BITS == 8) c[u] = __ldg(reinterpret_cast<const uint2*>(row) + chunk);
-    else if constexpr (BITS == 4) c[u].x = __ldg(reinterpret_cast<const uint32_t*>(row) + chunk);
-    else c[u].x = __ldg(reinterpret_cast<const uint16_t*>(row) + chunk);
-  }
-}
-__device__ __forceinline__ void load_codes(const uint8_t* rows, int bits, int chunk, uint2 (&c)[8]) {
-  if (bits == 8) load_codes<8>(rows, 128, chunk, c);
-  else if (bits == 4) load_codes<4>(rows, 64, chunk, c);
-  else load_codes<2>(rows, 32, chunk, c);
-}
-
-// Uniform codes: the thread's loads of quantized tile kt.  Keys past the end
-// are not read (Nq is a whole number of groups, so a thread's 8 keys are all
-// there or none).
-__device__ __forceinline__ void load_keys(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid, RawTile& r) {
-  const int cb = tid & 15, f = kt * kTile + (tid >> 4) * 8;
-  if (f >= src.tc.Nq) return;
-  const size_t tok = (size_t)src.s * G.qcap + f;
-  load_codes(L.k_codes + tok * G.krow, G.kb, cb, r.k);
-  if (G.gkc) {
-    const uint32_t* sc = L.k_scales + tok * 2 + (cb >> 3);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) r.ks[u] = __ldg(sc + 2 * u);
-  } else {
-    const uint4* sc = reinterpret_cast<const uint4*>(L.k_scales + ((size_t)src.s * G.gcap + f / kGroupTokens) * kHeadDim + 8 * cb);
-    const uint4 a = __ldg(sc), b = __ldg(sc + 1);
-    r.ks[0] = a.x, r.ks[1] = a.y, r.ks[2] = a.z, r.ks[3] = a.w;
-    r.ks[4] = b.x, r.ks[5] = b.y, r.ks[6] = b.z, r.ks[7] = b.w;
-  }
-}
-__device__ __forceinline__ void load_values(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid, RawTile& r) {
-  const int cb = tid & 15, f = kt * kTile + (tid >> 4) * 8;
-  if (f >= src.tc.Nq) return;
-  const size_t tok = (size_t)src.s * G.qcap + f;
-  load_codes(L.v_codes + tok * G.vrow, G.vb, cb, r.v);
-  const uint32_t* sc = L.v_scales + tok * G.nvg + 8 * cb / G.gv;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) r.vs[u] = __ldg(sc + u * G.nvg);
-}
-
-// Ask for quantized tile kt in L2 (one thread): codes and scales of its keys
-// are contiguous, whole multiples of 16 bytes.
+// Ask for bytes in L2 (whole multiples of 16).
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  if (bytes)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  if (bytes)
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+// Queue the copies of quantized tile kt into the slot at dst (one thread);
+// bar expects their bytes.  The keys of a tile are contiguous in every
+// region, and whole groups: sizes and starts are multiples of 16 bytes.
 template <bool V>
-__device__ __forceinline__ void prefetch_tile(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt) {
-  const int f = kt * kTile, n = min(kTile, src.tc.Nq - f);  // whole groups
-  if (n <= 0) return;
+__device__ __forceinline__ void load_tile(const Geometry& G, const LayerPtrs& L, const RawSlot& R, const TileSrc& src, int kt,
+                                          uint32_t dst, uint32_t bar) {
+  const int f = kt * kTile, n = min(kTile, src.tc.Nq - f);
   const size_t tok = (size_t)src.s * G.qcap + f;
-  prefetch_l2(L.k_codes + tok * G.krow, n * G.krow);
-  if (G.kb == 3) prefetch_l2(L.k_scales + tok, n * 4);
-  else if (G.gkc) prefetch_l2(L.k_scales + tok * G.nkg, n * G.nkg * 4);
-  else prefetch_l2(L.k_scales + tok * (kHeadDim / kGroupTokens), n * (kHeadDim / kGroupTokens) * 4);
+  const bool nuq = G.kb == 3;
+  const uint32_t ks = nuq ? 4 : G.gkc ? 4 * G.nkg : kHeadDim * 4 / kGroupTokens, vs = nuq ? 4 : 4 * G.nvg, no = nuq ? G.nout : 0;
+  const uint32_t bytes = n * (G.krow + ks + 3 * no + (V ? G.vrow + vs + 3 * no : 0));
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+  bulk_copy(dst, L.k_codes + tok * G.krow, n * G.krow, bar);
+  bulk_copy(dst + R.ks, reinterpret_cast<const uint8_t*>(L.k_scales) + tok * ks, n * ks, bar);
+  bulk_copy(dst + R.kcol, L.k_col + tok * no, n * no, bar);
+  bulk_copy(dst + R.kval, L.k_val + tok * no, n * no * 2, bar);
   if constexpr (V) {
-    prefetch_l2(L.v_codes + tok * G.vrow, n * G.vrow);
-    prefetch_l2(L.v_scales + tok * (G.vb == 3 ? 1 : G.nvg), n * (G.vb == 3 ? 1 : G.nvg) * 4);
+    bulk_copy(dst + R.v, L.v_codes + tok * G.vrow, n * G.vrow, bar);
+    bulk_copy(dst + R.vs, reinterpret_cast<const uint8_t*>(L.v_scales) + tok * vs, n * vs, bar);
+    bulk_copy(dst + R.vcol, L.v_col + tok * no, n * no, bar);
+    bulk_copy(dst + R.vval, L.v_val + tok * no, n * no * 2, bar);
   }
-  if (G.kb == 3 && G.nout) {
-    prefetch_l2(L.k_col + tok * G.nout, n * G.nout);
-    prefetch_l2(L.k_val + tok * G.nout, n * G.nout * 2);
-    if constexpr (V) {
-      prefetch_l2(L.v_col + tok * G.nout, n * G.nout);
-      prefetch_l2(L.v_val + tok * G.nout, n * G.nout * 2);
-    }
-  }
+}
+
+template <int BITS>
+__device__ __forceinline__ uint2 chunk_word(const uint8_t* rows, int t, int chunk) {
+  if constexpr (BITS == 8) return *reinterpret_cast<const uint2*>(rows + t * 128 + chunk * 8);
+  else if constexpr (BITS == 4) return make_uint2(*reinterpret_cast<const uint32_t*>(rows + t * 64 + chunk * 4), 0);
+  else return make_uint2(*reinterpret_cast<const uint16_t*>(rows + t * 32 + chunk * 2), 0);
 }
 
 // Channel pair i of a chunk in the operands' order: the index of its first
@@ -191,142 +148,170 @@ __device__ __forceinline__ constexpr int pair_a(int i) { return BITS == 8 ? 2 * 
 template <int BITS>
 __device__ __forceinline__ constexpr int pair_b(int i) { return BITS == 8 ? 2 * i + 1 : i + 4; }
 
+__device__ __forceinline__ void store_chunk(uint8_t* s, uint32_t off, const uint32_t (&w)[4]) {
+  *reinterpret_cast<uint4*>(s + off) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Keys of a uniform tile with a scale per channel and group of 32 tokens:
 //   k = c' s + (m + 2^(b-1) s),  c' = code - 2^(b-1).
 // The product c' s has 19 bits: its fp16 value hi and the rest neg = hi - c' s
 // are exact.  The other part is the same for the 32 keys of a group, so it
 // reaches the logits as one number per row and group, q . m + 2^(b-1) q . s:
-// rows 0..3 of sM hold the tile's groups' m, rows 4..7 their s (8 rows of 128
+// rows 0..2 of sM hold the tile's groups' m, rows 4..6 their s (8 rows of 128
 // channels, q_off<8>).  Half the instructions of an fp32 k split in two.
 template <int BITS>
-__device__ __forceinline__ void keys_channel(bool have, int tid, const RawTile& r, uint8_t* sK, uint8_t* sN) {
-  const int cb = tid & 15, t0 = (tid >> 4) * 8;
-  __half2 sc[4];
-  bool big = false;
+__device__ __forceinline__ void keys_channel(int groups, int tid, const uint8_t* raw, const uint32_t* scales, uint8_t* sK, uint8_t* sN) {
+  const int cb = tid & 15;
+#pragma unroll 1
+  for (int j = 0; j < kTile / 32; ++j) {
+    __half2 sc[4];
+    bool big = false;
+    if (j < groups) {
+      uint32_t w[8];
+      *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb];
+      *reinterpret_cast<uint4*>(w + 4) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb + 1];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    sc[i] = as_h2(__byte_perm(r.ks[pair_a<BITS>(i)], r.ks[pair_b<BITS>(i)], 0x7632));
-    const float2 f = __half22float2(sc[i]);
-    big = big || fmaxf(fabsf(f.x), fabsf(f.y)) * (1 << (BITS - 1)) > 65504.0f;  // c' s may pass the fp16 range
-  }
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    uint32_t hi[4] = {0, 0, 0, 0}, neg[4] = {0, 0, 0, 0};
-    if (have) {
-      __half2 c[4];
-      code_pairs<BITS, true>(r.k[u], c);
-      if (!big) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 h = __hmul2(c[i], sc[i]);
-          hi[i] = as_u32(h);
-          neg[i] = as_u32(__hfma2(__hneg2(c[i]), sc[i], h));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 a = __half22float2(c[i]), b = __half22float2(sc[i]);
-          split2(a.x * b.x, a.y * b.y, &hi[i], &neg[i]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        sc[i] = as_h2(__byte_perm(w[pair_a<BITS>(i)], w[pair_b<BITS>(i)], 0x7632));
+        const __half2 a = __habs2(sc[i]);
+        big = big || __hgt2_mask(a, h2_const(BITS == 8 ? 0x5FFF : BITS == 4 ? 0x6FFF : 0x77FF)) != 0;  // 2^(b-1) s > 65504
       }
     }
-    const uint32_t o = tile_off(t0 + u, cb);
-    *reinterpret_cast<uint4*>(sK + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(sN + o) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int t = 32 * j + (tid >> 4) + 16 * v;
+      uint32_t hi[4] = {0, 0, 0, 0}, neg[4] = {0, 0, 0, 0};
+      if (j < groups) {
+        __half2 c[4];
+        code_pairs<BITS, true>(chunk_word<BITS>(raw, t, cb), c);
+        if (!big) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 h = __hmul2(c[i], sc[i]);
+            hi[i] = as_u32(h);
+            neg[i] = as_u32(__hfma2(__hneg2(c[i]), sc[i], h));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = __half22float2(c[i]), b = __half22float2(sc[i]);
+            split2(a.x * b.x, a.y * b.y, &hi[i], &neg[i]);
+          }
+        }
+      }
+      const uint32_t o = tile_off(t, cb);
+      store_chunk(sK, o, hi);
+      store_chunk(sN, o, neg);
+    }
   }
 }
 template <int BITS>
-__device__ __forceinline__ void group_rows(bool have, int tid, const RawTile& r, uint8_t* sM) {
-  const int cb = tid & 15, tg = tid >> 4;
-  if (tg & 3) return;  // the first of the group's four threads of a channel chunk
-  uint32_t m[4] = {0, 0, 0, 0}, sc[4] = {0, 0, 0, 0};
-  if (have)
+__device__ __forceinline__ void group_rows(int groups, int tid, const uint32_t* scales, uint8_t* sM) {
+  if (tid >= 64) return;
+  const int cb = tid & 15, j = tid >> 4;  // (row 3: zeros)
+  uint32_t m[4] = {0, 0, 0, 0}, sc[4] = {0, 0, 0, 0}, w[8];
+  if (j < groups) {
+    *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb];
+    *reinterpret_cast<uint4*>(w + 4) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb + 1];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      m[i] = __byte_perm(r.ks[pair_a<BITS>(i)], r.ks[pair_b<BITS>(i)], 0x5410);
-      sc[i] = __byte_perm(r.ks[pair_a<BITS>(i)], r.ks[pair_b<BITS>(i)], 0x7632);
+      m[i] = __byte_perm(w[pair_a<BITS>(i)], w[pair_b<BITS>(i)], 0x5410);
+      sc[i] = __byte_perm(w[pair_a<BITS>(i)], w[pair_b<BITS>(i)], 0x7632);
     }
-  *reinterpret_cast<uint4*>(sM + q_off<8>(tg >> 2, cb)) = make_uint4(m[0], m[1], m[2], m[3]);
-  *reinterpret_cast<uint4*>(sM + q_off<8>(4 + (tg >> 2), cb)) = make_uint4(sc[0], sc[1], sc[2], sc[3]);
+  }
+  store_chunk(sM, q_off<8>(j, cb), m);
+  store_chunk(sM, q_off<8>(4 + j, cb), sc);
 }
 
 // Keys of a uniform tile with a scale per token and 64 channels (InnerQ):
 // k = (min + code * scale) * norm in fp32, split into two fp16 parts.
 template <int BITS>
-__device__ __forceinline__ void keys_token(const Geometry& G, const LayerPtrs& L, int s, bool have, int tid, const RawTile& r,
+__device__ __forceinline__ void keys_token(int groups, int tid, const uint8_t* raw, const uint32_t* scales, const float* norms,
                                            uint8_t* sK, uint8_t* sN) {
-  const int cb = tid & 15, t0 = (tid >> 4) * 8;
+  const int cb = tid & 15;
   float norm[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) norm[i] = G.knorm ? __ldg(L.k_norm + (size_t)s * kHeadDim + 8 * cb + i) : 1.0f;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
+  for (int i = 0; i < 8; ++i) norm[i] = norms ? __ldg(norms + 8 * cb + i) : 1.0f;
+#pragma unroll 1
+  for (int v = 0; v < kTile / 16; ++v) {
+    const int t = (tid >> 4) + 16 * v;
     uint32_t hi[4] = {0, 0, 0, 0}, neg[4] = {0, 0, 0, 0};
-    if (have) {
+    if ((v >> 1) < groups) {
       __half2 c[4];
-      code_pairs<BITS>(r.k[u], c);
-      const float2 ms = unpack_min_scale(r.ks[u]);
+      code_pairs<BITS>(chunk_word<BITS>(raw, t, cb), c);
+      const float2 ms = unpack_min_scale(scales[2 * t + (cb >> 3)]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(c[i]);
         split2(fmaf(f.x, ms.y, ms.x) * norm[pair_a<BITS>(i)], fmaf(f.y, ms.y, ms.x) * norm[pair_b<BITS>(i)], &hi[i], &neg[i]);
       }
     }
-    const uint32_t o = tile_off(t0 + u, cb);
-    *reinterpret_cast<uint4*>(sK + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(sN + o) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+    const uint32_t o = tile_off(t, cb);
+    store_chunk(sK, o, hi);
+    store_chunk(sN, o, neg);
   }
 }
 
 // Values of a uniform tile, rounded to fp16 once.
 template <int BITS>
-__device__ __forceinline__ void values_uniform(bool have, int tid, const RawTile& r, uint8_t* sV) {
-  const int cb = tid & 15, t0 = (tid >> 4) * 8;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    uint32_t v[4] = {0, 0, 0, 0};
-    if (have) {
+__device__ __forceinline__ void values_uniform(int groups, int tid, const uint8_t* raw, const uint32_t* scales, int nvg, int group,
+                                               uint8_t* sV) {
+  const int cb = tid & 15;
+#pragma unroll 2
+  for (int v = 0; v < kTile / 16; ++v) {
+    const int t = (tid >> 4) + 16 * v;
+    uint32_t y[4] = {0, 0, 0, 0};
+    if ((v >> 1) < groups) {
       __half2 c[4];
-      code_pairs<BITS>(r.v[u], c);
-      const __half2 ms = as_h2(r.vs[u]), mn = __low2half2(ms), sc = __high2half2(ms);
+      code_pairs<BITS>(chunk_word<BITS>(raw, t, cb), c);
+      const uint32_t w = scales[t * nvg + group];
+      const __half2 mn = __low2half2(as_h2(w)), sc = __high2half2(as_h2(w));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = as_u32(__hfma2(c[i], sc, mn));
+      for (int i = 0; i < 4; ++i) y[i] = as_u32(__hfma2(c[i], sc, mn));
+      // |min| from 2^15 on, or a scale from 2^7 (2^11, 2^13 for 4 and 2 bits) on:
       // the largest code's value may pass the fp16 range by the scale's rounding
-      if (fabsf(__low2float(ms)) + (float)((1 << BITS) - 1) * fabsf(__high2float(ms)) > 65504.0f) {
+      constexpr uint32_t kBig = BITS == 8 ? 0x28000800u : BITS == 4 ? 0x18000800u : 0x10000800u;
+      if (((w & 0x7FFF7FFFu) + kBig) & 0x80008000u) {
         const __half2 top = h2_const(0x7BFF), bottom = h2_const(0xFBFF);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(v[i]), top), bottom));
+        for (int i = 0; i < 4; ++i) y[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(y[i]), top), bottom));
       }
     }
-    *reinterpret_cast<uint4*>(sV + tile_off(t0 + u, cb)) = make_uint4(v[0], v[1], v[2], v[3]);
+    store_chunk(sV, tile_off(t, cb), y);
   }
 }
 
-__device__ __forceinline__ void fill_uniform_keys(const Geometry& G, const LayerPtrs& L, const TileSrc& src, int kt, int tid,
-                                                  const RawTile& r, uint8_t* sK, uint8_t* sN) {
-  const bool have = kt * kTile + (tid >> 4) * 8 < src.tc.Nq;
+__device__ __forceinline__ int tile_groups(const TileSrc& src, int kt) { return min(kTile / 32, (src.tc.Nq - kt * kTile) / 32); }
+
+__device__ __forceinline__ void fill_uniform_keys(const Geometry& G, const LayerPtrs& L, const RawSlot& R, const TileSrc& src, int kt,
+                                                  int tid, const uint8_t* raw, uint8_t* sK, uint8_t* sN) {
+  const int groups = tile_groups(src, kt);
+  const uint32_t* sc = reinterpret_cast<const uint32_t*>(raw + R.ks);
   if (G.gkc) {
-    if (G.kb == 8) keys_token<8>(G, L, src.s, have, tid, r, sK, sN);
-    else if (G.kb == 4) keys_token<4>(G, L, src.s, have, tid, r, sK, sN);
-    else keys_token<2>(G, L, src.s, have, tid, r, sK, sN);
+    const float* norm = G.knorm ? L.k_norm + (size_t)src.s * kHeadDim : nullptr;
+    if (G.kb == 8) keys_token<8>(groups, tid, raw, sc, norm, sK, sN);
+    else if (G.kb == 4) keys_token<4>(groups, tid, raw, sc, norm, sK, sN);
+    else keys_token<2>(groups, tid, raw, sc, norm, sK, sN);
   } else {
-    if (G.kb == 8) keys_channel<8>(have, tid, r, sK, sN);
-    else if (G.kb == 4) keys_channel<4>(have, tid, r, sK, sN);
-    else keys_channel<2>(have, tid, r, sK, sN);
+    if (G.kb == 8) keys_channel<8>(groups, tid, raw, sc, sK, sN);
+    else if (G.kb == 4) keys_channel<4>(groups, tid, raw, sc, sK, sN);
+    else keys_channel<2>(groups, tid, raw, sc, sK, sN);
   }
 }
-__device__ __forceinline__ void fill_group_rows(const Geometry& G, const TileSrc& src, int kt, int tid, const RawTile& r, uint8_t* sM) {
-  const bool have = kt * kTile + (tid >> 4) * 8 < src.tc.Nq;
-  if (G.kb == 8) group_rows<8>(have, tid, r, sM);
-  else if (G.kb == 4) group_rows<4>(have, tid, r, sM);
-  else group_rows<2>(have, tid, r, sM);
+__device__ __forceinline__ void fill_group_rows(const Geometry& G, const RawSlot& R, const TileSrc& src, int kt, int tid,
+                                                const uint8_t* raw, uint8_t* sM) {
+  const int groups = tile_groups(src, kt);
+  const uint32_t* sc = reinterpret_cast<const uint32_t*>(raw + R.ks);
+  if (G.kb == 8) group_rows<8>(groups, tid, sc, sM);
+  else group_rows<4>(groups, tid, sc, sM);  // 4 and 2 bits: the same pairs
 }
-__device__ __forceinline__ void fill_uniform_values(const Geometry& G, const TileSrc& src, int kt, int tid, const RawTile& r,
-                                                    uint8_t* sV) {
-  const bool have = kt * kTile + (tid >> 4) * 8 < src.tc.Nq;
-  if (G.vb == 8) values_uniform<8>(have, tid, r, sV);
-  else if (G.vb == 4) values_uniform<4>(have, tid, r, sV);
-  else values_uniform<2>(have, tid, r, sV);
+__device__ __forceinline__ void fill_uniform_values(const Geometry& G, const RawSlot& R, const TileSrc& src, int kt, int tid,
+                                                    const uint8_t* raw, uint8_t* sV) {
+  const int groups = tile_groups(src, kt), group = 8 * (tid & 15) / G.gv;
+  const uint32_t* sc = reinterpret_cast<const uint32_t*>(raw + R.vs);
+  if (G.vb == 8) values_uniform<8>(groups, tid, raw + R.v, sc, G.nvg, group, sV);
+  else if (G.vb == 4) values_uniform<4>(groups, tid, raw + R.v, sc, G.nvg, group, sV);
+  else values_uniform<2>(groups, tid, raw + R.v, sc, G.nvg, group, sV);
 }
 
 // ------------------------------------------- non-uniform codes, RoPE, fp16
@@ -335,50 +320,42 @@ __device__ __forceinline__ void fill_uniform_values(const Geometry& G, const Til
 __device__ __forceinline__ uint32_t codes3(const uint8_t* row, int chunk) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
   const int bit = 24 * chunk, i = bit >> 5;
-  return __funnelshift_r(__ldg(w + i), __ldg(w + min(i + 1, 11)), bit & 31) & 0xFFFFFFu;
+  return __funnelshift_r(w[i], w[min(i + 1, 11)], bit & 31) & 0xFFFFFFu;
 }
-__device__ __forceinline__ void values3(uint32_t w, float2 ms, const float* lut, float (&x)[8]) {
+// Channels of the chunks cb and cb + 8 of key t of a tile, non-uniform codes:
+// the dense values, then the outliers among them.
+__device__ __forceinline__ void general_row(const uint8_t* codes, const uint32_t* scales, const uint8_t* col, const uint16_t* val,
+                                            int nout, const float* lut, int t, int cb, float (&x)[2][8]) {
+  const float2 ms = unpack_min_scale(scales[t]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(ms.y, lut[(w >> (3 * i)) & 7], ms.x);
-}
-
-// A thread's share of a general tile: 4 consecutive tokens, the chunks cb and
-// cb + 8.  Non-uniform rows: the codes, {min, scale} and (one per lane of the
-// 8 that share the tokens) the outliers.  Uniform rows go through k_chunk.
-struct RawGeneral {
-  uint32_t w[4][2];   // 24 bits each
-  uint32_t ms[4];
-  uint32_t out[4];    // outlier (tid & 7): column << 16 | value
-};
-__device__ __forceinline__ void load_general(const uint8_t* codes, const uint32_t* scales, const uint8_t* col, const uint16_t* val,
-                                             int nout, size_t tok, int cb, RawGeneral& r) {
-  const uint8_t* row = codes + tok * 48;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w = codes3(codes + 48 * t, cb + 8 * h);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) r.w[u][h] = codes3(row + 48 * u, cb + 8 * h);
-    r.ms[u] = __ldg(scales + tok + u);
-    r.out[u] = 0xFFFF0000u;  // no channel
-    if (cb < nout) {
-      const size_t o = (tok + u) * nout + cb;
-      r.out[u] = (uint32_t)__ldg(col + o) << 16 | __ldg(val + o);
-    }
+    for (int i = 0; i < 8; ++i) x[h][i] = fmaf(ms.y, lut[(w >> (3 * i)) & 7], ms.x);
   }
-}
-__device__ __forceinline__ void general_values(const RawGeneral& r, int u, const float* lut, int nout, int cb, float (&x)[2][8]) {
-  const float2 ms = unpack_min_scale(r.ms[u]);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) values3(r.w[u][h], ms, lut, x[h]);
   for (int j = 0; j < nout; ++j) {
-    const uint32_t o = __shfl_sync(0xffffffffu, r.out[u], j, 8);
-    const int c = o >> 16;
+    const int c = col[t * nout + j];
     if (((c >> 3) & 7) == cb) {
-      const float v = half_bits_to_float((uint16_t)o);
+      const float v = half_bits_to_float(val[t * nout + j]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (c == 64 * h + 8 * cb + i) x[h][i] = v;
+    }
+  }
+}
+// The same of a uniform row (keys cached before RoPE: a scale per channel).
+__device__ __forceinline__ void uniform_key_row(const uint8_t* codes, int bits, const uint32_t* scales, int t, int cb, float (&x)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int c[8];
+    chunk_codes(codes + t * 16 * bits, bits, cb + 8 * h, c);
+    const uint32_t* sc = scales + (t >> 5) * kHeadDim + 8 * cb + 64 * h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 ms = unpack_min_scale(sc[i]);
+      x[h][i] = fmaf((float)c[i], ms.y, ms.x);
     }
   }
 }
@@ -388,11 +365,8 @@ __device__ __forceinline__ void store_keys(const float (&x)[8], int t, int chunk
 #pragma unroll
   for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], &hi[i], &neg[i]);
   const uint32_t o = tile_off(t, chunk);
-  *reinterpret_cast<uint4*>(sK + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(sN + o) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
-}
-__device__ __forceinline__ void zero_chunk(uint8_t* s, int t, int chunk) {
-  *reinterpret_cast<uint4*>(s + tile_off(t, chunk)) = make_uint4(0, 0, 0, 0);
+  store_chunk(sK, o, hi);
+  store_chunk(sN, o, neg);
 }
 __device__ __forceinline__ void rotate_pairs(float (&x)[2][8], const float2 (&e)[8]) {
 #pragma unroll
@@ -404,72 +378,49 @@ __device__ __forceinline__ void rotate_pairs(float (&x)[2][8], const float2 (&e)
 }
 
 // Keys of a quantized tile with non-uniform codes or RoPE.  The first of the
-// thread's 4 consecutive positions has its angles computed, the others
-// follow by one complex product each (step: e^{i theta}).
-__device__ __forceinline__ void fill_general_keys(const Geometry& G, const LayerPtrs& L, const unsigned long long* freq,
-                                                  const float* lut, const TileSrc& src, int kt, int tid, uint8_t* sK, uint8_t* sN) {
-  const int cb = tid & 7, t0 = (tid >> 3) * 4, f0 = kt * kTile + t0;
-  if (kt * kTile + (t0 & ~31) >= src.tc.Nq) {  // a whole group (and so a whole warp's 16 keys)
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) zero_chunk(sK, t0 + u, cb + 8 * h), zero_chunk(sN, t0 + u, cb + 8 * h);
-    return;
-  }
-  RawGeneral raw;
-  if (G.kb == 3)
-    load_general(L.k_codes, L.k_scales, L.k_col, L.k_val, G.nout, (size_t)src.s * G.qcap + f0, cb, raw);
-  float2 e[8], step[8];
+// thread's positions has its angles computed, the others, 32 apart, follow
+// by one complex product each.
+__device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSlot& R, const unsigned long long* freq, const float* lut,
+                                                  const TileSrc& src, int kt, int tid, const uint8_t* raw, uint8_t* sK, uint8_t* sN) {
+  const int cb = tid & 7, groups = tile_groups(src, kt);
+  float2 e[8];
   if (G.pre_rope) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      e[i] = phasor((uint32_t)(G.pos_offset + G.S + f0), freq[8 * cb + i]);
-      step[i] = phasor(1, freq[8 * cb + i]);
-    }
+    for (int i = 0; i < 8; ++i) e[i] = phasor((uint32_t)(G.pos_offset + G.S + kt * kTile + (tid >> 3)), freq[8 * cb + i]);
   }
+#pragma unroll 1
+  for (int j = 0; j < kTile / 32; ++j) {
+    const int t = 32 * j + (tid >> 3);
+    float x[2][8] = {};
+    if (j < groups) {
+      if (G.kb == 3)
+        general_row(raw, reinterpret_cast<const uint32_t*>(raw + R.ks), raw + R.kcol, reinterpret_cast<const uint16_t*>(raw + R.kval), G.nout,
+                    lut, t, cb, x);
+      else
+        uniform_key_row(raw, G.kb, reinterpret_cast<const uint32_t*>(raw + R.ks), t, cb, x);
+      if (G.pre_rope) {
+        rotate_pairs(x, e);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    float x[2][8];
-    if (G.kb == 3) {
-      general_values(raw, u, lut, G.nout, cb, x);
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) k_chunk(G, L, lut, src.s, f0 + u, cb + 8 * h, x[h]);
+        for (int i = 0; i < 8; ++i) e[i] = spec_cmul(e[i], phasor(32, freq[8 * cb + i]));
+      }
     }
-    if (G.pre_rope) {
-      rotate_pairs(x, e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = spec_cmul(e[i], step[i]);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) store_keys(x[h], t0 + u, cb + 8 * h, sK, sN);
+    for (int h = 0; h < 2; ++h) store_keys(x[h], t, cb + 8 * h, sK, sN);
   }
 }
-__device__ __forceinline__ void fill_general_values(const Geometry& G, const LayerPtrs& L, const float* lut, const TileSrc& src,
-                                                    int kt, int tid, uint8_t* sV) {
-  const int cb = tid & 7, t0 = (tid >> 3) * 4, f0 = kt * kTile + t0;
-  if (kt * kTile + (t0 & ~31) >= src.tc.Nq) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) zero_chunk(sV, t0 + u, cb + 8 * h);
-    return;
-  }
-  RawGeneral raw;
-  if (G.vb == 3)
-    load_general(L.v_codes, L.v_scales, L.v_col, L.v_val, G.nout, (size_t)src.s * G.qcap + f0, cb, raw);
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    float y[2][8];
-    if (G.vb == 3) {
-      general_values(raw, u, lut, G.nout, cb, y);
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) v_chunk(G, L, lut, src.s, f0 + u, cb + 8 * h, y[h]);
-    }
+__device__ __forceinline__ void fill_general_values(const Geometry& G, const RawSlot& R, const float* lut, const TileSrc& src, int kt,
+                                                    int tid, const uint8_t* raw, uint8_t* sV) {
+  const int cb = tid & 7, groups = tile_groups(src, kt);
+#pragma unroll 1
+  for (int j = 0; j < kTile / 32; ++j) {
+    const int t = 32 * j + (tid >> 3);
+    float y[2][8] = {};
+    if (j < groups)
+      general_row(raw + R.v, reinterpret_cast<const uint32_t*>(raw + R.vs), raw + R.vcol, reinterpret_cast<const uint16_t*>(raw + R.vval),
+                  G.nout, lut, t, cb, y);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint4*>(sV + tile_off(t0 + u, cb + 8 * h)) =
+      *reinterpret_cast<uint4*>(sV + tile_off(t, cb + 8 * h)) =
           make_uint4(pack_sat(y[h][0], y[h][1]), pack_sat(y[h][2], y[h][3]), pack_sat(y[h][4], y[h][5]), pack_sat(y[h][6], y[h][7]));
   }
 }
@@ -504,17 +455,17 @@ __device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtr
                                                const uint16_t* kd, const TileSrc& src, int kt, int tid, uint8_t* sK, uint8_t* sN) {
   if (!G.pre_rope) {
     const int cb = tid & 15;
-    uint4 v[8];
+    uint4 v[kTile / 16];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = load16_if(fp16_key(G, L.k_sink, L.k_ring, kd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
+    for (int u = 0; u < kTile / 16; ++u) v[u] = load16_if(fp16_key(G, L.k_sink, L.k_ring, kd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(sK + tile_off((tid >> 4) + 16 * u, cb)) = v[u];
+    for (int u = 0; u < kTile / 16; ++u) *reinterpret_cast<uint4*>(sK + tile_off((tid >> 4) + 16 * u, cb)) = v[u];
     return;
   }
   const int cb = tid & 7;
 #pragma unroll 1
-  for (int u = 0; u < 4; ++u) {
-    const int t = (tid >> 3) * 4 + u, f = kt * kTile + t;
+  for (int u = 0; u < kTile / 32; ++u) {
+    const int t = 32 * u + (tid >> 3), f = kt * kTile + t;
     const uint16_t* row = fp16_key(G, L.k_sink, L.k_ring, kd, src, f);
     float x[2][8];
 #pragma unroll
@@ -537,11 +488,11 @@ __device__ __forceinline__ bool fill_fp16_values(const Geometry& G, const LayerP
                                                  int kt, int tid, uint8_t* sV) {
   const int cb = tid & 15;
   bool bad = false;
-  uint4 v[8];
+  uint4 v[kTile / 16];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) v[u] = load16_if(fp16_key(G, L.v_sink, L.v_ring, vd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
+  for (int u = 0; u < kTile / 16; ++u) v[u] = load16_if(fp16_key(G, L.v_sink, L.v_ring, vd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
+  for (int u = 0; u < kTile / 16; ++u) {
     const int t = (tid >> 4) + 16 * u;
     if (kt * kTile + t >= src.tc.k1 && !finite8(v[u])) {
       bad = true;

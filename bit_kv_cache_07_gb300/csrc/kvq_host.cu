@@ -631,20 +631,19 @@ kvq_status kvq_decode_attn(const kvq_config* cfg, const void* layer_buf, int32_t
 // ---------------------------------------------------- many rows per KV head
 
 // Rows per block of the tile kernels, partial results per piece and rows of
-// each: 16 rows leave the consumer warps to the keys (4 partial results),
+// each: 16 rows leave the consumer warps to the keys (one partial result each),
 // more go to the tensor-core kernel (128 rows).
 static void spec_blocks(int64_t rows, int* rblk, int* sub, int* rstride) {
   *rblk = rows <= 16 ? 16 : 128;
-  *sub = rows <= 16 ? 4 : 1;
+  *sub = rows <= 16 ? 6 : 1;
   *rstride = (int)(rows <= 16 ? 16 : rows < 128 ? (rows + 15) / 16 * 16 : 128);
 }
 
-// RoPE frequencies: radians per position, and turns as 64-bit fractions.
-static void spec_rope(float base, double* theta, unsigned long long* freq) {
+// RoPE frequencies, turns per position as 64-bit fractions.
+static void spec_rope(float base, unsigned long long* freq) {
   for (int i = 0; i < kHeadDim / 2; ++i) {
-    theta[i] = std::pow((double)base, -2.0 * i / (double)kHeadDim);
-    const double turns = theta[i] * 0.15915494309189533576888376337251, whole = std::floor(turns);
-    freq[i] = (unsigned long long)std::ldexp(turns - whole, 64);  // (1 - 2^-53) 2^64 at most
+    const double turns = std::pow((double)base, -2.0 * i / (double)kHeadDim) * 0.15915494309189533576888376337251;
+    freq[i] = (unsigned long long)std::ldexp(turns - std::floor(turns), 64);  // (1 - 2^-53) 2^64 at most
   }
 }
 
@@ -724,7 +723,7 @@ kvq_status kvq_tree_attn(const kvq_config* cfg, const void* layer_buf, const int
     p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
     p.v_lut_off[i] = cfg->v_lut[i] - cfg->v_lut[0];
   }
-  if (g.pre_rope) spec_rope(cfg->rope_theta, p.theta, p.freq);
+  if (g.pre_rope) spec_rope(cfg->rope_theta, p.freq);
   int64_t total = 0, pairs = 0;
   bool any = false;
   for (int b = 0; b < g.B; ++b) {
@@ -764,26 +763,28 @@ kvq_status kvq_attn_mass(const kvq_config* cfg, const void* layer_buf, const int
     return KVQ_ERR_INVALID_ARG;
   kvq_layout L;
   build_layout(cfg, g, &L);
-  MassParams p;
+  TreeParams p;
   std::memset(&p, 0, sizeof(p));
   p.geo = g;
   layer_ptrs(L, const_cast<void*>(layer_buf), &p.L);
   p.q = q;
-  p.lse = lse;
+  p.row_lse = lse;
   p.weight = weight;
   p.mass = mass;
   p.n = n_rows;
+  p.rblk = g.g * n_rows;  // every row of a KV head meets a tile at once
   p.cap = cfg->max_tokens;
   p.decay = decay;
   p.q_scale = cfg->softmax_scale > 0.0f ? cfg->softmax_scale : (float)(1.0 / std::sqrt((double)kHeadDim));
   for (int i = 0; i < 8; ++i) p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
-  if (g.pre_rope) spec_rope(cfg->rope_theta, p.theta, p.freq);
+  if (g.pre_rope) spec_rope(cfg->rope_theta, p.freq);
   int64_t total = 0;
   for (int b = 0; b < g.B; ++b) {
     if (tokens[b] < 0) return KVQ_ERR_INVALID_ARG;
     if (tokens[b] > cfg->max_tokens) return KVQ_ERR_CAPACITY;
     const TileCounts tc = tile_counts(g, tokens[b], 0);
     p.rows.tokens[b] = tokens[b];
+    p.rows.nodes[b] = n_rows;
     p.rows.tile0[b] = (int)total;
     total += (int64_t)g.Hkv * (tc.qt + tc.ft);
     if (total > (1ll << 30)) return KVQ_ERR_UNSUPPORTED;

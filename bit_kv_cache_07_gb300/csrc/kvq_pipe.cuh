@@ -1,6 +1,7 @@
-// kvq_pipe.cuh -- what the two tree-attention kernels share: the pieces of a
-// CTA's range, barriers with a limit, and the producer warps that keep two
-// stages of dequantized tiles full.
+// kvq_pipe.cuh -- what the tile kernels (tree attention, recorded weight) share: the pieces of a
+// CTA's range, barriers with a limit, the thread that copies the stored bytes
+// of the tiles ahead, and the producer warps that keep two stages of
+// dequantized tiles full.
 #pragma once
 
 #include "kvq_fill.cuh"
@@ -10,15 +11,34 @@ namespace kvq {
 #ifdef __CUDACC__
 
 constexpr int kProducers = 256;
-constexpr uint32_t kTileBytes = kTile * kHeadDim * 2;  // 32 KB
+constexpr uint32_t kTileBytes = kTile * kHeadDim * 2;  // 24 KB
 constexpr uint32_t kStageBytes = 3 * kTileBytes;       // K hi, K neg, V
+constexpr uint32_t kKeyStageBytes = 2 * kTileBytes;    // K hi, K neg
 constexpr uint32_t kGroupRowBytes = 8 * kHeadDim * 2;  // the groups' min and scale rows
-constexpr int kAhead = 3;                              // tiles asked for in L2 ahead of their loads
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
 // ------------------------------------------------------------- barriers
@@ -28,9 +48,17 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
+// One arrival for a warp, after what every lane did (32 arrivals on one word
+// are 32 updates, one after the other).
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 // Wait for a phase, with a limit (well over any wait of a running kernel);
-// past it the CTA gives up: every role leaves its loop.
+// past it the CTA gives up: every role leaves its loop.  (gave_up null: a wait
+// for copies in flight on the way out.)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, volatile int* gave_up) {
+#pragma unroll 1
   for (int it = 0; it < (1 << 24); ++it) {
     uint32_t ok;
     asm volatile(
@@ -39,9 +67,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, volatile
         : "r"(bar), "r"(phase)
         : "memory");
     if (ok) return true;
-    if ((it & 255) == 255 && *gave_up) return false;
+    if ((it & 255) == 255 && gave_up && *gave_up) return false;
   }
-  *gave_up = 1;
+  if (gave_up) *gave_up = 1;
   return false;
 }
 
@@ -72,66 +100,132 @@ __device__ __forceinline__ Piece piece_at(const TreeParams& p, int x, int x_end)
   return c;
 }
 
-struct Bars {  // shared-memory addresses; by stage (o_done, done: one)
-  uint32_t full_k, full_v, empty_k, empty_v, s_full, p_full, o_done, done;
+struct Bars {  // shared-memory addresses; by stage (raw: by slot; o_done, q_full, done: one)
+  uint32_t full_k, full_v, empty_k, empty_v, s_full, p_full, raw_full, raw_empty, o_done, q_full, done;
 };
+constexpr int kBarBytes = (6 * 2 + 2 * kMaxRaw + 3) * 8;
+__device__ __forceinline__ Bars bars_at(uint32_t b) {
+  return Bars{b, b + 16, b + 32, b + 48, b + 64, b + 80, b + 96, b + 96 + 8 * kMaxRaw, b + 96 + 16 * kMaxRaw, b + 104 + 16 * kMaxRaw,
+              b + 112 + 16 * kMaxRaw};
+}
+// The shared-memory tail of a kernel: barriers, then these words.
+struct Tail {
+  uint64_t bars[kBarBytes / 8];
+  uint32_t tmem;
+  int gave_up;
+  int bad_piece[4];  // pieces that hold drafted values that are not finite, by number + 1
+  float lut[16];     // level offsets of K, of V
+};
+static_assert(sizeof(Tail) <= 512, "tail");
+
+__device__ __forceinline__ TileSrc tile_src(const TreeParams& p, const Piece& c) {
+  return TileSrc{c.tc, c.s, c.b, p.mask ? c.n_b : 0, c.tc.Nq % p.geo.ring, in_stream(p.geo, c.s) * p.n};
+}
+
+// ---------------------------------------------------------------- copies
+// One thread: the stored bytes of the quantized tiles into the raw slots, as
+// many tiles ahead as there are slots; fp16 tiles are asked for in L2.
+template <bool V>
+__device__ __forceinline__ void load_tiles(const TreeParams& p, const Bars& B, uint32_t raw, int x, int x_end, volatile int* gave_up) {
+  const Geometry& G = p.geo;
+  int slot = 0, turn = 0;
+  bool ok = true;
+  while (ok && x < x_end) {
+    const Piece c = piece_at(p, x, x_end);
+    const TileSrc src = tile_src(p, c);
+    for (int k = c.k0; k < c.k0 + c.cnt; ++k) {
+      if (!c.quant) {
+        // cached rows of the tile from the window's first slot on (the sinks are few)
+        const int f0 = max(k * kTile, c.tc.S_eff), f1 = min((k + 1) * kTile, c.tc.k1);
+        const int s0 = src.slot0 + f0 - c.tc.S_eff, n = min(f1 - f0, G.ring - s0);
+        if (n > 0) {
+          const size_t at = ((size_t)c.s * G.ring + s0) * kHeadDim;
+          prefetch_l2(p.L.k_ring + at, n * kHeadDim * 2);
+          if (V) prefetch_l2(p.L.v_ring + at, n * kHeadDim * 2);
+        }
+        continue;
+      }
+      if (turn && !(ok = mbar_wait(B.raw_empty + 8 * slot, (turn - 1) & 1, gave_up))) break;
+      load_tile<V>(G, p.L, p.raw, src, k, raw + slot * p.raw.bytes, B.raw_full + 8 * slot);
+      if (++slot == p.raw.slots) slot = 0, ++turn;
+    }
+    x += c.cnt;
+  }
+  if (*gave_up) {  // the copies in flight end before the CTA does
+    for (int i = 0; i < p.raw.slots; ++i) {
+      if (--slot < 0) slot = p.raw.slots - 1, --turn;
+      if (turn < 0) break;
+      mbar_wait(B.raw_full + 8 * slot, turn & 1, nullptr);
+    }
+  }
+}
 
 // ------------------------------------------------------------- producers
-template <int ROWS>
-__device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint8_t* sQ, uint8_t* stage0, uint8_t* sM, const float* lut,
-                                        volatile int* bad_piece, int x, int x_end, int tid, volatile int* gave_up) {
+// ROWS > 0: the producers also stage that many query rows of each piece.  V:
+// the values too.
+template <int ROWS, bool V>
+__device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint8_t* sQ, uint8_t* stage0, uint8_t* sM, const uint8_t* raw0,
+                                        Tail* tail, int x, int x_end, int tid, volatile int* gave_up) {
   const Geometry& G = p.geo;
   const bool general = G.pre_rope || G.kb == 3;
-  int i = 0;  // tiles so far
+  int i = 0, slot = 0, turn = 0;  // tiles so far, raw slot and its turn
   for (int piece = 0; x < x_end; ++piece) {
     const Piece c = piece_at(p, x, x_end);
-    const TileSrc src{c.tc, c.s, c.b, p.mask ? c.n_b : 0, c.tc.Nq % G.ring, in_stream(G, c.s) * p.n};
-    RawTile raw;
-    const bool uniform = c.quant && !general;
-    if (c.quant && tid == 0)
-      for (int k = c.k0 + (uniform ? 1 : 0); k < min(c.k0 + kAhead, c.k0 + c.cnt); ++k) prefetch_tile<true>(G, p.L, src, k);
-    if (uniform) load_keys(G, p.L, src, c.k0, tid, raw), load_values(G, p.L, src, c.k0, tid, raw);
-    // the previous piece's last product has read Q
-    if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
-    const uint16_t* qb = p.q + ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n * kHeadDim;
-    const bool paired = uniform && paired_order(G.kb);
+    const TileSrc src = tile_src(p, c);
+    if constexpr (ROWS > 0) {
+      // the previous piece's last logits are computed
+      if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
+      const uint16_t* qb = p.q + ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n * kHeadDim;
+      const bool paired = c.quant && !general && paired_order(G.kb);
 #pragma unroll
-    for (int u = 0; u < ROWS / 16; ++u) {
-      const int r = (tid >> 4) + 16 * u, ch = tid & 15;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < c.nr) {
-        const int j = (c.r0 + r) / c.n_b, node = c.r0 + r - j * c.n_b;
-        v = __ldg(reinterpret_cast<const uint4*>(qb + ((size_t)j * p.n + node) * kHeadDim) + ch);
-        if (paired) v = pair_chunk(v);
+      for (int u = 0; u < ROWS / 16; ++u) {
+        const int r = (tid >> 4) + 16 * u, ch = tid & 15;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < c.nr) {
+          const int j = (c.r0 + r) / c.n_b, node = c.r0 + r - j * c.n_b;
+          v = __ldg(reinterpret_cast<const uint4*>(qb + ((size_t)j * p.n + node) * kHeadDim) + ch);
+          if (paired) v = pair_chunk(v);
+        }
+        *reinterpret_cast<uint4*>(sQ + q_off<ROWS>(r, ch)) = v;
       }
-      *reinterpret_cast<uint4*>(sQ + q_off<ROWS>(r, ch)) = v;
     }
     bool bad = false;
+#pragma unroll 1
     for (int k = c.k0; k < c.k0 + c.cnt; ++k, ++i) {
       const int st = i & 1;
       const uint32_t again = ((i >> 1) - 1) & 1;
-      uint8_t *sK = stage0 + st * kStageBytes, *sN = sK + kTileBytes, *sV = sN + kTileBytes;
+      uint8_t *sK = stage0 + st * (V ? kStageBytes : kKeyStageBytes), *sN = sK + kTileBytes, *sV = sN + kTileBytes;
+      const uint8_t* raw = raw0 + slot * p.raw.bytes;
+      if (c.quant && !mbar_wait(B.raw_full + 8 * slot, turn & 1, gave_up)) return;
       if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
       if (!c.quant) fill_fp16_keys(G, p.L, p.freq, p.kd, src, k, tid, sK, sN);
-      else if (general) fill_general_keys(G, p.L, p.freq, lut, src, k, tid, sK, sN);
-      else fill_uniform_keys(G, p.L, src, k, tid, raw, sK, sN);
-      if (uniform && !G.gkc) {  // (one buffer: the tile before must have been read)
+      else if (general) fill_general_keys(G, p.raw, p.freq, tail->lut, src, k, tid, raw, sK, sN);
+      else fill_uniform_keys(G, p.L, p.raw, src, k, tid, raw, sK, sN);
+      if (c.quant && channel_scales(G)) {  // (one buffer: the tile before must have been read)
         if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
-        fill_group_rows(G, src, k, tid, raw, sM);
+        fill_group_rows(G, p.raw, src, k, tid, raw, sM);
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(B.full_k + 8 * st);
-      const bool more = k + 1 < c.k0 + c.cnt;
-      if (uniform && more) load_keys(G, p.L, src, k + 1, tid, raw);  // in flight under the values' conversion
-      if (c.quant && tid == 0 && k + kAhead < c.k0 + c.cnt) prefetch_tile<true>(G, p.L, src, k + kAhead);
-      if (i >= 2 && !mbar_wait(B.empty_v + 8 * st, again, gave_up)) return;
-      if (!c.quant) bad |= fill_fp16_values(G, p.L, p.vd, src, k, tid, sV);
-      else if (general) fill_general_values(G, p.L, lut + 8, src, k, tid, sV);
-      else fill_uniform_values(G, src, k, tid, raw, sV);
-      if (bad) bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(B.full_v + 8 * st);
-      if (uniform && more) load_values(G, p.L, src, k + 1, tid, raw);
+      if constexpr (!V) {
+        if (c.quant) {
+          mbar_arrive_warp(B.raw_empty + 8 * slot);
+          if (++slot == p.raw.slots) slot = 0, ++turn;
+        }
+        mbar_arrive_warp(B.full_k + 8 * st);
+      } else {
+        mbar_arrive_warp(B.full_k + 8 * st);
+        if (i >= 2 && !mbar_wait(B.empty_v + 8 * st, again, gave_up)) return;
+        if (!c.quant) bad |= fill_fp16_values(G, p.L, p.vd, src, k, tid, sV);
+        else if (G.vb == 3) fill_general_values(G, p.raw, tail->lut + 8, src, k, tid, raw, sV);
+        else fill_uniform_values(G, p.raw, src, k, tid, raw, sV);
+        if (bad) *(volatile int*)&tail->bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
+        if (c.quant) {
+          mbar_arrive_warp(B.raw_empty + 8 * slot);
+          if (++slot == p.raw.slots) slot = 0, ++turn;
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        mbar_arrive_warp(B.full_v + 8 * st);
+      }
     }
     x += c.cnt;
   }

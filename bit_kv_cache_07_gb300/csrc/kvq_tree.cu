@@ -13,29 +13,12 @@ namespace kvq {
 namespace {
 
 constexpr int kSmallRows = 16;
-constexpr int kConsumers = 128;
-constexpr int kThreadsSmall = kConsumers + kProducers;
-constexpr uint32_t kSmemSmall = 1024 + kSmallRows * kHeadDim * 2 + 2 * kStageBytes + kGroupRowBytes + 256;
-static_assert(kSmemSmall <= 227 * 1024, "shared memory of one CTA");
+constexpr int kConsumerWarps = kTile / 16;
+constexpr int kConsumers = 32 * kConsumerWarps;
+constexpr int kThreadsSmall = kConsumers + kProducers + 32;
+constexpr uint32_t kFixedSmall = 2 * kStageBytes + kSmallRows * kHeadDim * 2 + kGroupRowBytes + 512;
+constexpr uint32_t kSmemSmall = 227 * 1024;
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -43,11 +26,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // Up to 16 query rows per KV head: a 128-row tensor-core tile would be mostly
 // padding, and the dequantization of a tile costs more than its products.
-// The same producers fill the tiles; 4 warps take 32 keys of each with
+// The same producers fill the tiles; 6 warps take 16 keys of each with
 // mma.sync (m16n8k16), every warp with its own softmax state and partial
 // result.
 __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, const uint8_t* sQ, const uint8_t* stage0, const uint8_t* sM,
-                                        volatile int* bad_piece, int x, int x_end, int tid, volatile int* gave_up) {
+                                        Tail* tail, int x, int x_end, int tid, volatile int* gave_up) {
   auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
   const int lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3;
   const uint32_t aQ = (uint32_t)__cvta_generic_to_shared(sQ), a0 = (uint32_t)__cvta_generic_to_shared(stage0),
@@ -61,72 +44,60 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (g + 8 * e < c.nr) mask_row[e] = p.mask + ((size_t)c.b * p.n + (g + 8 * e) % c.n_b) * p.words;
-    uint32_t qa[8][4];
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+#pragma unroll 1
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
       const uint32_t aK = a0 + st * kStageBytes, aN = aK + kTileBytes, aV = aN + kTileBytes;
       if (!wait(B.full_k + 8 * st, i >> 1)) return;
-      if (t == 0) {
+      // logits of keys 16 w + 8 n + 2 tq + {0, 1}, rows g and g + 8
+      float z[2][4] = {}, zn[2][4] = {}, zg[4] = {};
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) ldsm4(qa[ks], aQ + q_off<kSmallRows>(lane & 15, 2 * ks + (lane >> 4)));
-      }
-      // logits of keys 32 w + 8 n + 2 tq + {0, 1}, rows g and g + 8
-      float z[4][4] = {}, zn[4][4] = {};
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-        for (int n = 0; n < 4; n += 2) {
-          const uint32_t off = tile_off(32 * w + 8 * n + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
-          uint32_t kb[4];
-          ldsm4(kb, aK + off);
-          mma16816(z[n], qa[ks], kb[0], kb[1]);
-          mma16816(z[n + 1], qa[ks], kb[2], kb[3]);
-          if (two) {
-            ldsm4(kb, aN + off);
-            mma16816(zn[n], qa[ks], kb[0], kb[1]);
-            mma16816(zn[n + 1], qa[ks], kb[2], kb[3]);
-          }
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t off = tile_off(16 * w + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1));
+        uint32_t qa[4], kb[4];
+        ldsm4(qa, aQ + q_off<kSmallRows>(lane & 15, 2 * ks + (lane >> 4)));
+        ldsm4(kb, aK + off);
+        mma16816(z[0], qa, kb[0], kb[1]);
+        mma16816(z[1], qa, kb[2], kb[3]);
+        if (two) {
+          ldsm4(kb, aN + off);
+          mma16816(zn[0], qa, kb[0], kb[1]);
+          mma16816(zn[1], qa, kb[2], kb[3]);
         }
-      float base[2] = {0.0f, 0.0f};  // rows g, g + 8: what the warp's 32 keys, one group, share
-      if (grouped) {
-        float zg[4] = {};
-#pragma unroll
-        for (int ks = 0; ks < 8; ks += 2) {
-          uint32_t kb[4];
-          ldsm4(kb, aM + q_off<8>(lane & 7, 2 * ks + (lane >> 3)));
-          mma16816(zg, qa[ks], kb[0], kb[1]);
-          mma16816(zg, qa[ks + 1], kb[2], kb[3]);
-        }
-        // column n (min of group n), 4 + n (its scale): lane 4 g + n / 2, element n & 1
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float a = (w & 1) ? zg[2 * e + 1] : zg[2 * e];
-          const float mn = __shfl_sync(0xffffffffu, a, (lane & ~3) + (w >> 1)), sc = __shfl_sync(0xffffffffu, a, (lane & ~3) + 2 + (w >> 1));
-          base[e] = fmaf((float)(1 << (p.geo.kb - 1)), sc, mn);
+        if (grouped) {
+          ldsm4(kb, aM + q_off<8>(lane & 7, 2 * ks + ((lane >> 3) & 1)));
+          mma16816(zg, qa, kb[0], kb[1]);
         }
       }
-      mbar_arrive(B.empty_k + 8 * st);
-      const int f0 = (c.k0 + t) * kTile + 32 * w;
-      uint32_t ok[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) ok[e] = seen(p, c, mask_row[e], f0);
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[n][e] = (ok[e >> 1] >> (8 * n + 2 * tq + (e & 1))) & 1 ? (z[n][e] - zn[n][e] + base[e >> 1]) * p.q_scale : -INFINITY;
-          mx[e >> 1] = fmaxf(mx[e >> 1], z[n][e]);
-        }
+      float base[2];  // rows g, g + 8: what the group of the warp's 16 keys shares
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        // column n (min of group n), 4 + n (its scale): lane 4 g + n / 2, element n & 1
+        const float a = (w >> 1) & 1 ? zg[2 * e + 1] : zg[2 * e];
+        const float mn = __shfl_sync(0xffffffffu, a, (lane & ~3) + (w >> 2)), sc = __shfl_sync(0xffffffffu, a, (lane & ~3) + 2 + (w >> 2));
+        base[e] = grouped ? fmaf((float)(1 << (p.geo.kb - 1)), sc, mn) : 0.0f;
+      }
+      mbar_arrive_warp(B.empty_k + 8 * st);
+      const int f0 = (c.k0 + t) * kTile + 32 * (w >> 1);
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t ok = seen(p, c, mask_row[e], f0) >> (16 * (w & 1));
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float& y = z[n][2 * e + q];
+            y = (ok >> (8 * n + 2 * tq + q)) & 1 ? (y - zn[n][2 * e + q] + base[e]) * p.q_scale : -INFINITY;
+            mx[e] = fmaxf(mx[e], y);
+          }
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
       }
-      // the maximum moves when a logit passes it by 2^8 (see the tensor-core kernel)
+      // the maximum moves when a logit passes it by 2^8: weights stay in fp16's range, O is rarely rescaled
       const bool move[2] = {mx[0] > m[0] + 8.0f, mx[1] > m[1] + 8.0f};
       if (__any_sync(0xffffffffu, move[0] || move[1])) {
 #pragma unroll
@@ -140,7 +111,7 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
       }
       const float mu[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           z[n][e] = ex2(z[n][e] - mu[e >> 1]);
@@ -148,24 +119,20 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
         }
       if (!wait(B.full_v + 8 * st, i >> 1)) return;
       // O += P V; P rounds to fp16 (relative 2^-11 of each weight, as the output does)
+      const uint32_t pa[4] = {pack2(z[0][0], z[0][1]), pack2(z[0][2], z[0][3]), pack2(z[1][0], z[1][1]), pack2(z[1][2], z[1][3])};
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const uint32_t pa[4] = {pack2(z[2 * ks][0], z[2 * ks][1]), pack2(z[2 * ks][2], z[2 * ks][3]),
-                                pack2(z[2 * ks + 1][0], z[2 * ks + 1][1]), pack2(z[2 * ks + 1][2], z[2 * ks + 1][3])};
-#pragma unroll
-        for (int n = 0; n < 16; n += 2) {
-          uint32_t vb[4];
-          ldsm4t(vb, aV + tile_off(32 * w + 16 * ks + (lane & 15), n + (lane >> 4)));
-          mma16816(o[n], pa, vb[0], vb[1]);
-          mma16816(o[n + 1], pa, vb[2], vb[3]);
-        }
+      for (int n = 0; n < 16; n += 2) {
+        uint32_t vb[4];
+        ldsm4t(vb, aV + tile_off(16 * w + (lane & 15), n + (lane >> 4)));
+        mma16816(o[n], pa, vb[0], vb[1]);
+        mma16816(o[n + 1], pa, vb[2], vb[3]);
       }
-      mbar_arrive(B.empty_v + 8 * st);
+      mbar_arrive_warp(B.empty_v + 8 * st);
     }
     // the piece's partial result; this thread holds slots 8 n + 2 tq + {0, 1} of the values' channel order
-    const bool paired = c.quant && !p.geo.pre_rope && p.geo.kb != 3 && paired_order(p.geo.vb);
+    const bool paired = c.quant && p.geo.vb != 3 && paired_order(p.geo.vb);
     if (tid == 0 && !c.quant) {
-      const uint32_t bad = bad_piece[piece & 3] == piece + 1;
+      const uint32_t bad = *(volatile int*)&tail->bad_piece[piece & 3] == piece + 1;
       for (int e = 0; e < p.sub; ++e) p.part_flag[(size_t)c.slot * p.sub + e] = bad;
     }
 #pragma unroll
@@ -189,31 +156,39 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
 }
 
 __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __grid_constant__ TreeParams p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + (1024 - ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023)) % 1024;
-  uint8_t *stage0 = smem, *sQ = stage0 + 2 * kStageBytes, *sM = sQ + kSmallRows * kHeadDim * 2, *tail = sM + kGroupRowBytes;
-  volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 132);
-  volatile int* bad_piece = reinterpret_cast<volatile int*>(tail + 208);
-  float* lut = reinterpret_cast<float*>(tail + 144);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *stage0 = smem, *sQ = stage0 + 2 * kStageBytes, *sM = sQ + kSmallRows * kHeadDim * 2;
+  Tail* tail = reinterpret_cast<Tail*>(sM + kGroupRowBytes);
+  uint8_t* raw0 = sM + kGroupRowBytes + 512;
+  volatile int* gave_up = &tail->gave_up;
   const int tid = threadIdx.x;
-  const uint32_t b0 = (uint32_t)__cvta_generic_to_shared(tail);
-  const Bars B{b0, b0 + 16, b0 + 32, b0 + 48, 0, 0, 0, 0};
+  const Bars B = bars_at((uint32_t)__cvta_generic_to_shared(tail->bars));
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(B.full_k + 8 * i, kProducers);
-      mbar_init(B.full_v + 8 * i, kProducers);
-      mbar_init(B.empty_k + 8 * i, kConsumers);
-      mbar_init(B.empty_v + 8 * i, kConsumers);
+      mbar_init(B.full_k + 8 * i, kProducers / 32);
+      mbar_init(B.full_v + 8 * i, kProducers / 32);
+      mbar_init(B.empty_k + 8 * i, kConsumerWarps);
+      mbar_init(B.empty_v + 8 * i, kConsumerWarps);
+    }
+    for (int i = 0; i < kMaxRaw; ++i) {
+      mbar_init(B.raw_full + 8 * i, 1);
+      mbar_init(B.raw_empty + 8 * i, kProducers / 32);
     }
     *gave_up = 0;
-    for (int i = 0; i < 4; ++i) bad_piece[i] = 0;
+    for (int i = 0; i < 4; ++i) tail->bad_piece[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (tid < 16) lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
+  if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
   __syncthreads();
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
-  if (tid < kConsumers) consume(p, B, sQ, stage0, sM, bad_piece, x, x_end, tid, gave_up);
-  else produce<kSmallRows>(p, B, sQ, stage0, sM, lut, bad_piece, x, x_end, tid - kConsumers, gave_up);
+  if (tid < kConsumers) {
+    consume(p, B, sQ, stage0, sM, tail, x, x_end, tid, gave_up);
+  } else if (tid < kConsumers + kProducers) {
+    produce<kSmallRows, true>(p, B, sQ, stage0, sM, raw0, tail, x, x_end, tid - kConsumers, gave_up);
+  } else {
+    if ((tid & 31) == 0) load_tiles<true>(p, B, (uint32_t)__cvta_generic_to_shared(raw0), x, x_end, gave_up);
+    __syncwarp();
+  }
   __syncthreads();
   if (*gave_up) {  // a wait ran out: every row of the range becomes NaN
     for (int y = x; y < x_end;) {
@@ -322,7 +297,9 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__
   if (p.lse && lane == 0) p.lse[orow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-cudaError_t launch_small(const TreeParams& p, cudaStream_t st) {
+cudaError_t launch_small(TreeParams& p, cudaStream_t st) {
+  p.raw = raw_slot(p.geo, true, kSmemSmall - kFixedSmall);
+  if (kFixedSmall + p.raw.slots * p.raw.bytes > kSmemSmall) return cudaErrorInvalidValue;
   static std::atomic<long long> memo[kMemoDevices];
   const cudaError_t e = ensure_smem_limit(tree_small_kernel, memo, (int)kSmemSmall);
   if (e != cudaSuccess) return e;
@@ -332,7 +309,7 @@ cudaError_t launch_small(const TreeParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st) {
+cudaError_t launch_tree_attn(TreeParams& p, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (p.total > 0) e = p.rblk == kSmallRows ? launch_small(p, st) : launch_tree_tc(p, st);
   if (e != cudaSuccess) return e;

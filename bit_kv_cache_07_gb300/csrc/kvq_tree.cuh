@@ -2,7 +2,8 @@
 // that run many query rows per KV head over the cache: kvq_tree_attn (a tree
 // of drafted tokens) and kvq_attn_mass (accumulated attention weight).
 //
-// Both cut a stream's tokens into tiles of 128 keys.  A tile is either
+// Both cut a stream's tokens into tiles of 96 keys (three groups: two stages
+// of a dequantized tile and three of its stored bytes fit shared memory).  A tile is either
 // quantized (positions [S, S + Nq)) or fp16 (sinks, window, then the drafted
 // tokens).  A tile's keys are dequantized once into shared memory and used
 // by every query row.
@@ -12,7 +13,8 @@
 
 namespace kvq {
 
-constexpr int kTile = 128;          // keys per tile
+constexpr int kTile = 96;           // keys per tile
+constexpr int kTileRows = 128;      // query rows of the tensor-core kernel
 constexpr int kMaxTreeNodes = 256;  // drafted tokens per sequence
 constexpr int kMaxSpecCtas = 160;   // CTAs of the tile kernels, one per SM at most (bounds the workspace)
 
@@ -30,6 +32,34 @@ struct SpecRows {
   int pair0[kMaxRaggedRows + 1];  // first (h, row block) pair of batch row b
 };
 
+// Stored bytes of a quantized tile as copied into shared memory: byte offsets
+// of its parts within a slot, and how many slots there are (2..kMaxRaw).
+constexpr int kMaxRaw = 4;
+struct RawSlot {
+  int slots, bytes;
+  int ks, kcol, kval, v, vs, vcol, vval;  // K codes at 0
+};
+inline RawSlot raw_slot(const Geometry& G, bool values, int room) {
+  RawSlot r;
+  int off = kTile * G.krow;
+  auto put = [&](int bytes) {
+    const int at = off;
+    off += (bytes + 15) / 16 * 16;
+    return at;
+  };
+  r.ks = put(G.kb == 3 ? kTile * 4 : G.gkc ? kTile * G.nkg * 4 : kTile / kGroupTokens * kHeadDim * 4);
+  r.kcol = put(kTile * G.nout);
+  r.kval = put(kTile * G.nout * 2);
+  r.v = put(values ? kTile * G.vrow : 0);
+  r.vs = put(values ? kTile * (G.vb == 3 ? 1 : G.nvg) * 4 : 0);
+  r.vcol = put(values ? kTile * G.nout : 0);
+  r.vval = put(values ? kTile * G.nout * 2 : 0);
+  r.bytes = (off + 127) / 128 * 128;
+  r.slots = room / (r.bytes > 0 ? r.bytes : 1);
+  r.slots = r.slots > kMaxRaw ? kMaxRaw : r.slots < 2 ? 2 : r.slots;
+  return r;
+}
+
 struct TreeParams {
   Geometry geo;
   LayerPtrs L;
@@ -39,6 +69,12 @@ struct TreeParams {
   const uint32_t* mask;  // [B][n][words] or null (no drafted keys)
   uint16_t* out;
   float* lse;
+  // the record of attention weight: rows' log-sum-exp and weights, [NS][cap] entries
+  const float* row_lse;
+  const float* weight;
+  float* mass;
+  float decay;
+  int cap;
   float2* part_ml;    // [slots][sub][rstride] (maximum in log2 units, sum)
   float* part_acc;    // [slots][sub][rstride][d]
   uint32_t* part_flag;  // [slots][sub] a drafted value of the piece is not finite
@@ -46,27 +82,11 @@ struct TreeParams {
   int rblk, sub;      // rows per block; partial results per piece
   int rstride;        // rows of a partial result
   int ncta, total;    // CTAs, tiles
-  float q_scale;      // softmax scale * log2(e)
+  RawSlot raw;        // stored bytes of a tile in shared memory
+  float q_scale;      // softmax scale * log2(e) (the record: the softmax scale)
   float hadamard_c;
   float k_lut_off[8], v_lut_off[8];
-  double theta[kHeadDim / 2];               // RoPE radians per position
   unsigned long long freq[kHeadDim / 2];    // RoPE turns per position, 64-bit fractions
-  SpecRows rows;
-};
-
-struct MassParams {
-  Geometry geo;
-  LayerPtrs L;
-  const uint16_t* q;     // [B][Hq][n][d]
-  const float* lse;      // [B][Hq][n]
-  const float* weight;   // [B][n] or null
-  float* mass;           // [NS][cap]
-  int n, cap;            // query rows per sequence, tokens per stream of the record
-  int ncta, total;       // CTAs, tiles
-  float decay, q_scale;  // q_scale: the softmax scale
-  float k_lut_off[8];
-  double theta[kHeadDim / 2];
-  unsigned long long freq[kHeadDim / 2];
   SpecRows rows;
 };
 
@@ -114,18 +134,11 @@ __device__ __forceinline__ uint32_t tile_off(int t, int chunk /* c / 8 */) {
   return (uint32_t)((chunk >> 3) * (kTile * 128) + t * 128 + (((chunk & 7) ^ (t & 7)) << 4));
 }
 
-// e^{i x} for an fp64 angle: reduced modulo 2 pi in fp64, then fp32.
-__device__ __forceinline__ float2 spec_expi(double x) {
-  const double turns = x * 0.15915494309189533576888376337251;
-  float sn, cs;
-  sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-  return make_float2(cs, sn);
-}
 __device__ __forceinline__ float2 spec_cmul(float2 a, float2 b) {
   return make_float2(a.x * b.x - a.y * b.y, a.x * b.y + a.y * b.x);
 }
 
-// The 8 codes of one 8-channel chunk of a packed row, as integers.
+// The 8 uniform codes of one 8-channel chunk of a packed row, as integers.
 __device__ __forceinline__ void chunk_codes(const uint8_t* row, int bits, int chunk, int (&c)[8]) {
   if (bits == 8) {
     const uint2 w = *reinterpret_cast<const uint2*>(row + chunk * 8);
@@ -135,85 +148,11 @@ __device__ __forceinline__ void chunk_codes(const uint8_t* row, int bits, int ch
     const uint32_t w = *reinterpret_cast<const uint32_t*>(row + chunk * 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = (w >> (4 * i)) & 15;
-  } else if (bits == 2) {
+  } else {
     const uint32_t w = *reinterpret_cast<const uint16_t*>(row + chunk * 2);
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = (w >> (2 * i)) & 3;
-  } else {  // 3 bits: 3 bytes, at no particular alignment
-    const uint8_t* b = row + chunk * 3;
-    const uint32_t w = (uint32_t)b[0] | ((uint32_t)b[1] << 8) | ((uint32_t)b[2] << 16);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = (w >> (3 * i)) & 7;
   }
-}
-
-// Outliers of one token that fall into an 8-channel chunk replace its values.
-__device__ __forceinline__ void chunk_outliers(const uint8_t* col, const uint16_t* val, int k, int chunk, float (&x)[8]) {
-  for (int j = 0; j < k; ++j) {
-    const int o = (int)col[j] - 8 * chunk;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i == o) x[i] = half_bits_to_float(val[j]);
-  }
-}
-
-// Dequantized channels [8 chunk, 8 chunk + 8) of quantized key i of stream s.
-__device__ __forceinline__ void k_chunk(const Geometry& G, const LayerPtrs& L, const float* lut_off, int s, int i, int chunk,
-                                        float (&x)[8]) {
-  const size_t tok = (size_t)s * G.qcap + i;
-  int c[8];
-  chunk_codes(L.k_codes + tok * G.krow, G.kb, chunk, c);
-  if (G.kb == 3) {
-    const float2 ms = unpack_min_scale(L.k_scales[tok]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf(ms.y, lut_off[c[j]], ms.x);
-    chunk_outliers(L.k_col + tok * G.nout, L.k_val + tok * G.nout, G.nout, chunk, x);
-  } else if (G.gkc) {
-    const float2 ms = unpack_min_scale(L.k_scales[tok * G.nkg + 8 * chunk / G.gkc]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf((float)c[j], ms.y, ms.x);
-    if (G.knorm)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= L.k_norm[(size_t)s * kHeadDim + 8 * chunk + j];
-  } else {
-    const uint32_t* sc = L.k_scales + ((size_t)s * G.gcap + i / kGroupTokens) * kHeadDim + 8 * chunk;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 ms = unpack_min_scale(sc[j]);
-      x[j] = fmaf((float)c[j], ms.y, ms.x);
-    }
-  }
-}
-
-// The same of value i (in the rotated domain when V is Hadamard-rotated).
-__device__ __forceinline__ void v_chunk(const Geometry& G, const LayerPtrs& L, const float* lut_off, int s, int i, int chunk,
-                                        float (&x)[8]) {
-  const size_t tok = (size_t)s * G.qcap + i;
-  int c[8];
-  chunk_codes(L.v_codes + tok * G.vrow, G.vb, chunk, c);
-  if (G.vb == 3) {
-    const float2 ms = unpack_min_scale(L.v_scales[tok]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf(ms.y, lut_off[c[j]], ms.x);
-    chunk_outliers(L.v_col + tok * G.nout, L.v_val + tok * G.nout, G.nout, chunk, x);
-  } else {
-    const float2 ms = unpack_min_scale(L.v_scales[tok * G.nvg + 8 * chunk / G.gv]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf((float)c[j], ms.y, ms.x);
-  }
-}
-
-// fp16 key f of a stream (f < k1): its row in the sinks or the window ring,
-// and its position in the sequence.
-__device__ __forceinline__ const uint16_t* fp16_row(const Geometry& G, const uint16_t* sink, const uint16_t* ring, int s,
-                                                    const TileCounts& tc, int f, int* pos) {
-  if (f < tc.S_eff) {
-    *pos = f;
-    return sink + ((size_t)s * G.S + f) * kHeadDim;
-  }
-  const int t = G.S + tc.Nq + (f - tc.S_eff);  // window token (f >= S_eff only when all S sinks are present)
-  *pos = t;
-  return ring + ((size_t)s * G.ring + (t - G.S) % G.ring) * kHeadDim;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
@@ -233,18 +172,6 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     x[2 * i] = f.x, x[2 * i + 1] = f.y;
   }
 }
-// x as hi + lo fp16 parts: 22 bits of x (hi saturates at the fp16 range, the
-// lo part takes what is left).
-__device__ __forceinline__ void split8(const float (&x)[8], uint4* hi, uint4* lo) {
-  float a[8], b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) a[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);
-  *hi = pack8(a);
-  unpack8(*hi, b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = x[i] - b[i];
-  *lo = pack8(b);
-}
 __device__ __forceinline__ bool finite8(const uint4& u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   bool ok = true;
@@ -255,8 +182,9 @@ __device__ __forceinline__ bool finite8(const uint4& u) {
 
 #endif  // __CUDACC__
 
-cudaError_t launch_tree_attn(const TreeParams& p, cudaStream_t st);
-cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t st);
-cudaError_t launch_attn_mass(const MassParams& p, cudaStream_t st);
+// (they place the stored bytes of a tile in shared memory: p.raw)
+cudaError_t launch_tree_attn(TreeParams& p, cudaStream_t st);
+cudaError_t launch_tree_tc(TreeParams& p, cudaStream_t st);
+cudaError_t launch_attn_mass(TreeParams& p, cudaStream_t st);
 
 }  // namespace kvq

@@ -1,32 +1,37 @@
 // kvq_tree_tc.cu -- the tree attention on the 5th-generation tensor cores, for
 // more than 16 query rows per KV head.
 //
-// One CTA per SM walks its range of 128-key tiles with 128 query rows:
+// One CTA per SM walks its range of 96-key tiles with 128 query rows:
+//   1 thread          copies the tiles' stored bytes ahead,
 //   8 producer warps  dequantize a tile into shared memory (two stages),
-//   1 warp            issues the matrix instructions (one thread),
+//   1 thread          issues the matrix instructions,
 //   4 warps           softmax, one thread per row.
-// S = Q K^T accumulates in TMEM (two buffers of 128 columns: the next tile's
-// logits are computed under this tile's exponentials), the weights return
-// there as fp16 over the logits they came from, and O += P V reads them from
-// TMEM (O in columns 256..383).  Quantized keys enter in two exact fp16 parts
-// (two passes of the 128-channel product), fp16 keys in one; what the 32 keys
-// of a per-channel group share comes from a 16-column product with the groups'
-// min and scale rows (columns 384 + 16 st).
-// The maximum moves only when a logit passes it by 2^8 (weights then stay
-// below fp16's range), so O is rarely rescaled.
-// 13 warps leave every thread 128 registers (17 would leave 96, and spills).
+// TMEM: Q as the fp16 operand A of the logits (columns 448..511), S = Q K^T in
+// two buffers (0, 128: the next tile's logits are computed under this tile's
+// exponentials), the weights as fp16 over the logits they came from, and
+// O += P V (256..383).  With Q in TMEM the logits' products read K alone from
+// shared memory, whose bandwidth 96 columns would not cover twice.
+// Quantized keys enter in two exact fp16 parts (two passes of the 128-channel
+// product), fp16 keys in one; what the 32 keys of a per-channel group share
+// comes from a 16-column product with the groups' min and scale rows (columns
+// 384 + 16 st).
+// A row's reference maximum comes from its first tile and moves only when a
+// tile's weights sum past 2^15 (fp16's range): one pass over the logits per
+// tile, and O is rarely rescaled.
+// 14 warps leave every thread 128 registers (17 would leave 96, and spills).
 #include "kvq_pipe.cuh"
 
 namespace kvq {
 namespace {
 
 constexpr int kSoftThreads = 128;
-constexpr int kThreadsTc = kSoftThreads + kProducers + 32;
+constexpr int kThreadsTc = kSoftThreads + kProducers + 64;
+constexpr float kTopSum = 32768.0f;  // a tile's weights stay below fp16's range
 // The 16-column product reads 8 rows behind the group rows as its columns
-// 8..15 (of no use): the kilobyte that holds the barriers.
-constexpr uint32_t kSmemTc = kTileBytes + 2 * kStageBytes + kGroupRowBytes + 1024;
-static_assert(kSmemTc <= 227 * 1024, "shared memory of one CTA");
-constexpr float kLazy = 8.0f;  // log2 units
+// 8..15 (of no use): the kilobyte that holds the tail.
+constexpr uint32_t kFixedTc = 2 * kStageBytes + kGroupRowBytes + 1024;
+constexpr uint32_t kSmemTc = 227 * 1024;
+constexpr uint32_t kTmemO = 256, kTmemGroup = 384, kTmemQ = 448;
 
 // ------------------------------------------------- tensor-core operands
 // Shared-memory operand with the 128-byte swizzle: start, leading and stride
@@ -35,18 +40,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) | (1ull << 46) |
          (2ull << 61);
 }
-// fp32 accumulator, fp16 operands, M = N = 128.
-constexpr uint32_t kIdesc = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);
-constexpr uint32_t kIdesc16 = (1u << 4) | ((16u / 8) << 17) | ((128u / 16) << 24);  // N = 16
+// fp32 accumulator, fp16 operands, M = 128, N columns.
+__host__ __device__ constexpr uint32_t idesc(uint32_t n) { return (1u << 4) | ((n / 8) << 17) | ((128u / 16) << 24); }
 constexpr uint32_t kNegB = 1u << 14, kRowsB = 1u << 16;  // B negated; B's keys along its rows
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
@@ -110,27 +107,37 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t (&r)[16
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 // ---------------------------------------------------------------- issuer
-__device__ __forceinline__ bool issue_pv(const Bars& B, uint32_t tmem, uint32_t stage0, int i, bool first, volatile int* gave_up) {
+// What the issuer remembers of a tile whose product with the values is due.
+struct Due {
+  bool first;  // of its piece: O starts anew
+  int piece;   // its number
+  int slot;    // the last of an fp16 piece: where the piece's flag goes; else -1
+};
+__device__ __forceinline__ bool issue_pv(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, const Tail* tail, int i,
+                                         const Due& due, volatile int* gave_up) {
   const int st = i & 1, ph = (i >> 1) & 1;
   if (!mbar_wait(B.p_full + 8 * st, ph, gave_up) || !mbar_wait(B.full_v + 8 * st, ph, gave_up)) return false;
   tc_after();
   const uint32_t v = stage0 + st * kStageBytes + 2 * kTileBytes;
 #pragma unroll
-  for (int ks = 0; ks < 8; ++ks)  // 16 keys: 16 rows of both 64-channel halves
-    mma_ts(tmem + 256, tmem + 128 * st + 8 * ks, smem_desc(v + ks * 2048, kTile * 128, 1024), kIdesc | kRowsB,
-           !(first && ks == 0));
+  for (int ks = 0; ks < kTile / 16; ++ks)  // 16 keys: 16 rows of both 64-channel halves
+    mma_ts(tmem + kTmemO, tmem + 128 * st + 8 * ks, smem_desc(v + ks * 2048, kTile * 128, 1024), idesc(128) | kRowsB,
+           !(due.first && ks == 0));
+  // (full_v was waited for at every tile of the piece)
+  if (due.slot >= 0) p.part_flag[due.slot] = *(volatile const int*)&tail->bad_piece[due.piece & 3] == due.piece + 1;
   mma_commit(B.empty_v + 8 * st);
   mma_commit(B.o_done);
   return true;
 }
-__device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t q, uint32_t stage0, uint32_t rows,
-                                      int x, int x_end, volatile int* gave_up) {
+__device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, uint32_t rows,
+                                      const Tail* tail, int x, int x_end, volatile int* gave_up) {
   int i = 0;
-  bool first_prev = false;
-  while (x < x_end) {
+  Due due{};
+  for (int piece = 0; x < x_end; ++piece) {
     const Piece c = piece_at(p, x, x_end);
     const int parts = c.quant || p.geo.pre_rope ? 2 : 1;
     const bool grouped = channel_scales(p.geo) && c.quant;
+    if (!mbar_wait(B.q_full, piece & 1, gave_up)) return;
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
       if (!mbar_wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
@@ -138,45 +145,86 @@ __device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32
       for (int part = 0; part < parts; ++part) {
         const uint32_t k = stage0 + st * kStageBytes + part * kTileBytes;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {  // 16 channels
-          const uint32_t off = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;
-          mma_ss(tmem + 128 * st, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), kIdesc | (part ? kNegB : 0),
-                 part + ks > 0);
-        }
+        for (int ks = 0; ks < 8; ++ks)  // 16 channels
+          mma_ts(tmem + 128 * st, tmem + kTmemQ + 8 * ks, smem_desc(k + (ks >> 2) * (kTile * 128) + (ks & 3) * 32, 16, 1024),
+                 idesc(kTile) | (part ? kNegB : 0), part + ks > 0);
       }
-      if (grouped) {  // q . m and q . s of the tile's four groups (columns 8..15 are of no use)
+      if (grouped) {  // q . m and q . s of the tile's groups (columns 8..15 are of no use)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ss(tmem + 384 + 16 * st, smem_desc(q + (ks >> 2) * (kTile * 128) + (ks & 3) * 32, 16, 1024),
-                 smem_desc(rows + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 1024), kIdesc16, ks > 0);
+          mma_ts(tmem + kTmemGroup + 16 * st, tmem + kTmemQ + 8 * ks, smem_desc(rows + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 1024),
+                 idesc(16), ks > 0);
       }
       mma_commit(B.s_full + 8 * st);
       mma_commit(B.empty_k + 8 * st);
       // the product of the tile before, whose weights are computed meanwhile
-      if (i && !issue_pv(B, tmem, stage0, i - 1, first_prev, gave_up)) return;
-      first_prev = t == 0;  // a piece's first tile starts O anew
+      if (i && !issue_pv(p, B, tmem, stage0, tail, i - 1, due, gave_up)) return;
+      due = Due{t == 0, piece, !c.quant && t == c.cnt - 1 ? c.slot : -1};
     }
     x += c.cnt;
   }
-  if (i) issue_pv(B, tmem, stage0, i - 1, first_prev, gave_up);
+  if (i) issue_pv(p, B, tmem, stage0, tail, i - 1, due, gave_up);
 }
 
 // --------------------------------------------------------------- softmax
-__device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint32_t tmem, volatile int* bad_piece, int x,
-                                        int x_end, int tid, volatile int* gave_up) {
+// The thread's query row of a piece into TMEM, in the keys' channel order.
+__device__ __forceinline__ void put_q(const TreeParams& p, const Bars& B, const Piece& c, uint32_t tmem_lane, int r) {
+  const Geometry& G = p.geo;
+  const bool paired = c.quant && channel_scales(G) && paired_order(G.kb), paired_iq = c.quant && G.gkc && paired_order(G.kb);
+  const uint4* row = nullptr;
+  if (r < c.nr) {
+    const int j = (c.r0 + r) / c.n_b, node = c.r0 + r - j * c.n_b;
+    row = reinterpret_cast<const uint4*>(p.q + (((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g + j) * p.n + node) * kHeadDim);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[32];
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row) v = __ldg(row + 8 * h + ch);
+      if (paired || paired_iq) v = pair_chunk(v);
+      w[4 * ch] = v.x, w[4 * ch + 1] = v.y, w[4 * ch + 2] = v.z, w[4 * ch + 3] = v.w;
+    }
+    tm_store32(tmem_lane + kTmemQ + 32 * h, w);
+  }
+  tm_wait_st();
+  tc_before();
+  mbar_arrive_warp(B.q_full);
+}
+
+// Two logits to two weights: packed multiply-add, two exponentials.
+__device__ __forceinline__ float2 weights2(uint32_t s0, uint32_t s1, float2 scale, float2 off) {
+  float2 z;
+  asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(z.x), "=f"(z.y)
+      : "r"(s0), "r"(s1), "f"(scale.x), "f"(scale.y), "f"(off.x), "f"(off.y));
+  return make_float2(ex2(z.x), ex2(z.y));
+}
+__device__ __forceinline__ void add2(float2& l, float2 a) {
+  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%0, %1};\nmov.b64 b, {%2, %3};\nadd.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(l.x), "+f"(l.y)
+      : "f"(a.x), "f"(a.y));
+}
+
+__device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint32_t tmem, int x, int x_end, int tid, volatile int* gave_up) {
   // warp-uniform: the TMEM loads are for whole warps
   auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
+  constexpr int kCh = kTile / 32;
   const int r = tid;
-  const uint32_t lane0 = (uint32_t)(r & ~31) << 16, O = tmem + 256 + lane0;
+  const uint32_t lane0 = (uint32_t)(r & ~31) << 16, O = tmem + kTmemO + lane0;
+  const float centre = (float)(1 << (p.geo.kb - 1));
   int i = 0;
-  for (int piece = 0; x < x_end; ++piece) {
-    const Piece c = piece_at(p, x, x_end);
+  Piece c = piece_at(p, x, x_end);
+  put_q(p, B, c, tmem + lane0, r);
+  while (x < x_end) {
     const bool work = (r & ~31) < c.nr;  // the warp holds rows
     const uint32_t* mask_row =
         p.mask && !c.quant && r < c.nr ? p.mask + ((size_t)c.b * p.n + (c.r0 + r) % c.n_b) * p.words : nullptr;
     const bool grouped = channel_scales(p.geo) && c.quant;
-    const float centre = (float)(1 << (p.geo.kb - 1));
     float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
       const uint32_t S = tmem + 128 * st + lane0;
@@ -184,89 +232,107 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
       tc_after();
       if (work) {
         const int f0 = (c.k0 + t) * kTile;
-        uint32_t ok[4], v[32];
-        float top = -INFINITY, base[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // the groups' share of the logits
+        uint32_t ok[kCh], v[32], h[16 * kCh];
+        float base[kCh] = {};  // the groups' share of the logits
+        bool whole = true;     // every key is seen
+#pragma unroll
+        for (int ch = 0; ch < kCh; ++ch) {
+          ok[ch] = seen(p, c, mask_row, f0 + 32 * ch);
+          whole = whole && ok[ch] == 0xFFFFFFFFu;
+        }
+        whole = __all_sync(0xffffffffu, whole);
         if (grouped) {
           uint32_t y[8];
-          tm_load8(y, tmem + 384 + 16 * st + lane0);
+          tm_load8(y, tmem + kTmemGroup + 16 * st + lane0);
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch)
+          for (int ch = 0; ch < kCh; ++ch)
             base[ch] = fmaf(centre, __uint_as_float(y[4 + ch]), __uint_as_float(y[ch])) * p.q_scale;
         }
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          ok[ch] = seen(p, c, mask_row, f0 + 32 * ch);
-          tm_load32(v, S + 32 * ch);
-          tm_wait_ld(v);
-          float mx = -INFINITY;
-          if (ok[ch] == 0xFFFFFFFFu) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if ((ok[ch] >> e) & 1) mx = fmaxf(mx, __uint_as_float(v[e]));
-          }
-          top = fmaxf(top, fmaf(mx, p.q_scale, base[ch]));
-        }
-        const bool move = top > m + kLazy;
-        if (__any_sync(0xffffffffu, move)) {
-          const float al = move ? ex2(m - top) : 1.0f;
-          if (move) m = top, l *= al;
-          if (t > 0) {
-            if (!wait(B.o_done, i - 1)) return;  // the products so far
-            tc_after();
+        float sum = 0.0f;
+        bool search = t == 0;  // the row's maximum is to be found
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              tm_load32(v, O + 32 * ch);
+        for (int pass = 0; pass < 2; ++pass) {
+          if (search || __any_sync(0xffffffffu, m == -INFINITY)) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int ch = 0; ch < kCh; ++ch) {
+              tm_load32(v, S + 32 * ch);
               tm_wait_ld(v);
+              float mx = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
-              tm_store32(O + 32 * ch, v);
+              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (ok[ch] >> e) & 1 ? __uint_as_float(v[e]) : -INFINITY);
+              top = fmaxf(top, fmaf(mx, p.q_scale, base[ch]));
             }
-            tm_wait_st();
+            const bool move = top > m;
+            if (__any_sync(0xffffffffu, move)) {
+              const float al = move ? ex2(m - top) : 1.0f;
+              if (move) m = top, l *= al;
+              if (t > 0) {
+                if (!wait(B.o_done, i - 1)) return;  // the products so far
+                tc_after();
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                  tm_load32(v, O + 32 * ch);
+                  tm_wait_ld(v);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * al);
+                  tm_store32(O + 32 * ch, v);
+                }
+                tm_wait_st();
+              }
+            }
           }
+          const float mu = m == -INFINITY ? 0.0f : m;
+          float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int ch = 0; ch < kCh; ++ch) {
+            tm_load32(v, S + 32 * ch);
+            tm_wait_ld(v);
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = (ok[ch] >> e) & 1 ? v[e] : 0xFF800000u;  // -inf
+            }
+            const float2 scale = make_float2(p.q_scale, p.q_scale), off = make_float2(base[ch] - mu, base[ch] - mu);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 w = weights2(v[2 * e], v[2 * e + 1], scale, off);
+              add2(part, w);
+              h[16 * ch + e] = as_u32(__floats2half2_rn(w.x, w.y));
+            }
+          }
+          sum = part.x + part.y;
+          // past the range (or not a number): find the maximum and do it again
+          if (search || __all_sync(0xffffffffu, sum <= kTopSum)) break;
+          search = true;
         }
-        const float mu = m == -INFINITY ? 0.0f : m;
+        l += sum;
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tm_load32(v, S + 32 * ch);
-          tm_wait_ld(v);
-          uint32_t h[16];
-          const float off = base[ch] - mu;
-          if (ok[ch] != 0xFFFFFFFFu) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (ok[ch] >> e) & 1 ? v[e] : 0xFF800000u;  // -inf
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float a = ex2(fmaf(__uint_as_float(v[2 * e]), p.q_scale, off));
-            const float b = ex2(fmaf(__uint_as_float(v[2 * e + 1]), p.q_scale, off));
-            l += a + b;
-            h[e] = as_u32(__floats2half2_rn(a, b));
-          }
-          tm_store16(S + 16 * ch, h);  // over logits that are read
-        }
+        for (int ch = 0; ch < kCh; ++ch) tm_store16(S + 16 * ch, reinterpret_cast<const uint32_t(&)[16]>(h[16 * ch]));  // over the logits
         tm_wait_st();
       }
       tc_before();
-      mbar_arrive(B.p_full + 8 * st);
+      mbar_arrive_warp(B.p_full + 8 * st);
     }
-    // the piece's partial result
-    if (!wait(B.o_done, i - 1) || !wait(B.full_v + 8 * ((i - 1) & 1), (i - 1) >> 1)) return;
-    if (r == 0 && !c.quant) p.part_flag[c.slot] = bad_piece[piece & 3] == piece + 1;
+    // the next piece's Q (this piece's logits are all computed), then this piece's partial result
+    const Piece d = c;
+    x += d.cnt;
+    if (x < x_end) {
+      c = piece_at(p, x, x_end);
+      put_q(p, B, c, tmem + lane0, r);
+    }
+    if (!wait(B.o_done, i - 1)) return;
     tc_after();
     if (work) {
-      const size_t at = (size_t)c.slot * p.rstride + r;
-      if (r < c.nr) p.part_ml[at] = make_float2(m, l);
-      const bool paired = c.quant && !p.geo.pre_rope && p.geo.kb != 3 && paired_order(p.geo.vb);
+      const size_t at = (size_t)d.slot * p.rstride + r;
+      if (r < d.nr) p.part_ml[at] = make_float2(m, l);
+      const bool paired = d.quant && p.geo.vb != 3 && paired_order(p.geo.vb);
       float* acc = p.part_acc + at * kHeadDim;
 #pragma unroll 1
       for (int ch = 0; ch < 4; ++ch) {
         uint32_t v[32];
         tm_load32(v, O + 32 * ch);
         tm_wait_ld(v);
-        if (r < c.nr) {
+        if (r < d.nr) {
           uint4* dst = reinterpret_cast<uint4*>(acc + 32 * ch);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -278,62 +344,66 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
       }
       tc_before();  // O is read before the next piece's weights are announced
     }
-    x += c.cnt;
   }
 }
 
 __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_constant__ TreeParams p) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *sQ = smem_raw, *stage0 = sQ + kTileBytes, *sM = stage0 + 2 * kStageBytes, *tail = sM + kGroupRowBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 128);
-  volatile int* gave_up = reinterpret_cast<volatile int*>(tail + 132);
-  float* lut = reinterpret_cast<float*>(tail + 144);  // K levels, V levels
-  volatile int* bad_piece = reinterpret_cast<volatile int*>(tail + 208);  // [4] pieces with drafted values that are not finite
+  // (the swizzle's 1024-byte alignment: there is no other shared memory to shift the start)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *stage0 = smem, *sM = stage0 + 2 * kStageBytes;
+  Tail* tail = reinterpret_cast<Tail*>(sM + kGroupRowBytes);
+  uint8_t* raw0 = sM + kGroupRowBytes + 1024;
+  volatile int* gave_up = &tail->gave_up;
   const int tid = threadIdx.x, w = tid >> 5;
-  const uint32_t b0 = (uint32_t)__cvta_generic_to_shared(bars);
-  const Bars B{b0, b0 + 16, b0 + 32, b0 + 48, b0 + 64, b0 + 80, b0 + 96, b0 + 112};
+  const Bars B = bars_at((uint32_t)__cvta_generic_to_shared(tail->bars));
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(B.full_k + 8 * i, kProducers);
-      mbar_init(B.full_v + 8 * i, kProducers);
+      mbar_init(B.full_k + 8 * i, kProducers / 32);
+      mbar_init(B.full_v + 8 * i, kProducers / 32);
       mbar_init(B.empty_k + 8 * i, 1);
       mbar_init(B.empty_v + 8 * i, 1);
       mbar_init(B.s_full + 8 * i, 1);
-      mbar_init(B.p_full + 8 * i, kSoftThreads);
+      mbar_init(B.p_full + 8 * i, kSoftThreads / 32);
+    }
+    for (int i = 0; i < kMaxRaw; ++i) {
+      mbar_init(B.raw_full + 8 * i, 1);
+      mbar_init(B.raw_empty + 8 * i, kProducers / 32);
     }
     mbar_init(B.o_done, 1);
+    mbar_init(B.q_full, kSoftThreads / 32);
     mbar_init(B.done, 1);
-    // (the swizzle's 1024-byte alignment: there is no other shared memory to shift the start)
-    *gave_up = ((uint32_t)__cvta_generic_to_shared(smem_raw) & 1023) != 0;
-    for (int i = 0; i < 4; ++i) bad_piece[i] = 0;
+    *gave_up = ((uint32_t)__cvta_generic_to_shared(smem) & 1023) != 0;
+    for (int i = 0; i < 4; ++i) tail->bad_piece[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (tid < 16) lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
-  const int issuer = (kSoftThreads + kProducers) / 32;
+  if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
+  constexpr int issuer = (kSoftThreads + kProducers) / 32, loader = issuer + 1;
   if (w == issuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
-                     (uint32_t)__cvta_generic_to_shared(tmem_slot))
+                     (uint32_t)__cvta_generic_to_shared(&tail->tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const uint32_t tmem = *(volatile uint32_t*)&tail->tmem;
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
   if (*gave_up) {
   } else if (w < kSoftThreads / 32) {
-    softmax(p, B, tmem, bad_piece, x, x_end, tid, gave_up);
+    softmax(p, B, tmem, x, x_end, tid, gave_up);
   } else if (w < issuer) {
-    produce<kTile>(p, B, sQ, stage0, sM, lut, bad_piece, x, x_end, tid - kSoftThreads, gave_up);
-  } else {
+    produce<0, true>(p, B, nullptr, stage0, sM, raw0, tail, x, x_end, tid - kSoftThreads, gave_up);
+  } else if (w == issuer) {
     if ((tid & 31) == 0) {
-      issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(sQ), (uint32_t)__cvta_generic_to_shared(stage0),
-            (uint32_t)__cvta_generic_to_shared(sM), x, x_end, gave_up);
+      issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(stage0), (uint32_t)__cvta_generic_to_shared(sM), tail, x,
+            x_end, gave_up);
       mma_commit(B.done);  // whatever is in flight ends before TMEM is freed
-      mbar_wait(B.done, 0, gave_up);
+      mbar_wait(B.done, 0, nullptr);
     }
+    __syncwarp();
+  } else if (w == loader) {
+    if ((tid & 31) == 0) load_tiles<true>(p, B, (uint32_t)__cvta_generic_to_shared(raw0), x, x_end, gave_up);
     __syncwarp();
   }
   tc_before();
@@ -352,7 +422,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
 
 }  // namespace
 
-cudaError_t launch_tree_tc(const TreeParams& p, cudaStream_t st) {
+cudaError_t launch_tree_tc(TreeParams& p, cudaStream_t st) {
+  p.raw = raw_slot(p.geo, true, kSmemTc - kFixedTc);
+  if (kFixedTc + p.raw.slots * p.raw.bytes > kSmemTc) return cudaErrorInvalidValue;
   static std::atomic<long long> memo[kMemoDevices];
   const cudaError_t e = ensure_smem_limit(tree_tc_kernel, memo, (int)kSmemTc);
   if (e != cudaSuccess) return e;
