@@ -221,6 +221,36 @@ def _ptr(t, what: str, dtype=None, numel: int | None = None, allow_none=False):
     return t.data_ptr()
 
 
+def _arg(t, what: str, dtype, nbytes: int):
+    """_ptr for the calls whose host time counts: the checks of a proper
+    tensor in one line, anything else to _ptr for its errors."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.nbytes >= nbytes:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, what, dtype, nbytes)
+
+
+def _stream_of(stream, t):
+    """A stream's handle; None: the current stream of tensor t's device."""
+    if stream is None:
+        if isinstance(t, int):
+            return _stream(None)
+        import torch
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on_device(*tensors):
+    """The calls launch on the current device: their tensors live there."""
+    import torch
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.device.index != here:
+            raise ValueError(f"tensors must be on the current device cuda:{here}, got {t.device}")
+
+
 def _stream(stream):
     if stream is None:
         import torch
@@ -261,12 +291,23 @@ def kvq_decode_attn(cfg, layer_buf, tokens: int, q, out, lse=None, workspace=Non
     _check("kvq_decode_attn", st)
 
 
+_row_arrays = {}
+
+
+def _row_array(batch: int):
+    """The ctypes array type of `batch` int32 (made once per size)."""
+    t = _row_arrays.get(batch)
+    if t is None:
+        t = _row_arrays[batch] = C.c_int32 * batch
+    return t
+
+
 def _rows(values, batch: int, what: str):
     """A host int32 array of one value per batch row."""
     vals = [int(v) for v in values]
     if len(vals) != batch:
         raise ValueError(f"{what}: one value per batch row ({batch}), got {len(vals)}")
-    return (C.c_int32 * batch)(*vals)
+    return _row_array(batch)(*vals)
 
 
 def kvq_append_ragged(cfg, layer_buf, tokens_before, n_new, k_new, v_new, stream=None):
@@ -441,16 +482,18 @@ def kvq_tree_attn(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse=No
         raise ValueError("q must be [B, Hq, n, d]")
     n = int(q.shape[2])
     nq, nk = c.batch * hq * n * c.head_dim * 2, c.batch * hkv * n * c.head_dim * 2
-    st = lib().kvq_tree_attn(
-        C.byref(c), _ptr(layer_buf, "layer_buf", numel=lay.layer_bytes), _rows(tokens, c.batch, "tokens"),
-        _ptr(q, "q", torch.float16, nq),
-        _ptr(k_draft, "k_draft", torch.float16, nk, allow_none=mask is None),
-        _ptr(v_draft, "v_draft", torch.float16, nk, allow_none=mask is None),
-        _ptr(mask, "mask", torch.int32, c.batch * n * ((n + 31) // 32) * 4, allow_none=True), n,
-        None if nodes is None else _rows(nodes, c.batch, "nodes"), _ptr(out, "out", torch.float16, nq),
-        _ptr(lse, "lse", torch.float32, c.batch * hq * n * 4, allow_none=True),
-        _ptr(workspace, "workspace", allow_none=True),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    h, f = torch.float16, torch.float32
+    layer = _arg(layer_buf, "layer_buf", torch.uint8, lay.layer_bytes)
+    qp, op = _arg(q, "q", h, nq), _arg(out, "out", h, nq)
+    kp = vp = mp = None
+    if mask is not None:
+        kp, vp = _arg(k_draft, "k_draft", h, nk), _arg(v_draft, "v_draft", h, nk)
+        mp = _arg(mask, "mask", torch.int32, c.batch * n * ((n + 31) // 32) * 4)
+    lp = None if lse is None else _arg(lse, "lse", f, c.batch * hq * n * 4)
+    wp, wn = (None, 0) if workspace is None else (_arg(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+    _on_device(layer_buf, q, k_draft, v_draft, mask, out, lse, workspace)
+    st = lib().kvq_tree_attn(c, layer, _rows(tokens, c.batch, "tokens"), qp, kp, vp, mp, n,
+                             None if nodes is None else _rows(nodes, c.batch, "nodes"), op, lp, wp, wn, _stream_of(stream, q))
     _check("kvq_tree_attn", st)
 
 
@@ -472,11 +515,13 @@ def kvq_attn_mass(cfg, layer_buf, tokens, q, lse, mass, weight=None, decay: floa
     if q.dim() not in (3, 4):
         raise ValueError("q must be [B, Hq, n, d] or [B, Hq, d]")
     n = int(q.shape[2]) if q.dim() == 4 else 1
-    st = lib().kvq_attn_mass(
-        C.byref(c), _ptr(layer_buf, "layer_buf", numel=lay.layer_bytes), _rows(tokens, c.batch, "tokens"),
-        _ptr(q, "q", torch.float16, c.batch * hq * n * c.head_dim * 2), _ptr(lse, "lse", torch.float32, c.batch * hq * n * 4),
-        _ptr(weight, "weight", torch.float32, c.batch * n * 4, allow_none=True), n, float(decay),
-        _ptr(mass, "mass", torch.float32, c.batch * c.n_kv_heads * c.max_tokens * 4), _stream(stream))
+    f = torch.float32
+    layer = _arg(layer_buf, "layer_buf", torch.uint8, lay.layer_bytes)
+    qp, lp = _arg(q, "q", torch.float16, c.batch * hq * n * c.head_dim * 2), _arg(lse, "lse", f, c.batch * hq * n * 4)
+    wp = None if weight is None else _arg(weight, "weight", f, c.batch * n * 4)
+    mp = _arg(mass, "mass", f, c.batch * c.n_kv_heads * c.max_tokens * 4)
+    _on_device(layer_buf, q, lse, weight, mass)
+    st = lib().kvq_attn_mass(c, layer, _rows(tokens, c.batch, "tokens"), qp, lp, wp, n, float(decay), mp, _stream_of(stream, q))
     _check("kvq_attn_mass", st)
 
 
@@ -492,12 +537,12 @@ def kvq_evict(cfg, layer_buf, tokens, n_groups, mass, mass_out, source=None, wor
     rows, drop = _rows(tokens, c.batch, "tokens"), _rows(n_groups, c.batch, "n_groups")
     record = c.batch * c.n_kv_heads * c.max_tokens * 4
     slots = max(0, c.max_tokens - c.n_sink - c.n_recent) // 32
-    st = lib().kvq_evict(
-        C.byref(c), _ptr(layer_buf, "layer_buf", numel=lay.layer_bytes), rows, drop,
-        _ptr(mass, "mass", torch.float32, record), _ptr(mass_out, "mass_out", torch.float32, record),
-        _ptr(source, "source", torch.int32, c.batch * c.n_kv_heads * slots * 4, allow_none=True),
-        _ptr(workspace, "workspace", allow_none=True),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    layer = _arg(layer_buf, "layer_buf", torch.uint8, lay.layer_bytes)
+    ip, op = _arg(mass, "mass", torch.float32, record), _arg(mass_out, "mass_out", torch.float32, record)
+    sp = None if source is None else _arg(source, "source", torch.int32, c.batch * c.n_kv_heads * slots * 4)
+    wp, wn = (None, 0) if workspace is None else (_arg(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+    _on_device(layer_buf, mass, mass_out, source, workspace)
+    st = lib().kvq_evict(c, layer, rows, drop, ip, op, sp, wp, wn, _stream_of(stream, mass))
     _check("kvq_evict", st)
     return [t - 32 * e for t, e in zip(rows, drop)]
 

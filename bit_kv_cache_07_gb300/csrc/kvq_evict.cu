@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kSumThreads = 256;
 constexpr int kSelThreads = 1024;
+constexpr int kOwn = 4;  // keys per thread of the selection in registers
 constexpr int kMoveThreads = 256;
 
 // A float as its signed 24-bit mantissa and exponent (of the last bit).
@@ -153,8 +154,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   int* mover = p.mover + (size_t)s * p.cap;
   int* source = p.source ? p.source + (size_t)s * p.cap : nullptr;
   int nmoves = 0;
-  // each thread's contiguous groups
+  // each thread's contiguous groups; up to kOwn of them stay in registers over
+  // the counting (from L2 each of up to 64 counts would wait a round trip)
   const int per = (ng + kSelThreads - 1) / kSelThreads, j0 = min(ng, tid * per), j1 = min(ng, j0 + per);
+  unsigned long long own[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) own[i] = j0 + i < j1 && E > 0 ? keys[j0 + i] : ~0ull;
+  auto count_below = [&](unsigned long long bound) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) c += own[i] < bound;  // (absent: the largest key, below nothing)
+    for (int j = j0 + kOwn; j < j1; ++j) c += keys[j] < bound;
+    return block_sum(c, sh);
+  };
   if (E > 0) {
     unsigned long long bound = ~0ull;
     int below = 0;  // keys < bound
@@ -162,9 +174,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
       unsigned long long lo = 0;  // at most E keys are below it
       for (int bit = 63; bit >= 0; --bit) {
         const unsigned long long mid = lo | (1ull << bit);
-        int c = 0;
-        for (int j = j0; j < j1; ++j) c += keys[j] < mid;
-        c = block_sum(c, sh);
+        const int c = count_below(mid);
         if (c <= E) {
           lo = mid;
           below = c;
@@ -213,8 +223,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   float* out = p.mass_out + (size_t)s * p.max_tokens;
   const int first = min(p.S, T) + (ng > 0 ? kGroupTokens * left : 0);
   if (in != out)
-    for (int t = tid; t < first; t += kSelThreads) out[t] = in[t];
+    for (int t0 = 0; t0 < first; t0 += 8 * kSelThreads) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = t0 + i * kSelThreads + tid < first ? in[t0 + i * kSelThreads + tid] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (t0 + i * kSelThreads + tid < first) out[t0 + i * kSelThreads + tid] = v[i];
+    }
   __syncthreads();
+#pragma unroll 4
   for (int i = tid; i < nmoves * kGroupTokens; i += kSelThreads)
     out[p.S + hole[i >> 5] * kGroupTokens + (i & 31)] = in[p.S + mover[i >> 5] * kGroupTokens + (i & 31)];
   const int shift = kGroupTokens * E;
@@ -230,8 +248,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_
   for (int t = T - shift + tid; t < T; t += kSelThreads) out[t] = 0.0f;
 }
 
-__device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, int bytes, int lane) {
-  for (int i = 16 * lane; i < bytes; i += 512) *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
+// bytes from src to dst (apart from each other), 8 chunks of 16 per lane in flight.
+__device__ __noinline__ void copy_bytes(uint8_t* __restrict__ dst, const uint8_t* __restrict__ src, int bytes, int lane) {
+  for (int i = 16 * lane; i < bytes; i += 8 * 512) {
+    uint4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + 512 * u < bytes) v[u] = *reinterpret_cast<const uint4*>(src + i + 512 * u);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + 512 * u < bytes) *reinterpret_cast<uint4*>(dst + i + 512 * u) = v[u];
+  }
 }
 
 // The moves, one warp per group; window rows from the workspace.
@@ -247,11 +274,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
       if (k >= p.moves[s]) continue;
       const size_t to = p.hole[(size_t)s * p.cap + k], from = p.mover[(size_t)s * p.cap + k];
       if (G.fp16_mode) {
-        const size_t base = (size_t)s * G.ring + p.S;
-        uint8_t *kr = reinterpret_cast<uint8_t*>(p.L.k_ring), *vr = reinterpret_cast<uint8_t*>(p.L.v_ring);
+        const size_t base = ((size_t)s * G.ring + p.S) * 256;
+        uint8_t *kr = reinterpret_cast<uint8_t*>(p.L.k_ring) + base, *vr = reinterpret_cast<uint8_t*>(p.L.v_ring) + base;
         constexpr int kBytes = kGroupTokens * kHeadDim * 2;
-        copy_bytes(kr + (base * 256 + to * kBytes), kr + (base * 256 + from * kBytes), kBytes, lane);
-        copy_bytes(vr + (base * 256 + to * kBytes), vr + (base * 256 + from * kBytes), kBytes, lane);
+        copy_bytes(kr + to * kBytes, kr + from * kBytes, kBytes, lane);
+        copy_bytes(vr + to * kBytes, vr + from * kBytes, kBytes, lane);
         continue;
       }
       const size_t row = (size_t)s * G.gcap;  // groups before this stream's
@@ -302,7 +329,7 @@ cudaError_t launch_evict(EvictParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int per = kSumThreads / 4;
   p.sum_blocks = p.most ? p.geo.NS * ((p.cap + per - 1) / per) : 0;
-  p.save_blocks = p.most && p.save_rows ? 2 * sms : 0;
+  p.save_blocks = p.most && p.save_rows ? 8 * sms : 0;
   if (p.most) {
     evict_sum_kernel<<<p.sum_blocks + p.save_blocks, kSumThreads, 0, st>>>(p);
     e = cudaGetLastError();
@@ -311,9 +338,9 @@ cudaError_t launch_evict(EvictParams& p, cudaStream_t st) {
   e = launch_dependent(evict_select_kernel, dim3(p.geo.NS), dim3(kSelThreads), 0, st, p);
   if (e != cudaSuccess || !p.most) return e;
   const bool apart = p.geo.fp16_mode;
-  e = launch_dependent(evict_move_kernel, dim3(4 * sms), dim3(kMoveThreads), 0, st, p, 1, apart ? 0 : 1);
+  e = launch_dependent(evict_move_kernel, dim3(8 * sms), dim3(kMoveThreads), 0, st, p, 1, apart ? 0 : 1);
   if (e == cudaSuccess && apart && p.save_rows)
-    e = launch_dependent(evict_move_kernel, dim3(4 * sms), dim3(kMoveThreads), 0, st, p, 0, 1);
+    e = launch_dependent(evict_move_kernel, dim3(8 * sms), dim3(kMoveThreads), 0, st, p, 0, 1);
   return e;
 }
 

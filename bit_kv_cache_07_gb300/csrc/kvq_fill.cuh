@@ -159,68 +159,87 @@ __device__ __forceinline__ void store_chunk(uint8_t* s, uint32_t off, const uint
 // reaches the logits as one number per row and group, q . m + 2^(b-1) q . s:
 // rows 0..2 of sM hold the tile's groups' m, rows 4..6 their s (8 rows of 128
 // channels, q_off<8>).  Half the instructions of an fp32 k split in two.
-template <int BITS>
-__device__ __forceinline__ void keys_channel(int groups, int tid, const uint8_t* raw, const uint32_t* scales, uint8_t* sK, uint8_t* sN) {
-  const int cb = tid & 15;
-#pragma unroll 1
-  for (int j = 0; j < kTile / 32; ++j) {
-    __half2 sc[4];
-    bool big = false;
-    if (j < groups) {
-      uint32_t w[8];
-      *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb];
-      *reinterpret_cast<uint4*>(w + 4) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb + 1];
+//
+// Straight-line code without branches, every shared-memory load ahead of the
+// arithmetic: with two producer warps per scheduler the tile's time is its
+// latency, and branches (rare cases, missing groups) each cost a round trip.
+// Scales so large that c' s passes the fp16 range take the second form (SAT):
+// fp32 products, hi saturated.
+template <int BITS, bool SAT>
+__device__ __forceinline__ void key_products(const __half2 (&c)[4], const __half2 (&sc)[4], uint32_t (&hi)[4], uint32_t (&neg)[4]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sc[i] = as_h2(__byte_perm(w[pair_a<BITS>(i)], w[pair_b<BITS>(i)], 0x7632));
-        const __half2 a = __habs2(sc[i]);
-        big = big || __hgt2_mask(a, h2_const(BITS == 8 ? 0x5FFF : BITS == 4 ? 0x6FFF : 0x77FF)) != 0;  // 2^(b-1) s > 65504
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int t = 32 * j + (tid >> 4) + 16 * v;
-      uint32_t hi[4] = {0, 0, 0, 0}, neg[4] = {0, 0, 0, 0};
-      if (j < groups) {
-        __half2 c[4];
-        code_pairs<BITS, true>(chunk_word<BITS>(raw, t, cb), c);
-        if (!big) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __half2 h = __hmul2(c[i], sc[i]);
-            hi[i] = as_u32(h);
-            neg[i] = as_u32(__hfma2(__hneg2(c[i]), sc[i], h));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 a = __half22float2(c[i]), b = __half22float2(sc[i]);
-            split2(a.x * b.x, a.y * b.y, &hi[i], &neg[i]);
-          }
-        }
-      }
-      const uint32_t o = tile_off(t, cb);
-      store_chunk(sK, o, hi);
-      store_chunk(sN, o, neg);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (SAT) {
+      const float2 a = __half22float2(c[i]), b = __half22float2(sc[i]);
+      split2(a.x * b.x, a.y * b.y, &hi[i], &neg[i]);
+    } else {
+      const __half2 h = __hmul2(c[i], sc[i]);
+      hi[i] = as_u32(h);
+      neg[i] = as_u32(__hfma2(__hneg2(c[i]), sc[i], h));
     }
   }
 }
 template <int BITS>
-__device__ __forceinline__ void group_rows(int groups, int tid, const uint32_t* scales, uint8_t* sM) {
-  if (tid >= 64) return;
-  const int cb = tid & 15, j = tid >> 4;  // (row 3: zeros)
-  uint32_t m[4] = {0, 0, 0, 0}, sc[4] = {0, 0, 0, 0}, w[8];
-  if (j < groups) {
-    *reinterpret_cast<uint4*>(w) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb];
-    *reinterpret_cast<uint4*>(w + 4) = reinterpret_cast<const uint4*>(scales + j * kHeadDim)[2 * cb + 1];
+__device__ __forceinline__ void keys_channel(int groups, int tid, const uint8_t* raw, const uint32_t* scales, const uint32_t* zeros,
+                                             uint8_t* sK, uint8_t* sN, uint8_t* sM) {
+  constexpr int kG = kTile / 32;
+  const int cb = tid & 15, t0 = tid >> 4;
+  uint2 w[2 * kG];
+  uint32_t sw[kG][8];
+#pragma unroll
+  for (int j = 0; j < kG; ++j) {
+    // a tile's missing groups (stale bytes in the slot): zero scales, so zero keys and rows
+    const uint4* p = reinterpret_cast<const uint4*>(j < groups ? scales + j * kHeadDim : zeros) + 2 * cb;
+    *reinterpret_cast<uint4*>(&sw[j][0]) = p[0];
+    *reinterpret_cast<uint4*>(&sw[j][4]) = p[1];
+  }
+#pragma unroll
+  for (int v = 0; v < 2 * kG; ++v) w[v] = chunk_word<BITS>(raw, t0 + 16 * v, cb);
+  __half2 most = h2_const(0);
+#pragma unroll
+  for (int j = 0; j < kG; ++j) {
+    __half2 sc[4];
+    uint32_t m2[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      m[i] = __byte_perm(w[pair_a<BITS>(i)], w[pair_b<BITS>(i)], 0x5410);
-      sc[i] = __byte_perm(w[pair_a<BITS>(i)], w[pair_b<BITS>(i)], 0x7632);
+      sc[i] = as_h2(__byte_perm(sw[j][pair_a<BITS>(i)], sw[j][pair_b<BITS>(i)], 0x7632));
+      m2[i] = __byte_perm(sw[j][pair_a<BITS>(i)], sw[j][pair_b<BITS>(i)], 0x5410);
+      most = __hmax2(most, sc[i]);
+    }
+    if (t0 == j) {
+      const uint32_t s2[4] = {as_u32(sc[0]), as_u32(sc[1]), as_u32(sc[2]), as_u32(sc[3])};
+      store_chunk(sM, q_off<8>(j, cb), m2);
+      store_chunk(sM, q_off<8>(4 + j, cb), s2);
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const uint32_t o = tile_off(t0 + 32 * j + 16 * v, cb);
+      __half2 c[4];
+      uint32_t hi[4], neg[4];
+      code_pairs<BITS, true>(w[2 * j + v], c);
+      key_products<BITS, false>(c, sc, hi, neg);
+      store_chunk(sK, o, hi);
+      store_chunk(sN, o, neg);
     }
   }
-  store_chunk(sM, q_off<8>(j, cb), m);
-  store_chunk(sM, q_off<8>(4 + j, cb), sc);
+  // c' s past the fp16 range: 2^(b-1) s > 65504, s from 512 (8192, 32768) on
+  const float2 top = __half22float2(most);
+  if (fmaxf(top.x, top.y) * (1 << (BITS - 1)) > 65504.0f) {
+#pragma unroll 1
+    for (int v = 0; v < 2 * kG; ++v) {
+      __half2 c[4], sc[4];
+      uint32_t hi[4], neg[4];
+      code_pairs<BITS, true>(chunk_word<BITS>(raw, t0 + 16 * v, cb), c);
+      const uint32_t* p = scales + (v >> 1) * kHeadDim + 8 * cb;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sc[i] = (v >> 1) < groups ? as_h2(__byte_perm(p[pair_a<BITS>(i)], p[pair_b<BITS>(i)], 0x7632)) : h2_const(0);
+      key_products<BITS, true>(c, sc, hi, neg);
+      const uint32_t o = tile_off(t0 + 16 * v, cb);
+      store_chunk(sK, o, hi);
+      store_chunk(sN, o, neg);
+    }
+  }
 }
 
 // Keys of a uniform tile with a scale per token and 64 channels (InnerQ):
@@ -256,35 +275,46 @@ __device__ __forceinline__ void keys_token(int groups, int tid, const uint8_t* r
 template <int BITS>
 __device__ __forceinline__ void values_uniform(int groups, int tid, const uint8_t* raw, const uint32_t* scales, int nvg, int group,
                                                uint8_t* sV) {
-  const int cb = tid & 15;
-#pragma unroll 2
-  for (int v = 0; v < kTile / 16; ++v) {
-    const int t = (tid >> 4) + 16 * v;
-    uint32_t y[4] = {0, 0, 0, 0};
-    if ((v >> 1) < groups) {
-      __half2 c[4];
-      code_pairs<BITS>(chunk_word<BITS>(raw, t, cb), c);
-      const uint32_t w = scales[t * nvg + group];
-      const __half2 mn = __low2half2(as_h2(w)), sc = __high2half2(as_h2(w));
+  constexpr int kN = kTile / 16;
+  const int cb = tid & 15, t0 = tid >> 4;
+  uint2 w[kN];
+  uint32_t sw[kN];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = as_u32(__hfma2(c[i], sc, mn));
-      // |min| from 2^15 on, or a scale from 2^7 (2^11, 2^13 for 4 and 2 bits) on:
-      // the largest code's value may pass the fp16 range by the scale's rounding
-      constexpr uint32_t kBig = BITS == 8 ? 0x28000800u : BITS == 4 ? 0x18000800u : 0x10000800u;
-      if (((w & 0x7FFF7FFFu) + kBig) & 0x80008000u) {
-        const __half2 top = h2_const(0x7BFF), bottom = h2_const(0xFBFF);
+  for (int v = 0; v < kN; ++v) {
+    w[v] = chunk_word<BITS>(raw, t0 + 16 * v, cb);
+    sw[v] = scales[(t0 + 16 * v) * nvg + group];
+  }
+  // the largest code's value may pass the fp16 range by the scale's rounding
+  __half2 most = h2_const(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(y[i]), top), bottom));
-      }
+  for (int v = 0; v < kN; ++v) {
+    if (v >= 2) sw[v] = (v >> 1) < groups ? sw[v] : 0;  // missing groups: zeros
+    most = __hmax2(most, __habs2(as_h2(sw[v])));
+  }
+  const float2 far = __half22float2(most);
+  const bool sat = far.x + far.y * ((1 << BITS) - 1) > 65504.0f;
+#pragma unroll
+  for (int v = 0; v < kN; ++v) {
+    __half2 c[4];
+    uint32_t y[4];
+    code_pairs<BITS>(w[v], c);
+    const __half2 mn = __low2half2(as_h2(sw[v])), sc = __high2half2(as_h2(sw[v]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = as_u32(__hfma2(c[i], sc, mn));
+    if (sat) {
+      const __half2 top = h2_const(0x7BFF), bottom = h2_const(0xFBFF);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(y[i]), top), bottom));
     }
-    store_chunk(sV, tile_off(t, cb), y);
+    store_chunk(sV, tile_off(t0 + 16 * v, cb), y);
   }
 }
 
 __device__ __forceinline__ int tile_groups(const TileSrc& src, int kt) { return min(kTile / 32, (src.tc.Nq - kt * kTile) / 32); }
 
 __device__ __forceinline__ void fill_uniform_keys(const Geometry& G, const LayerPtrs& L, const RawSlot& R, const TileSrc& src, int kt,
-                                                  int tid, const uint8_t* raw, uint8_t* sK, uint8_t* sN) {
+                                                  int tid, const uint8_t* raw, const uint32_t* zeros, uint8_t* sK, uint8_t* sN,
+                                                  uint8_t* sM) {
   const int groups = tile_groups(src, kt);
   const uint32_t* sc = reinterpret_cast<const uint32_t*>(raw + R.ks);
   if (G.gkc) {
@@ -293,17 +323,10 @@ __device__ __forceinline__ void fill_uniform_keys(const Geometry& G, const Layer
     else if (G.kb == 4) keys_token<4>(groups, tid, raw, sc, norm, sK, sN);
     else keys_token<2>(groups, tid, raw, sc, norm, sK, sN);
   } else {
-    if (G.kb == 8) keys_channel<8>(groups, tid, raw, sc, sK, sN);
-    else if (G.kb == 4) keys_channel<4>(groups, tid, raw, sc, sK, sN);
-    else keys_channel<2>(groups, tid, raw, sc, sK, sN);
+    if (G.kb == 8) keys_channel<8>(groups, tid, raw, sc, zeros, sK, sN, sM);
+    else if (G.kb == 4) keys_channel<4>(groups, tid, raw, sc, zeros, sK, sN, sM);
+    else keys_channel<2>(groups, tid, raw, sc, zeros, sK, sN, sM);
   }
-}
-__device__ __forceinline__ void fill_group_rows(const Geometry& G, const RawSlot& R, const TileSrc& src, int kt, int tid,
-                                                const uint8_t* raw, uint8_t* sM) {
-  const int groups = tile_groups(src, kt);
-  const uint32_t* sc = reinterpret_cast<const uint32_t*>(raw + R.ks);
-  if (G.kb == 8) group_rows<8>(groups, tid, sc, sM);
-  else group_rows<4>(groups, tid, sc, sM);  // 4 and 2 bits: the same pairs
 }
 __device__ __forceinline__ void fill_uniform_values(const Geometry& G, const RawSlot& R, const TileSrc& src, int kt, int tid,
                                                     const uint8_t* raw, uint8_t* sV) {

@@ -19,7 +19,7 @@ namespace {
 constexpr int kConsumerWarps = kTile / 16;
 constexpr int kConsumers = 32 * kConsumerWarps;
 constexpr int kThreadsMass = kConsumers + kProducers + 32;
-constexpr uint32_t kFixedMass = 2 * kKeyStageBytes + kGroupRowBytes + 512;
+constexpr uint32_t kFixedMass = 2 * kKeyStageBytes + 2 * kGroupRowBytes + kTailBytes;
 constexpr uint32_t kSmemMass = 227 * 1024;
 
 // 8 query rows as the mma's columns: this thread's operand words (row g of
@@ -97,7 +97,7 @@ __device__ __forceinline__ void weigh(const TreeParams& p, const Bars& B, const 
             mma16816(zn, ka, qb[ks][0], qb[ks][1]);
           }
           if (grouped) {  // 8 rows: the groups' min and scale rows (the mma's rows 8..15: the same)
-            ldsm4(ka, aM + q_off<8>(lane & 7, 2 * ks + (lane >> 4)));
+            ldsm4(ka, aM + st * kGroupRowBytes + q_off<8>(lane & 7, 2 * ks + (lane >> 4)));
             mma16816(zg, ka, qb[ks][0], qb[ks][1]);
           }
         }
@@ -136,8 +136,8 @@ template <bool ONE>
 __global__ void __launch_bounds__(kThreadsMass, 1) mass_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *stage0 = smem, *sM = stage0 + 2 * kKeyStageBytes;
-  Tail* tail = reinterpret_cast<Tail*>(sM + kGroupRowBytes);
-  uint8_t* raw0 = sM + kGroupRowBytes + 512;
+  Tail* tail = reinterpret_cast<Tail*>(sM + 2 * kGroupRowBytes);
+  uint8_t* raw0 = sM + 2 * kGroupRowBytes + kTailBytes;
   volatile int* gave_up = &tail->gave_up;
   const int tid = threadIdx.x;
   const Bars B = bars_at((uint32_t)__cvta_generic_to_shared(tail->bars));
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kThreadsMass, 1) mass_kernel(const __grid_cons
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid < 8) tail->lut[tid] = p.k_lut_off[tid];
+  if (tid < kHeadDim) tail->zeros[tid] = 0;
   __syncthreads();
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
   if (tid < kConsumers) {

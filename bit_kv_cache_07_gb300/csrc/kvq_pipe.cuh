@@ -14,7 +14,7 @@ constexpr int kProducers = 256;
 constexpr uint32_t kTileBytes = kTile * kHeadDim * 2;  // 24 KB
 constexpr uint32_t kStageBytes = 3 * kTileBytes;       // K hi, K neg, V
 constexpr uint32_t kKeyStageBytes = 2 * kTileBytes;    // K hi, K neg
-constexpr uint32_t kGroupRowBytes = 8 * kHeadDim * 2;  // the groups' min and scale rows
+constexpr uint32_t kGroupRowBytes = 8 * kHeadDim * 2;  // a stage's groups' min and scale rows
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -100,6 +100,7 @@ __device__ __forceinline__ Piece piece_at(const TreeParams& p, int x, int x_end)
   return c;
 }
 
+constexpr uint32_t kTailBytes = 1024;
 struct Bars {  // shared-memory addresses; by stage (raw: by slot; o_done, q_full, done: one)
   uint32_t full_k, full_v, empty_k, empty_v, s_full, p_full, raw_full, raw_empty, o_done, q_full, done;
 };
@@ -115,8 +116,9 @@ struct Tail {
   int gave_up;
   int bad_piece[4];  // pieces that hold drafted values that are not finite, by number + 1
   float lut[16];     // level offsets of K, of V
+  alignas(16) uint32_t zeros[kHeadDim];  // the scales of groups that a tile lacks
 };
-static_assert(sizeof(Tail) <= 512, "tail");
+static_assert(sizeof(Tail) <= kTailBytes, "tail");
 
 __device__ __forceinline__ TileSrc tile_src(const TreeParams& p, const Piece& c) {
   return TileSrc{c.tc, c.s, c.b, p.mask ? c.n_b : 0, c.tc.Nq % p.geo.ring, in_stream(p.geo, c.s) * p.n};
@@ -200,11 +202,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
       if (!c.quant) fill_fp16_keys(G, p.L, p.freq, p.kd, src, k, tid, sK, sN);
       else if (general) fill_general_keys(G, p.raw, p.freq, tail->lut, src, k, tid, raw, sK, sN);
-      else fill_uniform_keys(G, p.L, p.raw, src, k, tid, raw, sK, sN);
-      if (c.quant && channel_scales(G)) {  // (one buffer: the tile before must have been read)
-        if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
-        fill_group_rows(G, p.raw, src, k, tid, raw, sM);
-      }
+      else fill_uniform_keys(G, p.L, p.raw, src, k, tid, raw, tail->zeros, sK, sN, sM + st * kGroupRowBytes);
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       if constexpr (!V) {
         if (c.quant) {

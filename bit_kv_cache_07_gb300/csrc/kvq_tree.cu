@@ -16,7 +16,7 @@ constexpr int kSmallRows = 16;
 constexpr int kConsumerWarps = kTile / 16;
 constexpr int kConsumers = 32 * kConsumerWarps;
 constexpr int kThreadsSmall = kConsumers + kProducers + 32;
-constexpr uint32_t kFixedSmall = 2 * kStageBytes + kSmallRows * kHeadDim * 2 + kGroupRowBytes + 512;
+constexpr uint32_t kFixedSmall = 2 * kStageBytes + kSmallRows * kHeadDim * 2 + 2 * kGroupRowBytes + kTailBytes;
 constexpr uint32_t kSmemSmall = 227 * 1024;
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -68,7 +68,7 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
           mma16816(zn[1], qa, kb[2], kb[3]);
         }
         if (grouped) {
-          ldsm4(kb, aM + q_off<8>(lane & 7, 2 * ks + ((lane >> 3) & 1)));
+          ldsm4(kb, aM + st * kGroupRowBytes + q_off<8>(lane & 7, 2 * ks + ((lane >> 3) & 1)));
           mma16816(zg, qa, kb[0], kb[1]);
         }
       }
@@ -158,9 +158,10 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
 __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *stage0 = smem, *sQ = stage0 + 2 * kStageBytes, *sM = sQ + kSmallRows * kHeadDim * 2;
-  Tail* tail = reinterpret_cast<Tail*>(sM + kGroupRowBytes);
-  uint8_t* raw0 = sM + kGroupRowBytes + 512;
+  Tail* tail = reinterpret_cast<Tail*>(sM + 2 * kGroupRowBytes);
+  uint8_t* raw0 = sM + 2 * kGroupRowBytes + kTailBytes;
   volatile int* gave_up = &tail->gave_up;
+  grid_dep_trigger();  // the merge may be launched; it waits for this grid's end
   const int tid = threadIdx.x;
   const Bars B = bars_at((uint32_t)__cvta_generic_to_shared(tail->bars));
   if (tid == 0) {
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __gr
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
+  if (tid < kHeadDim) tail->zeros[tid] = 0;
   __syncthreads();
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
   if (tid < kConsumers) {
@@ -200,67 +202,92 @@ __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __gr
   }
 }
 
-// Join the pieces of each row: one CTA per row, 4 warps stride over the
-// pieces (lane l owns channels 4 l .. 4 l + 3), quantized and fp16 pieces
-// summed apart, the quantized sum rotated back once.
-__global__ void __launch_bounds__(128) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+// Join the pieces of each row: one CTA per row.  The partial maxima and sums
+// first, one per thread, and from them every partial result's weight; then
+// 4 warps add the weighted partial results (lane l owns channels 4 l .. 4 l +
+// 3), all loads independent.  Quantized and fp16 pieces are summed apart, the
+// quantized sum rotated back once.
+constexpr int kMergeThreads = 128;
+constexpr int kMaxParts = kMaxSpecCtas * kConsumerWarps;  // of one kind of a row
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   const Geometry& G = p.geo;
   const int b = blockIdx.z, h = blockIdx.y, n_b = p.rows.nodes[b], r = blockIdx.x;
   if (r >= G.g * n_b) return;
   const int j = r / n_b, node = r - j * n_b, rb = r / p.rblk, rr = r - rb * p.rblk;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int nrb = (G.g * n_b + p.rblk - 1) / p.rblk, pair = h * nrb + rb;
   const TileCounts tc = tile_counts(G, p.rows.tokens[b], p.mask ? n_b : 0);
   const int t0 = p.rows.tile0[b] + pair * (tc.qt + tc.ft);
+  __shared__ float sW[2 * kMaxParts];
   __shared__ float sM[4], sL[4];
   __shared__ __align__(16) float sAcc[4][2][kHeadDim];
   __shared__ uint32_t sFlag;
-  if (threadIdx.x == 0) sFlag = 0;
-  grid_dep_wait();
-  __syncthreads();
-  float M = -INFINITY, L = 0.0f;
-  float4 a[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+  if (tid == 0) sFlag = 0;
+  // the partial results of a kind are consecutive in (slot, sub)
+  size_t at0[2];
+  int np[2];
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
     const int first = kind ? t0 + tc.qt : t0, tiles = kind ? tc.ft : tc.qt;
-    if (tiles == 0) continue;
-    const int item = 2 * (p.rows.pair0[b] + pair) + kind;
-    const int c0 = tile_owner(p.ncta, p.total, first), c1 = tile_owner(p.ncta, p.total, first + tiles - 1);
-    const int np = (c1 - c0 + 1) * p.sub;
-    for (int i = w; i < np; i += 4) {
-      const size_t sl = (size_t)(c0 + item) * p.sub + i, at = sl * p.rstride + rr;
-      const float2 ml = p.part_ml[at];
-      if (kind && p.part_flag[sl]) sFlag = 1;
-      if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // nothing seen
-      const float4 v = *reinterpret_cast<const float4*>(p.part_acc + at * kHeadDim + 4 * lane);
-      const float mn = fmaxf(M, ml.x), wo = M == -INFINITY ? 0.0f : ex2(M - mn), wn = ml.x == -INFINITY ? 1.0f : ex2(ml.x - mn);
-      M = mn;
-      L = L * wo + ml.y * wn;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        a[q].x *= wo, a[q].y *= wo, a[q].z *= wo, a[q].w *= wo;
-        if (q == kind)
-          a[q].x += v.x * wn, a[q].y += v.y * wn, a[q].z += v.z * wn, a[q].w += v.w * wn;
-      }
+    np[kind] = 0;
+    at0[kind] = 0;
+    if (tiles) {
+      const int c0 = tile_owner(p.ncta, p.total, first), c1 = tile_owner(p.ncta, p.total, first + tiles - 1);
+      np[kind] = (c1 - c0 + 1) * p.sub;
+      at0[kind] = (size_t)(c0 + 2 * (p.rows.pair0[b] + pair) + kind) * p.sub;
     }
   }
-  if (lane == 0) sM[w] = M, sL[w] = L;
+  grid_dep_wait();
+  __syncthreads();
+  const int all = np[0] + np[1];
+  auto index = [&](int i) { return i < np[0] ? at0[0] + i : at0[1] + (i - np[0]); };
+  float M = -INFINITY;
+  bool bad = false;  // not a number somewhere: the row becomes that
+  for (int i = tid; i < all; i += kMergeThreads) {
+    const size_t sl = index(i);
+    const float2 ml = p.part_ml[sl * p.rstride + rr];
+    if (i >= np[0] && p.part_flag[sl]) sFlag = 1;
+    M = fmaxf(M, ml.x);
+    bad = bad || ml.x != ml.x || ml.y != ml.y;
+  }
+  M = warp_max(M);
+  if (lane == 0) sM[w] = M;
+  bad = __syncthreads_or(bad);
+  M = fmaxf(fmaxf(sM[0], sM[1]), fmaxf(sM[2], sM[3]));
+  float L = 0.0f;
+  for (int i = tid; i < all; i += kMergeThreads) {
+    const float2 ml = p.part_ml[index(i) * p.rstride + rr];
+    const float wt = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
+    sW[i] = wt;
+    L += wt * ml.y;
+  }
+  L = warp_sum(L);
+  if (lane == 0) sL[w] = L;
+  __syncthreads();
+  L = bad ? NAN : sL[0] + sL[1] + sL[2] + sL[3];
+  float4 a[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const float* acc = p.part_acc + (at0[kind] * p.rstride + rr) * kHeadDim + 4 * lane;
+    const float* wt = sW + (kind ? np[0] : 0);
+#pragma unroll 4
+    for (int i = w; i < np[kind]; i += 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(acc + (size_t)i * p.rstride * kHeadDim));
+      const float c = wt[i];
+      if (c != 0.0f) a[kind].x += v.x * c, a[kind].y += v.y * c, a[kind].z += v.z * c, a[kind].w += v.w * c;
+    }
+  }
 #pragma unroll
   for (int q = 0; q < 2; ++q) *reinterpret_cast<float4*>(&sAcc[w][q][4 * lane]) = a[q];
   __syncthreads();
   if (w) return;
-  M = fmaxf(fmaxf(sM[0], sM[1]), fmaxf(sM[2], sM[3]));
-  L = 0.0f;
   float x[2][4] = {};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float wt = sM[i] == -INFINITY ? (sL[i] == 0.0f ? 0.0f : 1.0f) : ex2(sM[i] - M);
-    L += sL[i] * wt;
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[q][e] += sAcc[i][q][4 * lane + e] * wt;
-  }
+      for (int e = 0; e < 4; ++e) x[q][e] += sAcc[i][q][4 * lane + e];
   if (G.hadamard) {
     // Hn = H / sqrt(d): butterflies of width 1, 2 within the lane, 4 .. 64 across lanes
     float* y = x[0];

@@ -29,7 +29,7 @@ constexpr int kThreadsTc = kSoftThreads + kProducers + 64;
 constexpr float kTopSum = 32768.0f;  // a tile's weights stay below fp16's range
 // The 16-column product reads 8 rows behind the group rows as its columns
 // 8..15 (of no use): the kilobyte that holds the tail.
-constexpr uint32_t kFixedTc = 2 * kStageBytes + kGroupRowBytes + 1024;
+constexpr uint32_t kFixedTc = 2 * kStageBytes + 2 * kGroupRowBytes + kTailBytes;
 constexpr uint32_t kSmemTc = 227 * 1024;
 constexpr uint32_t kTmemO = 256, kTmemGroup = 384, kTmemQ = 448;
 
@@ -152,7 +152,7 @@ __device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32
       if (grouped) {  // q . m and q . s of the tile's groups (columns 8..15 are of no use)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + kTmemGroup + 16 * st, tmem + kTmemQ + 8 * ks, smem_desc(rows + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 1024),
+          mma_ts(tmem + kTmemGroup + 16 * st, tmem + kTmemQ + 8 * ks, smem_desc(rows + st * kGroupRowBytes + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 1024),
                  idesc(16), ks > 0);
       }
       mma_commit(B.s_full + 8 * st);
@@ -351,9 +351,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
   // (the swizzle's 1024-byte alignment: there is no other shared memory to shift the start)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *stage0 = smem, *sM = stage0 + 2 * kStageBytes;
-  Tail* tail = reinterpret_cast<Tail*>(sM + kGroupRowBytes);
-  uint8_t* raw0 = sM + kGroupRowBytes + 1024;
+  Tail* tail = reinterpret_cast<Tail*>(sM + 2 * kGroupRowBytes);
+  uint8_t* raw0 = sM + 2 * kGroupRowBytes + kTailBytes;
   volatile int* gave_up = &tail->gave_up;
+  grid_dep_trigger();  // the merge may be launched; it waits for this grid's end
   const int tid = threadIdx.x, w = tid >> 5;
   const Bars B = bars_at((uint32_t)__cvta_generic_to_shared(tail->bars));
   if (tid == 0) {
@@ -377,6 +378,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
+  if (tid < kHeadDim) tail->zeros[tid] = 0;
   constexpr int issuer = (kSoftThreads + kProducers) / 32, loader = issuer + 1;
   if (w == issuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
