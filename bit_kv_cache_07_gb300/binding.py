@@ -229,7 +229,18 @@ def _arg(t, what: str, dtype, nbytes: int):
             return t.data_ptr()
     except AttributeError:
         pass
-    return _ptr(t, what, dtype, nbytes)
+    import torch
+    return _ptr(t, what, None if dtype is torch.uint8 else dtype, nbytes)
+
+
+def _scratch(workspace):
+    """(address, bytes) of a workspace tensor."""
+    import torch
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch tensor")
+    return _arg(workspace, "workspace", torch.uint8, 0), workspace.nbytes
 
 
 def _stream_of(stream, t):
@@ -490,7 +501,7 @@ def kvq_tree_attn(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse=No
         kp, vp = _arg(k_draft, "k_draft", h, nk), _arg(v_draft, "v_draft", h, nk)
         mp = _arg(mask, "mask", torch.int32, c.batch * n * ((n + 31) // 32) * 4)
     lp = None if lse is None else _arg(lse, "lse", f, c.batch * hq * n * 4)
-    wp, wn = (None, 0) if workspace is None else (_arg(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+    wp, wn = _scratch(workspace)
     _on_device(layer_buf, q, k_draft, v_draft, mask, out, lse, workspace)
     st = lib().kvq_tree_attn(c, layer, _rows(tokens, c.batch, "tokens"), qp, kp, vp, mp, n,
                              None if nodes is None else _rows(nodes, c.batch, "nodes"), op, lp, wp, wn, _stream_of(stream, q))
@@ -540,7 +551,7 @@ def kvq_evict(cfg, layer_buf, tokens, n_groups, mass, mass_out, source=None, wor
     layer = _arg(layer_buf, "layer_buf", torch.uint8, lay.layer_bytes)
     ip, op = _arg(mass, "mass", torch.float32, record), _arg(mass_out, "mass_out", torch.float32, record)
     sp = None if source is None else _arg(source, "source", torch.int32, c.batch * c.n_kv_heads * slots * 4)
-    wp, wn = (None, 0) if workspace is None else (_arg(workspace, "workspace", torch.uint8, 0), workspace.nbytes)
+    wp, wn = _scratch(workspace)
     _on_device(layer_buf, mass, mass_out, source, workspace)
     st = lib().kvq_evict(c, layer, rows, drop, ip, op, sp, wp, wn, _stream_of(stream, mass))
     _check("kvq_evict", st)

@@ -787,7 +787,7 @@ kvq_status kvq_attn_mass(const kvq_config* cfg, const void* layer_buf, const int
     p.rows.nodes[b] = n_rows;
     p.rows.tile0[b] = (int)total;
     total += (int64_t)g.Hkv * (tc.qt + tc.ft);
-    if (total > (1ll << 30)) return KVQ_ERR_UNSUPPORTED;
+    if (total > (1ll << 28)) return KVQ_ERR_UNSUPPORTED;
   }
   if (total == 0) return KVQ_OK;  // every row is empty
   p.rows.tile0[g.B] = (int)total;

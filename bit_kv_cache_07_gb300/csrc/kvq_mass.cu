@@ -191,6 +191,7 @@ cudaError_t launch_t(TreeParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_mass(TreeParams& p, cudaStream_t st) {
+  if (mass_stream_eligible(p.geo)) return launch_mass_stream(p, st);
   return p.geo.g * p.n <= 8 ? launch_t<true>(p, st) : launch_t<false>(p, st);
 }
 

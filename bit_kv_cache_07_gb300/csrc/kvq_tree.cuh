@@ -186,5 +186,7 @@ __device__ __forceinline__ bool finite8(const uint4& u) {
 cudaError_t launch_tree_attn(TreeParams& p, cudaStream_t st);
 cudaError_t launch_tree_tc(TreeParams& p, cudaStream_t st);
 cudaError_t launch_attn_mass(TreeParams& p, cudaStream_t st);
+bool mass_stream_eligible(const Geometry& G);
+cudaError_t launch_mass_stream(const TreeParams& t, cudaStream_t st);
 
 }  // namespace kvq

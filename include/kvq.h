@@ -498,7 +498,7 @@ KVQ_API kvq_status kvq_merge_attn(int32_t n_parts, int64_t rows, int32_t head_di
  * weights to fp16; logits, maxima and sums are fp32.  The result does not
  * depend on timing.  Two launches.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (n_nodes > 256, batch >
- * 256, max_tokens > 2^30, more than 2^30 tiles of 128 keys), KVQ_ERR_CAPACITY,
+ * 256, max_tokens > 2^30, more than 2^30 tiles of 96 keys), KVQ_ERR_CAPACITY,
  * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA. */
 KVQ_API kvq_status kvq_tree_attn(const kvq_config *cfg, const void *layer_buf, const int32_t *tokens, const uint16_t *q,
                          const uint16_t *k_draft, const uint16_t *v_draft, const uint32_t *mask, int32_t n_nodes,
@@ -535,10 +535,11 @@ KVQ_API kvq_status kvq_tree_workspace(const kvq_config *cfg, int32_t n_nodes, ui
  *   mass       device f32 [B][n_kv_heads][max_tokens], in the cache's own
  *              stream order; the caller zero-fills it once.  Entries from
  *              tokens[b] on are left as they are
- * One pass over the keys, one launch, no workspace; every entry is summed by
- * one thread in a fixed order.
+ * No workspace; a pass over the keys, and a launch, per 8 rows of a KV head
+ * (one for all rows of non-uniform or pre-RoPE keys); every entry is summed
+ * in a fixed order.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (batch > 256, max_tokens >
- * 2^30, n_rows > 2^20, more than 2^30 tiles of 128 keys), KVQ_ERR_CAPACITY,
+ * 2^30, n_rows > 2^20, more than 2^28 tiles of 96 keys), KVQ_ERR_CAPACITY,
  * KVQ_ERR_CUDA. */
 KVQ_API kvq_status kvq_attn_mass(const kvq_config *cfg, const void *layer_buf, const int32_t *tokens, const uint16_t *q,
                          const float *lse, const float *weight, int32_t n_rows, float decay, float *mass,
