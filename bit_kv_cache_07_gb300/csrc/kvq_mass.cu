@@ -5,167 +5,278 @@
 // KV head's group, row i) that attended it:
 //   mass_t <- decay * mass_t + sum_r w_i exp(scale * q_r . k_t - lse_r)
 // with the log-sum-exp that the attention returned: the rows' softmax is not
-// computed again, one pass over the keys is enough.
+// computed again, one pass over the keys is enough.  Up to 8 rows per KV head
+// over uniform codes go through kvq_mass_stream.cu; this is the kernel for
+// more rows, non-uniform codes and keys cached before RoPE.
 //
-// The tile kernels' copies and producers, for keys alone; 6 warps take 16
-// keys of a tile each as the rows of mma.sync (m16n8k16), the query rows pass
-// as its columns, 8 at a time, so that a key's weights are summed within a
-// quad of lanes.
+// The tile kernels' copies and producers, for keys alone.  A tile's keys are
+// the matrix product's rows (operand A, 96 of 128), the query rows its
+// columns (B, up to 256): a key's logits land in one lane of TMEM, so its
+// weights are summed by one thread, in fp32 and in order.  What a group's 32
+// keys share (kvq_fill.cuh: keys_channel) is computed per tile by one warp
+// with mma.sync and enters the exponent together with -lse; a group's keys
+// are one warp's, so it is read like a constant.
+#include "kvq_tc.cuh"
 #include "kvq_pipe.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kConsumerWarps = kTile / 16;
-constexpr int kConsumers = 32 * kConsumerWarps;
-constexpr int kThreadsMass = kConsumers + kProducers + 32;
-constexpr uint32_t kFixedMass = 2 * kKeyStageBytes + 2 * kGroupRowBytes + kTailBytes;
+constexpr int kWeighWarps = kTile / 32;  // one per group of a tile; then the warp that prepares their offsets
+constexpr int kThreadsMass = 128 + kProducers + 64;
+constexpr int kMaxCols = 256;
+constexpr uint32_t kQBytes = kMaxCols * kHeadDim * 2;
+constexpr uint32_t kOffBytes = kTile / 32 * kMaxCols * 4;
+// (operand A reads 32 rows behind a tile: the next one's, or Q's)
+constexpr uint32_t kFixedMass = 2 * kKeyStageBytes + kQBytes + 2 * kGroupRowBytes + 2 * kOffBytes + kMaxCols * 4 + kTailBytes;
 constexpr uint32_t kSmemMass = 227 * 1024;
 
-// 8 query rows as the mma's columns: this thread's operand words (row g of
-// the 8, channels 16 ks + 2 tq, + 1 and + 8, + 9), in the keys' channel order.
-__device__ __forceinline__ void load_rows(const uint16_t* q, int left, bool paired, int lane, uint32_t (&b)[8][2]) {
-  const int g = lane >> 2, tq = lane & 3;
-  const bool have = g < left;
-  const uint16_t* row = q + (size_t)g * kHeadDim;
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // slots 2 tq, 2 tq + 1 of chunk 2 ks + h: channels 2 tq, 2 tq + 1, or (paired) tq, tq + 4
-      const uint16_t* c = row + 8 * (2 * ks + h);
-      uint32_t w = 0;
-      if (have) w = paired ? (uint32_t)__ldg(c + tq) | (uint32_t)__ldg(c + tq + 4) << 16 : __ldg(reinterpret_cast<const uint32_t*>(c) + tq);
-      b[ks][h] = w;
-    }
-}
-// Their log-sum-exps and weights: columns 2 tq, 2 tq + 1.
-__device__ __forceinline__ void load_weights(const TreeParams& p, size_t row0, int b, int r0, int M, int tq, float2 (&lw)[2]) {
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = r0 + 2 * tq + e;
-    lw[e] = make_float2(0.0f, 0.0f);
-    if (r < M) {
-      const float lse = __ldg(p.row_lse + row0 + r), wt = p.weight ? __ldg(p.weight + (size_t)b * p.n + r % p.n) : 1.0f;
-      if (lse != -INFINITY) lw[e] = make_float2(lse, wt);  // (a row that saw nothing)
-    }
-  }
+// Byte offset of a 16-byte chunk of query row r (cols rows in all).
+__device__ __forceinline__ uint32_t col_off(int cols, int r, int chunk) {
+  return (uint32_t)((chunk >> 3) * (cols * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
 }
 
-// ONE: at most 8 rows per KV head, whose operand stays in registers.
-template <bool ONE>
-__device__ __forceinline__ void weigh(const TreeParams& p, const Bars& B, const uint8_t* stage0, const uint8_t* sM, int x, int x_end,
-                                      int tid, volatile int* gave_up) {
-  auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
+struct MassSmem {
+  uint8_t *stage0, *sQ, *sM;
+  float *off, *wt;  // [2][3][kMaxCols], [kMaxCols]
+};
+
+// The piece's query rows as operand B, their weights, by 128 threads.  A row
+// that does not count (weight 0, or nothing seen) is staged as zeros: its
+// weights of 1 meet a factor of 0, whatever it held.
+__device__ __forceinline__ void put_rows(const TreeParams& p, const Bars& B, const Piece& c, const MassSmem& m, int cols, int tid) {
   const Geometry& G = p.geo;
-  const int lane = tid & 31, w = tid >> 5, g = lane >> 2, tq = lane & 3, M = G.g * p.n;
-  const uint32_t a0 = (uint32_t)__cvta_generic_to_shared(stage0), aM = (uint32_t)__cvta_generic_to_shared(sM);
-  int i = 0;
-  while (x < x_end) {
-    const Piece c = piece_at(p, x, x_end);
-    const bool two = c.quant || G.pre_rope, grouped = channel_scales(G) && c.quant;
-    const bool paired = c.quant && !G.pre_rope && G.kb != 3 && paired_order(G.kb);
-    const size_t row0 = ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n;
-    const uint16_t* q = p.q + row0 * kHeadDim;
-    uint32_t qb[8][2];
-    float2 lw[2];
-    if (ONE) {
-      load_rows(q, M, paired, lane, qb);
-      load_weights(p, row0, c.b, 0, M, tq, lw);
+  const bool paired = c.quant && !G.pre_rope && G.kb != 3 && paired_order(G.kb);
+  const size_t row0 = ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n + p.r0;
+  for (int r = tid; r < cols; r += 128) {
+    float w = 0.0f;
+    if (r < p.nr && __ldg(p.row_lse + row0 + r) != -INFINITY) w = p.weight ? __ldg(p.weight + (size_t)c.b * p.n + (p.r0 + r) % p.n) : 1.0f;
+    m.wt[r] = w;
+    const uint4* row = reinterpret_cast<const uint4*>(p.q + (row0 + r) * kHeadDim);
+#pragma unroll
+    for (int ch = 0; ch < 16; ++ch) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (w != 0.0f) v = __ldg(row + ch);
+      if (paired) v = pair_chunk(v);
+      *reinterpret_cast<uint4*>(m.sQ + col_off(cols, r, ch)) = v;
     }
-#pragma unroll 1
+  }
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+  mbar_arrive_warp(B.q_full);
+}
+
+__device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, uint32_t q, int cols, int x,
+                                      int x_end, volatile int* gave_up) {
+  int i = 0;
+  for (int piece = 0; x < x_end; ++piece) {
+    const Piece c = piece_at(p, x, x_end);
+    const int parts = c.quant || p.geo.pre_rope ? 2 : 1;
+    if (!mbar_wait(B.q_full, piece & 1, gave_up)) return;
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
-      const uint32_t aK = a0 + st * kKeyStageBytes, aN = aK + kTileBytes;
-      if (!wait(B.full_k + 8 * st, i >> 1)) return;
-      float sum[2] = {0.0f, 0.0f};  // keys 16 w + g, + 8
-#pragma unroll 1
-      for (int r0 = 0; r0 < M; r0 += 8) {
-        if (!ONE) {
-          load_rows(q + (size_t)r0 * kHeadDim, M - r0, paired, lane, qb);
-          load_weights(p, row0, c.b, r0, M, tq, lw);
-        }
-        float z[4] = {}, zn[4] = {}, zg[4] = {};
+      if (!mbar_wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
+      if (i >= 2 && !mbar_wait(B.p_full + 8 * st, ((i >> 1) - 1) & 1, gave_up)) return;  // the accumulator is read
+      tc_after();
+      for (int part = 0; part < parts; ++part) {
+        const uint32_t k = stage0 + st * kKeyStageBytes + part * kTileBytes;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          uint32_t ka[4];
-          const uint32_t off = tile_off(16 * w + (lane & 15), 2 * ks + (lane >> 4));
-          ldsm4(ka, aK + off);
-          mma16816(z, ka, qb[ks][0], qb[ks][1]);
-          if (two) {
-            ldsm4(ka, aN + off);
-            mma16816(zn, ka, qb[ks][0], qb[ks][1]);
-          }
-          if (grouped) {  // 8 rows: the groups' min and scale rows (the mma's rows 8..15: the same)
-            ldsm4(ka, aM + st * kGroupRowBytes + q_off<8>(lane & 7, 2 * ks + (lane >> 4)));
-            mma16816(zg, ka, qb[ks][0], qb[ks][1]);
-          }
-        }
-        // columns 2 tq + e: min of the warp's group (row w / 2), its scale (row 4 + w / 2)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mn = __shfl_sync(0xffffffffu, zg[e], 4 * (w >> 1) + tq), sc = __shfl_sync(0xffffffffu, zg[e], 16 + 4 * (w >> 1) + tq);
-          const float base = grouped ? fmaf((float)(1 << (G.kb - 1)), sc, mn) : 0.0f;
-          if (lw[e].y != 0.0f) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float s = z[2 * k + e] - zn[2 * k + e] + base;
-              sum[k] += lw[e].y * ex2(fmaf(s, p.q_scale, -lw[e].x) * 1.4426950408889634f);
-            }
-          }
-        }
+        for (int ks = 0; ks < 8; ++ks)  // 16 channels
+          mma_ss(tmem + 256 * st, smem_desc(k + (ks >> 2) * (kTile * 128) + (ks & 3) * 32, 16, 1024),
+                 smem_desc(q + (ks >> 2) * (cols * 128) + (ks & 3) * 32, 16, 1024), idesc(cols) | (part ? kNegA : 0), part + ks > 0);
       }
-      mbar_arrive_warp(B.empty_k + 8 * st);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-        const int f = (c.k0 + t) * kTile + 16 * w + g + 8 * k;
-        if (tq == 0 && f < (c.quant ? c.tc.Nq : c.tc.k1)) {
-          const int pos = c.quant ? G.S + f : f < c.tc.S_eff ? f : G.S + c.tc.Nq + (f - c.tc.S_eff);
-          float* m = p.mass + (size_t)c.s * p.cap + pos;
-          *m = fmaf(p.decay, *m, sum[k]);
-        }
-      }
+      mma_commit(B.empty_k + 8 * st);
+      mma_commit(B.s_full + 8 * st);
     }
     x += c.cnt;
   }
 }
 
-template <bool ONE>
+// The offsets of a tile: off[group][row] = scale * (q . m + 2^(b-1) q . s) - lse
+// (-lse alone where keys come whole), by one warp.
+__device__ __forceinline__ void offsets(const TreeParams& p, const Bars& B, const MassSmem& m, int cols, int x, int x_end, int lane,
+                                        volatile int* gave_up) {
+  auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
+  const Geometry& G = p.geo;
+  const uint32_t aQ = (uint32_t)__cvta_generic_to_shared(m.sQ), aM = (uint32_t)__cvta_generic_to_shared(m.sM);
+  const float centre = (float)(1 << (G.kb - 1));
+  int i = 0;
+  Piece c = piece_at(p, x, x_end);
+  put_rows(p, B, c, m, cols, 32 * kWeighWarps + lane);
+  for (int piece = 0; x < x_end; ++piece) {
+    const bool grouped = channel_scales(G) && c.quant;
+    const float* lse = p.row_lse + ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n + p.r0;
+    if (!wait(B.q_full, piece)) return;
+    for (int t = 0; t < c.cnt; ++t, ++i) {
+      const int st = i & 1;
+      float* off = m.off + st * (kTile / 32) * kMaxCols;
+      if (i >= 2 && !wait(B.p_full + 8 * st, (i >> 1) - 1)) return;  // the offsets of tile i - 2 are read
+      if (!grouped) {
+        for (int r = lane; r < cols; r += 32) {
+          const float v = r < p.nr && m.wt[r] != 0.0f ? -__ldg(lse + r) : 0.0f;
+#pragma unroll
+          for (int g = 0; g < kTile / 32; ++g) off[g * kMaxCols + r] = v;
+        }
+      } else {
+        if (!wait(B.full_k + 8 * st, i >> 1)) return;
+        uint32_t a[8][4];
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) ldsm4(a[ks], aM + st * kGroupRowBytes + q_off<8>(lane & 7, 2 * ks + (lane >> 4)));
+#pragma unroll 1
+        for (int r0 = 0; r0 < cols; r0 += 16) {
+          float z[2][4] = {};
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            uint32_t qb[4];
+            ldsm4(qb, aQ + col_off(cols, r0 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
+            mma16816(z[0], a[ks], qb[0], qb[1]);
+            mma16816(z[1], a[ks], qb[2], qb[3]);
+          }
+          // lane 4 g + tq: q . m of group g (g < 3), q . s of group g - 4 (4 <= g < 7), rows r0 + 8 n + 2 tq + e
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float s = __shfl_down_sync(0xffffffffu, z[n][e], 16);
+              const int r = r0 + 8 * n + 2 * (lane & 3) + e;
+              if (lane < 4 * (kTile / 32))
+                off[(lane >> 2) * kMaxCols + r] =
+                    r < p.nr && m.wt[r] != 0.0f ? fmaf(fmaf(centre, s, z[n][e]), p.q_scale, -__ldg(lse + r)) : 0.0f;
+            }
+        }
+      }
+      mbar_arrive_warp(B.empty_k + 8 * st);  // the group rows are read
+      mbar_arrive_warp(B.full_v + 8 * st);   // the tile's offsets are there
+    }
+    x += c.cnt;
+    if (x < x_end) {
+      // every product of this piece is done before its rows are replaced; and every reader of its weights
+      if (!wait(B.s_full + 8 * ((i - 1) & 1), (i - 1) >> 1) || !wait(B.p_full + 8 * ((i - 1) & 1), (i - 1) >> 1)) return;
+      c = piece_at(p, x, x_end);
+      put_rows(p, B, c, m, cols, 32 * kWeighWarps + lane);
+    }
+  }
+}
+
+// Two logits' share of a key's sum: d = v * scale + off, sum += w * 2^(d log2 e).
+__device__ __forceinline__ void add_weights(float2& sum, uint32_t v0, uint32_t v1, float scale, float2 off, float2 w) {
+  const float2 d = __ffma2_rn(make_float2(__uint_as_float(v0), __uint_as_float(v1)), make_float2(scale, scale), off);
+  const float2 y = __fmul2_rn(d, make_float2(1.4426950408889634f, 1.4426950408889634f));
+  sum = __ffma2_rn(w, make_float2(ex2(y.x), ex2(y.y)), sum);
+}
+
+__device__ __forceinline__ void weigh(const TreeParams& p, const Bars& B, uint32_t tmem, const MassSmem& m, int cols, int x, int x_end,
+                                      int tid, volatile int* gave_up) {
+  auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
+  const Geometry& G = p.geo;
+  const int w = tid >> 5;
+  const uint32_t lane0 = (uint32_t)(tid & ~31) << 16;
+  int i = 0;
+  Piece c = piece_at(p, x, x_end);
+  put_rows(p, B, c, m, cols, tid);
+  for (int piece = 0; x < x_end; ++piece) {
+    if (!wait(B.q_full, piece)) return;  // all rows' weights are there
+    for (int t = 0; t < c.cnt; ++t, ++i) {
+      const int st = i & 1, f = (c.k0 + t) * kTile + tid;
+      const bool have = f < (c.quant ? c.tc.Nq : c.tc.k1);
+      float* at = p.mass + (size_t)c.s * p.cap + (c.quant ? G.S + f : f < c.tc.S_eff ? f : G.S + c.tc.Nq + (f - c.tc.S_eff));
+      const float old = have ? *at : 0.0f;
+      const float4* off = reinterpret_cast<const float4*>(m.off + (st * (kTile / 32) + w) * kMaxCols);
+      const float4* wt = reinterpret_cast<const float4*>(m.wt);
+      if (!wait(B.full_v + 8 * st, i >> 1) || !wait(B.s_full + 8 * st, i >> 1)) return;
+      tc_after();
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+      for (int r0 = 0; r0 < cols; r0 += 32) {
+        uint32_t v[32];
+        tm_load32(v, tmem + 256 * st + lane0 + r0);
+        tm_wait_ld(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 o = off[r0 / 4 + e], u = wt[r0 / 4 + e];
+          add_weights(sum, v[4 * e], v[4 * e + 1], p.q_scale, make_float2(o.x, o.y), make_float2(u.x, u.y));
+          add_weights(sum, v[4 * e + 2], v[4 * e + 3], p.q_scale, make_float2(o.z, o.w), make_float2(u.z, u.w));
+        }
+      }
+      tc_before();
+      mbar_arrive_warp(B.p_full + 8 * st);
+      if (have) *at = fmaf(p.decay, old, sum.x + sum.y);
+    }
+    x += c.cnt;
+    if (x < x_end) {
+      // (the last product is done: its logits were read; every warp is done with the weights)
+      if (!wait(B.p_full + 8 * ((i - 1) & 1), (i - 1) >> 1)) return;
+      c = piece_at(p, x, x_end);
+      put_rows(p, B, c, m, cols, tid);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreadsMass, 1) mass_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *stage0 = smem, *sM = stage0 + 2 * kKeyStageBytes;
-  Tail* tail = reinterpret_cast<Tail*>(sM + 2 * kGroupRowBytes);
-  uint8_t* raw0 = sM + 2 * kGroupRowBytes + kTailBytes;
+  MassSmem m;
+  m.stage0 = smem;
+  m.sQ = m.stage0 + 2 * kKeyStageBytes;
+  m.sM = m.sQ + kQBytes;
+  m.off = reinterpret_cast<float*>(m.sM + 2 * kGroupRowBytes);
+  m.wt = m.off + 2 * kOffBytes / 4;
+  Tail* tail = reinterpret_cast<Tail*>(m.wt + kMaxCols);
+  uint8_t* raw0 = reinterpret_cast<uint8_t*>(tail) + kTailBytes;
   volatile int* gave_up = &tail->gave_up;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, w = tid >> 5, cols = (p.nr + 31) / 32 * 32;
   const Bars B = bars_at((uint32_t)__cvta_generic_to_shared(tail->bars));
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(B.full_k + 8 * i, kProducers / 32);
-      mbar_init(B.empty_k + 8 * i, kConsumerWarps);
+      mbar_init(B.empty_k + 8 * i, 2);            // the products, the offsets' warp
+      mbar_init(B.s_full + 8 * i, 1);             // logits
+      mbar_init(B.p_full + 8 * i, kWeighWarps);   // logits and offsets are read
+      mbar_init(B.full_v + 8 * i, 1);             // offsets (there are no values)
     }
     for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(B.raw_full + 8 * i, 1);
       mbar_init(B.raw_empty + 8 * i, kProducers / 32);
     }
-    *gave_up = 0;
+    mbar_init(B.q_full, 4);
+    mbar_init(B.done, 1);
+    *gave_up = ((uint32_t)__cvta_generic_to_shared(smem) & 1023) != 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid < 8) tail->lut[tid] = p.k_lut_off[tid];
   if (tid < kHeadDim) tail->zeros[tid] = 0;
+  constexpr int issuer = 4 + kProducers / 32;  // then the copies' warp
+  if (w == issuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(&tail->tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  tc_before();
   __syncthreads();
+  tc_after();
+  const uint32_t tmem = *(volatile uint32_t*)&tail->tmem;
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
-  if (tid < kConsumers) {
-    weigh<ONE>(p, B, stage0, sM, x, x_end, tid, gave_up);
-  } else if (tid < kConsumers + kProducers) {
-    produce<0, false>(p, B, nullptr, stage0, sM, raw0, tail, x, x_end, tid - kConsumers, gave_up);
+  if (*gave_up) {
+  } else if (w < kWeighWarps) {
+    weigh(p, B, tmem, m, cols, x, x_end, tid, gave_up);
+  } else if (w < 4) {
+    offsets(p, B, m, cols, x, x_end, tid & 31, gave_up);
+  } else if (w < issuer) {
+    produce<0, false>(p, B, nullptr, m.stage0, m.sM, raw0, tail, x, x_end, tid - 128, gave_up);
+  } else if (w == issuer) {
+    if ((tid & 31) == 0) {
+      issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(m.stage0), (uint32_t)__cvta_generic_to_shared(m.sQ), cols, x, x_end, gave_up);
+      mma_commit(B.done);  // whatever is in flight ends before TMEM is freed
+      mbar_wait(B.done, 0, nullptr);
+    }
+    __syncwarp();
   } else {
     if ((tid & 31) == 0) load_tiles<false>(p, B, (uint32_t)__cvta_generic_to_shared(raw0), x, x_end, gave_up);
     __syncwarp();
   }
+  tc_before();
   __syncthreads();
+  tc_after();
+  if (w == issuer) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
   if (*gave_up) {  // a wait ran out: the range's entries become NaN
     for (int y = x; y < x_end;) {
       const Piece c = piece_at(p, y, x_end);
@@ -177,22 +288,23 @@ __global__ void __launch_bounds__(kThreadsMass, 1) mass_kernel(const __grid_cons
   }
 }
 
-template <bool ONE>
-cudaError_t launch_t(TreeParams& p, cudaStream_t st) {
-  static std::atomic<long long> memo[kMemoDevices];
-  p.raw = raw_slot(p.geo, false, kSmemMass - kFixedMass);
-  if (kFixedMass + p.raw.slots * p.raw.bytes > kSmemMass) return cudaErrorInvalidValue;
-  const cudaError_t e = ensure_smem_limit(mass_kernel<ONE>, memo, (int)kSmemMass);
-  if (e != cudaSuccess) return e;
-  mass_kernel<ONE><<<p.ncta, kThreadsMass, kSmemMass, st>>>(p);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_attn_mass(TreeParams& p, cudaStream_t st) {
-  if (mass_stream_eligible(p.geo)) return launch_mass_stream(p, st);
-  return p.geo.g * p.n <= 8 ? launch_t<true>(p, st) : launch_t<false>(p, st);
+  const int M = p.geo.g * p.n;
+  if (M <= 8 && mass_stream_eligible(p.geo)) return launch_mass_stream(p, st);
+  static std::atomic<long long> memo[kMemoDevices];
+  p.raw = raw_slot(p.geo, false, kSmemMass - kFixedMass);
+  if (kFixedMass + p.raw.slots * p.raw.bytes > kSmemMass) return cudaErrorInvalidValue;
+  cudaError_t e = ensure_smem_limit(mass_kernel, memo, (int)kSmemMass);
+  // rows beyond one accumulator's columns: further passes add to the record
+  for (p.r0 = 0; e == cudaSuccess && p.r0 < M; p.r0 += kMaxCols) {
+    p.nr = M - p.r0 < kMaxCols ? M - p.r0 : kMaxCols;
+    mass_kernel<<<p.ncta, kThreadsMass, kSmemMass, st>>>(p);
+    e = cudaGetLastError();
+    p.decay = 1.0f;
+  }
+  return e;
 }
 
 }  // namespace kvq

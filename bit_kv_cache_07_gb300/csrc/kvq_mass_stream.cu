@@ -1,6 +1,6 @@
 // kvq_mass_stream.cu -- accumulated attention weight for up to 8 query rows per
-// KV head and pass, over uniform codes (and fp16 tokens) without RoPE: every
-// call after a decode, and after small trees.
+// KV head, over uniform codes (and fp16 tokens) without RoPE: every call after
+// a decode, and after small trees.
 //
 // With few rows a tile of dequantized keys costs far more than its products,
 // so the codes go to the tensor cores as they are (the decode's key side,
@@ -13,8 +13,7 @@
 // no barrier between warps.
 //
 // Every warp walks an equal range of 32-token items (quantized groups, then
-// fp16 items, stream after stream).  More rows take passes of 8: the first
-// decays the record, the others add to it.
+// fp16 items, stream after stream).
 #include <cstring>
 
 #include "kvq_decode_mma.cuh"
@@ -24,7 +23,6 @@ namespace kvq {
 namespace {
 
 constexpr int kStreamWarps = 4;  // per CTA
-constexpr int kMaxRows = 8;
 
 struct StreamParams {
   Geometry geo;
@@ -34,7 +32,7 @@ struct StreamParams {
   const float* weight;
   float* mass;
   float decay, scale;
-  int n, cap, r0, nr;  // rows per sequence, tokens of a record's row; this pass's rows of a KV head
+  int n, cap, nr;      // rows per sequence, tokens of a record's row; rows of a KV head
   int nwarps, total;   // warps, 32-token items
   int tokens[kMaxRaggedRows];
   int item0[kMaxRaggedRows + 1];
@@ -251,7 +249,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 4) mass_stream_kernel(const
     const int ng = Nq / kGroupTokens, k1 = S_eff + W, per = ng + (k1 + 31) / 32;
     const int off = x - p.item0[b], h = off / per, k0 = off - h * per, s = b * G.Hkv + h;
     const int k_end = min(per, k0 + x_end - x);
-    const size_t row0 = ((size_t)b * G.Hq_tot + (size_t)layer_head(G, h) * G.g) * p.n + p.r0;
+    const size_t row0 = ((size_t)b * G.Hq_tot + (size_t)layer_head(G, h) * G.g) * p.n;
     const uint16_t* q = p.q + row0 * kHeadDim;
     float* rec = p.mass + (size_t)s * p.cap;
     // the lane's rows: log-sum-exp (log2 units) and weight; a row that saw nothing counts as 0
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 4) mass_stream_kernel(const
       lse[i] = wt[i] = 0.0f;
       if (r < p.nr) {
         const float l = __ldg(p.row_lse + row0 + r);
-        if (l != -INFINITY) lse[i] = l, wt[i] = p.weight ? __ldg(p.weight + (size_t)b * p.n + (p.r0 + r) % p.n) : 1.0f;
+        if (l != -INFINITY) lse[i] = l, wt[i] = p.weight ? __ldg(p.weight + (size_t)b * p.n + r % p.n) : 1.0f;
       }
     }
     if (k0 < ng) {
@@ -355,7 +353,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 4) mass_stream_kernel(const
         lf[i] = wf[i] = 0.0f;
         if (r < p.nr) {
           const float l = __ldg(p.row_lse + row0 + r);
-          if (l != -INFINITY) lf[i] = l, wf[i] = p.weight ? __ldg(p.weight + (size_t)b * p.n + (p.r0 + r) % p.n) : 1.0f;
+          if (l != -INFINITY) lf[i] = l, wf[i] = p.weight ? __ldg(p.weight + (size_t)b * p.n + r % p.n) : 1.0f;
         }
       }
       const int slot0 = Nq % G.ring;
@@ -449,14 +447,9 @@ cudaError_t launch_mass_stream(const TreeParams& t, cudaStream_t st) {
   if (p.geo.sm_budget > 0 && p.geo.sm_budget < sms) sms = p.geo.sm_budget;
   const long long warps = (long long)sms * 4 * kStreamWarps;
   p.nwarps = (int)(warps < total ? warps : total);
-  const int M = p.geo.g * p.n;
-  for (p.r0 = 0; p.r0 < M; p.r0 += kMaxRows) {
-    p.nr = M - p.r0 < kMaxRows ? M - p.r0 : kMaxRows;
-    p.decay = p.r0 ? 1.0f : t.decay;
-    e = p.geo.fp16_mode || p.geo.kb == 2 ? launch_kb<2>(p, st) : p.geo.kb == 4 ? launch_kb<4>(p, st) : launch_kb<8>(p, st);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  p.nr = p.geo.g * p.n;
+  p.decay = t.decay;
+  return p.geo.fp16_mode || p.geo.kb == 2 ? launch_kb<2>(p, st) : p.geo.kb == 4 ? launch_kb<4>(p, st) : launch_kb<8>(p, st);
 }
 
 }  // namespace kvq

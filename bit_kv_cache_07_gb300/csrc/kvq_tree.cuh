@@ -75,6 +75,7 @@ struct TreeParams {
   float* mass;
   float decay;
   int cap;
+  int r0, nr;          // rows of a KV head in this pass
   float2* part_ml;    // [slots][sub][rstride] (maximum in log2 units, sum)
   float* part_acc;    // [slots][sub][rstride][d]
   uint32_t* part_flag;  // [slots][sub] a drafted value of the piece is not finite

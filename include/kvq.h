@@ -535,9 +535,8 @@ KVQ_API kvq_status kvq_tree_workspace(const kvq_config *cfg, int32_t n_nodes, ui
  *   mass       device f32 [B][n_kv_heads][max_tokens], in the cache's own
  *              stream order; the caller zero-fills it once.  Entries from
  *              tokens[b] on are left as they are
- * No workspace; a pass over the keys, and a launch, per 8 rows of a KV head
- * (one for all rows of non-uniform or pre-RoPE keys); every entry is summed
- * in a fixed order.
+ * No workspace; one launch and one pass over the keys per 256 rows of a KV
+ * head; every entry is summed by one thread (or one quad) in a fixed order.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (batch > 256, max_tokens >
  * 2^30, n_rows > 2^20, more than 2^28 tiles of 96 keys), KVQ_ERR_CAPACITY,
  * KVQ_ERR_CUDA. */
