@@ -105,34 +105,65 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  if (bytes)
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-                 : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+               : "memory");
 }
-// Queue the copies of quantized tile kt into the slot at dst (one thread);
-// bar expects their bytes.  The keys of a tile are contiguous in every
-// region, and whole groups: sizes and starts are multiples of 16 bytes.
+// The copies of a stream's quantized tiles by one thread: sources and sizes
+// per tile are set up once per piece, a tile is a few instructions (a lone
+// warp pays an instruction fetch for most of what it executes).  The keys of a
+// tile are contiguous in every region, and whole groups: sizes and starts are
+// multiples of 16 bytes.
 template <bool V>
-__device__ __forceinline__ void load_tile(const Geometry& G, const LayerPtrs& L, const RawSlot& R, const TileSrc& src, int kt,
-                                          uint32_t dst, uint32_t bar) {
-  const int f = kt * kTile, n = min(kTile, src.tc.Nq - f);
-  const size_t tok = (size_t)src.s * G.qcap + f;
-  const bool nuq = G.kb == 3;
-  const uint32_t ks = nuq ? 4 : G.gkc ? 4 * G.nkg : kHeadDim * 4 / kGroupTokens, vs = nuq ? 4 : 4 * G.nvg, no = nuq ? G.nout : 0;
-  const uint32_t bytes = n * (G.krow + ks + 3 * no + (V ? G.vrow + vs + 3 * no : 0));
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
-  bulk_copy(dst, L.k_codes + tok * G.krow, n * G.krow, bar);
-  bulk_copy(dst + R.ks, reinterpret_cast<const uint8_t*>(L.k_scales) + tok * ks, n * ks, bar);
-  bulk_copy(dst + R.kcol, L.k_col + tok * no, n * no, bar);
-  bulk_copy(dst + R.kval, L.k_val + tok * no, n * no * 2, bar);
-  if constexpr (V) {
-    bulk_copy(dst + R.v, L.v_codes + tok * G.vrow, n * G.vrow, bar);
-    bulk_copy(dst + R.vs, reinterpret_cast<const uint8_t*>(L.v_scales) + tok * vs, n * vs, bar);
-    bulk_copy(dst + R.vcol, L.v_col + tok * no, n * no, bar);
-    bulk_copy(dst + R.vval, L.v_val + tok * no, n * no * 2, bar);
+struct TileCopies {
+  const uint8_t *k, *ks, *v, *vs;         // the next tile's
+  const uint8_t *kcol, *kval, *vcol, *vval;
+  uint32_t nk, nks, nv, nvs, no;          // bytes per key; outliers per key
+  __device__ __forceinline__ TileCopies(const Geometry& G, const LayerPtrs& L, int s, int kt) {
+    const size_t tok = (size_t)s * G.qcap + (size_t)kt * kTile;
+    const bool nuq = G.kb == 3;
+    nk = G.krow;
+    nks = nuq ? 4 : G.gkc ? 4 * G.nkg : kHeadDim * 4 / kGroupTokens;
+    nv = V ? G.vrow : 0;
+    nvs = V ? (nuq ? 4 : 4 * G.nvg) : 0;
+    no = nuq ? G.nout : 0;
+    k = L.k_codes + tok * nk;
+    ks = reinterpret_cast<const uint8_t*>(L.k_scales) + tok * nks;
+    v = L.v_codes + tok * nv;
+    vs = reinterpret_cast<const uint8_t*>(L.v_scales) + tok * nvs;
+    kcol = L.k_col + tok * no;
+    kval = reinterpret_cast<const uint8_t*>(L.k_val) + tok * no * 2;
+    vcol = L.v_col + tok * no;
+    vval = reinterpret_cast<const uint8_t*>(L.v_val) + tok * no * 2;
   }
-}
+  // n keys into the slot at dst; bar expects their bytes.
+  __device__ __forceinline__ void next(const RawSlot& R, uint32_t n, uint32_t dst, uint32_t bar) {
+    const uint32_t o = no * (V ? 6 : 3);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(n * (nk + nks + nv + nvs + o)) : "memory");
+    bulk_copy(dst, k, n * nk, bar);
+    bulk_copy(dst + R.ks, ks, n * nks, bar);
+    k += kTile * nk;
+    ks += kTile * nks;
+    if constexpr (V) {
+      bulk_copy(dst + R.v, v, n * nv, bar);
+      bulk_copy(dst + R.vs, vs, n * nvs, bar);
+      v += kTile * nv;
+      vs += kTile * nvs;
+    }
+    if (no) {
+      bulk_copy(dst + R.kcol, kcol, n * no, bar);
+      bulk_copy(dst + R.kval, kval, n * no * 2, bar);
+      kcol += kTile * no;
+      kval += kTile * no * 2;
+      if constexpr (V) {
+        bulk_copy(dst + R.vcol, vcol, n * no, bar);
+        bulk_copy(dst + R.vval, vval, n * no * 2, bar);
+        vcol += kTile * no;
+        vval += kTile * no * 2;
+      }
+    }
+  }
+};
 
 template <int BITS>
 __device__ __forceinline__ uint2 chunk_word(const uint8_t* rows, int t, int chunk) {

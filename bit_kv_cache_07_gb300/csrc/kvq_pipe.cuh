@@ -135,8 +135,8 @@ __device__ __forceinline__ void load_tiles(const TreeParams& p, const Bars& B, u
   while (ok && x < x_end) {
     const Piece c = piece_at(p, x, x_end);
     const TileSrc src = tile_src(p, c);
-    for (int k = c.k0; k < c.k0 + c.cnt; ++k) {
-      if (!c.quant) {
+    if (!c.quant) {
+      for (int k = c.k0; k < c.k0 + c.cnt; ++k) {
         // cached rows of the tile from the window's first slot on (the sinks are few)
         const int f0 = max(k * kTile, c.tc.S_eff), f1 = min((k + 1) * kTile, c.tc.k1);
         const int s0 = src.slot0 + f0 - c.tc.S_eff, n = min(f1 - f0, G.ring - s0);
@@ -145,11 +145,16 @@ __device__ __forceinline__ void load_tiles(const TreeParams& p, const Bars& B, u
           prefetch_l2(p.L.k_ring + at, n * kHeadDim * 2);
           if (V) prefetch_l2(p.L.v_ring + at, n * kHeadDim * 2);
         }
-        continue;
       }
-      if (turn && !(ok = mbar_wait(B.raw_empty + 8 * slot, (turn - 1) & 1, gave_up))) break;
-      load_tile<V>(G, p.L, p.raw, src, k, raw + slot * p.raw.bytes, B.raw_full + 8 * slot);
-      if (++slot == p.raw.slots) slot = 0, ++turn;
+    } else {
+      TileCopies<V> copies(G, p.L, c.s, c.k0);
+      int left = c.tc.Nq - c.k0 * kTile;
+#pragma unroll 1
+      for (int t = 0; t < c.cnt; ++t, left -= kTile) {
+        if (turn && !(ok = mbar_wait(B.raw_empty + 8 * slot, (turn - 1) & 1, gave_up))) break;
+        copies.next(p.raw, min(kTile, left), raw + slot * p.raw.bytes, B.raw_full + 8 * slot);
+        if (++slot == p.raw.slots) slot = 0, ++turn;
+      }
     }
     x += c.cnt;
   }

@@ -6,19 +6,20 @@
 //   8 producer warps  dequantize a tile into shared memory (two stages),
 //   1 thread          issues the matrix instructions,
 //   4 warps           softmax, one thread per row.
-// TMEM: Q as the fp16 operand A of the logits (columns 448..511), S = Q K^T in
-// two buffers (0, 128: the next tile's logits are computed under this tile's
-// exponentials), the weights as fp16 over the logits they came from, and
-// O += P V (256..383).  With Q in TMEM the logits' products read K alone from
-// shared memory, whose bandwidth 96 columns would not cover twice.
+// TMEM: Q as the fp16 operand A of the logits, S = Q K^T and the fp16 weights
+// in two buffers each (the next tile's logits are computed under this tile's
+// exponentials), O += P V.  With Q in TMEM the logits' products read K alone
+// from shared memory, whose bandwidth 96 columns would not cover twice.
 // Quantized keys enter in two exact fp16 parts (two passes of the 128-channel
 // product), fp16 keys in one; what the 32 keys of a per-channel group share
-// comes from a 16-column product with the groups' min and scale rows (columns
-// 384 + 16 st).
+// comes from a 16-column product with the groups' min and scale rows.
 // A row's reference maximum comes from its first tile and moves only when a
 // tile's weights sum past 2^15 (fp16's range): one pass over the logits per
 // tile, and O is rarely rescaled.
 // 14 warps leave every thread 128 registers (17 would leave 96, and spills).
+// The roles' loops share the instruction cache: rolled per 32 columns, the
+// softmax fits beside the producers (unrolled, four fetches in ten missed and
+// the kernel took half as long again).
 #include "kvq_tc.cuh"
 #include "kvq_pipe.cuh"
 
@@ -32,7 +33,8 @@ constexpr float kTopSum = 32768.0f;  // a tile's weights stay below fp16's range
 // 8..15 (of no use): the kilobyte that holds the tail.
 constexpr uint32_t kFixedTc = 2 * kStageBytes + 2 * kGroupRowBytes + kTailBytes;
 constexpr uint32_t kSmemTc = 227 * 1024;
-constexpr uint32_t kTmemO = 256, kTmemGroup = 384, kTmemQ = 448;
+// TMEM columns: S of stage st, its weights 96 behind; O; the groups' products; Q.
+constexpr uint32_t kTmemS = 144, kTmemP = 96, kTmemO = 288, kTmemGroup = 416, kTmemQ = 448;
 
 // ---------------------------------------------------------------- issuer
 // What the issuer remembers of a tile whose product with the values is due.
@@ -41,16 +43,15 @@ struct Due {
   int piece;   // its number
   int slot;    // the last of an fp16 piece: where the piece's flag goes; else -1
 };
-__device__ __forceinline__ bool issue_pv(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, const Tail* tail, int i,
+__device__ __forceinline__ bool issue_pv(const TreeParams& p, const Bars& B, uint32_t tmem, uint64_t vd, const Tail* tail, int i,
                                          const Due& due, volatile int* gave_up) {
   const int st = i & 1, ph = (i >> 1) & 1;
   if (!mbar_wait(B.p_full + 8 * st, ph, gave_up) || !mbar_wait(B.full_v + 8 * st, ph, gave_up)) return false;
   tc_after();
-  const uint32_t v = stage0 + st * kStageBytes + 2 * kTileBytes;
+  const uint64_t v = vd + st * (kStageBytes >> 4);
 #pragma unroll
   for (int ks = 0; ks < kTile / 16; ++ks)  // 16 keys: 16 rows of both 64-channel halves
-    mma_ts(tmem + kTmemO, tmem + 128 * st + 8 * ks, smem_desc(v + ks * 2048, kTile * 128, 1024), idesc(128) | kRowsB,
-           !(due.first && ks == 0));
+    mma_ts(tmem + kTmemO, tmem + kTmemS * st + kTmemP + 8 * ks, v + ks * (2048 >> 4), idesc(128) | kRowsB, ks > 0 || !due.first);
   // (full_v was waited for at every tile of the piece)
   if (due.slot >= 0) p.part_flag[due.slot] = *(volatile const int*)&tail->bad_piece[due.piece & 3] == due.piece + 1;
   mma_commit(B.empty_v + 8 * st);
@@ -59,6 +60,8 @@ __device__ __forceinline__ bool issue_pv(const TreeParams& p, const Bars& B, uin
 }
 __device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, uint32_t rows,
                                       const Tail* tail, int x, int x_end, volatile int* gave_up) {
+  // descriptors of stage 0; stages, parts and k-steps add to their addresses
+  const uint64_t kd = smem_desc(stage0, 16, 1024), vd = smem_desc(stage0 + 2 * kTileBytes, kTile * 128, 1024), md = smem_desc(rows, 16, 1024);
   int i = 0;
   Due due{};
   for (int piece = 0; x < x_end; ++piece) {
@@ -70,28 +73,31 @@ __device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32
       const int st = i & 1;
       if (!mbar_wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
       tc_after();
-      for (int part = 0; part < parts; ++part) {
-        const uint32_t k = stage0 + st * kStageBytes + part * kTileBytes;
+      const uint32_t S = tmem + kTmemS * st;
+      const uint64_t k = kd + st * (kStageBytes >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 channels
-          mma_ts(tmem + 128 * st, tmem + kTmemQ + 8 * ks, smem_desc(k + (ks >> 2) * (kTile * 128) + (ks & 3) * 32, 16, 1024),
-                 idesc(kTile) | (part ? kNegB : 0), part + ks > 0);
-      }
-      if (grouped) {  // q . m and q . s of the tile's groups (columns 8..15 are of no use)
+      for (int ks = 0; ks < 8; ++ks)  // 16 channels
+        mma_ts(S, tmem + kTmemQ + 8 * ks, k + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, idesc(kTile), ks > 0);
+      if (parts == 2) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + kTmemGroup + 16 * st, tmem + kTmemQ + 8 * ks, smem_desc(rows + st * kGroupRowBytes + (ks >> 2) * 1024 + (ks & 3) * 32, 16, 1024),
-                 idesc(16), ks > 0);
+          mma_ts(S, tmem + kTmemQ + 8 * ks, k + (kTileBytes >> 4) + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, idesc(kTile) | kNegB, 1);
+      }
+      if (grouped) {  // q . m and q . s of the tile's groups (columns 8..15 are of no use)
+        const uint64_t r = md + st * (kGroupRowBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(tmem + kTmemGroup + 16 * st, tmem + kTmemQ + 8 * ks, r + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc(16), ks > 0);
       }
       mma_commit(B.s_full + 8 * st);
       mma_commit(B.empty_k + 8 * st);
       // the product of the tile before, whose weights are computed meanwhile
-      if (i && !issue_pv(p, B, tmem, stage0, tail, i - 1, due, gave_up)) return;
+      if (i && !issue_pv(p, B, tmem, vd, tail, i - 1, due, gave_up)) return;
       due = Due{t == 0, piece, !c.quant && t == c.cnt - 1 ? c.slot : -1};
     }
     x += c.cnt;
   }
-  if (i) issue_pv(p, B, tmem, stage0, tail, i - 1, due, gave_up);
+  if (i) issue_pv(p, B, tmem, vd, tail, i - 1, due, gave_up);
 }
 
 // --------------------------------------------------------------- softmax
@@ -155,20 +161,12 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
 #pragma unroll 1
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
-      const uint32_t S = tmem + 128 * st + lane0;
+      const uint32_t S = tmem + kTmemS * st + lane0;
       if (!wait(B.s_full + 8 * st, i >> 1)) return;
       tc_after();
       if (work) {
         const int f0 = (c.k0 + t) * kTile;
-        uint32_t ok[kCh], v[32], h[16 * kCh];
         float base[kCh] = {};  // the groups' share of the logits
-        bool whole = true;     // every key is seen
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch) {
-          ok[ch] = seen(p, c, mask_row, f0 + 32 * ch);
-          whole = whole && ok[ch] == 0xFFFFFFFFu;
-        }
-        whole = __all_sync(0xffffffffu, whole);
         if (grouped) {
           uint32_t y[8];
           tm_load8(y, tmem + kTmemGroup + 16 * st + lane0);
@@ -176,20 +174,32 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
           for (int ch = 0; ch < kCh; ++ch)
             base[ch] = fmaf(centre, __uint_as_float(y[4 + ch]), __uint_as_float(y[ch])) * p.q_scale;
         }
+        auto base_of = [&](int ch) { return ch == 0 ? base[0] : ch == 1 ? base[1] : base[2]; };
+        static_assert(kCh == 3, "groups of a tile");
+        // 32 logits, those that the row does not see as -inf
+        uint32_t v[32];
+        auto logits = [&](int ch) {
+          tm_load32(v, S + 32 * ch);
+          const uint32_t ok = seen(p, c, mask_row, f0 + 32 * ch);
+          tm_wait_ld(v);
+          if (__any_sync(0xffffffffu, ok != 0xFFFFFFFFu)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (ok >> e) & 1 ? v[e] : 0xFF800000u;
+          }
+        };
         float sum = 0.0f;
         bool search = t == 0;  // the row's maximum is to be found
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
           if (search || __any_sync(0xffffffffu, m == -INFINITY)) {
             float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int ch = 0; ch < kCh; ++ch) {
-              tm_load32(v, S + 32 * ch);
-              tm_wait_ld(v);
+              logits(ch);
               float mx = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (ok[ch] >> e) & 1 ? __uint_as_float(v[e]) : -INFINITY);
-              top = fmaxf(top, fmaf(mx, p.q_scale, base[ch]));
+              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
+              top = fmaxf(top, fmaf(mx, p.q_scale, base_of(ch)));
             }
             const bool move = top > m;
             if (__any_sync(0xffffffffu, move)) {
@@ -212,21 +222,19 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
           }
           const float mu = m == -INFINITY ? 0.0f : m;
           float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
+          const float2 scale = make_float2(p.q_scale, p.q_scale);
+#pragma unroll 1
           for (int ch = 0; ch < kCh; ++ch) {
-            tm_load32(v, S + 32 * ch);
-            tm_wait_ld(v);
-            if (!whole) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (ok[ch] >> e) & 1 ? v[e] : 0xFF800000u;  // -inf
-            }
-            const float2 scale = make_float2(p.q_scale, p.q_scale), off = make_float2(base[ch] - mu, base[ch] - mu);
+            logits(ch);
+            const float o = base_of(ch) - mu;
+            uint32_t h[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 w = weights2(v[2 * e], v[2 * e + 1], scale, off);
+              const float2 w = weights2(v[2 * e], v[2 * e + 1], scale, make_float2(o, o));
               add2(part, w);
-              h[16 * ch + e] = as_u32(__floats2half2_rn(w.x, w.y));
+              h[e] = as_u32(__floats2half2_rn(w.x, w.y));
             }
+            tm_store16(S + kTmemP + 16 * ch, h);
           }
           sum = part.x + part.y;
           // past the range (or not a number): find the maximum and do it again
@@ -234,10 +242,11 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
           search = true;
         }
         l += sum;
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch) tm_store16(S + 16 * ch, reinterpret_cast<const uint32_t(&)[16]>(h[16 * ch]));  // over the logits
         tm_wait_st();
       }
+      // a wait tells two phases apart, not three: before this tile's product can
+      // be issued, see the one before it done (then the wait below is for this one)
+      if (t == c.cnt - 1 && i > 0 && !wait(B.o_done, i - 1)) return;
       tc_before();
       mbar_arrive_warp(B.p_full + 8 * st);
     }
