@@ -215,26 +215,34 @@ __device__ __forceinline__ void keys_channel(int groups, int tid, const uint8_t*
                                              uint8_t* sK, uint8_t* sN, uint8_t* sM) {
   constexpr int kG = kTile / 32;
   const int cb = tid & 15, t0 = tid >> 4;
-  uint2 w[2 * kG];
-  uint32_t sw[kG][8];
-#pragma unroll
+  const uint32_t o0 = tile_off(t0, cb);  // keys 16 apart keep their swizzle
+  // a chunk's 8 scale words as two loads; half of the lanes take the second 16
+  // bytes first, so that 8 lanes 32 bytes apart cover all banks
+  const int swap = (cb >> 2) & 1;
+  const uint32_t sel_s = swap ? 0x3276u : 0x7632u, sel_m = swap ? 0x1054u : 0x5410u;
+  __half2 most = h2_const(0);
+#pragma unroll 1
   for (int j = 0; j < kG; ++j) {
     // a tile's missing groups (stale bytes in the slot): zero scales, so zero keys and rows
+    uint32_t sw[8];
     const uint4* p = reinterpret_cast<const uint4*>(j < groups ? scales + j * kHeadDim : zeros) + 2 * cb;
-    *reinterpret_cast<uint4*>(&sw[j][0]) = p[0];
-    *reinterpret_cast<uint4*>(&sw[j][4]) = p[1];
-  }
+    *reinterpret_cast<uint4*>(&sw[0]) = p[swap];
+    *reinterpret_cast<uint4*>(&sw[4]) = p[swap ^ 1];
+    uint2 w[2];
 #pragma unroll
-  for (int v = 0; v < 2 * kG; ++v) w[v] = chunk_word<BITS>(raw, t0 + 16 * v, cb);
-  __half2 most = h2_const(0);
-#pragma unroll
-  for (int j = 0; j < kG; ++j) {
+    for (int v = 0; v < 2; ++v) w[v] = chunk_word<BITS>(raw, t0 + 32 * j + 16 * v, cb);
     __half2 sc[4];
     uint32_t m2[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sc[i] = as_h2(__byte_perm(sw[j][pair_a<BITS>(i)], sw[j][pair_b<BITS>(i)], 0x7632));
-      m2[i] = __byte_perm(sw[j][pair_a<BITS>(i)], sw[j][pair_b<BITS>(i)], 0x5410);
+      if constexpr (BITS == 8) {  // pairs (2 i, 2 i + 1): swapped lanes hold pairs 2, 3, 0, 1
+        const int a = 2 * i, b = 2 * (i ^ 2);
+        sc[i] = as_h2(__byte_perm(swap ? sw[b] : sw[a], swap ? sw[b + 1] : sw[a + 1], 0x7632));
+        m2[i] = __byte_perm(swap ? sw[b] : sw[a], swap ? sw[b + 1] : sw[a + 1], 0x5410);
+      } else {  // pairs (i, i + 4): swapped lanes hold (i + 4, i)
+        sc[i] = as_h2(__byte_perm(sw[i], sw[i + 4], sel_s));
+        m2[i] = __byte_perm(sw[i], sw[i + 4], sel_m);
+      }
       most = __hmax2(most, sc[i]);
     }
     if (t0 == j) {
@@ -244,10 +252,10 @@ __device__ __forceinline__ void keys_channel(int groups, int tid, const uint8_t*
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      const uint32_t o = tile_off(t0 + 32 * j + 16 * v, cb);
+      const uint32_t o = o0 + (32 * j + 16 * v) * 128;
       __half2 c[4];
       uint32_t hi[4], neg[4];
-      code_pairs<BITS, true>(w[2 * j + v], c);
+      code_pairs<BITS, true>(w[v], c);
       key_products<BITS, false>(c, sc, hi, neg);
       store_chunk(sK, o, hi);
       store_chunk(sN, o, neg);
@@ -306,38 +314,43 @@ __device__ __forceinline__ void keys_token(int groups, int tid, const uint8_t* r
 template <int BITS>
 __device__ __forceinline__ void values_uniform(int groups, int tid, const uint8_t* raw, const uint32_t* scales, int nvg, int group,
                                                uint8_t* sV) {
-  constexpr int kN = kTile / 16;
   const int cb = tid & 15, t0 = tid >> 4;
-  uint2 w[kN];
-  uint32_t sw[kN];
-#pragma unroll
-  for (int v = 0; v < kN; ++v) {
-    w[v] = chunk_word<BITS>(raw, t0 + 16 * v, cb);
-    sw[v] = scales[(t0 + 16 * v) * nvg + group];
-  }
-  // the largest code's value may pass the fp16 range by the scale's rounding
+  const uint32_t o0 = tile_off(t0, cb);
   __half2 most = h2_const(0);
+#pragma unroll 1
+  for (int j = 0; j < kTile / 32; ++j) {
+    uint2 w[2];
+    uint32_t sw[2];
 #pragma unroll
-  for (int v = 0; v < kN; ++v) {
-    if (v >= 2) sw[v] = (v >> 1) < groups ? sw[v] : 0;  // missing groups: zeros
-    most = __hmax2(most, __habs2(as_h2(sw[v])));
-  }
-  const float2 far = __half22float2(most);
-  const bool sat = far.x + far.y * ((1 << BITS) - 1) > 65504.0f;
-#pragma unroll
-  for (int v = 0; v < kN; ++v) {
-    __half2 c[4];
-    uint32_t y[4];
-    code_pairs<BITS>(w[v], c);
-    const __half2 mn = __low2half2(as_h2(sw[v])), sc = __high2half2(as_h2(sw[v]));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = as_u32(__hfma2(c[i], sc, mn));
-    if (sat) {
-      const __half2 top = h2_const(0x7BFF), bottom = h2_const(0xFBFF);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(y[i]), top), bottom));
+    for (int v = 0; v < 2; ++v) {
+      const int t = t0 + 32 * j + 16 * v;
+      w[v] = chunk_word<BITS>(raw, t, cb);
+      sw[v] = j < groups ? scales[t * nvg + group] : 0;  // missing groups: zeros
     }
-    store_chunk(sV, tile_off(t0 + 16 * v, cb), y);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      __half2 c[4];
+      uint32_t y[4];
+      code_pairs<BITS>(w[v], c);
+      const __half2 mn = __low2half2(as_h2(sw[v])), sc = __high2half2(as_h2(sw[v]));
+      most = __hmax2(most, __habs2(as_h2(sw[v])));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = as_u32(__hfma2(c[i], sc, mn));
+      store_chunk(sV, o0 + (32 * j + 16 * v) * 128, y);
+    }
+  }
+  // the largest code's value may pass the fp16 range by the scale's rounding: it saturates
+  const float2 far = __half22float2(most);
+  if (far.x + far.y * ((1 << BITS) - 1) > 65504.0f) {
+#pragma unroll 1
+    for (int v = 0; v < kTile / 16; ++v) {
+      uint4* at = reinterpret_cast<uint4*>(sV + o0 + 16 * v * 128);
+      uint32_t y[4];
+      *reinterpret_cast<uint4*>(y) = *at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(y[i]), h2_const(0x7BFF)), h2_const(0xFBFF)));
+      *at = *reinterpret_cast<uint4*>(y);
+    }
   }
 }
 
@@ -538,13 +551,13 @@ __device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtr
 // Values of an fp16 tile.  A drafted value that is not finite enters as zero
 // (a weight of zero must not meet it); true is returned then, and the merge
 // adds it to the rows that see it.
-__device__ __forceinline__ bool fill_fp16_values(const Geometry& G, const LayerPtrs& L, const uint16_t* vd, const TileSrc& src,
-                                                 int kt, int tid, uint8_t* sV) {
-  const int cb = tid & 15;
-  bool bad = false;
-  uint4 v[kTile / 16];
+__device__ __forceinline__ void load_fp16_values(const Geometry& G, const LayerPtrs& L, const uint16_t* vd, const TileSrc& src, int kt,
+                                                 int tid, uint4 (&v)[kTile / 16]) {
 #pragma unroll
-  for (int u = 0; u < kTile / 16; ++u) v[u] = load16_if(fp16_key(G, L.v_sink, L.v_ring, vd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
+  for (int u = 0; u < kTile / 16; ++u) v[u] = load16_if(fp16_key(G, L.v_sink, L.v_ring, vd, src, kt * kTile + (tid >> 4) + 16 * u), tid & 15);
+}
+__device__ __forceinline__ bool store_fp16_values(const TileSrc& src, int kt, int tid, uint4 (&v)[kTile / 16], uint8_t* sV) {
+  bool bad = false;
 #pragma unroll
   for (int u = 0; u < kTile / 16; ++u) {
     const int t = (tid >> 4) + 16 * u;
@@ -556,7 +569,7 @@ __device__ __forceinline__ bool fill_fp16_values(const Geometry& G, const LayerP
       for (int i = 0; i < 8; ++i) y[i] = isfinite(y[i]) ? y[i] : 0.0f;
       v[u] = pack8(y);
     }
-    *reinterpret_cast<uint4*>(sV + tile_off(t, cb)) = v[u];
+    *reinterpret_cast<uint4*>(sV + tile_off(t, tid & 15)) = v[u];
   }
   return bad;
 }

@@ -59,15 +59,16 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
 // for copies in flight on the way out.)
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, volatile int* gave_up) {
 #pragma unroll 1
-  for (int it = 0; it < (1 << 24); ++it) {
+  for (int it = 0; it < (1 << 22); ++it) {
     uint32_t ok;
+    // asleep for up to 4 us a try: a polling warp takes issue slots from the working ones
     asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 4000;\nselp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
         : "r"(bar), "r"(phase)
         : "memory");
     if (ok) return true;
-    if ((it & 255) == 255 && gave_up && *gave_up) return false;
+    if ((it & 63) == 63 && gave_up && *gave_up) return false;
   }
   if (gave_up) *gave_up = 1;
   return false;
@@ -169,7 +170,9 @@ __device__ __forceinline__ void load_tiles(const TreeParams& p, const Bars& B, u
 
 // ------------------------------------------------------------- producers
 // ROWS > 0: the producers also stage that many query rows of each piece.  V:
-// the values too.
+// the values too.  (Eight warps one half after the other: with eight more for
+// the values side by side, the kernel's loops outgrow the instruction cache and
+// it takes longer.)
 template <int ROWS, bool V>
 __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint8_t* sQ, uint8_t* stage0, uint8_t* sM, const uint8_t* raw0,
                                         Tail* tail, int x, int x_end, int tid, volatile int* gave_up) {
@@ -203,7 +206,12 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       const uint32_t again = ((i >> 1) - 1) & 1;
       uint8_t *sK = stage0 + st * (V ? kStageBytes : kKeyStageBytes), *sN = sK + kTileBytes, *sV = sN + kTileBytes;
       const uint8_t* raw = raw0 + slot * p.raw.bytes;
-      if (c.quant && !mbar_wait(B.raw_full + 8 * slot, turn & 1, gave_up)) return;
+      uint4 held[V ? kTile / 16 : 1];  // an fp16 tile's values, in flight under its keys
+      if (c.quant) {
+        if (!mbar_wait(B.raw_full + 8 * slot, turn & 1, gave_up)) return;
+      } else if constexpr (V) {
+        load_fp16_values(G, p.L, p.vd, src, k, tid, held);
+      }
       if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
       if (!c.quant) fill_fp16_keys(G, p.L, p.freq, p.kd, src, k, tid, sK, sN);
       else if (general) fill_general_keys(G, p.raw, p.freq, tail->lut, src, k, tid, raw, sK, sN);
@@ -218,15 +226,15 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       } else {
         mbar_arrive_warp(B.full_k + 8 * st);
         if (i >= 2 && !mbar_wait(B.empty_v + 8 * st, again, gave_up)) return;
-        if (!c.quant) bad |= fill_fp16_values(G, p.L, p.vd, src, k, tid, sV);
+        if (!c.quant) bad |= store_fp16_values(src, k, tid, held, sV);
         else if (G.vb == 3) fill_general_values(G, p.raw, tail->lut + 8, src, k, tid, raw, sV);
         else fill_uniform_values(G, p.raw, src, k, tid, raw, sV);
         if (bad) *(volatile int*)&tail->bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         if (c.quant) {
           mbar_arrive_warp(B.raw_empty + 8 * slot);
           if (++slot == p.raw.slots) slot = 0, ++turn;
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         mbar_arrive_warp(B.full_v + 8 * st);
       }
     }

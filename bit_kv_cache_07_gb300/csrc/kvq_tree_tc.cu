@@ -16,7 +16,6 @@
 // A row's reference maximum comes from its first tile and moves only when a
 // tile's weights sum past 2^15 (fp16's range): one pass over the logits per
 // tile, and O is rarely rescaled.
-// 14 warps leave every thread 128 registers (17 would leave 96, and spills).
 // The roles' loops share the instruction cache: rolled per 32 columns, the
 // softmax fits beside the producers (unrolled, four fetches in ten missed and
 // the kernel took half as long again).
@@ -316,7 +315,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
   }
   if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
   if (tid < kHeadDim) tail->zeros[tid] = 0;
-  constexpr int issuer = (kSoftThreads + kProducers) / 32, loader = issuer + 1;
+  constexpr int issuer = (kSoftThreads + kProducers) / 32;  // then the copies' warp
   if (w == issuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(&tail->tmem))
@@ -341,7 +340,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
       mbar_wait(B.done, 0, nullptr);
     }
     __syncwarp();
-  } else if (w == loader) {
+  } else {
     if ((tid & 31) == 0) load_tiles<true>(p, B, (uint32_t)__cvta_generic_to_shared(raw0), x, x_end, gave_up);
     __syncwarp();
   }
