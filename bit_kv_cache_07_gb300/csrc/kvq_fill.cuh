@@ -78,11 +78,12 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t* hi, uint32_
 
 // Turns of position pos at frequency f (turns per position as a 64-bit
 // fraction): the product's wrap is the reduction, so the angle is exact to
-// 2^-32 turns at every position below 2^31.
+// 2^-32 turns at every position below 2^31.  The hardware sine and cosine of
+// an angle in [-pi, pi] are 5e-7 off at most.
 __device__ __forceinline__ float2 phasor(uint32_t pos, unsigned long long f) {
   const uint32_t turns = pos * (uint32_t)(f >> 32) + __umulhi(pos, (uint32_t)f);
   float sn, cs;
-  sincospif((float)(int)turns * 4.656612873077393e-10f /* 2^-31: half turns */, &sn, &cs);
+  __sincosf((float)(int)turns * 1.4629180792671596e-9f /* 2 pi / 2^32 */, &sn, &cs);
   return make_float2(cs, sn);
 }
 
@@ -394,12 +395,15 @@ __device__ __forceinline__ uint32_t codes3(const uint8_t* row, int chunk) {
 __device__ __forceinline__ void general_row(const uint8_t* codes, const uint32_t* scales, const uint8_t* col, const uint16_t* val,
                                             int nout, const float* lut, int t, int cb, float (&x)[2][8]) {
   const float2 ms = unpack_min_scale(scales[t]);
+  const uint32_t w[2] = {codes3(codes + 48 * t, cb), codes3(codes + 48 * t, cb + 8)};
+  const char* table = reinterpret_cast<const char*>(lut);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w = codes3(codes + 48 * t, cb + 8 * h);
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[h][i] = fmaf(ms.y, lut[(w >> (3 * i)) & 7], ms.x);
-  }
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t at = (i == 0 ? w[h] << 2 : w[h] >> (3 * i - 2)) & 28;  // 4 bytes a level
+      x[h][i] = fmaf(ms.y, *reinterpret_cast<const float*>(table + at), ms.x);
+    }
   for (int j = 0; j < nout; ++j) {
     const int c = col[t * nout + j];
     if (((c >> 3) & 7) == cb) {
@@ -435,26 +439,16 @@ __device__ __forceinline__ void store_keys(const float (&x)[8], int t, int chunk
   store_chunk(sK, o, hi);
   store_chunk(sN, o, neg);
 }
-__device__ __forceinline__ void rotate_pairs(float (&x)[2][8], const float2 (&e)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = x[0][i], c = x[1][i];
-    x[0][i] = a * e[i].x - c * e[i].y;
-    x[1][i] = c * e[i].x + a * e[i].y;
-  }
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float2 e) {
+  const float x = a, y = b;
+  a = x * e.x - y * e.y;
+  b = y * e.x + x * e.y;
 }
 
-// Keys of a quantized tile with non-uniform codes or RoPE.  The first of the
-// thread's positions has its angles computed, the others, 32 apart, follow
-// by one complex product each.
+// Keys of a quantized tile with non-uniform codes or RoPE.
 __device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSlot& R, const unsigned long long* freq, const float* lut,
                                                   const TileSrc& src, int kt, int tid, const uint8_t* raw, uint8_t* sK, uint8_t* sN) {
   const int cb = tid & 7, groups = tile_groups(src, kt);
-  float2 e[8];
-  if (G.pre_rope) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = phasor((uint32_t)(G.pos_offset + G.S + kt * kTile + (tid >> 3)), freq[8 * cb + i]);
-  }
 #pragma unroll 1
   for (int j = 0; j < kTile / 32; ++j) {
     const int t = 32 * j + (tid >> 3);
@@ -466,9 +460,14 @@ __device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSl
       else
         uniform_key_row(raw, G.kb, reinterpret_cast<const uint32_t*>(raw + R.ks), t, cb, x);
       if (G.pre_rope) {
-        rotate_pairs(x, e);
+        const uint32_t pos = (uint32_t)(G.pos_offset + G.S + kt * kTile + t);
+        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(freq + 8 * cb);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = spec_cmul(e[i], phasor(32, freq[8 * cb + i]));
+        for (int i = 0; i < 8; i += 2) {
+          const ulonglong2 f2 = f[i / 2];
+          rotate_pair(x[0][i], x[1][i], phasor(pos, f2.x));
+          rotate_pair(x[0][i + 1], x[1][i + 1], phasor(pos, f2.y));
+        }
       }
     }
 #pragma unroll
@@ -538,10 +537,9 @@ __device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtr
 #pragma unroll
     for (int h = 0; h < 2; ++h) unpack8(load16_if(row, cb + 8 * h), x[h]);
     if (f < src.tc.k1) {
-      float2 e[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = phasor((uint32_t)(G.pos_offset + fp16_pos(src, G.S, f)), freq[8 * cb + i]);
-      rotate_pairs(x, e);
+      for (int i = 0; i < 8; ++i)
+        rotate_pair(x[0][i], x[1][i], phasor((uint32_t)(G.pos_offset + fp16_pos(src, G.S, f)), freq[8 * cb + i]));
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) store_keys(x[h], t, cb + 8 * h, sK, sN);

@@ -101,7 +101,7 @@ __device__ __forceinline__ Piece piece_at(const TreeParams& p, int x, int x_end)
   return c;
 }
 
-constexpr uint32_t kTailBytes = 1024;
+constexpr uint32_t kTailBytes = 1408;
 struct Bars {  // shared-memory addresses; by stage (raw: by slot; o_done, q_full, done: one)
   uint32_t full_k, full_v, empty_k, empty_v, s_full, p_full, raw_full, raw_empty, o_done, q_full, done;
 };
@@ -117,6 +117,7 @@ struct Tail {
   int gave_up;
   int bad_piece[4];  // pieces that hold drafted values that are not finite, by number + 1
   float lut[16];     // level offsets of K, of V
+  alignas(16) unsigned long long freq[kHeadDim / 2];  // RoPE turns per position
   alignas(16) uint32_t zeros[kHeadDim];  // the scales of groups that a tile lacks
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
@@ -213,8 +214,8 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
         load_fp16_values(G, p.L, p.vd, src, k, tid, held);
       }
       if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
-      if (!c.quant) fill_fp16_keys(G, p.L, p.freq, p.kd, src, k, tid, sK, sN);
-      else if (general) fill_general_keys(G, p.raw, p.freq, tail->lut, src, k, tid, raw, sK, sN);
+      if (!c.quant) fill_fp16_keys(G, p.L, tail->freq, p.kd, src, k, tid, sK, sN);
+      else if (general) fill_general_keys(G, p.raw, tail->freq, tail->lut, src, k, tid, raw, sK, sN);
       else fill_uniform_keys(G, p.L, p.raw, src, k, tid, raw, tail->zeros, sK, sN, sM + st * kGroupRowBytes);
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       if constexpr (!V) {

@@ -135,10 +135,6 @@ __device__ __forceinline__ uint32_t tile_off(int t, int chunk /* c / 8 */) {
   return (uint32_t)((chunk >> 3) * (kTile * 128) + t * 128 + (((chunk & 7) ^ (t & 7)) << 4));
 }
 
-__device__ __forceinline__ float2 spec_cmul(float2 a, float2 b) {
-  return make_float2(a.x * b.x - a.y * b.y, a.x * b.y + a.y * b.x);
-}
-
 // The 8 uniform codes of one 8-channel chunk of a packed row, as integers.
 __device__ __forceinline__ void chunk_codes(const uint8_t* row, int bits, int chunk, int (&c)[8]) {
   if (bits == 8) {
