@@ -65,27 +65,33 @@ __device__ __forceinline__ void put_rows(const TreeParams& p, const Bars& B, con
   mbar_arrive_warp(B.q_full);
 }
 
-__device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, uint32_t q, int cols, int x,
+__device__ __forceinline__ void issue(uint32_t lead, const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, uint32_t q, int cols, int x,
                                       int x_end, volatile int* gave_up) {
+  auto wait = [&](uint32_t bar, int phase, volatile int* g) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase, g)); };
+  const uint64_t kd = smem_desc(stage0, 16, 1024), qd = smem_desc(q, 16, 1024);  // stage 0; the rest adds to the address
   int i = 0;
   for (int piece = 0; x < x_end; ++piece) {
     const Piece c = piece_at(p, x, x_end);
     const int parts = c.quant || p.geo.pre_rope ? 2 : 1;
-    if (!mbar_wait(B.q_full, piece & 1, gave_up)) return;
+    if (!wait(B.q_full, piece & 1, gave_up)) return;
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
-      if (!mbar_wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
-      if (i >= 2 && !mbar_wait(B.p_full + 8 * st, ((i >> 1) - 1) & 1, gave_up)) return;  // the accumulator is read
+      if (!wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
+      if (i >= 2 && !wait(B.p_full + 8 * st, ((i >> 1) - 1) & 1, gave_up)) return;  // the accumulator is read
       tc_after();
-      for (int part = 0; part < parts; ++part) {
-        const uint32_t k = stage0 + st * kKeyStageBytes + part * kTileBytes;
+      const uint64_t k = kd + st * (kKeyStageBytes >> 4);
+      const uint32_t half = cols * 128 >> 4;  // from a row's first 64 channels to the others
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 channels
-          mma_ss(tmem + 256 * st, smem_desc(k + (ks >> 2) * (kTile * 128) + (ks & 3) * 32, 16, 1024),
-                 smem_desc(q + (ks >> 2) * (cols * 128) + (ks & 3) * 32, 16, 1024), idesc(cols) | (part ? kNegA : 0), part + ks > 0);
+      for (int ks = 0; ks < 8; ++ks)  // 16 channels
+        mma_ss(lead, tmem + 256 * st, k + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, qd + (ks >> 2) * half + (ks & 3) * 2, idesc(cols), ks > 0);
+      if (parts == 2) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(lead, tmem + 256 * st, k + (kTileBytes >> 4) + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2,
+                 qd + (ks >> 2) * half + (ks & 3) * 2, idesc(cols) | kNegA, 1);
       }
-      mma_commit(B.empty_k + 8 * st);
-      mma_commit(B.s_full + 8 * st);
+      mma_commit(lead, B.empty_k + 8 * st);
+      mma_commit(lead, B.s_full + 8 * st);
     }
     x += c.cnt;
   }
@@ -264,11 +270,10 @@ __global__ void __launch_bounds__(kThreadsMass, 1) mass_kernel(const __grid_cons
   } else if (w < issuer) {
     produce<0, false>(p, B, nullptr, m.stage0, m.sM, raw0, tail, x, x_end, tid - 128, gave_up);
   } else if (w == issuer) {
-    if ((tid & 31) == 0) {
-      issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(m.stage0), (uint32_t)__cvta_generic_to_shared(m.sQ), cols, x, x_end, gave_up);
-      mma_commit(B.done);  // whatever is in flight ends before TMEM is freed
-      mbar_wait(B.done, 0, nullptr);
-    }
+    const uint32_t lead = elect_lead();
+    issue(lead, p, B, tmem, (uint32_t)__cvta_generic_to_shared(m.stage0), (uint32_t)__cvta_generic_to_shared(m.sQ), cols, x, x_end, gave_up);
+    mma_commit(lead, B.done);  // whatever is in flight ends before TMEM is freed
+    mbar_wait(B.done, 0, nullptr);
     __syncwarp();
   } else {
     if ((tid & 31) == 0) load_tiles<false>(p, B, (uint32_t)__cvta_generic_to_shared(raw0), x, x_end, gave_up);

@@ -42,23 +42,25 @@ struct Due {
   int piece;   // its number
   int slot;    // the last of an fp16 piece: where the piece's flag goes; else -1
 };
-__device__ __forceinline__ bool issue_pv(const TreeParams& p, const Bars& B, uint32_t tmem, uint64_t vd, const Tail* tail, int i,
+__device__ __forceinline__ bool issue_pv(uint32_t lead, const TreeParams& p, const Bars& B, uint32_t tmem, uint64_t vd, const Tail* tail, int i,
                                          const Due& due, volatile int* gave_up) {
+  auto wait = [&](uint32_t bar, int phase, volatile int* g) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase, g)); };
   const int st = i & 1, ph = (i >> 1) & 1;
-  if (!mbar_wait(B.p_full + 8 * st, ph, gave_up) || !mbar_wait(B.full_v + 8 * st, ph, gave_up)) return false;
+  if (!wait(B.p_full + 8 * st, ph, gave_up) || !wait(B.full_v + 8 * st, ph, gave_up)) return false;
   tc_after();
   const uint64_t v = vd + st * (kStageBytes >> 4);
 #pragma unroll
   for (int ks = 0; ks < kTile / 16; ++ks)  // 16 keys: 16 rows of both 64-channel halves
-    mma_ts(tmem + kTmemO, tmem + kTmemS * st + kTmemP + 8 * ks, v + ks * (2048 >> 4), idesc(128) | kRowsB, ks > 0 || !due.first);
+    mma_ts(lead, tmem + kTmemO, tmem + kTmemS * st + kTmemP + 8 * ks, v + ks * (2048 >> 4), idesc(128) | kRowsB, ks > 0 || !due.first);
   // (full_v was waited for at every tile of the piece)
-  if (due.slot >= 0) p.part_flag[due.slot] = *(volatile const int*)&tail->bad_piece[due.piece & 3] == due.piece + 1;
-  mma_commit(B.empty_v + 8 * st);
-  mma_commit(B.o_done);
+  if (due.slot >= 0 && lead) p.part_flag[due.slot] = *(volatile const int*)&tail->bad_piece[due.piece & 3] == due.piece + 1;
+  mma_commit(lead, B.empty_v + 8 * st);
+  mma_commit(lead, B.o_done);
   return true;
 }
-__device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, uint32_t rows,
+__device__ __forceinline__ void issue(uint32_t lead, const TreeParams& p, const Bars& B, uint32_t tmem, uint32_t stage0, uint32_t rows,
                                       const Tail* tail, int x, int x_end, volatile int* gave_up) {
+  auto wait = [&](uint32_t bar, int phase, volatile int* g) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase, g)); };
   // descriptors of stage 0; stages, parts and k-steps add to their addresses
   const uint64_t kd = smem_desc(stage0, 16, 1024), vd = smem_desc(stage0 + 2 * kTileBytes, kTile * 128, 1024), md = smem_desc(rows, 16, 1024);
   int i = 0;
@@ -67,36 +69,36 @@ __device__ __forceinline__ void issue(const TreeParams& p, const Bars& B, uint32
     const Piece c = piece_at(p, x, x_end);
     const int parts = c.quant || p.geo.pre_rope ? 2 : 1;
     const bool grouped = channel_scales(p.geo) && c.quant;
-    if (!mbar_wait(B.q_full, piece & 1, gave_up)) return;
+    if (!wait(B.q_full, piece & 1, gave_up)) return;
     for (int t = 0; t < c.cnt; ++t, ++i) {
       const int st = i & 1;
-      if (!mbar_wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
+      if (!wait(B.full_k + 8 * st, (i >> 1) & 1, gave_up)) return;
       tc_after();
       const uint32_t S = tmem + kTmemS * st;
       const uint64_t k = kd + st * (kStageBytes >> 4);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)  // 16 channels
-        mma_ts(S, tmem + kTmemQ + 8 * ks, k + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, idesc(kTile), ks > 0);
+        mma_ts(lead, S, tmem + kTmemQ + 8 * ks, k + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, idesc(kTile), ks > 0);
       if (parts == 2) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts(S, tmem + kTmemQ + 8 * ks, k + (kTileBytes >> 4) + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, idesc(kTile) | kNegB, 1);
+          mma_ts(lead, S, tmem + kTmemQ + 8 * ks, k + (kTileBytes >> 4) + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, idesc(kTile) | kNegB, 1);
       }
       if (grouped) {  // q . m and q . s of the tile's groups (columns 8..15 are of no use)
         const uint64_t r = md + st * (kGroupRowBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tmem + kTmemGroup + 16 * st, tmem + kTmemQ + 8 * ks, r + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc(16), ks > 0);
+          mma_ts(lead, tmem + kTmemGroup + 16 * st, tmem + kTmemQ + 8 * ks, r + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc(16), ks > 0);
       }
-      mma_commit(B.s_full + 8 * st);
-      mma_commit(B.empty_k + 8 * st);
+      mma_commit(lead, B.s_full + 8 * st);
+      mma_commit(lead, B.empty_k + 8 * st);
       // the product of the tile before, whose weights are computed meanwhile
-      if (i && !issue_pv(p, B, tmem, vd, tail, i - 1, due, gave_up)) return;
+      if (i && !issue_pv(lead, p, B, tmem, vd, tail, i - 1, due, gave_up)) return;
       due = Due{t == 0, piece, !c.quant && t == c.cnt - 1 ? c.slot : -1};
     }
     x += c.cnt;
   }
-  if (i) issue_pv(p, B, tmem, vd, tail, i - 1, due, gave_up);
+  if (i) issue_pv(lead, p, B, tmem, vd, tail, i - 1, due, gave_up);
 }
 
 // --------------------------------------------------------------- softmax
@@ -334,12 +336,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
   } else if (w < issuer) {
     produce<0, true>(p, B, nullptr, stage0, sM, raw0, tail, x, x_end, tid - kSoftThreads, gave_up);
   } else if (w == issuer) {
-    if ((tid & 31) == 0) {
-      issue(p, B, tmem, (uint32_t)__cvta_generic_to_shared(stage0), (uint32_t)__cvta_generic_to_shared(sM), tail, x,
+    const uint32_t lead = elect_lead();
+    issue(lead, p, B, tmem, (uint32_t)__cvta_generic_to_shared(stage0), (uint32_t)__cvta_generic_to_shared(sM), tail, x,
             x_end, gave_up);
-      mma_commit(B.done);  // whatever is in flight ends before TMEM is freed
-      mbar_wait(B.done, 0, nullptr);
-    }
+    mma_commit(lead, B.done);  // whatever is in flight ends before TMEM is freed
+    mbar_wait(B.done, 0, nullptr);
     __syncwarp();
   } else {
     if ((tid & 31) == 0) load_tiles<true>(p, B, (uint32_t)__cvta_generic_to_shared(raw0), x, x_end, gave_up);
