@@ -87,6 +87,10 @@ __device__ __forceinline__ float2 phasor(uint32_t pos, unsigned long long f) {
   return make_float2(cs, sn);
 }
 
+// Place of channel pair i's frequency in the kernels' table: 8 lanes that read
+// the same two pairs of 8 chunks read 128 bytes in a row.
+__device__ __forceinline__ int freq_at(int i) { return 2 * (8 * ((i >> 1) & 3) + (i >> 3)) + (i & 1); }
+
 // Byte offset of a 16-byte chunk of row r among ROWS rows of 128 channels
 // (two halves of 64 channels, swizzled like the tiles).
 template <int ROWS>
@@ -390,10 +394,8 @@ __device__ __forceinline__ uint32_t codes3(const uint8_t* row, int chunk) {
   const int bit = 24 * chunk, i = bit >> 5;
   return __funnelshift_r(w[i], w[min(i + 1, 11)], bit & 31) & 0xFFFFFFu;
 }
-// Channels of the chunks cb and cb + 8 of key t of a tile, non-uniform codes:
-// the dense values, then the outliers among them.
-__device__ __forceinline__ void general_row(const uint8_t* codes, const uint32_t* scales, const uint8_t* col, const uint16_t* val,
-                                            int nout, const float* lut, int t, int cb, float (&x)[2][8]) {
+// Channels of the chunks cb and cb + 8 of key t of a tile, non-uniform codes.
+__device__ __forceinline__ void general_row(const uint8_t* codes, const uint32_t* scales, const float* lut, int t, int cb, float (&x)[2][8]) {
   const float2 ms = unpack_min_scale(scales[t]);
   const uint32_t w[2] = {codes3(codes + 48 * t, cb), codes3(codes + 48 * t, cb + 8)};
   const char* table = reinterpret_cast<const char*>(lut);
@@ -404,16 +406,15 @@ __device__ __forceinline__ void general_row(const uint8_t* codes, const uint32_t
       const uint32_t at = (i == 0 ? w[h] << 2 : w[h] >> (3 * i - 2)) & 28;  // 4 bytes a level
       x[h][i] = fmaf(ms.y, *reinterpret_cast<const float*>(table + at), ms.x);
     }
-  for (int j = 0; j < nout; ++j) {
-    const int c = col[t * nout + j];
-    if (((c >> 3) & 7) == cb) {
-      const float v = half_bits_to_float(val[t * nout + j]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c == 64 * h + 8 * cb + i) x[h][i] = v;
-    }
+}
+// The outliers of the rows that a warp filled, one lane an outlier, over the
+// dense values in the tile: f(row, its outlier list, channel, value).
+template <class F>
+__device__ __forceinline__ void each_outlier(const uint8_t* col, const uint16_t* val, int nout, int groups, int tid, F f) {
+  __syncwarp();  // the warp's rows are written
+  for (int k = tid & 31; k < 4 * groups * nout; k += 32) {
+    const int r = k / nout, t = 32 * (r >> 2) + 4 * (tid >> 5) + (r & 3), at = t * nout + k - r * nout;
+    f(t, t * nout, col[at] & 127, half_bits_to_float(val[at]));
   }
 }
 // The same of a uniform row (keys cached before RoPE: a scale per channel).
@@ -455,16 +456,15 @@ __device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSl
     float x[2][8] = {};
     if (j < groups) {
       if (G.kb == 3)
-        general_row(raw, reinterpret_cast<const uint32_t*>(raw + R.ks), raw + R.kcol, reinterpret_cast<const uint16_t*>(raw + R.kval), G.nout,
-                    lut, t, cb, x);
+        general_row(raw, reinterpret_cast<const uint32_t*>(raw + R.ks), lut, t, cb, x);
       else
         uniform_key_row(raw, G.kb, reinterpret_cast<const uint32_t*>(raw + R.ks), t, cb, x);
       if (G.pre_rope) {
         const uint32_t pos = (uint32_t)(G.pos_offset + G.S + kt * kTile + t);
-        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(freq + 8 * cb);
+        const ulonglong2* f = reinterpret_cast<const ulonglong2*>(freq) + cb;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const ulonglong2 f2 = f[i / 2];
+          const ulonglong2 f2 = f[4 * i];
           rotate_pair(x[0][i], x[1][i], phasor(pos, f2.x));
           rotate_pair(x[0][i + 1], x[1][i + 1], phasor(pos, f2.y));
         }
@@ -473,6 +473,33 @@ __device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSl
 #pragma unroll
     for (int h = 0; h < 2; ++h) store_keys(x[h], t, cb + 8 * h, sK, sN);
   }
+  if (G.nout == 0) return;
+  const uint8_t* col = raw + R.kcol;
+  const uint16_t* val = reinterpret_cast<const uint16_t*>(raw + R.kval);
+  each_outlier(col, val, G.nout, groups, tid, [&](int t, int list, int c, float x) {
+    float other = 0.0f;  // the channel that RoPE pairs with c
+    const int d = c ^ 64;
+    if (G.pre_rope) {
+      const float2 ms = unpack_min_scale(reinterpret_cast<const uint32_t*>(raw + R.ks)[t]);
+      other = fmaf(ms.y, lut[codes3(raw + 48 * t, d >> 3) >> (3 * (d & 7)) & 7], ms.x);
+      for (int j = 0; j < G.nout; ++j)
+        if (col[list + j] == d) other = half_bits_to_float(val[list + j]);
+      // (a pair of two outliers is written twice, the same)
+      const float2 e = phasor((uint32_t)(G.pos_offset + G.S + kt * kTile + t), freq[freq_at(c & 63)]);
+      if (c < 64) rotate_pair(x, other, e);
+      else rotate_pair(other, x, e);
+    }
+    uint32_t hi, neg;
+    split2(x, other, &hi, &neg);
+    const uint32_t o = tile_off(t, c >> 3) + 2 * (c & 7);
+    *reinterpret_cast<uint16_t*>(sK + o) = (uint16_t)hi;
+    *reinterpret_cast<uint16_t*>(sN + o) = (uint16_t)neg;
+    if (G.pre_rope) {
+      const uint32_t od = tile_off(t, d >> 3) + 2 * (d & 7);
+      *reinterpret_cast<uint16_t*>(sK + od) = (uint16_t)(hi >> 16);
+      *reinterpret_cast<uint16_t*>(sN + od) = (uint16_t)(neg >> 16);
+    }
+  });
 }
 __device__ __forceinline__ void fill_general_values(const Geometry& G, const RawSlot& R, const float* lut, const TileSrc& src, int kt,
                                                     int tid, const uint8_t* raw, uint8_t* sV) {
@@ -482,13 +509,16 @@ __device__ __forceinline__ void fill_general_values(const Geometry& G, const Raw
     const int t = 32 * j + (tid >> 3);
     float y[2][8] = {};
     if (j < groups)
-      general_row(raw + R.v, reinterpret_cast<const uint32_t*>(raw + R.vs), raw + R.vcol, reinterpret_cast<const uint16_t*>(raw + R.vval),
-                  G.nout, lut, t, cb, y);
+      general_row(raw + R.v, reinterpret_cast<const uint32_t*>(raw + R.vs), lut, t, cb, y);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       *reinterpret_cast<uint4*>(sV + tile_off(t, cb + 8 * h)) =
           make_uint4(pack_sat(y[h][0], y[h][1]), pack_sat(y[h][2], y[h][3]), pack_sat(y[h][4], y[h][5]), pack_sat(y[h][6], y[h][7]));
   }
+  if (G.nout)
+    each_outlier(raw + R.vcol, reinterpret_cast<const uint16_t*>(raw + R.vval), G.nout, groups, tid, [&](int t, int, int c, float y) {
+      *reinterpret_cast<uint16_t*>(sV + tile_off(t, c >> 3) + 2 * (c & 7)) = (uint16_t)pack_sat(y, y);
+    });
 }
 
 // Row of fp16 key f: sinks, then the window ring (slot0: the slot of its first
@@ -539,7 +569,7 @@ __device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtr
     if (f < src.tc.k1) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        rotate_pair(x[0][i], x[1][i], phasor((uint32_t)(G.pos_offset + fp16_pos(src, G.S, f)), freq[8 * cb + i]));
+        rotate_pair(x[0][i], x[1][i], phasor((uint32_t)(G.pos_offset + fp16_pos(src, G.S, f)), freq[freq_at(8 * cb + i)]));
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) store_keys(x[h], t, cb + 8 * h, sK, sN);

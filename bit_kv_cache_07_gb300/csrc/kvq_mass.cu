@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreadsMass, 1) mass_kernel(const __grid_cons
   }
   if (tid < 8) tail->lut[tid] = p.k_lut_off[tid];
   if (tid < kHeadDim) tail->zeros[tid] = 0;
-  if (tid < kHeadDim / 2) tail->freq[tid] = p.freq[tid];
+  if (tid < kHeadDim / 2) tail->freq[freq_at(tid)] = p.freq[tid];
   constexpr int issuer = 4 + kProducers / 32;  // then the copies' warp
   if (w == issuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(

@@ -179,6 +179,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
                                         Tail* tail, int x, int x_end, int tid, volatile int* gave_up) {
   const Geometry& G = p.geo;
   const bool general = G.pre_rope || G.kb == 3;
+  constexpr bool kAsync = ROWS == 0;  // the tensor core reads the tiles (staged rows: ldmatrix does)
   int i = 0, slot = 0, turn = 0;  // tiles so far, raw slot and its turn
   for (int piece = 0; x < x_end; ++piece) {
     const Piece c = piece_at(p, x, x_end);
@@ -217,7 +218,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       if (!c.quant) fill_fp16_keys(G, p.L, tail->freq, p.kd, src, k, tid, sK, sN);
       else if (general) fill_general_keys(G, p.raw, tail->freq, tail->lut, src, k, tid, raw, sK, sN);
       else fill_uniform_keys(G, p.L, p.raw, src, k, tid, raw, tail->zeros, sK, sN, sM + st * kGroupRowBytes);
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      if constexpr (kAsync) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       if constexpr (!V) {
         if (c.quant) {
           mbar_arrive_warp(B.raw_empty + 8 * slot);
@@ -231,7 +232,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
         else if (G.vb == 3) fill_general_values(G, p.raw, tail->lut + 8, src, k, tid, raw, sV);
         else fill_uniform_values(G, p.raw, src, k, tid, raw, sV);
         if (bad) *(volatile int*)&tail->bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        if constexpr (kAsync) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         if (c.quant) {
           mbar_arrive_warp(B.raw_empty + 8 * slot);
           if (++slot == p.raw.slots) slot = 0, ++turn;

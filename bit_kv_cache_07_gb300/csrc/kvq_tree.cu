@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __gr
   }
   if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
   if (tid < kHeadDim) tail->zeros[tid] = 0;
-  if (tid < kHeadDim / 2) tail->freq[tid] = p.freq[tid];
+  if (tid < kHeadDim / 2) tail->freq[freq_at(tid)] = p.freq[tid];
   __syncthreads();
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
   if (tid < kConsumers) {

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
   }
   if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
   if (tid < kHeadDim) tail->zeros[tid] = 0;
-  if (tid < kHeadDim / 2) tail->freq[tid] = p.freq[tid];
+  if (tid < kHeadDim / 2) tail->freq[freq_at(tid)] = p.freq[tid];
   constexpr int issuer = (kSoftThreads + kProducers) / 32;  // then the copies' warp
   if (w == issuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
