@@ -395,16 +395,19 @@ __device__ __forceinline__ uint32_t codes3(const uint8_t* row, int chunk) {
   return __funnelshift_r(w[i], w[min(i + 1, 11)], bit & 31) & 0xFFFFFFu;
 }
 // Channels of the chunks cb and cb + 8 of key t of a tile, non-uniform codes.
-__device__ __forceinline__ void general_row(const uint8_t* codes, const uint32_t* scales, const float* lut, int t, int cb, float (&x)[2][8]) {
+__device__ __forceinline__ void general_row(const uint8_t* codes, const uint32_t* scales, const uint8_t* pairs, int t, int cb,
+                                            float (&x)[2][8]) {
   const float2 ms = unpack_min_scale(scales[t]);
   const uint32_t w[2] = {codes3(codes + 48 * t, cb), codes3(codes + 48 * t, cb + 8)};
-  const char* table = reinterpret_cast<const char*>(lut);
+  const uint32_t copy = (threadIdx.x & 15) * 8;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t at = (i == 0 ? w[h] << 2 : w[h] >> (3 * i - 2)) & 28;  // 4 bytes a level
-      x[h][i] = fmaf(ms.y, *reinterpret_cast<const float*>(table + at), ms.x);
+    for (int i = 0; i < 4; ++i) {  // 128 bytes an entry
+      const uint32_t at = lop_and_or(i == 0 ? w[h] << 7 : i == 1 ? w[h] << 1 : w[h] >> (6 * i - 7), 63 << 7, copy);
+      const float2 y = *reinterpret_cast<const float2*>(pairs + at);
+      x[h][2 * i] = fmaf(ms.y, y.x, ms.x);
+      x[h][2 * i + 1] = fmaf(ms.y, y.y, ms.x);
     }
 }
 // The outliers of the rows that a warp filled, one lane an outlier, over the
@@ -448,7 +451,7 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float2 e) {
 
 // Keys of a quantized tile with non-uniform codes or RoPE.
 __device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSlot& R, const unsigned long long* freq, const float* lut,
-                                                  const TileSrc& src, int kt, int tid, const uint8_t* raw, uint8_t* sK, uint8_t* sN) {
+                                                  const uint8_t* pairs, const TileSrc& src, int kt, int tid, const uint8_t* raw, uint8_t* sK, uint8_t* sN) {
   const int cb = tid & 7, groups = tile_groups(src, kt);
 #pragma unroll 1
   for (int j = 0; j < kTile / 32; ++j) {
@@ -456,7 +459,7 @@ __device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSl
     float x[2][8] = {};
     if (j < groups) {
       if (G.kb == 3)
-        general_row(raw, reinterpret_cast<const uint32_t*>(raw + R.ks), lut, t, cb, x);
+        general_row(raw, reinterpret_cast<const uint32_t*>(raw + R.ks), pairs, t, cb, x);
       else
         uniform_key_row(raw, G.kb, reinterpret_cast<const uint32_t*>(raw + R.ks), t, cb, x);
       if (G.pre_rope) {
@@ -501,15 +504,15 @@ __device__ __forceinline__ void fill_general_keys(const Geometry& G, const RawSl
     }
   });
 }
-__device__ __forceinline__ void fill_general_values(const Geometry& G, const RawSlot& R, const float* lut, const TileSrc& src, int kt,
-                                                    int tid, const uint8_t* raw, uint8_t* sV) {
+__device__ __forceinline__ void fill_general_values(const Geometry& G, const RawSlot& R, const uint8_t* pairs, const TileSrc& src,
+                                                    int kt, int tid, const uint8_t* raw, uint8_t* sV) {
   const int cb = tid & 7, groups = tile_groups(src, kt);
 #pragma unroll 1
   for (int j = 0; j < kTile / 32; ++j) {
     const int t = 32 * j + (tid >> 3);
     float y[2][8] = {};
     if (j < groups)
-      general_row(raw + R.v, reinterpret_cast<const uint32_t*>(raw + R.vs), lut, t, cb, y);
+      general_row(raw + R.v, reinterpret_cast<const uint32_t*>(raw + R.vs), pairs, t, cb, y);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       *reinterpret_cast<uint4*>(sV + tile_off(t, cb + 8 * h)) =

@@ -247,9 +247,7 @@ __global__ void __launch_bounds__(kThreadsMass, 1) mass_kernel(const __grid_cons
     *gave_up = ((uint32_t)__cvta_generic_to_shared(smem) & 1023) != 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (tid < 8) tail->lut[tid] = p.k_lut_off[tid];
-  if (tid < kHeadDim) tail->zeros[tid] = 0;
-  if (tid < kHeadDim / 2) tail->freq[freq_at(tid)] = p.freq[tid];
+  put_tables<false>(p, tail, raw0, tid);
   constexpr int issuer = 4 + kProducers / 32;  // then the copies' warp
   if (w == issuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
@@ -301,7 +299,7 @@ cudaError_t launch_attn_mass(TreeParams& p, cudaStream_t st) {
   if (M <= 8 && mass_stream_eligible(p.geo)) return launch_mass_stream(p, st);
   static std::atomic<long long> memo[kMemoDevices];
   p.raw = raw_slot(p.geo, false, kSmemMass - kFixedMass);
-  if (kFixedMass + p.raw.slots * p.raw.bytes > kSmemMass) return cudaErrorInvalidValue;
+  if (kFixedMass + raw_bytes(p.geo, p.raw, false) > kSmemMass) return cudaErrorInvalidValue;
   cudaError_t e = ensure_smem_limit(mass_kernel, memo, (int)kSmemMass);
   // rows beyond one accumulator's columns: further passes add to the record
   for (p.r0 = 0; e == cudaSuccess && p.r0 < M; p.r0 += kMaxCols) {

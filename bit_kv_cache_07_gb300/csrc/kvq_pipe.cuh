@@ -116,11 +116,25 @@ struct Tail {
   uint32_t tmem;
   int gave_up;
   int bad_piece[4];  // pieces that hold drafted values that are not finite, by number + 1
-  float lut[16];     // level offsets of K, of V
+  float lut[8];      // level offsets of K
   alignas(16) unsigned long long freq[kHeadDim / 2];  // RoPE turns per position
   alignas(16) uint32_t zeros[kHeadDim];  // the scales of groups that a tile lacks
 };
 static_assert(sizeof(Tail) <= kTailBytes, "tail");
+
+// The tables, by a whole CTA (a barrier follows).
+template <bool V>
+__device__ __forceinline__ void put_tables(const TreeParams& p, Tail* tail, uint8_t* raw0, int tid) {
+  if (tid < 8) tail->lut[tid] = p.k_lut_off[tid];
+  if (tid < kHeadDim) tail->zeros[tid] = 0;
+  if (tid < kHeadDim / 2) tail->freq[freq_at(tid)] = p.freq[tid];
+  if (p.geo.kb != 3) return;
+  float2* pairs = reinterpret_cast<float2*>(raw0 + p.raw.pairs);
+  for (int i = tid; i < (V ? 2 : 1) * 1024; i += blockDim.x) {
+    const float* lut = V && i >= 1024 ? p.v_lut_off : p.k_lut_off;
+    pairs[i] = make_float2(lut[(i >> 4) & 7], lut[(i >> 7) & 7]);
+  }
+}
 
 __device__ __forceinline__ TileSrc tile_src(const TreeParams& p, const Piece& c) {
   return TileSrc{c.tc, c.s, c.b, p.mask ? c.n_b : 0, c.tc.Nq % p.geo.ring, in_stream(p.geo, c.s) * p.n};
@@ -216,7 +230,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       }
       if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
       if (!c.quant) fill_fp16_keys(G, p.L, tail->freq, p.kd, src, k, tid, sK, sN);
-      else if (general) fill_general_keys(G, p.raw, tail->freq, tail->lut, src, k, tid, raw, sK, sN);
+      else if (general) fill_general_keys(G, p.raw, tail->freq, tail->lut, raw0 + p.raw.pairs, src, k, tid, raw, sK, sN);
       else fill_uniform_keys(G, p.L, p.raw, src, k, tid, raw, tail->zeros, sK, sN, sM + st * kGroupRowBytes);
       if constexpr (kAsync) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       if constexpr (!V) {
@@ -229,7 +243,7 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
         mbar_arrive_warp(B.full_k + 8 * st);
         if (i >= 2 && !mbar_wait(B.empty_v + 8 * st, again, gave_up)) return;
         if (!c.quant) bad |= store_fp16_values(src, k, tid, held, sV);
-        else if (G.vb == 3) fill_general_values(G, p.raw, tail->lut + 8, src, k, tid, raw, sV);
+        else if (G.vb == 3) fill_general_values(G, p.raw, raw0 + p.raw.pairs + kLevelPairBytes, src, k, tid, raw, sV);
         else fill_uniform_values(G, p.raw, src, k, tid, raw, sV);
         if (bad) *(volatile int*)&tail->bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
         if constexpr (kAsync) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");

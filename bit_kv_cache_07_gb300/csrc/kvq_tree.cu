@@ -179,9 +179,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __gr
     for (int i = 0; i < 4; ++i) tail->bad_piece[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
-  if (tid < kHeadDim) tail->zeros[tid] = 0;
-  if (tid < kHeadDim / 2) tail->freq[freq_at(tid)] = p.freq[tid];
+  put_tables<true>(p, tail, raw0, tid);
   __syncthreads();
   const int x = cta_first_tile(p.ncta, p.total, blockIdx.x), x_end = cta_first_tile(p.ncta, p.total, blockIdx.x + 1);
   if (tid < kConsumers) {
@@ -327,7 +325,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 
 cudaError_t launch_small(TreeParams& p, cudaStream_t st) {
   p.raw = raw_slot(p.geo, true, kSmemSmall - kFixedSmall);
-  if (kFixedSmall + p.raw.slots * p.raw.bytes > kSmemSmall) return cudaErrorInvalidValue;
+  if (kFixedSmall + raw_bytes(p.geo, p.raw, true) > kSmemSmall) return cudaErrorInvalidValue;
   static std::atomic<long long> memo[kMemoDevices];
   const cudaError_t e = ensure_smem_limit(tree_small_kernel, memo, (int)kSmemSmall);
   if (e != cudaSuccess) return e;

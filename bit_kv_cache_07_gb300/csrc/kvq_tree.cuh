@@ -34,9 +34,12 @@ struct SpecRows {
 
 // Stored bytes of a quantized tile as copied into shared memory: byte offsets
 // of its parts within a slot, and how many slots there are (2..kMaxRaw).
+// Non-uniform codes are looked up two at a time: behind the slots lie the
+// level pairs of K, then of V, in 16 copies, one per bank pair of a half-warp.
 constexpr int kMaxRaw = 4;
+constexpr int kLevelPairBytes = 64 * 16 * 8;
 struct RawSlot {
-  int slots, bytes;
+  int slots, bytes, pairs;
   int ks, kcol, kval, v, vs, vcol, vval;  // K codes at 0
 };
 inline RawSlot raw_slot(const Geometry& G, bool values, int room) {
@@ -55,9 +58,16 @@ inline RawSlot raw_slot(const Geometry& G, bool values, int room) {
   r.vcol = put(values ? kTile * G.nout : 0);
   r.vval = put(values ? kTile * G.nout * 2 : 0);
   r.bytes = (off + 127) / 128 * 128;
+  if (G.kb == 3) room -= (values ? 2 : 1) * kLevelPairBytes;
   r.slots = room / (r.bytes > 0 ? r.bytes : 1);
   r.slots = r.slots > kMaxRaw ? kMaxRaw : r.slots < 2 ? 2 : r.slots;
+  r.pairs = r.slots * r.bytes;
   return r;
+}
+
+// Shared memory behind a kernel's fixed part.
+inline uint32_t raw_bytes(const Geometry& G, const RawSlot& r, bool values) {
+  return r.pairs + (G.kb == 3 ? (values ? 2 : 1) * kLevelPairBytes : 0);
 }
 
 struct TreeParams {

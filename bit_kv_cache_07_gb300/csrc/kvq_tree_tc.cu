@@ -315,9 +315,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
     for (int i = 0; i < 4; ++i) tail->bad_piece[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (tid < 16) tail->lut[tid] = tid < 8 ? p.k_lut_off[tid] : p.v_lut_off[tid - 8];
-  if (tid < kHeadDim) tail->zeros[tid] = 0;
-  if (tid < kHeadDim / 2) tail->freq[freq_at(tid)] = p.freq[tid];
+  put_tables<true>(p, tail, raw0, tid);
   constexpr int issuer = (kSoftThreads + kProducers) / 32;  // then the copies' warp
   if (w == issuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
@@ -364,7 +362,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
 
 cudaError_t launch_tree_tc(TreeParams& p, cudaStream_t st) {
   p.raw = raw_slot(p.geo, true, kSmemTc - kFixedTc);
-  if (kFixedTc + p.raw.slots * p.raw.bytes > kSmemTc) return cudaErrorInvalidValue;
+  if (kFixedTc + raw_bytes(p.geo, p.raw, true) > kSmemTc) return cudaErrorInvalidValue;
   static std::atomic<long long> memo[kMemoDevices];
   const cudaError_t e = ensure_smem_limit(tree_tc_kernel, memo, (int)kSmemTc);
   if (e != cudaSuccess) return e;
