@@ -29,6 +29,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // The same producers fill the tiles; 6 warps take 16 keys of each with
 // mma.sync (m16n8k16), every warp with its own softmax state and partial
 // result.
+//
+// Measured with the merge, 32 KV heads: 8 x 4k tokens KV4 and 16 nodes 174 us
+// (0.99 TB/s); 64k tokens of 3-bit codes with 2 outliers a vector and RoPE, 8
+// nodes 511 us (0.48 TB/s).  Bound by the producers: some 4,000 cycles a tile
+// of uniform codes, 6,900 of non-uniform rotated ones, at an issue slot in two.
+// Sent through the tensor-core kernel instead, the two took 173 and 702 us where
+// this one took 171 and 695, and 4 nodes over 1k tokens 19 against 18: the
+// producers are the same, but fewer rows are padding here.  A second team of
+// producer warps for every other tile: 208 us against 170 for the first (their
+// registers are taken from the consumers).
 __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, const uint8_t* sQ, const uint8_t* stage0, const uint8_t* sM,
                                         Tail* tail, int x, int x_end, int tid, volatile int* gave_up) {
   auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
@@ -118,14 +128,21 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
           l[e >> 1] += z[n][e];
         }
       if (!wait(B.full_v + 8 * st, i >> 1)) return;
-      // O += P V; P rounds to fp16 (relative 2^-11 of each weight, as the output does)
-      const uint32_t pa[4] = {pack2(z[0][0], z[0][1]), pack2(z[0][2], z[0][3]), pack2(z[1][0], z[1][1]), pack2(z[1][2], z[1][3])};
+      // O += P V with P in two fp16 parts (22 bits): the products are few, and V's
+      // own rounding stays the only one before the output's
+      uint32_t pa[4], pn[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2(z[e >> 1][2 * (e & 1)], z[e >> 1][2 * (e & 1) + 1], &pa[e], &pn[e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pn[e] ^= 0x80008000u;
 #pragma unroll
       for (int n = 0; n < 16; n += 2) {
         uint32_t vb[4];
         ldsm4t(vb, aV + tile_off(16 * w + (lane & 15), n + (lane >> 4)));
         mma16816(o[n], pa, vb[0], vb[1]);
         mma16816(o[n + 1], pa, vb[2], vb[3]);
+        mma16816(o[n], pn, vb[0], vb[1]);
+        mma16816(o[n + 1], pn, vb[2], vb[3]);
       }
       mbar_arrive_warp(B.empty_v + 8 * st);
     }

@@ -4,12 +4,17 @@
 // One CTA per SM walks its range of 96-key tiles with 128 query rows:
 //   1 thread          copies the tiles' stored bytes ahead,
 //   8 producer warps  dequantize a tile into shared memory (two stages),
-//   1 thread          issues the matrix instructions,
+//   1 warp            issues the matrix instructions (one elected lane; run by a
+//                     converged warp the operands stay in uniform registers:
+//                     alone, a thread took 337 us for the first workload below),
 //   4 warps           softmax, one thread per row.
-// TMEM: Q as the fp16 operand A of the logits, S = Q K^T and the fp16 weights
-// in two buffers each (the next tile's logits are computed under this tile's
-// exponentials), O += P V.  With Q in TMEM the logits' products read K alone
-// from shared memory, whose bandwidth 96 columns would not cover twice.
+// TMEM: Q as the fp16 operand A of the logits, S = Q K^T in two buffers (the
+// next tile's logits are computed under this tile's exponentials), the weights
+// P, O += P V.  With Q in TMEM the logits' products read K alone from shared
+// memory, whose bandwidth 96 columns would not cover twice.
+// P enters in two fp16 parts like the keys: rounded to one, its error adds to
+// V's and the output's (1.6 times the output's own rounding instead of 1.3; the
+// second product costs 2 to 5 % of the time).
 // Quantized keys enter in two exact fp16 parts (two passes of the 128-channel
 // product), fp16 keys in one; what the 32 keys of a per-channel group share
 // comes from a 16-column product with the groups' min and scale rows.
@@ -19,6 +24,13 @@
 // The roles' loops share the instruction cache: rolled per 32 columns, the
 // softmax fits beside the producers (unrolled, four fetches in ten missed and
 // the kernel took half as long again).
+//
+// Measured with the merge, 32 heads on 8: 8 x 32k tokens KV4 and 32 nodes 294 us
+// (468 TFLOP/s of the formula's 4 d rows T; the second parts of K and P double
+// that on the tensor cores, 48 % of 1969); 28 heads on 4, 16 x up to 8k tokens
+// K4V2 rotated, 21 nodes 92 us; 2 x 8191 fp16, 63 nodes 71 us.  What bounds it:
+// the producers' conversion (some 3,100 of a tile's 3,900 cycles, 96 keys once
+// per 128 rows), at an issue slot in two; DRAM idles (17 % of its rate).
 #include "kvq_tc.cuh"
 #include "kvq_pipe.cuh"
 
@@ -29,11 +41,12 @@ constexpr int kSoftThreads = 128;
 constexpr int kThreadsTc = kSoftThreads + kProducers + 64;
 constexpr float kTopSum = 32768.0f;  // a tile's weights stay below fp16's range
 // The 16-column product reads 8 rows behind the group rows as its columns
-// 8..15 (of no use): the kilobyte that holds the tail.
+// 8..15 (of no use): the first kilobyte of the tail.
 constexpr uint32_t kFixedTc = 2 * kStageBytes + 2 * kGroupRowBytes + kTailBytes;
 constexpr uint32_t kSmemTc = 227 * 1024;
-// TMEM columns: S of stage st, its weights 96 behind; O; the groups' products; Q.
-constexpr uint32_t kTmemS = 144, kTmemP = 96, kTmemO = 288, kTmemGroup = 416, kTmemQ = 448;
+// TMEM columns: S of stage st; the weights (what is left of them 48 behind);
+// O; the groups' products; Q.
+constexpr uint32_t kTmemS = 96, kTmemP = 192, kTmemO = 288, kTmemGroup = 416, kTmemQ = 448;
 
 // ---------------------------------------------------------------- issuer
 // What the issuer remembers of a tile whose product with the values is due.
@@ -50,8 +63,11 @@ __device__ __forceinline__ bool issue_pv(uint32_t lead, const TreeParams& p, con
   tc_after();
   const uint64_t v = vd + st * (kStageBytes >> 4);
 #pragma unroll
-  for (int ks = 0; ks < kTile / 16; ++ks)  // 16 keys: 16 rows of both 64-channel halves
-    mma_ts(lead, tmem + kTmemO, tmem + kTmemS * st + kTmemP + 8 * ks, v + ks * (2048 >> 4), idesc(128) | kRowsB, ks > 0 || !due.first);
+  for (int part = 0; part < 2; ++part)
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks)  // 16 keys: 16 rows of both 64-channel halves
+      mma_ts(lead, tmem + kTmemO, tmem + kTmemP + kTile / 2 * part + 8 * ks, v + ks * (2048 >> 4), idesc(128) | kRowsB,
+             part > 0 || ks > 0 || !due.first);
   // (full_v was waited for at every tile of the piece)
   if (due.slot >= 0 && lead) p.part_flag[due.slot] = *(volatile const int*)&tail->bad_piece[due.piece & 3] == due.piece + 1;
   mma_commit(lead, B.empty_v + 8 * st);
@@ -143,6 +159,16 @@ __device__ __forceinline__ void add2(float2& l, float2 a) {
       : "f"(a.x), "f"(a.y));
 }
 
+// Two weights as two fp16 parts each (22 bits).
+__device__ __forceinline__ void weight_parts(float2 w, uint32_t* hi, uint32_t* rest) {
+  *hi = as_u32(__floats2half2_rn(w.x, w.y));
+  const float2 h = __half22float2(as_h2(*hi));
+  asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%0, %1};\nmov.b64 b, {%2, %3};\nmov.b64 c, {%4, %4};\nfma.rn.f32x2 d, b, c, a;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(w.x), "+f"(w.y)
+      : "f"(h.x), "f"(h.y), "f"(-1.0f));
+  *rest = as_u32(__floats2half2_rn(w.x, w.y));
+}
+
 __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint32_t tmem, int x, int x_end, int tid, volatile int* gave_up) {
   // warp-uniform: the TMEM loads are for whole warps
   auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
@@ -228,14 +254,19 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
           for (int ch = 0; ch < kCh; ++ch) {
             logits(ch);
             const float o = base_of(ch) - mu;
-            uint32_t h[16];
+            uint32_t h[16], rest[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 w = weights2(v[2 * e], v[2 * e + 1], scale, make_float2(o, o));
               add2(part, w);
-              h[e] = as_u32(__floats2half2_rn(w.x, w.y));
+              weight_parts(w, &h[e], &rest[e]);
             }
-            tm_store16(S + kTmemP + 16 * ch, h);
+            if (ch == 0 && i > 0) {  // the product that reads the weights before is done
+              if (!wait(B.o_done, i - 1)) return;
+              tc_after();
+            }
+            tm_store16(tmem + kTmemP + lane0 + 16 * ch, h);
+            tm_store16(tmem + kTmemP + kTile / 2 + lane0 + 16 * ch, rest);
           }
           sum = part.x + part.y;
           // past the range (or not a number): find the maximum and do it again
@@ -245,9 +276,8 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
         l += sum;
         tm_wait_st();
       }
-      // a wait tells two phases apart, not three: before this tile's product can
-      // be issued, see the one before it done (then the wait below is for this one)
-      if (t == c.cnt - 1 && i > 0 && !wait(B.o_done, i - 1)) return;
+      // a wait tells two phases apart, not three: a warp without rows sees them all too
+      if (!work && i > 0 && !wait(B.o_done, i - 1)) return;
       tc_before();
       mbar_arrive_warp(B.p_full + 8 * st);
     }
