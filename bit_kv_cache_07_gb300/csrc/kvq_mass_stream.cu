@@ -14,6 +14,10 @@
 //
 // Every warp walks an equal range of 32-token items (quantized groups, then
 // fp16 items, stream after stream).
+//
+// Measured: 16 x 32k tokens KV2, 8 KV heads, 4 query rows each: 86 us (2.78 TB/s);
+// 777 tokens KV8: 11 us, the host's time of a call.  Bound by instructions (64 %
+// of the issue slots): the group's Q' and an exponential per key and row.
 #include <cstring>
 
 #include "kvq_decode_mma.cuh"

@@ -222,7 +222,9 @@ __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __gr
 // first, one per thread, and from them every partial result's weight; then
 // 4 warps add the weighted partial results (lane l owns channels 4 l .. 4 l +
 // 3), all loads independent.  Quantized and fp16 pieces are summed apart, the
-// quantized sum rotated back once.
+// quantized sum rotated back once.  Bound by reading the partial results, which
+// are in L2: 19 to 23 us of 8 x 32 KV heads x 16 rows (6 partial results a piece)
+// and of 8 x 8 x 128, timed alone on a cold L2.
 constexpr int kMergeThreads = 128;
 constexpr int kMaxParts = kMaxSpecCtas * kConsumerWarps;  // of one kind of a row
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
