@@ -94,11 +94,48 @@ class MixedLayer:
         """decode with batch row b attending over its own tokens[b] tokens."""
         self._side_by_side(lambda layer, ws, s: layer.decode_ragged(tokens, q, out, lse, ws, s), stream)
 
-    def _side_by_side(self, call, stream):
+    def tree_attn(self, tokens, q, k_draft, v_draft, mask, out, lse=None, workspace=None, nodes=None, stream=None):
+        """binding.kvq_tree_attn over the layer (all heads); workspace as
+        new_tree_workspace gives it."""
+        self._side_by_side(lambda layer, ws, s: layer.tree_attn(tokens, q, k_draft, v_draft, mask, out, lse, ws, nodes, s),
+                           stream, self._each(workspace, "workspace"))
+
+    def attn_mass(self, tokens, q, lse, mass, weight=None, decay: float = 1.0, stream=None):
+        """binding.kvq_attn_mass over the layer; mass as new_mass gives it (a
+        record per part, of the part's heads)."""
+        self._side_by_side(lambda layer, m, s: layer.attn_mass(tokens, q, lse, m, weight, decay, s), stream, self._each(mass, "mass"))
+
+    def evict(self, tokens, n_groups, mass, mass_out, source=None, workspace=None, stream=None):
+        """binding.kvq_evict of every part: rows drop as many groups in each,
+        every head its own.  mass, mass_out, source (or None) and workspace:
+        one per part.  Returns the rows' tokens afterwards."""
+        n = len(self.parts)
+        each = list(zip(self._each(mass, "mass"), self._each(mass_out, "mass_out"),
+                        [None] * n if source is None else self._each(source, "source"), self._each(workspace, "workspace")))
+        left = []
+        self._side_by_side(lambda layer, a, s: left.append(layer.evict(tokens, n_groups, *a, s)), stream, each)
+        return left[0]
+
+    def new_tree_workspace(self, n_nodes: int):
+        return [binding.new_tree_workspace(layer.cfg, n_nodes, layer.buf.device) for _, _, layer in self.parts]
+
+    def new_evict_workspace(self):
+        return [binding.new_evict_workspace(layer.cfg, layer.buf.device) for _, _, layer in self.parts]
+
+    def new_mass(self):
+        return [binding.new_mass(layer.cfg, layer.buf.device) for _, _, layer in self.parts]
+
+    def _each(self, values, what: str):
+        if not isinstance(values, (list, tuple)) or len(values) != len(self.parts):
+            raise ValueError(f"{what}: a list of one per part ({len(self.parts)})")
+        return values
+
+    def _side_by_side(self, call, stream, each=None):
         import torch
+        each = self.ws if each is None else each
         main = stream if stream is not None else torch.cuda.current_stream()
         if len(self.parts) == 1:
-            call(self.parts[0][2], self.ws[0], main)
+            call(self.parts[0][2], each[0], main)
             return
         fork = torch.cuda.Event()
         fork.record(main)
@@ -107,7 +144,7 @@ class MixedLayer:
             s = main if i == 0 else self.side[i - 1]
             if i:
                 s.wait_event(fork)
-            call(layer, self.ws[i], s)
+            call(layer, each[i], s)
             if i:
                 e = torch.cuda.Event()
                 e.record(s)
