@@ -3,7 +3,7 @@
 // values as fp16, rows of 128 bytes with the 128-byte swizzle (tile_off).
 //
 // A tile's stored bytes come to shared memory by asynchronous bulk copies,
-// several tiles ahead (load_tile); 256 threads convert them in short loops,
+// several tiles ahead (load_tiles); 256 threads convert them in short loops,
 // whose code stays in the instruction caches (unrolled over registers, the
 // fetches cost as much as the work).  Thread (tid & 15) owns 8 channels,
 // tid >> 4 the keys 32 j + (tid >> 4) and + 16 of group j; with RoPE or
