@@ -534,9 +534,6 @@ __device__ __forceinline__ const uint16_t* fp16_key(const Geometry& G, const uin
   if (slot >= G.ring) slot -= G.ring;  // the window is at most one turn of the ring
   return ring + ((size_t)src.s * G.ring + slot) * kHeadDim;
 }
-__device__ __forceinline__ int fp16_pos(const TileSrc& src, int S, int f) {  // position of cached fp16 key f
-  return f < src.tc.S_eff ? f : S + src.tc.Nq + (f - src.tc.S_eff);
-}
 // 16 bytes at p (zeros where p is null), as one predicated load.
 __device__ __forceinline__ uint4 load16_if(const uint16_t* p, int chunk) {
   uint4 v;
@@ -548,15 +545,38 @@ __device__ __forceinline__ uint4 load16_if(const uint16_t* p, int chunk) {
   return v;
 }
 
+// The thread's 16-byte pieces of a tile's fp16 rows.  RUN: a tile that lies in
+// one run of the window's slots (nearly all of an unquantized cache) is read
+// without an address per row.
+template <bool RUN>
+__device__ __forceinline__ void load_fp16_rows(const Geometry& G, const uint16_t* sink, const uint16_t* ring, const uint16_t* draft,
+                                               const TileSrc& src, int kt, int tid, uint4 (&v)[kTile / 16]) {
+  if constexpr (RUN) {
+    const int f = kt * kTile;
+    int slot = src.slot0 + f - src.tc.S_eff;
+    if (slot >= G.ring) slot -= G.ring;
+    if (f >= src.tc.S_eff && f + kTile <= src.tc.k1 && slot + kTile <= G.ring) {
+      const uint4* at = reinterpret_cast<const uint4*>(ring + ((size_t)src.s * G.ring + slot) * kHeadDim) + tid;
+#pragma unroll
+      for (int u = 0; u < kTile / 16; ++u) v[u] = __ldg(at + 256 * u);
+      return;
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kTile / 16; ++u) v[u] = load16_if(fp16_key(G, sink, ring, draft, src, kt * kTile + (tid >> 4) + 16 * u), tid & 15);
+}
+__device__ __forceinline__ int fp16_pos(const TileSrc& src, int S, int f) {  // position of cached fp16 key f
+  return f < src.tc.S_eff ? f : S + src.tc.Nq + (f - src.tc.S_eff);
+}
 // fp16 tile: cached keys (rotated when they were cached before RoPE; then in
 // two parts), drafted keys as they are, zeros behind them.
+template <bool RUN>
 __device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtrs& L, const unsigned long long* freq,
                                                const uint16_t* kd, const TileSrc& src, int kt, int tid, uint8_t* sK, uint8_t* sN) {
   if (!G.pre_rope) {
     const int cb = tid & 15;
     uint4 v[kTile / 16];
-#pragma unroll
-    for (int u = 0; u < kTile / 16; ++u) v[u] = load16_if(fp16_key(G, L.k_sink, L.k_ring, kd, src, kt * kTile + (tid >> 4) + 16 * u), cb);
+    load_fp16_rows<RUN>(G, L.k_sink, L.k_ring, kd, src, kt, tid, v);
 #pragma unroll
     for (int u = 0; u < kTile / 16; ++u) *reinterpret_cast<uint4*>(sK + tile_off((tid >> 4) + 16 * u, cb)) = v[u];
     return;
@@ -582,10 +602,10 @@ __device__ __forceinline__ void fill_fp16_keys(const Geometry& G, const LayerPtr
 // Values of an fp16 tile.  A drafted value that is not finite enters as zero
 // (a weight of zero must not meet it); true is returned then, and the merge
 // adds it to the rows that see it.
+template <bool RUN>
 __device__ __forceinline__ void load_fp16_values(const Geometry& G, const LayerPtrs& L, const uint16_t* vd, const TileSrc& src, int kt,
                                                  int tid, uint4 (&v)[kTile / 16]) {
-#pragma unroll
-  for (int u = 0; u < kTile / 16; ++u) v[u] = load16_if(fp16_key(G, L.v_sink, L.v_ring, vd, src, kt * kTile + (tid >> 4) + 16 * u), tid & 15);
+  load_fp16_rows<RUN>(G, L.v_sink, L.v_ring, vd, src, kt, tid, v);
 }
 __device__ __forceinline__ bool store_fp16_values(const TileSrc& src, int kt, int tid, uint4 (&v)[kTile / 16], uint8_t* sV) {
   bool bad = false;

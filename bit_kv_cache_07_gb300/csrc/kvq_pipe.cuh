@@ -187,8 +187,8 @@ __device__ __forceinline__ void load_tiles(const TreeParams& p, const Bars& B, u
 // ROWS > 0: the producers also stage that many query rows of each piece.  V:
 // the values too.  (Eight warps one half after the other: with eight more for
 // the values side by side, the kernel's loops outgrow the instruction cache and
-// it takes longer.)
-template <int ROWS, bool V>
+// it takes longer.)  FP16: every tile is an fp16 one.
+template <int ROWS, bool V, bool FP16 = false>
 __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint8_t* sQ, uint8_t* stage0, uint8_t* sM, const uint8_t* raw0,
                                         Tail* tail, int x, int x_end, int tid, volatile int* gave_up) {
   const Geometry& G = p.geo;
@@ -198,11 +198,12 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
   for (int piece = 0; x < x_end; ++piece) {
     const Piece c = piece_at(p, x, x_end);
     const TileSrc src = tile_src(p, c);
+    const bool quant = !FP16 && c.quant;
     if constexpr (ROWS > 0) {
       // the previous piece's last logits are computed
       if (i && !mbar_wait(B.empty_k + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, gave_up)) return;
       const uint16_t* qb = p.q + ((size_t)c.b * G.Hq_tot + (size_t)layer_head(G, c.h) * G.g) * p.n * kHeadDim;
-      const bool paired = c.quant && !general && paired_order(G.kb);
+      const bool paired = quant && !general && paired_order(G.kb);
 #pragma unroll
       for (int u = 0; u < ROWS / 16; ++u) {
         const int r = (tid >> 4) + 16 * u, ch = tid & 15;
@@ -223,18 +224,18 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       uint8_t *sK = stage0 + st * (V ? kStageBytes : kKeyStageBytes), *sN = sK + kTileBytes, *sV = sN + kTileBytes;
       const uint8_t* raw = raw0 + slot * p.raw.bytes;
       uint4 held[V ? kTile / 16 : 1];  // an fp16 tile's values, in flight under its keys
-      if (c.quant) {
+      if (quant) {
         if (!mbar_wait(B.raw_full + 8 * slot, turn & 1, gave_up)) return;
       } else if constexpr (V) {
-        load_fp16_values(G, p.L, p.vd, src, k, tid, held);
+        load_fp16_values<FP16>(G, p.L, p.vd, src, k, tid, held);
       }
       if (i >= 2 && !mbar_wait(B.empty_k + 8 * st, again, gave_up)) return;
-      if (!c.quant) fill_fp16_keys(G, p.L, tail->freq, p.kd, src, k, tid, sK, sN);
+      if (!quant) fill_fp16_keys<FP16>(G, p.L, tail->freq, p.kd, src, k, tid, sK, sN);
       else if (general) fill_general_keys(G, p.raw, tail->freq, tail->lut, raw0 + p.raw.pairs, src, k, tid, raw, sK, sN);
       else fill_uniform_keys(G, p.L, p.raw, src, k, tid, raw, tail->zeros, sK, sN, sM + st * kGroupRowBytes);
       if constexpr (kAsync) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       if constexpr (!V) {
-        if (c.quant) {
+        if (quant) {
           mbar_arrive_warp(B.raw_empty + 8 * slot);
           if (++slot == p.raw.slots) slot = 0, ++turn;
         }
@@ -242,12 +243,12 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Bars& B, uint
       } else {
         mbar_arrive_warp(B.full_k + 8 * st);
         if (i >= 2 && !mbar_wait(B.empty_v + 8 * st, again, gave_up)) return;
-        if (!c.quant) bad |= store_fp16_values(src, k, tid, held, sV);
+        if (!quant) bad |= store_fp16_values(src, k, tid, held, sV);
         else if (G.vb == 3) fill_general_values(G, p.raw, raw0 + p.raw.pairs + kLevelPairBytes, src, k, tid, raw, sV);
         else fill_uniform_values(G, p.raw, src, k, tid, raw, sV);
         if (bad) *(volatile int*)&tail->bad_piece[piece & 3] = piece + 1;  // (at most 2 tiles, so 2 pieces, ahead of the reader)
         if constexpr (kAsync) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        if (c.quant) {
+        if (quant) {
           mbar_arrive_warp(B.raw_empty + 8 * slot);
           if (++slot == p.raw.slots) slot = 0, ++turn;
         }

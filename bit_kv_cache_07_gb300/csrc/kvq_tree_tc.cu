@@ -28,7 +28,7 @@
 // Measured with the merge, 32 heads on 8: 8 x 32k tokens KV4 and 32 nodes 294 us
 // (468 TFLOP/s of the formula's 4 d rows T; the second parts of K and P double
 // that on the tensor cores, 48 % of 1969); 28 heads on 4, 16 x up to 8k tokens
-// K4V2 rotated, 21 nodes 92 us; 2 x 8191 fp16, 63 nodes 71 us.  What bounds it:
+// K4V2 rotated, 21 nodes 92 us; 2 x 8191 fp16, 63 nodes 62 us.  What bounds it:
 // the producers' conversion (some 3,100 of a tile's 3,900 cycles, 96 keys once
 // per 128 rows), at an issue slot in two; DRAM idles (17 % of its rate).
 #include "kvq_tc.cuh"
@@ -315,6 +315,9 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
   }
 }
 
+// FP16: the unquantized cache, without the quantized tiles' code (63 nodes over
+// 2 x 8191 tokens: 71 us with it).
+template <bool FP16>
 __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_constant__ TreeParams p) {
   // (the swizzle's 1024-byte alignment: there is no other shared memory to shift the start)
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
   } else if (w < kSoftThreads / 32) {
     softmax(p, B, tmem, x, x_end, tid, gave_up);
   } else if (w < issuer) {
-    produce<0, true>(p, B, nullptr, stage0, sM, raw0, tail, x, x_end, tid - kSoftThreads, gave_up);
+    produce<0, true, FP16>(p, B, nullptr, stage0, sM, raw0, tail, x, x_end, tid - kSoftThreads, gave_up);
   } else if (w == issuer) {
     const uint32_t lead = elect_lead();
     issue(lead, p, B, tmem, (uint32_t)__cvta_generic_to_shared(stage0), (uint32_t)__cvta_generic_to_shared(sM), tail, x,
@@ -390,14 +393,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) tree_tc_kernel(const __grid_con
 
 }  // namespace
 
+template <bool FP16>
+static cudaError_t launch(TreeParams& p, cudaStream_t st) {
+  static std::atomic<long long> memo[kMemoDevices];
+  const cudaError_t e = ensure_smem_limit(tree_tc_kernel<FP16>, memo, (int)kSmemTc);
+  if (e != cudaSuccess) return e;
+  tree_tc_kernel<FP16><<<p.ncta, kThreadsTc, kSmemTc, st>>>(p);
+  return cudaGetLastError();
+}
 cudaError_t launch_tree_tc(TreeParams& p, cudaStream_t st) {
   p.raw = raw_slot(p.geo, true, kSmemTc - kFixedTc);
   if (kFixedTc + raw_bytes(p.geo, p.raw, true) > kSmemTc) return cudaErrorInvalidValue;
-  static std::atomic<long long> memo[kMemoDevices];
-  const cudaError_t e = ensure_smem_limit(tree_tc_kernel, memo, (int)kSmemTc);
-  if (e != cudaSuccess) return e;
-  tree_tc_kernel<<<p.ncta, kThreadsTc, kSmemTc, st>>>(p);
-  return cudaGetLastError();
+  return p.geo.fp16_mode ? launch<true>(p, st) : launch<false>(p, st);
 }
 
 }  // namespace kvq
