@@ -30,9 +30,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // mma.sync (m16n8k16), every warp with its own softmax state and partial
 // result.
 //
-// Measured with the merge, 32 KV heads: 8 x 4k tokens KV4 and 16 nodes 174 us
-// (0.99 TB/s); 64k tokens of 3-bit codes with 2 outliers a vector and RoPE, 8
-// nodes 511 us (0.48 TB/s).  Bound by the producers: some 4,000 cycles a tile
+// Measured with the merge, 32 KV heads: 8 x 4k tokens KV4 and 16 nodes 173 us
+// (1.0 TB/s); 64k tokens of 3-bit codes with 2 outliers a vector and RoPE, 8
+// nodes 506 us (0.48 TB/s).  Bound by the producers: some 4,000 cycles a tile
 // of uniform codes, 6,900 of non-uniform rotated ones, at an issue slot in two.
 // Sent through the tensor-core kernel instead, the two took 173 and 702 us where
 // this one took 171 and 695, and 4 nodes over 1k tokens 19 against 18: the
@@ -172,6 +172,9 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
   }
 }
 
+// FP16: the unquantized cache, without the quantized tiles' code (8 x 16k tokens, 8
+// KV heads, 16 rows each: 193 us, 2.8 TB/s; with it 230).
+template <bool FP16>
 __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *stage0 = smem, *sQ = stage0 + 2 * kStageBytes, *sM = sQ + kSmallRows * kHeadDim * 2;
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1) tree_small_kernel(const __gr
   if (tid < kConsumers) {
     consume(p, B, sQ, stage0, sM, tail, x, x_end, tid, gave_up);
   } else if (tid < kConsumers + kProducers) {
-    produce<kSmallRows, true>(p, B, sQ, stage0, sM, raw0, tail, x, x_end, tid - kConsumers, gave_up);
+    produce<kSmallRows, true, FP16>(p, B, sQ, stage0, sM, raw0, tail, x, x_end, tid - kConsumers, gave_up);
   } else {
     if ((tid & 31) == 0) load_tiles<true>(p, B, (uint32_t)__cvta_generic_to_shared(raw0), x, x_end, gave_up);
     __syncwarp();
@@ -342,13 +345,14 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   if (p.lse && lane == 0) p.lse[orow] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+template <bool FP16>
 cudaError_t launch_small(TreeParams& p, cudaStream_t st) {
   p.raw = raw_slot(p.geo, true, kSmemSmall - kFixedSmall);
   if (kFixedSmall + raw_bytes(p.geo, p.raw, true) > kSmemSmall) return cudaErrorInvalidValue;
   static std::atomic<long long> memo[kMemoDevices];
-  const cudaError_t e = ensure_smem_limit(tree_small_kernel, memo, (int)kSmemSmall);
+  const cudaError_t e = ensure_smem_limit(tree_small_kernel<FP16>, memo, (int)kSmemSmall);
   if (e != cudaSuccess) return e;
-  tree_small_kernel<<<p.ncta, kThreadsSmall, kSmemSmall, st>>>(p);
+  tree_small_kernel<FP16><<<p.ncta, kThreadsSmall, kSmemSmall, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -356,7 +360,7 @@ cudaError_t launch_small(TreeParams& p, cudaStream_t st) {
 
 cudaError_t launch_tree_attn(TreeParams& p, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-  if (p.total > 0) e = p.rblk == kSmallRows ? launch_small(p, st) : launch_tree_tc(p, st);
+  if (p.total > 0) e = p.rblk != kSmallRows ? launch_tree_tc(p, st) : p.geo.fp16_mode ? launch_small<true>(p, st) : launch_small<false>(p, st);
   if (e != cudaSuccess) return e;
   return launch_dependent(tree_merge_kernel, dim3(p.geo.g * p.n, p.geo.Hkv, p.geo.B), dim3(128), 0, st, p);
 }
