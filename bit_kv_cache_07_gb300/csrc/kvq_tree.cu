@@ -238,26 +238,14 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int nrb = (G.g * n_b + p.rblk - 1) / p.rblk, pair = h * nrb + rb;
   const TileCounts tc = tile_counts(G, p.rows.tokens[b], p.mask ? n_b : 0);
-  const int t0 = p.rows.tile0[b] + pair * (tc.qt + tc.ft);
   __shared__ float sW[2 * kMaxParts];
   __shared__ float sM[4], sL[4];
   __shared__ __align__(16) float sAcc[4][2][kHeadDim];
   __shared__ uint32_t sFlag;
   if (tid == 0) sFlag = 0;
-  // the partial results of a kind are consecutive in (slot, sub)
-  size_t at0[2];
-  int np[2];
-#pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int first = kind ? t0 + tc.qt : t0, tiles = kind ? tc.ft : tc.qt;
-    np[kind] = 0;
-    at0[kind] = 0;
-    if (tiles) {
-      const int c0 = tile_owner(p.ncta, p.total, first), c1 = tile_owner(p.ncta, p.total, first + tiles - 1);
-      np[kind] = (c1 - c0 + 1) * p.sub;
-      at0[kind] = (size_t)(c0 + 2 * (p.rows.pair0[b] + pair) + kind) * p.sub;
-    }
-  }
+  const PartSpan span[2] = {part_span(p, tc, b, pair, 0), part_span(p, tc, b, pair, 1)};
+  const size_t at0[2] = {span[0].at, span[1].at};
+  const int np[2] = {span[0].n, span[1].n};
   grid_dep_wait();
   __syncthreads();
   const int all = np[0] + np[1];
@@ -267,7 +255,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
   for (int i = tid; i < all; i += kMergeThreads) {
     const size_t sl = index(i);
     const float2 ml = p.part_ml[sl * p.rstride + rr];
-    if (i >= np[0] && p.part_flag[sl]) sFlag = 1;
+    if (i >= np[0] && names_drafted(p, ml, p.part_flag[sl])) sFlag = 1;
     M = fmaxf(M, ml.x);
     bad = bad || ml.x != ml.x || ml.y != ml.y;
   }

@@ -131,6 +131,26 @@ __host__ __device__ inline int row_of(const int* tab, int rows, int v) {
   return lo;
 }
 
+// Where the merge finds the partial results of one kind (0: quantized tiles,
+// 1: fp16 tiles) of a (b, h, row block): n of them, consecutive in (slot, sub).
+struct PartSpan {
+  size_t at;
+  int n;
+};
+__host__ __device__ inline PartSpan part_span(const TreeParams& p, const TileCounts& tc, int b, int pair, int kind) {
+  const int tiles = kind ? tc.ft : tc.qt;
+  if (!tiles) return PartSpan{0, 0};
+  const int first = p.rows.tile0[b] + pair * (tc.qt + tc.ft) + (kind ? tc.qt : 0);
+  const int c0 = tile_owner(p.ncta, p.total, first), c1 = tile_owner(p.ncta, p.total, first + tiles - 1);
+  return PartSpan{(size_t)(c0 + 2 * (p.rows.pair0[b] + pair) + kind) * p.sub, (c1 - c0 + 1) * p.sub};
+}
+// Whether a partial result of an fp16 piece names drafted values that are not
+// finite.  A piece whose CTA gave up has NaN in ml and no flag written: its flag
+// is whatever the scratch held and says nothing.
+__host__ __device__ inline bool names_drafted(const TreeParams& p, float2 ml, uint32_t flag) {
+  return p.mask && ml.x == ml.x && flag;
+}
+
 // Keys with a scale per channel and group that the tile kernels take apart
 // (kvq_fill.cuh: keys_channel).
 __host__ __device__ inline bool channel_scales(const Geometry& G) { return !G.pre_rope && G.kb != 3 && !G.gkc && !G.fp16_mode; }

@@ -496,7 +496,9 @@ KVQ_API kvq_status kvq_merge_attn(int32_t n_parts, int64_t rows, int32_t head_di
  *              Calls that share it must not overlap on the GPU.
  * Keys are dequantized to 22 bits (hi + lo fp16 parts), values to fp16;
  * attention weights enter in two fp16 parts; logits, maxima and sums are fp32.  The result does not
- * depend on timing.  Two launches.
+ * depend on timing.  Two launches.  Waits inside the kernels are bounded: should
+ * one run out (some 15 s), the rows it was for become NaN in out and lse; the
+ * call itself, being asynchronous, has returned KVQ_OK by then.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (n_nodes > 256, batch >
  * 256, max_tokens > 2^30, more than 2^30 tiles of 96 keys), KVQ_ERR_CAPACITY,
  * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA. */
@@ -537,6 +539,7 @@ KVQ_API kvq_status kvq_tree_workspace(const kvq_config *cfg, int32_t n_nodes, ui
  *              tokens[b] on are left as they are
  * No workspace; one launch and one pass over the keys per 256 rows of a KV
  * head; every entry is summed by one thread (or one quad) in a fixed order.
+ * A bounded wait that runs out leaves NaN in the entries it was for.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (batch > 256, max_tokens >
  * 2^30, n_rows > 2^20, more than 2^28 tiles of 96 keys), KVQ_ERR_CAPACITY,
  * KVQ_ERR_CUDA. */
