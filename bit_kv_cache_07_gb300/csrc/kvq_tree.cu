@@ -107,13 +107,14 @@ __device__ __forceinline__ void consume(const TreeParams& p, const Bars& B, cons
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
       }
-      // the maximum moves when a logit passes it by 2^8: weights stay in fp16's range, O is rarely rescaled
-      const bool move[2] = {mx[0] > m[0] + 8.0f, mx[1] > m[1] + 8.0f};
+      // the reference lies 12 octaves below the maximum it was taken from and moves when a logit passes it by 15:
+      // weights stay in fp16's range, down to 2^-37 of the largest (kvq_tree_tc.cu), and O is rarely rescaled
+      const bool move[2] = {mx[0] > m[0] + 15.0f, mx[1] > m[1] + 15.0f};
       if (__any_sync(0xffffffffu, move[0] || move[1])) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float al = move[e] ? ex2(m[e] - mx[e]) : 1.0f;
-          if (move[e]) m[e] = mx[e];
+          const float to = mx[e] - 12.0f, al = move[e] ? ex2(m[e] - to) : 1.0f;
+          if (move[e]) m[e] = to;
           l[e] *= al;
 #pragma unroll
           for (int n = 0; n < 16; ++n) o[n][2 * e] *= al, o[n][2 * e + 1] *= al;

@@ -494,11 +494,12 @@ KVQ_API kvq_status kvq_merge_attn(int32_t n_parts, int64_t rows, int32_t head_di
  *   workspace  device scratch of >= kvq_tree_workspace bytes, 16-byte aligned;
  *              its contents need not be zero and mean nothing afterwards.
  *              Calls that share it must not overlap on the GPU.
- * Keys are dequantized to 22 bits (hi + lo fp16 parts), values to fp16;
- * attention weights enter in two fp16 parts; logits, maxima and sums are fp32.  The result does not
- * depend on timing.  Two launches.  Waits inside the kernels are bounded: should
- * one run out (some 15 s), the rows it was for become NaN in out and lse; the
- * call itself, being asynchronous, has returned KVQ_OK by then.
+ * Keys are dequantized to 22 bits (hi + lo fp16 parts), values to fp16.  A
+ * row's attention weights enter in two fp16 parts: 22 bits, and no finer than
+ * 2^-33 of its largest weight.  Logits, maxima and sums are fp32.  The result
+ * does not depend on timing.  Two launches.  Waits inside the kernels are
+ * bounded: should one run out (some 15 s), the rows it was for become NaN in out
+ * and lse; the call itself, being asynchronous, has returned KVQ_OK by then.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (n_nodes > 256, batch >
  * 256, max_tokens > 2^30, more than 2^30 tiles of 96 keys), KVQ_ERR_CAPACITY,
  * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA. */
