@@ -5,9 +5,10 @@
 // With few rows a tile of dequantized keys costs far more than its products,
 // so the codes go to the tensor cores as they are (the decode's key side,
 // kvq_decode_mma.cuh): S = Kcodes . Q', Q' = q * scale_k per channel in hi + lo
-// fp16 parts, the codes centred (code - 2^(b-1): the record is fp32, and the
-// offset of 1024 that the decode leaves in its codes would cost it 10 bits),
-// the minimum's share in one number per row.  A thread's operand is 32 consecutive channels of a token, so
+// fp16 parts (q brought into (-1, 1) by a power of two per row), the codes
+// centred (code - 2^(b-1): the record is fp32, and the offset of 1024 that the
+// decode leaves in its codes would cost it 10 bits), the minimum's share in one
+// number per row.  A thread's operand is 32 consecutive channels of a token, so
 // a warp reads whole rows from global memory straight into its fragments,
 // the next 32 tokens' ahead of this one's products: no shared memory for keys,
 // no barrier between warps.
@@ -15,7 +16,7 @@
 // Every warp walks an equal range of 32-token items (quantized groups, then
 // fp16 items, stream after stream).
 //
-// Measured: 16 x 32k tokens KV2, 8 KV heads, 4 query rows each: 86 us (2.78 TB/s);
+// Measured: 16 x 32k tokens KV2, 8 KV heads, 4 query rows each: 87 us (2.75 TB/s);
 // 777 tokens KV8: 11 us, the host's time of a call.  Bound by instructions (64 %
 // of the issue slots): the group's Q' and an exponential per key and row.
 #include <cstring>
@@ -47,6 +48,7 @@ struct WarpSmem {
   alignas(16) float qw[4 * NT][kHeadDim];  // q * softmax scale, in the Q' build's channel order
   mma::MmaWarpSmem<NT> m;
   alignas(8) float qsum[4 * NT][2];  // InnerQ: sum of q n over each channel group
+  float up[4 * NT];                  // the rows' powers of two
 };
 
 // The keys of a group in flight: this thread's 32-channel slices of tokens gq + 8 i.
@@ -97,6 +99,16 @@ __device__ __forceinline__ void load_group(const StreamParams& p, int s, int grp
     r.s01 = __ldg(reinterpret_cast<const uint2*>(sc + c0));
     r.s23 = __ldg(reinterpret_cast<const uint2*>(sc + c0 + mma::qb_pair_dist<KB>()));
   }
+}
+
+// The power of two that brings a row whose largest element is `most` into
+// (-1, 1), and the one back.  Q' then stays below the scales themselves, so
+// within fp16's range (with large rows over wide channels q * scale_k does not),
+// and both are exact.
+__device__ __forceinline__ void unit_range(float most, float* down, float* back) {
+  const uint32_t e = min(__float_as_uint(most) >> 23, 252u);  // biased; most < 2^(e - 126)
+  *down = __uint_as_float((253 - e) << 23);
+  *back = __uint_as_float((e + 1) << 23);
 }
 
 // x as hi + 2^-11 lo, both fp16 (the rest is scaled up: unscaled it would lie in
@@ -269,16 +281,25 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 4) mass_stream_kernel(const
     }
     if (k0 < ng) {
       // the rows, scaled, in the Q' build's order; a row that does not count may hold anything
+      const float* norm = IQ && G.knorm ? p.L.k_norm + (size_t)s * kHeadDim : nullptr;
       __syncwarp();
 #pragma unroll 1
-      for (int r = 0; r < p.nr; ++r)
+      for (int r = 0; r < p.nr; ++r) {
+        float x[4], most = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = lane + 32 * j;
-          sm.qw[r][mma::qb_perm_pos<KB>(c)] = half_bits_to_float(__ldg(q + (size_t)r * kHeadDim + c)) * p.scale;
+          x[j] = half_bits_to_float(__ldg(q + (size_t)r * kHeadDim + c)) * p.scale;
+          most = fmaxf(most, fabsf(norm ? x[j] * __ldg(norm + c) : x[j]));
         }
+        float down, back;
+        unit_range(warp_max(most), &down, &back);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sm.qw[r][mma::qb_perm_pos<KB>(lane + 32 * j)] = x[j] * down;
+        if (lane == 0) sm.up[r] = back;
+      }
       __syncwarp();
-      if constexpr (IQ) build_q_token<KB, NT>(sm, G.knorm ? p.L.k_norm + (size_t)s * kHeadDim : nullptr, p.nr, lane);
+      if constexpr (IQ) build_q_token<KB, NT>(sm, norm, p.nr, lane);
       GroupRegs<KB> cur;
       load_group<KB, IQ>(p, s, k0, lane, cur);
       const int ke = min(k_end, ng);
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 4) mass_stream_kernel(const
               } else {
                 z = a + c + sm.m.bias[r < p.nr ? r : 0];
               }
-              if (wt[i] != 0.0f) add = fmaf(wt[i], mma::ex2((z - lse[i]) * 1.4426950408889634f), add);
+              if (wt[i] != 0.0f) add = fmaf(wt[i], mma::ex2(fmaf(z, sm.up[r < p.nr ? r : 0], -lse[i]) * 1.4426950408889634f), add);
             }
             sum[2 * mt + rh] = add;
           }
