@@ -5,12 +5,14 @@ kernels of libkvq.so.  There is no fallback: if the library is missing the
 import of any entry point raises.
 
 Tensors are torch CUDA tensors (or raw device addresses as ints); the
-binding checks device, dtype, contiguity and size before calling so that a
+binding checks device, dtype, contiguity and size (of the speculative calls the
+shape too) before calling so that a
 wrong pointer becomes a Python exception rather than a GPU fault.
 """
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 
 from . import build as _build
@@ -231,6 +233,29 @@ def _arg(t, what: str, dtype, nbytes: int):
         pass
     import torch
     return _ptr(t, what, None if dtype is torch.uint8 else dtype, nbytes)
+
+
+def _fits(shape, want) -> bool:
+    """Whether a contiguous tensor of `shape`, of enough elements, is read right
+    where `want` is expected: the same but for further leading rows, a flat
+    buffer, or the same elements grouped otherwise.  (Any other would be read
+    with the strides of `want`: a draft padded to more nodes, say.)"""
+    if len(shape) == len(want):
+        return tuple(shape[1:]) == tuple(want[1:])
+    return len(shape) == 1 or math.prod(shape) == math.prod(want)
+
+
+def _shaped(t, what: str, dtype, want):
+    """The address of tensor t (or t, an address), which holds `want`."""
+    try:
+        if t.dtype is dtype and t.shape == want and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _ptr(t, what, dtype, math.prod(want) * dtype.itemsize)
+    if not isinstance(t, int) and not _fits(t.shape, want):
+        raise ValueError(f"{what}: expected shape {tuple(want)}, got {tuple(t.shape)}")
+    return p
 
 
 def _scratch(workspace):
@@ -491,16 +516,15 @@ def kvq_tree_attn(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse=No
     hkv, hq = _totals(c)
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, n, d]")
-    n = int(q.shape[2])
-    nq, nk = c.batch * hq * n * c.head_dim * 2, c.batch * hkv * n * c.head_dim * 2
-    h, f = torch.float16, torch.float32
+    n, d, h = int(q.shape[2]), c.head_dim, torch.float16
     layer = _arg(layer_buf, "layer_buf", torch.uint8, lay.layer_bytes)
-    qp, op = _arg(q, "q", h, nq), _arg(out, "out", h, nq)
+    rows, draft = (c.batch, hq, n, d), (c.batch, hkv, n, d)
+    qp, op = _shaped(q, "q", h, rows), _shaped(out, "out", h, rows)
     kp = vp = mp = None
     if mask is not None:
-        kp, vp = _arg(k_draft, "k_draft", h, nk), _arg(v_draft, "v_draft", h, nk)
-        mp = _arg(mask, "mask", torch.int32, c.batch * n * ((n + 31) // 32) * 4)
-    lp = None if lse is None else _arg(lse, "lse", f, c.batch * hq * n * 4)
+        kp, vp = _shaped(k_draft, "k_draft", h, draft), _shaped(v_draft, "v_draft", h, draft)
+        mp = _shaped(mask, "mask", torch.int32, (c.batch, n, (n + 31) // 32))
+    lp = None if lse is None else _shaped(lse, "lse", torch.float32, rows[:3])
     wp, wn = _scratch(workspace)
     _on_device(layer_buf, q, k_draft, v_draft, mask, out, lse, workspace)
     st = lib().kvq_tree_attn(c, layer, _rows(tokens, c.batch, "tokens"), qp, kp, vp, mp, n,
@@ -528,9 +552,10 @@ def kvq_attn_mass(cfg, layer_buf, tokens, q, lse, mass, weight=None, decay: floa
     n = int(q.shape[2]) if q.dim() == 4 else 1
     f = torch.float32
     layer = _arg(layer_buf, "layer_buf", torch.uint8, lay.layer_bytes)
-    qp, lp = _arg(q, "q", torch.float16, c.batch * hq * n * c.head_dim * 2), _arg(lse, "lse", f, c.batch * hq * n * 4)
-    wp = None if weight is None else _arg(weight, "weight", f, c.batch * n * 4)
-    mp = _arg(mass, "mass", f, c.batch * c.n_kv_heads * c.max_tokens * 4)
+    qp = _shaped(q, "q", torch.float16, (c.batch, hq, n, c.head_dim) if q.dim() == 4 else (c.batch, hq, c.head_dim))
+    lp = _shaped(lse, "lse", f, (c.batch, hq, n))
+    wp = None if weight is None else _shaped(weight, "weight", f, (c.batch, n))
+    mp = _shaped(mass, "mass", f, (c.batch, c.n_kv_heads, c.max_tokens))
     _on_device(layer_buf, q, lse, weight, mass)
     st = lib().kvq_attn_mass(c, layer, _rows(tokens, c.batch, "tokens"), qp, lp, wp, n, float(decay), mp, _stream_of(stream, q))
     _check("kvq_attn_mass", st)
@@ -546,11 +571,11 @@ def kvq_evict(cfg, layer_buf, tokens, n_groups, mass, mass_out, source=None, wor
     c = _cfg(cfg)
     lay = kvq_layout_query(c)
     rows, drop = _rows(tokens, c.batch, "tokens"), _rows(n_groups, c.batch, "n_groups")
-    record = c.batch * c.n_kv_heads * c.max_tokens * 4
+    record, f = (c.batch, c.n_kv_heads, c.max_tokens), torch.float32
     slots = max(0, c.max_tokens - c.n_sink - c.n_recent) // 32
     layer = _arg(layer_buf, "layer_buf", torch.uint8, lay.layer_bytes)
-    ip, op = _arg(mass, "mass", torch.float32, record), _arg(mass_out, "mass_out", torch.float32, record)
-    sp = None if source is None else _arg(source, "source", torch.int32, c.batch * c.n_kv_heads * slots * 4)
+    ip, op = _shaped(mass, "mass", f, record), _shaped(mass_out, "mass_out", f, record)
+    sp = None if source is None else _shaped(source, "source", torch.int32, (c.batch, c.n_kv_heads, slots))
     wp, wn = _scratch(workspace)
     _on_device(layer_buf, mass, mass_out, source, workspace)
     st = lib().kvq_evict(c, layer, rows, drop, ip, op, sp, wp, wn, _stream_of(stream, mass))
