@@ -139,18 +139,19 @@ class MixedLayer:
             return
         fork = torch.cuda.Event()
         fork.record(main)
-        joins = []
-        for i, (_, _, layer) in enumerate(self.parts):
-            s = main if i == 0 else self.side[i - 1]
-            if i:
-                s.wait_event(fork)
-            call(layer, each[i], s)
-            if i:
+        used = []
+        try:
+            for i, (_, _, layer) in enumerate(self.parts):
+                s = main if i == 0 else self.side[i - 1]
+                if i:
+                    s.wait_event(fork)
+                    used.append(s)
+                call(layer, each[i], s)
+        finally:  # also when a part is refused: what was launched is joined
+            for s in used:
                 e = torch.cuda.Event()
                 e.record(s)
-                joins.append(e)
-        for e in joins:
-            main.wait_event(e)
+                main.wait_event(e)
 
     def workspace_bytes(self) -> int:
         return max(layer.layout.workspace_bytes for _, _, layer in self.parts)
