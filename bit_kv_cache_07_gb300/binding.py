@@ -17,7 +17,7 @@ import os
 
 from . import build as _build
 
-KVQ_OK = 0
+KVQ_OK, KVQ_ERR_INVALID_ARG, KVQ_ERR_WORKSPACE = 0, -1, -4
 STATUS = {0: "KVQ_OK", -1: "KVQ_ERR_INVALID_ARG", -2: "KVQ_ERR_UNSUPPORTED",
           -3: "KVQ_ERR_CAPACITY", -4: "KVQ_ERR_WORKSPACE", -5: "KVQ_ERR_CUDA"}
 
@@ -543,6 +543,12 @@ def kvq_attn_mass(cfg, layer_buf, tokens, q, lse, mass, weight=None, decay: floa
     """Add the attention weights of the rows q [B, Hq, n, d] (or [B, Hq, d]),
     whose log-sum-exp the attention returned as lse, to the record mass
     [B, Hkv, max_tokens] f32 of the cache's tokens; weight [B, n] f32."""
+    c, args = _mass_args(cfg, layer_buf, tokens, q, lse, mass, weight, decay)
+    _check("kvq_attn_mass", lib().kvq_attn_mass(c, *args, _stream_of(stream, q)))
+
+
+def _mass_args(cfg, layer_buf, tokens, q, lse, mass, weight, decay):
+    """kvq_attn_mass's config and checked arguments (all but the stream)."""
     import torch
     c = _cfg(cfg)
     lay = kvq_layout_query(c)
@@ -557,8 +563,7 @@ def kvq_attn_mass(cfg, layer_buf, tokens, q, lse, mass, weight=None, decay: floa
     wp = None if weight is None else _shaped(weight, "weight", f, (c.batch, n))
     mp = _shaped(mass, "mass", f, (c.batch, c.n_kv_heads, c.max_tokens))
     _on_device(layer_buf, q, lse, weight, mass)
-    st = lib().kvq_attn_mass(c, layer, _rows(tokens, c.batch, "tokens"), qp, lp, wp, n, float(decay), mp, _stream_of(stream, q))
-    _check("kvq_attn_mass", st)
+    return c, (layer, _rows(tokens, c.batch, "tokens"), qp, lp, wp, n, float(decay), mp)
 
 
 def kvq_evict(cfg, layer_buf, tokens, n_groups, mass, mass_out, source=None, workspace=None, stream=None):
@@ -567,6 +572,13 @@ def kvq_evict(cfg, layer_buf, tokens, n_groups, mass, mass_out, source=None, wor
     tensor) becomes the compacted cache's record; source int32 [B, Hkv, group
     slots] tells where each slot's group came from.  Returns the rows' tokens
     afterwards."""
+    c, args = _evict_args(cfg, layer_buf, tokens, n_groups, mass, mass_out, source, workspace)
+    _check("kvq_evict", lib().kvq_evict(c, *args, _stream_of(stream, mass)))
+    return [t - 32 * e for t, e in zip(args[1], args[2])]
+
+
+def _evict_args(cfg, layer_buf, tokens, n_groups, mass, mass_out, source, workspace):
+    """kvq_evict's config and checked arguments (all but the stream)."""
     import torch
     c = _cfg(cfg)
     lay = kvq_layout_query(c)
@@ -578,9 +590,18 @@ def kvq_evict(cfg, layer_buf, tokens, n_groups, mass, mass_out, source=None, wor
     sp = None if source is None else _shaped(source, "source", torch.int32, (c.batch, c.n_kv_heads, slots))
     wp, wn = _scratch(workspace)
     _on_device(layer_buf, mass, mass_out, source, workspace)
-    st = lib().kvq_evict(c, layer, rows, drop, ip, op, sp, wp, wn, _stream_of(stream, mass))
-    _check("kvq_evict", st)
-    return [t - 32 * e for t, e in zip(rows, drop)]
+    return c, (layer, rows, drop, ip, op, sp, wp, wn)
+
+
+def _evict_accepted(c, args):
+    """Raises what kvq_evict would refuse of one cache but not of another of the
+    same layer (configuration, scratch, records that overlap), without a launch."""
+    _, _, _, ip, op, _, wp, wn = args
+    need, record = kvq_evict_workspace(c), c.batch * c.n_kv_heads * c.max_tokens * 4
+    if not wp or wp % 16 or wn < need:
+        raise KvqError("kvq_evict", KVQ_ERR_WORKSPACE)
+    if ip != op and abs(ip - op) < record:
+        raise KvqError("kvq_evict", KVQ_ERR_INVALID_ARG)
 
 
 def kvq_evict_workspace(cfg) -> int:

@@ -103,18 +103,29 @@ class MixedLayer:
     def attn_mass(self, tokens, q, lse, mass, weight=None, decay: float = 1.0, stream=None):
         """binding.kvq_attn_mass over the layer; mass as new_mass gives it (a
         record per part, of the part's heads)."""
-        self._side_by_side(lambda layer, m, s: layer.attn_mass(tokens, q, lse, m, weight, decay, s), stream, self._each(mass, "mass"))
+        # every part's arguments are checked before the first record changes
+        calls = [binding._mass_args(layer.cfg, layer.buf, tokens, q, lse, m, weight, decay)
+                 for (_, _, layer), m in zip(self.parts, self._each(mass, "mass"))]
+        self._side_by_side(lambda _, a, s: self._run("kvq_attn_mass", a, s), stream, calls)
 
     def evict(self, tokens, n_groups, mass, mass_out, source=None, workspace=None, stream=None):
         """binding.kvq_evict of every part: rows drop as many groups in each,
         every head its own.  mass, mass_out, source (or None) and workspace:
         one per part.  Returns the rows' tokens afterwards."""
-        n = len(self.parts)
-        each = list(zip(self._each(mass, "mass"), self._each(mass_out, "mass_out"),
-                        [None] * n if source is None else self._each(source, "source"), self._each(workspace, "workspace")))
-        left = []
-        self._side_by_side(lambda layer, a, s: left.append(layer.evict(tokens, n_groups, *a, s)), stream, each)
-        return left[0]
+        # every part's arguments are checked before the first cache changes
+        source = [None] * len(self.parts) if source is None else self._each(source, "source")
+        calls = [binding._evict_args(layer.cfg, layer.buf, tokens, n_groups, *a) for (_, _, layer), *a in
+                 zip(self.parts, self._each(mass, "mass"), self._each(mass_out, "mass_out"), source, self._each(workspace, "workspace"))]
+        for c, args in calls:
+            binding._evict_accepted(c, args)
+        self._side_by_side(lambda _, a, s: self._run("kvq_evict", a, s), stream, calls)
+        _, rows, drop, *_ = calls[0][1]
+        return [t - 32 * e for t, e in zip(rows, drop)]
+
+    @staticmethod
+    def _run(name: str, call, stream):
+        c, args = call
+        binding._check(name, getattr(binding.lib(), name)(c, *args, stream.cuda_stream))
 
     def new_tree_workspace(self, n_nodes: int):
         return [binding.new_tree_workspace(layer.cfg, n_nodes, layer.buf.device) for _, _, layer in self.parts]

@@ -41,3 +41,60 @@ def test_a_part_that_raises_leaves_the_others_joined(B):
     seen = x[-1:].clone()
     torch.cuda.synchronize()
     assert seen.item() == 50.0
+
+
+def setup(B, seed=80):
+    """A filled layer of three parts, its records and the state that a refused
+    call must leave."""
+    from bit_kv_cache_07_gb300.mixed import MixedLayer
+    rng = np.random.default_rng(seed)
+    mixed = MixedLayer(config("kv4", 2, 6, 3, 500), PAIRS)
+    k, v = (torch.from_numpy(x).cuda() for x in random_kv(rng, (2, 3, 500, 128), big=False))
+    mixed.append_ragged([0, 0], [500, 300], k, v)
+    mass = mixed.new_mass()
+    for m in mass:
+        m.copy_(torch.from_numpy(rng.random(m.shape).astype(np.float32)))
+    torch.cuda.synchronize()
+    state = [x.clone() for x in [layer.buf for _, _, layer in mixed.parts] + mass]
+    return mixed, mass, state
+
+
+def unchanged(mixed, mass, state):
+    torch.cuda.synchronize()
+    return all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+               for a, b in zip([layer.buf for _, _, layer in mixed.parts] + mass, state))
+
+
+def test_an_eviction_refused_for_one_part_changes_none(B):
+    mixed, mass, state = setup(B)
+    ws, src = mixed.new_evict_workspace(), [torch.zeros(2, 1, 14, dtype=torch.int32, device="cuda") for _ in range(3)]
+    for i in (1, 2):  # the part that is refused, after others that are not
+        def put(values, x):
+            return values[:i] + [x] + values[i + 1:]
+        overlap = torch.zeros(2 * 500 + 32, device="cuda")
+        for bad in (dict(mass=put(mass, mass[i].double())), dict(mass=put(mass, mass[i][:, :, :400].contiguous())),
+                    dict(out=put(mass, mass[i].cpu())), dict(ws=put(ws, ws[i][:64])), dict(ws=put(ws, None)), dict(ws=put(ws, ws[i][8:])),
+                    dict(src=put(src, src[i].long())), dict(src=put(src, src[i][:, :, :9].contiguous())),
+                    dict(mass=put(mass, overlap[:1000].view(2, 1, 500)), out=put(mass, overlap[32:].view(2, 1, 500)))):
+            a = dict(dict(mass=mass, out=mass, ws=ws, src=src), **bad)
+            with pytest.raises((ValueError, TypeError, B.KvqError)):
+                mixed.evict([500, 300], [2, 1], a["mass"], a["out"], a["src"], a["ws"])
+            assert unchanged(mixed, mass, state), (i, list(bad))
+    for tokens, drop in (([500, 301, 0], [1, 1, 0]), ([500, 501], [1, 1]), ([500, 300], [1, 9]), (iter([500, 300]), [1, 1])):
+        with pytest.raises((ValueError, B.KvqError)):  # refused for every part
+            mixed.evict(tokens, drop, mass, mass, src, ws)
+        assert unchanged(mixed, mass, state)
+    assert mixed.evict([500, 300], [2, 1], mass, mass, src, ws) == [436, 268]
+    assert not unchanged(mixed, mass, state)
+
+
+def test_a_record_refused_for_one_part_changes_none(B):
+    mixed, mass, state = setup(B, 81)
+    q, lse = torch.zeros(2, 6, 3, 128, dtype=torch.float16, device="cuda"), torch.full((2, 6, 3), 6.0, device="cuda")
+    for i in (1, 2):
+        for x in (mass[i].double(), mass[i][:, :, :400].contiguous(), mass[i].cpu(), None):
+            with pytest.raises((ValueError, TypeError)):
+                mixed.attn_mass([500, 300], q, lse, mass[:i] + [x] + mass[i + 1:])
+            assert unchanged(mixed, mass, state), i
+    mixed.attn_mass([500, 300], q, lse, mass)
+    assert not unchanged(mixed, mass, state)
