@@ -593,11 +593,25 @@ def _evict_args(cfg, layer_buf, tokens, n_groups, mass, mass_out, source, worksp
     return c, (layer, rows, drop, ip, op, sp, wp, wn)
 
 
+def _record_entries(c) -> int:
+    return c.batch * c.n_kv_heads * c.max_tokens
+
+
+def _evict_spans(c, args):
+    """(address, bytes) of the tensors that kvq_evict reads, and of those that it writes."""
+    _, _, _, ip, op, sp, wp, wn = args
+    record, slots = 4 * _record_entries(c), max(0, c.max_tokens - c.n_sink - c.n_recent) // 32
+    out = [(op, record), (wp, wn)]
+    if sp is not None:
+        out.append((sp, 4 * c.batch * c.n_kv_heads * slots))
+    return [(ip, record)], out
+
+
 def _evict_accepted(c, args):
     """Raises what kvq_evict would refuse of one cache but not of another of the
     same layer (configuration, scratch, records that overlap), without a launch."""
     _, _, _, ip, op, _, wp, wn = args
-    need, record = kvq_evict_workspace(c), c.batch * c.n_kv_heads * c.max_tokens * 4
+    need, record = kvq_evict_workspace(c), 4 * _record_entries(c)
     if not wp or wp % 16 or wn < need:
         raise KvqError("kvq_evict", KVQ_ERR_WORKSPACE)
     if ip != op and abs(ip - op) < record:

@@ -96,9 +96,11 @@ class MixedLayer:
 
     def tree_attn(self, tokens, q, k_draft, v_draft, mask, out, lse=None, workspace=None, nodes=None, stream=None):
         """binding.kvq_tree_attn over the layer (all heads); workspace as
-        new_tree_workspace gives it."""
+        new_tree_workspace gives it (one per part, apart from each other)."""
+        workspace = self._each(workspace, "workspace")
+        self._apart([[(w.data_ptr(), w.nbytes)] for w in workspace if hasattr(w, "data_ptr")])
         self._side_by_side(lambda layer, ws, s: layer.tree_attn(tokens, q, k_draft, v_draft, mask, out, lse, ws, nodes, s),
-                           stream, self._each(workspace, "workspace"))
+                           stream, workspace)
 
     def attn_mass(self, tokens, q, lse, mass, weight=None, decay: float = 1.0, stream=None):
         """binding.kvq_attn_mass over the layer; mass as new_mass gives it (a
@@ -106,6 +108,7 @@ class MixedLayer:
         # every part's arguments are checked before the first record changes
         calls = [binding._mass_args(layer.cfg, layer.buf, tokens, q, lse, m, weight, decay)
                  for (_, _, layer), m in zip(self.parts, self._each(mass, "mass"))]
+        self._apart([[(a[-1], 4 * binding._record_entries(c))] for c, a in calls])
         self._side_by_side(lambda _, a, s: self._run("kvq_attn_mass", a, s), stream, calls)
 
     def evict(self, tokens, n_groups, mass, mass_out, source=None, workspace=None, stream=None):
@@ -118,9 +121,24 @@ class MixedLayer:
                  zip(self.parts, self._each(mass, "mass"), self._each(mass_out, "mass_out"), source, self._each(workspace, "workspace"))]
         for c, args in calls:
             binding._evict_accepted(c, args)
+        spans = [binding._evict_spans(c, args) for c, args in calls]
+        self._apart([out for _, out in spans], [into for into, _ in spans])
         self._side_by_side(lambda _, a, s: self._run("kvq_evict", a, s), stream, calls)
         _, rows, drop, *_ = calls[0][1]
         return [t - 32 * e for t, e in zip(rows, drop)]
+
+    @staticmethod
+    def _apart(written, read=()):
+        """The parts run side by side: what one of them writes, (address, bytes)
+        spans per part, no other part may write or read."""
+        spans = sorted((a, a + n, part, writes) for writes, lists in ((True, written), (False, read))
+                       for part, mine in enumerate(lists) for a, n in mine)
+        for k, (_, end, part, writes) in enumerate(spans):
+            for a, _, other, writes_too in spans[k + 1:]:
+                if a >= end:
+                    break
+                if part != other and (writes or writes_too):
+                    raise ValueError("parts share a tensor that one of them writes")
 
     @staticmethod
     def _run(name: str, call, stream):

@@ -98,3 +98,31 @@ def test_a_record_refused_for_one_part_changes_none(B):
             assert unchanged(mixed, mass, state), i
     mixed.attn_mass([500, 300], q, lse, mass)
     assert not unchanged(mixed, mass, state)
+
+
+def test_parts_that_share_a_tensor_are_refused(B):
+    """The parts run side by side: one scratch, record or source for two of
+    them is a race."""
+    mixed, mass, state = setup(B, 82)
+    ws, src = mixed.new_evict_workspace(), [torch.zeros(2, 1, 14, dtype=torch.int32, device="cuda") for _ in range(3)]
+    out = mixed.new_mass()
+    big = torch.empty(ws[0].numel() + 64, dtype=torch.uint8, device="cuda")
+    for bad in (dict(mass=[mass[0], mass[1], mass[0]], out=[mass[0], mass[1], mass[0]]), dict(out=[out[0], out[0], out[2]]),
+                dict(src=[src[0], src[1], src[1]]), dict(ws=[ws[0], ws[0], ws[2]]), dict(ws=[big[:-64], ws[1], big[64:]]),
+                dict(mass=[out[1], mass[1], mass[2]], out=out)):
+        a = dict(dict(mass=mass, out=out, ws=ws, src=src), **bad)
+        with pytest.raises(ValueError):
+            mixed.evict([500, 300], [2, 1], a["mass"], a["out"], a["src"], a["ws"])
+        assert unchanged(mixed, mass, state), list(bad)
+    q, lse = torch.zeros(2, 6, 3, 128, dtype=torch.float16, device="cuda"), torch.full((2, 6, 3), 6.0, device="cuda")
+    with pytest.raises(ValueError):
+        mixed.attn_mass([500, 300], q, lse, [mass[0], mass[1], mass[0]])
+    tree = mixed.new_tree_workspace(3)
+    for shared in ([tree[0]] * 3, [tree[0], tree[1], tree[1][16:]]):
+        with pytest.raises(ValueError):
+            mixed.tree_attn([500, 300], q, None, None, None, q.clone(), lse, shared)
+    assert unchanged(mixed, mass, state)
+    # one record read by two parts is no race
+    mixed.evict([500, 300], [2, 1], [mass[0], mass[1], mass[0]], out, src, ws)
+    mixed.tree_attn([436, 268], q, None, None, None, q.clone(), lse, tree)
+    torch.cuda.synchronize()
