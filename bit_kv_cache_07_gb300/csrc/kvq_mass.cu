@@ -174,6 +174,21 @@ __device__ __forceinline__ void add_weights(float2& sum, uint32_t v0, uint32_t v
   sum = __ffma2_rn(w, make_float2(ex2(y.x), ex2(y.y)), sum);
 }
 
+// A key's sum over the rows that count alone: a row of zeros (one that does not
+// count, or padding) meets a key that is not finite as 0 * inf.
+__device__ __noinline__ float counted(uint32_t logits, const float* off, const float* wt, int cols, float scale) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int r0 = 0; r0 < cols; r0 += 8) {
+    uint32_t v[8];
+    tm_load8(v, logits + r0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (wt[r0 + e] != 0.0f) sum = fmaf(wt[r0 + e], ex2(fmaf(__uint_as_float(v[e]), scale, off[r0 + e]) * 1.4426950408889634f), sum);
+  }
+  return sum;
+}
+
 __device__ __forceinline__ void weigh(const TreeParams& p, const Bars& B, uint32_t tmem, const MassSmem& m, int cols, int x, int x_end,
                                       int tid, volatile int* gave_up) {
   auto wait = [&](uint32_t bar, int phase) { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, phase & 1, gave_up)); };
@@ -207,9 +222,11 @@ __device__ __forceinline__ void weigh(const TreeParams& p, const Bars& B, uint32
           add_weights(sum, v[4 * e + 2], v[4 * e + 3], p.q_scale, make_float2(o.z, o.w), make_float2(u.z, u.w));
         }
       }
+      float total = sum.x + sum.y;
+      if (__any_sync(0xffffffffu, total != total)) total = counted(tmem + 256 * st + lane0, &off[0].x, m.wt, cols, p.q_scale);
       tc_before();
       mbar_arrive_warp(B.p_full + 8 * st);
-      if (have) *at = fmaf(p.decay, old, sum.x + sum.y);
+      if (have) *at = fmaf(p.decay, old, total);
     }
     x += c.cnt;
     if (x < x_end) {

@@ -67,3 +67,34 @@ def test_a_query_times_a_wide_channel(B, form, g, n):
     q = (0.5 * rng.standard_normal((2, hkv * g, n, 128))).astype(np.float16)
     q[..., 0] = 25.0
     check_mass(B, cfg, lengths, K, V, q)
+
+
+@pytest.mark.parametrize("form", ["fp16", "kv4"])
+@pytest.mark.parametrize("g,n", [(3, 1), (3, 4), (4, 8), (5, 13)])
+def test_keys_of_minus_infinity(B, form, g, n):
+    """Cached fp16 keys that no query attends (-inf where every query is
+    positive): their weight is zero, whatever number of rows meets them and
+    whether all of them count."""
+    rng = np.random.default_rng(71)
+    T, hkv = 500, 2
+    cfg = config(form, 1, hkv * g, hkv, T, n_recent=100)
+    K, V = random_kv(rng, (1, hkv, T, 128), big=False)
+    gone = np.r_[1, 3, T - 90:T - 60, T - 1] if form == "kv4" else np.r_[1, 3, 40:70, 200, T - 1]  # sinks and window; anywhere
+    q = rng.standard_normal((1, hkv * g, n, 128)).astype(np.float16)
+    t = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    K[:, :, gone, 0] = -np.inf
+    q[..., 0] = np.abs(q[..., 0]) + np.float16(0.25)
+    check_mass(B, cfg, [T], K, V, q)
+    # rows that do not count beside the others
+    layer, lse = B.Layer(cfg), torch.full((1, hkv * g, n), 6.0, device="cuda")
+    layer.append(0, t(K), t(V))
+    weight = torch.ones(1, n, device="cuda")
+    weight[0, n // 2:] = 0.0
+    got, want = B.new_mass(cfg), B.new_mass(cfg)
+    layer.attn_mass([T], t(q), lse, got, weight)
+    if n > 1:
+        layer.attn_mass([T], t(q[:, :, :n // 2]), lse[:, :, :n // 2].contiguous(), want)
+    torch.cuda.synchronize()
+    # both within e^E - 1 + 2^-16 of the sum, E <= 2^-20 * 16 (sum |q k| scale of the finite keys)
+    assert torch.allclose(got, want, rtol=2.0 ** -14, atol=0.0)
+    assert (got[0, :, torch.from_numpy(gone).cuda()] == 0).all()
