@@ -174,12 +174,13 @@ __device__ __forceinline__ void load_tiles(const TreeParams& p, const Bars& B, u
     }
     x += c.cnt;
   }
-  if (*gave_up) {  // the copies in flight end before the CTA does
-    for (int i = 0; i < p.raw.slots; ++i) {
-      if (--slot < 0) slot = p.raw.slots - 1, --turn;
-      if (turn < 0) break;
-      mbar_wait(B.raw_full + 8 * slot, turn & 1, nullptr);
-    }
+  // the copies in flight end before the CTA does, also when another warp gives
+  // up after the last of them was started: the last fill of every slot
+#pragma unroll 1
+  for (int i = 0; i < p.raw.slots; ++i) {
+    if (--slot < 0) slot = p.raw.slots - 1, --turn;
+    if (turn < 0) break;
+    mbar_wait(B.raw_full + 8 * slot, turn & 1, nullptr);
   }
 }
 
