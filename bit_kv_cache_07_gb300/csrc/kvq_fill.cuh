@@ -200,7 +200,8 @@ __device__ __forceinline__ void store_chunk(uint8_t* s, uint32_t off, const uint
 // arithmetic: with two producer warps per scheduler the tile's time is its
 // latency, and branches (rare cases, missing groups) each cost a round trip.
 // Scales so large that c' s passes the fp16 range take the second form (SAT):
-// fp32 products, hi saturated.
+// fp32 products, hi saturated, and neg holds what exceeds it, up to 288 (8-bit
+// codes), 4,400 (4) or 21,856 (2), to half a step of fp16: 1/8, 2 or 8.
 template <int BITS, bool SAT>
 __device__ __forceinline__ void key_products(const __half2 (&c)[4], const __half2 (&sc)[4], uint32_t (&hi)[4], uint32_t (&neg)[4]) {
 #pragma unroll
