@@ -143,7 +143,7 @@ class MixedLayer:
     @staticmethod
     def _run(name: str, call, stream):
         c, args = call
-        binding._check(name, getattr(binding.lib(), name)(c, *args, stream.cuda_stream))
+        binding._check(name, getattr(binding.lib(), name)(c, *args, binding._stream(stream)))
 
     def new_tree_workspace(self, n_nodes: int):
         return [binding.new_tree_workspace(layer.cfg, n_nodes, layer.buf.device) for _, _, layer in self.parts]

@@ -126,3 +126,23 @@ def test_parts_that_share_a_tensor_are_refused(B):
     mixed.evict([500, 300], [2, 1], [mass[0], mass[1], mass[0]], out, src, ws)
     mixed.tree_attn([436, 268], q, None, None, None, q.clone(), lse, tree)
     torch.cuda.synchronize()
+
+
+def test_one_part_takes_a_stream_handle(B):
+    """A layer of equal heads is one part and takes the streams that its Layer takes."""
+    from bit_kv_cache_07_gb300.mixed import MixedLayer
+    rng = np.random.default_rng(83)
+    cfg = config("kv4", 1, 4, 2, 300)
+    k, v = (torch.from_numpy(x).cuda() for x in random_kv(rng, (1, 2, 300, 128), big=False))
+    q, lse = torch.zeros(1, 4, 2, 128, dtype=torch.float16, device="cuda"), torch.full((1, 4, 2), 6.0, device="cuda")
+    got = []
+    for stream in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        mixed = MixedLayer(cfg, [(4, 4)] * 2)
+        mixed.append(0, k, v)
+        mass, ws = mixed.new_mass(), mixed.new_evict_workspace()
+        torch.cuda.synchronize()
+        mixed.attn_mass([300], q, lse, mass, stream=stream)
+        assert mixed.evict([300], [3], mass, mass, None, ws, stream=stream) == [204]
+        torch.cuda.synchronize()
+        got.append((mass[0], mixed.parts[0][2].buf))
+    assert all(torch.equal(a, b) for other in got[1:] for a, b in zip(got[0], other))
