@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kSumThreads) evict_sum_kernel(const __grid_con
     for (int i = 0; i < 8; ++i) {
       decompose(x[i], &mant[i], &exp[i]);
       if (mant[i]) top = max(top, exp[i]);
-      plain += x[i];
+      plain += exp[i] == 255 ? x[i] : 0.0f;  // finite ones cannot move an infinity, their fp32 sum could
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {

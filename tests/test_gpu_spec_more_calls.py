@@ -135,3 +135,29 @@ def test_evictions_on_two_streams(B, form):
         torch.cuda.synchronize()
         for (layer, record, *_), (buf, mass) in zip(jobs, want):
             assert torch.equal(layer.buf, buf) and torch.equal(record, mass)
+
+
+def test_infinite_records(B):
+    """A group's total is the sum in 64 bits: an infinity beside entries whose
+    fp32 sum would overflow the other way stays that infinity (equal totals:
+    the lower group leaves first), opposite infinities are not a number and
+    stay longest."""
+    T = 36 + 32 * 6
+    cfg = config("kv2", 1, 1, 1, T)
+    layer, ws = B.Layer(cfg), B.new_evict_workspace(cfg)
+    mass = np.zeros((1, 1, T), np.float32)
+    g = mass[0, 0, 4:4 + 192].reshape(6, 32)
+    g[0, 0], g[0, 1] = np.inf, -np.inf         # not a number
+    g[1, 0], g[1, 8:] = np.inf, -3e38          # +inf
+    g[2, 5] = np.inf                           # +inf
+    g[3, :] = 3e38                             # finite in 64 bits
+    g[4, 3], g[4, 4:20] = -np.inf, 3e38        # -inf
+    g[5, :] = 1.0
+    gone = [4, 5, 3, 1, 2, 0]                  # in this order
+    for E in range(1, 6):
+        record = torch.from_numpy(mass).cuda()
+        source = torch.full((1, 1, 6), -1, dtype=torch.int32, device="cuda")
+        layer.evict([T], [E], record, record, source, ws)
+        torch.cuda.synchronize()
+        kept = sorted(set(range(6)) - set(gone[:E]))
+        assert sorted(source[0, 0, :6 - E].tolist()) == kept, E
