@@ -16,11 +16,13 @@
 // moves.  The unquantized cache, whose window lands where groups leave from,
 // writes its window in a fourth.
 //
-// Measured: 16 x 32k tokens K8V4, 8 KV heads, a quarter leaves: 94 us (4.2 TB/s
-// of the moves' and the record's bytes), of which the moves are 60; 4 ragged
-// rows up to 8k fp16, three tenths: 27 us (1.7 TB/s); one sequence of 2k: 37 us of
-// host time.  Bound by the moves' scattered copies of 2 to 8 KB, then by the
-// selection, a chain of CTA-wide steps per stream.
+// Measured: 16 x 32k tokens K8V4, 8 KV heads, a quarter leaves: 93 us (4.2 TB/s
+// over the whole call), of which the moves are 60 (some 350 MB read and written
+// in copies of 4 KB to 256 bytes: 5.8 TB/s), the totals 15 and the selection, a
+// chain of CTA-wide steps per stream, 17; 4 ragged rows up to 8k fp16, three
+// tenths: 27 us (1.7 TB/s); one sequence of 2k: 37 to 46 us, which is the host's
+// time (21 on the GPU).  What bounds the large call: the totals and the
+// selection before the moves, a third of it for 17 MB of record.
 #include "kvq_evict.cuh"
 
 namespace kvq {

@@ -18,7 +18,7 @@
 // are one warp's, so it is read like a constant.
 //
 // Measured: 4 ragged rows up to 32k tokens of InnerQ KV4 keys, 8 KV heads, 68
-// query rows each: 91 us (0.73 TB/s).  Bound by the producers' fp32 conversion of
+// query rows each: 92 us (0.72 TB/s).  Bound by the producers' fp32 conversion of
 // keys with a scale per token, at 56 % of the issue slots.
 #include "kvq_tc.cuh"
 #include "kvq_pipe.cuh"

@@ -22,16 +22,17 @@
 // tile's weights sum past fp16's range: one pass over the logits per tile, and O
 // is rarely rescaled.  It lies 8 octaves below the maximum (96 weights of 2^8
 // stay in range): fp16 ends at 2^-24, so a weight keeps its parts down to 2^-33
-// of the largest.  With the reference at the maximum, weights 17 nats below it
-// (all tokens beside an attention sink) lose 4 % of their sum, at 18 nats 27 %.
+// of the largest.  With the reference at the maximum, weights more than 17 nats
+// below it (all tokens beside an attention sink) vanish from the product: of
+// logits spread by 0.4 around 17.9 nats nine tenths of the sum.
 // The roles' loops share the instruction cache: rolled per 32 columns, the
 // softmax fits beside the producers (unrolled, four fetches in ten missed and
 // the kernel took half as long again).
 //
-// Measured with the merge, 32 heads on 8: 8 x 32k tokens KV4 and 32 nodes 294 us
-// (468 TFLOP/s of the formula's 4 d rows T; the second parts of K and P double
+// Measured with the merge, 32 heads on 8: 8 x 32k tokens KV4 and 32 nodes 295 us
+// (467 TFLOP/s of the formula's 4 d rows T; the second parts of K and P double
 // that on the tensor cores, 48 % of 1969); 28 heads on 4, 16 x up to 8k tokens
-// K4V2 rotated, 21 nodes 92 us; 2 x 8191 fp16, 63 nodes 62 us.  What bounds it:
+// K4V2 rotated, 21 nodes 93 us; 2 x 8191 fp16, 63 nodes 62 us.  What bounds it:
 // the producers' conversion (some 3,100 of a tile's 3,900 cycles, 96 keys once
 // per 128 rows), at an issue slot in two; DRAM idles (17 % of its rate).
 #include "kvq_tc.cuh"

@@ -539,6 +539,13 @@ KVQ_API kvq_status kvq_tree_workspace(const kvq_config *cfg, int32_t n_nodes, ui
  *   mass       device f32 [B][n_kv_heads][max_tokens], in the cache's own
  *              stream order; the caller zero-fills it once.  Entries from
  *              tokens[b] on are left as they are
+ * The record is of cached tokens.  What a tree's rows give to drafted tokens is
+ * part of their lse and recorded nowhere, so tokens accepted from a tree start
+ * at the 0 of their entries, where the same tokens decoded one by one would
+ * have their own rows' weight and their successors': they leave the sooner once
+ * the window has passed them, unless the caller adds to their entries.  Every
+ * row counts for every t < tokens[b]; there is no limit per row, so a prompt's
+ * rows, of which each attends its own prefix, cannot be recorded in one call.
  * No workspace; one launch and one pass over the keys per 256 rows of a KV
  * head; every entry is summed by one thread (or one quad) in a fixed order.
  * A bounded wait that runs out leaves NaN in the entries it was for.
