@@ -510,6 +510,12 @@ def kvq_tree_attn(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse=No
     row b's tokens[b] cached tokens and the drafted tokens k_draft, v_draft
     [B, Hkv, n, d] that mask (int32 words, see tree_mask) lets each see; mask
     None: the cache alone.  nodes: how many of the n slots each row uses."""
+    c, args = _tree_args(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse, workspace, nodes)
+    _check("kvq_tree_attn", lib().kvq_tree_attn(c, *args, _stream_of(stream, q)))
+
+
+def _tree_args(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse, workspace, nodes):
+    """kvq_tree_attn's config and checked arguments (all but the stream)."""
     import torch
     c = _cfg(cfg)
     lay = kvq_layout_query(c)
@@ -527,9 +533,16 @@ def kvq_tree_attn(cfg, layer_buf, tokens, q, k_draft, v_draft, mask, out, lse=No
     lp = None if lse is None else _shaped(lse, "lse", torch.float32, rows[:3])
     wp, wn = _scratch(workspace)
     _on_device(layer_buf, q, k_draft, v_draft, mask, out, lse, workspace)
-    st = lib().kvq_tree_attn(c, layer, _rows(tokens, c.batch, "tokens"), qp, kp, vp, mp, n,
-                             None if nodes is None else _rows(nodes, c.batch, "nodes"), op, lp, wp, wn, _stream_of(stream, q))
-    _check("kvq_tree_attn", st)
+    return c, (layer, _rows(tokens, c.batch, "tokens"), qp, kp, vp, mp, n,
+               None if nodes is None else _rows(nodes, c.batch, "nodes"), op, lp, wp, wn)
+
+
+def _scratch_accepted(name: str, args, need: int):
+    """Raises what the library would refuse of the scratch that ends `args`,
+    without a launch."""
+    wp, wn = args[-2:]
+    if not wp or wp % 16 or wn < need:
+        raise KvqError(name, KVQ_ERR_WORKSPACE)
 
 
 def kvq_tree_workspace(cfg, n_nodes: int) -> int:
@@ -610,11 +623,9 @@ def _evict_spans(c, args):
 def _evict_accepted(c, args):
     """Raises what kvq_evict would refuse of one cache but not of another of the
     same layer (configuration, scratch, records that overlap), without a launch."""
-    _, _, _, ip, op, _, wp, wn = args
-    need, record = kvq_evict_workspace(c), 4 * _record_entries(c)
-    if not wp or wp % 16 or wn < need:
-        raise KvqError("kvq_evict", KVQ_ERR_WORKSPACE)
-    if ip != op and abs(ip - op) < record:
+    _scratch_accepted("kvq_evict", args, kvq_evict_workspace(c))
+    ip, op = args[3:5]
+    if ip != op and abs(ip - op) < 4 * _record_entries(c):
         raise KvqError("kvq_evict", KVQ_ERR_INVALID_ARG)
 
 

@@ -97,10 +97,13 @@ class MixedLayer:
     def tree_attn(self, tokens, q, k_draft, v_draft, mask, out, lse=None, workspace=None, nodes=None, stream=None):
         """binding.kvq_tree_attn over the layer (all heads); workspace as
         new_tree_workspace gives it (one per part, apart from each other)."""
-        workspace = self._each(workspace, "workspace")
-        self._apart([[(w.data_ptr(), w.nbytes)] for w in workspace if hasattr(w, "data_ptr")])
-        self._side_by_side(lambda layer, ws, s: layer.tree_attn(tokens, q, k_draft, v_draft, mask, out, lse, ws, nodes, s),
-                           stream, workspace)
+        # every part's arguments are checked before the first launch
+        calls = [binding._tree_args(layer.cfg, layer.buf, tokens, q, k_draft, v_draft, mask, out, lse, ws, nodes)
+                 for (_, _, layer), ws in zip(self.parts, self._each(workspace, "workspace"))]
+        self._apart([[args[-2:]] for _, args in calls if args[-2]])
+        for c, args in calls:
+            binding._scratch_accepted("kvq_tree_attn", args, binding.kvq_tree_workspace(c, q.shape[2]))
+        self._side_by_side(lambda _, a, s: self._run("kvq_tree_attn", a, s), stream, calls)
 
     def attn_mass(self, tokens, q, lse, mass, weight=None, decay: float = 1.0, stream=None):
         """binding.kvq_attn_mass over the layer; mass as new_mass gives it (a

@@ -146,3 +146,18 @@ def test_one_part_takes_a_stream_handle(B):
         torch.cuda.synchronize()
         got.append((mass[0], mixed.parts[0][2].buf))
     assert all(torch.equal(a, b) for other in got[1:] for a, b in zip(got[0], other))
+
+
+def test_a_tree_refused_for_one_part_starts_none(B):
+    mixed, mass, state = setup(B, 84)
+    q, lse = torch.zeros(2, 6, 3, 128, dtype=torch.float16, device="cuda"), torch.full((2, 6, 3), 6.0, device="cuda")
+    out, ws = torch.full_like(q, 7.0), mixed.new_tree_workspace(3)
+    for i in (1, 2):
+        for x in (ws[i][:4096], ws[i][8:], ws[i].cpu(), None):
+            with pytest.raises((ValueError, TypeError, B.KvqError)):
+                mixed.tree_attn([500, 300], q, None, None, None, out, lse, ws[:i] + [x] + ws[i + 1:])
+            torch.cuda.synchronize()
+            assert (out == 7.0).all() and (lse == 6.0).all()
+    mixed.tree_attn([500, 300], q, None, None, None, out, lse, ws)
+    torch.cuda.synchronize()
+    assert (out != 7.0).any() and (lse != 6.0).all() and unchanged(mixed, mass, state)
