@@ -85,15 +85,19 @@ __device__ __forceinline__ void issue(uint32_t lead, const TreeParams& p, const 
       tc_after();
       const uint64_t k = kd + st * (kKeyStageBytes >> 4);
       const uint32_t half = cols * 128 >> 4;  // from a row's first 64 channels to the others
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)  // 16 channels
-        mma_ss(lead, tmem + 256 * st, k + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, qd + (ks >> 2) * half + (ks & 3) * 2, idesc(cols), ks > 0);
+      // the keys' small parts first: the sum is small while they enter, so only
+      // the large parts' 8 steps cut it at its final size (InnerQ keys, 17 rows: error
+      // against 64 bits 1.1e-6 to 5.9e-7, that of plain fp32 6.5e-7)
       if (parts == 2) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int ks = 0; ks < 8; ++ks)  // 16 channels
           mma_ss(lead, tmem + 256 * st, k + (kTileBytes >> 4) + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2,
-                 qd + (ks >> 2) * half + (ks & 3) * 2, idesc(cols) | kNegA, 1);
+                 qd + (ks >> 2) * half + (ks & 3) * 2, idesc(cols) | kNegA, ks > 0);
       }
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        mma_ss(lead, tmem + 256 * st, k + (ks >> 2) * (kTile * 128 >> 4) + (ks & 3) * 2, qd + (ks >> 2) * half + (ks & 3) * 2, idesc(cols),
+               parts == 2 || ks > 0);
       mma_commit(lead, B.empty_k + 8 * st);
       mma_commit(lead, B.s_full + 8 * st);
     }
