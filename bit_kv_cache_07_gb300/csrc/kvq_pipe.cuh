@@ -57,9 +57,9 @@ __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
 // Wait for a phase, with a limit (well over any wait of a running kernel);
 // past it the CTA gives up: every role leaves its loop.  (gave_up null: a wait
 // for copies in flight on the way out.)
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, volatile int* gave_up) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t phase, volatile int* gave_up, int tries = 1 << 22) {
 #pragma unroll 1
-  for (int it = 0; it < (1 << 22); ++it) {
+  for (int it = 0; it < tries; ++it) {
     uint32_t ok;
     // asleep for up to 4 us a try: a polling warp takes issue slots from the working ones
     asm volatile(
