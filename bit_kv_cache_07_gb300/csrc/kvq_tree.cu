@@ -30,9 +30,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // mma.sync (m16n8k16), every warp with its own softmax state and partial
 // result.
 //
-// Measured with the merge, 32 KV heads: 8 x 4k tokens KV4 and 16 nodes 174 us
+// Measured with the merge, 32 KV heads: 8 x 4k tokens KV4 and 16 nodes 175 us
 // (1.0 TB/s); 64k tokens of 3-bit codes with 2 outliers a vector and RoPE, 8
-// nodes 506 us (0.48 TB/s).  Bound by the producers: some 4,000 cycles a tile
+// nodes 508 us (0.48 TB/s).  Bound by the producers: some 4,000 cycles a tile
 // of uniform codes, 6,900 of non-uniform rotated ones, at an issue slot in two.
 // Sent through the tensor-core kernel instead, the two took 173 and 702 us where
 // this one took 171 and 695, and 4 nodes over 1k tokens 19 against 18: the

@@ -20,17 +20,21 @@
 // comes from a 16-column product with the groups' min and scale rows.
 // A row's reference comes from its first tile's maximum and moves only when a
 // tile's weights sum past fp16's range: one pass over the logits per tile, and O
-// is rarely rescaled.  It lies 8 octaves below the maximum (96 weights of 2^8
-// stay in range): fp16 ends at 2^-24, so a weight keeps its parts down to 2^-33
-// of the largest.  With the reference at the maximum, weights more than 17 nats
-// below it (all tokens beside an attention sink) vanish from the product: of
-// logits spread by 0.4 around 17.9 nats nine tenths of the sum.
+// is rarely rescaled.  It lies 6 octaves below the maximum: fp16 ends at 2^-24,
+// so a weight keeps its parts down to 2^-31 of the largest.  With the reference
+// at the maximum, weights more than 17 nats below it (all tokens beside an
+// attention sink) vanish from the product: of logits spread by 0.4 around 17.9
+// nats nine tenths of the sum.  Each octave of that room is one less before a
+// row moves: for the first workload below, logits of deviation 1, 2, 4 and 8
+// take 293, 306, 353 and 398 us (295, 314, 368 and 410 with 8 octaves).  A move
+// takes the whole warp's references along, by their rows' sums of the tile
+// (searching the maxima again: 326 and 386 us for 2 and 4 with 8 octaves).
 // The roles' loops share the instruction cache: rolled per 32 columns, the
 // softmax fits beside the producers (unrolled, four fetches in ten missed and
 // the kernel took half as long again).
 //
-// Measured with the merge, 32 heads on 8: 8 x 32k tokens KV4 and 32 nodes 295 us
-// (467 TFLOP/s of the formula's 4 d rows T; the second parts of K and P double
+// Measured with the merge, 32 heads on 8: 8 x 32k tokens KV4 and 32 nodes 293 us
+// (469 TFLOP/s of the formula's 4 d rows T; the second parts of K and P double
 // that on the tensor cores, 48 % of 1969); 28 heads on 4, 16 x up to 8k tokens
 // K4V2 rotated, 21 nodes 93 us; 2 x 8191 fp16, 63 nodes 62 us.  What bounds it:
 // the producers' conversion (some 3,100 of a tile's 3,900 cycles, 96 keys once
@@ -44,7 +48,7 @@ namespace {
 constexpr int kSoftThreads = 128;
 constexpr int kThreadsTc = kSoftThreads + kProducers + 64;
 constexpr float kTopSum = 65504.0f;  // a tile's weights stay within fp16's range
-constexpr float kRoom = 8.0f;        // octaves from a row's reference to the maximum it was taken from
+constexpr float kRoom = 6.0f;        // octaves from a row's reference to the maximum (or sum) it was taken from
 // The 16-column product reads 8 rows behind the group rows as its columns
 // 8..15 (of no use): the first kilobyte of the tail.
 constexpr uint32_t kFixedTc = 2 * kStageBytes + 2 * kGroupRowBytes + kTailBytes;
@@ -149,6 +153,12 @@ __device__ __forceinline__ void put_q(const TreeParams& p, const Bars& B, const 
   mbar_arrive_warp(B.q_full);
 }
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two logits to two weights: packed multiply-add, two exponentials.
 __device__ __forceinline__ float2 weights2(uint32_t s0, uint32_t s1, float2 scale, float2 off) {
   float2 z;
@@ -223,21 +233,25 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
         bool search = t == 0;  // the row's maximum is to be found
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
-          if (search || __any_sync(0xffffffffu, m == -INFINITY)) {
-            float top = -INFINITY;
+          if (pass || search || __any_sync(0xffffffffu, m == -INFINITY)) {
+            // past the range: the warp's references follow their rows' sums of the tile (then 2^kRoom)
+            float to = m + lg2(sum) - kRoom;
+            if (!pass || search) {
+              float top = -INFINITY;
 #pragma unroll 1
-            for (int ch = 0; ch < kCh; ++ch) {
-              logits(ch);
-              float mx = -INFINITY;
+              for (int ch = 0; ch < kCh; ++ch) {
+                logits(ch);
+                float mx = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
-              top = fmaxf(top, fmaf(mx, p.q_scale, base_of(ch)));
+                for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
+                top = fmaxf(top, fmaf(mx, p.q_scale, base_of(ch)));
+              }
+              to = top - kRoom;
             }
-            top -= kRoom;
-            const bool move = top > m;
+            const bool move = to > m;
             if (__any_sync(0xffffffffu, move)) {
-              const float al = move ? ex2(m - top) : 1.0f;
-              if (move) m = top, l *= al;
+              const float al = move ? ex2(m - to) : 1.0f;
+              if (move) m = to, l *= al;
               if (t > 0) {
                 if (!wait(B.o_done, i - 1)) return;  // the products so far
                 tc_after();
@@ -275,9 +289,9 @@ __device__ __forceinline__ void softmax(const TreeParams& p, const Bars& B, uint
             tm_store16(tmem + kTmemP + kTile / 2 + lane0 + 16 * ch, rest);
           }
           sum = part.x + part.y;
-          // past the range (or not a number): find the maximum and do it again
+          // past the range: do it again, with the maximum where the sum does not tell it
           if (search || __all_sync(0xffffffffu, sum <= kTopSum)) break;
-          search = true;
+          search = __any_sync(0xffffffffu, !(sum < INFINITY));
         }
         l += sum;
         tm_wait_st();

@@ -497,7 +497,7 @@ KVQ_API kvq_status kvq_merge_attn(int32_t n_parts, int64_t rows, int32_t head_di
  * Keys are dequantized to 22 bits (hi + lo fp16 parts; keys of a channel whose
  * codes span more than fp16's range to 14 bits or more), values to fp16.  A
  * row's attention weights enter in two fp16 parts: 22 bits, and no finer than
- * 2^-33 of its largest weight.  Logits, maxima and sums are fp32.  The result
+ * 2^-31 of its largest weight.  Logits, maxima and sums are fp32.  The result
  * does not depend on timing.  Two launches.  Waits inside the kernels are
  * bounded: should one run out (some 15 s), the rows it was for become NaN in out
  * and lse; the call itself, being asynchronous, has returned KVQ_OK by then.
