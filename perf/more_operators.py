@@ -199,7 +199,10 @@ def _prepare_pool(st, c, z, g):
         part.copy_((_randn(part.shape, g) * 100).clamp_(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).view(torch.uint8))
     st["codes"] = codes
     # exponents around -7: a maximum of 3.5
-    st["scales"] = (127 - 7 + torch.randint(-1, 2, (z["n_blocks"], H, 2), generator=g, device="cuda")).to(torch.uint8)
+    n = z["n_blocks"] * H * 2
+    room = torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device="cuda")  # padded
+    st["scales"] = room[:n].view(z["n_blocks"], H, 2)
+    st["scales"].copy_(127 - 7 + torch.randint(-1, 2, st["scales"].shape, generator=g, device="cuda"))
     half = torch.float16
     if c["op"] == "append":
         hq = c["hq"]
