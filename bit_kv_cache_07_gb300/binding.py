@@ -57,11 +57,31 @@ class kvq_layout(C.Structure):
         ("ring_slots", C.c_int32), ("q_cap", C.c_int32), ("k_norm", kvq_region), ("rows", kvq_region)]
 
 
+class kvq_block_config(C.Structure):
+    _fields_ = [
+        ("batch", C.c_int32), ("n_tokens", C.c_int32), ("n_q_heads", C.c_int32), ("n_kv_heads", C.c_int32),
+        ("head_dim", C.c_int32), ("n_blocks", C.c_int32), ("max_blocks", C.c_int32), ("window", C.c_int32),
+        ("n_first", C.c_int32), ("softmax_scale", C.c_float), ("rope_theta", C.c_float), ("norm_eps", C.c_float),
+    ]
+
+
+BLOCK_TABLES = ["block_table", "free_list", "free_count", "lens", "start", "unit0", "token_row", "position", "slot"]
+
+
+class kvq_block_tables(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in BLOCK_TABLES]
+
+
+class kvq_block_layout(C.Structure):
+    _fields_ = [("codes_bytes", C.c_uint64), ("scales_bytes", C.c_uint64), ("workspace_bytes", C.c_uint64)]
+
+
 EXPORTS = ["kvq_layout_query", "kvq_append", "kvq_decode_attn", "kvq_decode_plan",
            "kvq_decode_path", "kvq_status_string", "kvq_decode_attn_noalloc", "kvq_context_shard",
            "kvq_merge_attn", "kvq_fit_nuq_lut", "kvq_measure_distortion", "kvq_rate_allocate",
            "kvq_append_ragged", "kvq_decode_attn_ragged", "kvq_tree_attn", "kvq_tree_workspace",
-           "kvq_attn_mass", "kvq_evict", "kvq_evict_workspace"]
+           "kvq_attn_mass", "kvq_evict", "kvq_evict_workspace", "kvq_block_layout_query", "kvq_block_plan",
+           "kvq_block_append", "kvq_block_attn"]
 NUQ_FIT_WORKSPACE_BYTES = 3 * 65538 * 8
 
 _lib = None
@@ -125,6 +145,15 @@ def lib():
         L.kvq_evict.restype = C.c_int
         L.kvq_evict_workspace.argtypes = [C.POINTER(kvq_config), C.POINTER(C.c_uint64)]
         L.kvq_evict_workspace.restype = C.c_int
+        bcp, btp, i64 = C.POINTER(kvq_block_config), C.POINTER(kvq_block_tables), C.c_int64
+        L.kvq_block_layout_query.argtypes = [bcp, C.POINTER(kvq_block_layout)]
+        L.kvq_block_layout_query.restype = C.c_int
+        L.kvq_block_plan.argtypes = [bcp, btp, vp, vp, vp, vp]
+        L.kvq_block_plan.restype = C.c_int
+        L.kvq_block_append.argtypes = [bcp, btp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+        L.kvq_block_append.restype = C.c_int
+        L.kvq_block_attn.argtypes = [bcp, btp, vp, vp, vp, vp, vp, vp, C.c_uint64, vp]
+        L.kvq_block_attn.restype = C.c_int
         L.kvq_status_string.argtypes = [C.c_int]
         L.kvq_status_string.restype = C.c_char_p
         _lib = L

@@ -1,0 +1,195 @@
+// kvq_block.cuh -- what the calls on the block cache share: sizes, parameters,
+// what the device-side tables say of a request, and its visible tiles.
+#pragma once
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+constexpr int kBlockTokens = 32;
+constexpr int kMaxBlockBatch = 1024;
+constexpr int kBlockSide = kBlockTokens * kHeadDim;  // bytes of a block's keys (or values) of one head
+constexpr int kScaleBias = 127;                      // E8M0: 2^(byte - 127)
+constexpr int kScaleNaN = 255;
+constexpr int kMinExp = -40, kMaxExp = 40;           // exponents that the append gives
+
+struct BlockGeo {
+  int B, N, Hq, Hkv, g, n_blocks, max_blocks;
+};
+
+// What the tables say of request b.  Anything that the plan would not write
+// makes n 0: the request is left out.
+struct BlockRequest {
+  int n;       // tokens of the step
+  int first;   // their first token slot
+  int before;  // tokens held before them
+};
+__host__ __device__ inline BlockRequest block_request(const BlockGeo& G, int len, int start, int end) {
+  BlockRequest r;
+  r.first = start;
+  r.n = 0;
+  r.before = len;
+  if (start < 0 || end <= start || end > G.N || len < end - start || len > G.max_blocks * kBlockTokens) return r;
+  r.n = end - start;
+  r.before = len - r.n;
+  return r;
+}
+
+struct BlockPlanParams {
+  BlockGeo geo;
+  kvq_block_tables t;
+  const int *lens_before, *free_before, *n_new;
+};
+
+struct BlockAppendParams {
+  BlockGeo geo;
+  kvq_block_tables t;
+  uint8_t *codes, *scales;
+  const uint16_t *k, *v, *q, *q_weight, *k_weight;
+  uint16_t* q_out;
+  long long ks, vs, qs;  // elements from a token slot to the next
+  int rotate;
+  float eps;
+  int units, heads_per_warp, q_chunks;
+  unsigned long long freq[kHeadDim / 2];  // turns per position, times 2^64
+};
+
+struct BlockAttnParams {
+  BlockGeo geo;
+  kvq_block_tables t;
+  const uint8_t *codes, *scales;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  unsigned* counters;  // [CTAs] tickets
+  float* part_ml;      // [2 CTAs][rows][2]
+  float* part_acc;     // [2 CTAs][rows][128]
+  float q_scale;       // softmax_scale * log2(e)
+  int window, n_first; // window: kNoWindow or 1..
+};
+constexpr int kNoWindow = 1 << 30;
+constexpr int kMaxBlockCtas = 256;
+constexpr int kMaxBlockRows = 64;  // (token, head) rows that read a KV head's blocks together
+
+// The blocks that rows of tokens i0..i1 of a request see: the first `ns`, then
+// those from `lo` on, `cnt` in all.
+struct BlockTiles {
+  int ns, lo, cnt;
+};
+__host__ __device__ inline BlockTiles block_tiles(int window, int n_first, int p0, int p1) {
+  BlockTiles t;
+  const int hi = p1 / kBlockTokens;
+  t.ns = 0;
+  t.lo = 0;
+  if (window < kNoWindow) {
+    const int f = n_first > p1 ? p1 + 1 : n_first;
+    t.ns = (f + kBlockTokens - 1) / kBlockTokens;
+    const int w0 = p0 - window + 1;
+    t.lo = w0 > 0 ? w0 / kBlockTokens : 0;
+    if (t.lo < t.ns) t.lo = t.ns;
+  }
+  t.cnt = t.ns + (hi >= t.lo ? hi - t.lo + 1 : 0);
+  return t;
+}
+// The most blocks that any `rows` consecutive (token, head) rows of a request see.
+__host__ __device__ inline int block_tiles_max(int window, int n_first, const BlockRequest& r, int g, int rows) {
+  if (r.n * g <= rows) return block_tiles(window, n_first, r.before, r.before + r.n - 1).cnt;
+  const int all = (r.before + r.n - 1) / kBlockTokens + 1;
+  if (window >= kNoWindow) return all;
+  const int last = r.before + r.n - 1;
+  const int f = n_first > last ? last + 1 : n_first;
+  const int span = (rows + g - 1) / g + 1;  // tokens that `rows` rows touch, at most
+  const long long wide = ((long long)window + span + kBlockTokens - 3) / kBlockTokens + 1;
+  const long long most = (f + kBlockTokens - 1) / kBlockTokens + wide;
+  return most < all ? (int)most : all;
+}
+
+// ------------------------------------------------- the attention's schedule
+// The tiles of all (request, head, row block) lie end to end; CTA c takes
+// [c per, (c + 1) per).  (Shared with a host check.)
+constexpr int kBlockWarps = 8;
+// A CTA's range: at least a tile for each of its warps.
+__host__ __device__ inline long long block_range(long long total, int ctas) {
+  const long long per = (total + ctas - 1) / ctas;
+  return per < kBlockWarps ? kBlockWarps : per;
+}
+// Where CTA c leaves its part of what begins at x and spans CTAs: a CTA has at
+// most two such parts, the one that its range begins with and the one that it
+// ends with.
+__host__ __device__ inline int piece_slot(long long x, long long per, int c) { return 2 * c + (x > c * per ? 1 : 0); }
+
+__host__ __device__ inline BlockRequest request_at(const BlockAttnParams& p, int b) {
+#ifdef __CUDA_ARCH__
+  return block_request(p.geo, __ldg(p.t.lens + b), __ldg(p.t.start + b), __ldg(p.t.start + b + 1));
+#else
+  return block_request(p.geo, p.t.lens[b], p.t.start[b], p.t.start[b + 1]);
+#endif
+}
+
+// One segment: tiles k0..k1 of a (request, head, row block).
+struct BlockSegment {
+  int b, h, first, before, n;  // request
+  int r0, rows;                // rows of the block
+  int k0, k1, ns, lo;          // its visible tiles in the CTA's range (k1 <= the block's own count)
+  long long x;                 // where the (request, head, row block) begins
+  int cnt;                     // and its tiles in the schedule
+};
+
+template <int ROWS>
+struct BlockWalk {
+  long long x, x1;  // the range left
+  int b, j, k;      // next: request, (head, row block) of it, tile
+  int streams, nrb, cnt;
+  BlockRequest r;
+
+  __host__ __device__ inline void load(const BlockAttnParams& p) {
+    r = request_at(p, b);
+    size(p, r, &nrb, &streams, &cnt);
+  }
+  __host__ __device__ static inline void size(const BlockAttnParams& p, const BlockRequest& r, int* nrb, int* streams, int* cnt) {
+    *nrb = (int)(((long long)r.n * p.geo.g + ROWS - 1) / ROWS);
+    *streams = *nrb * p.geo.Hkv;
+    *cnt = r.n ? block_tiles_max(p.window, p.n_first, r, p.geo.g, ROWS) : 0;
+  }
+  // the range [x, x1), whose first tile is tile x - xb of request b
+  __host__ __device__ inline void begin(const BlockAttnParams& p, long long x_, long long x1_, int b_, long long xb) {
+    x = x_, x1 = x1_, b = b_;
+    load(p);
+    const long long at = x - xb;
+    j = cnt ? (int)(at / cnt) : 0;
+    k = cnt ? (int)(at - (long long)j * cnt) : 0;
+  }
+  __host__ __device__ inline bool next(const BlockAttnParams& p, BlockSegment& s) {
+    const BlockGeo& G = p.geo;
+    if (x >= x1) return false;
+    while (j >= streams) {
+      if (++b >= G.B) return false;
+      j = 0;
+      load(p);
+    }
+    s.b = b, s.first = r.first, s.before = r.before, s.n = r.n;
+    s.h = j / nrb;
+    s.r0 = (j - s.h * nrb) * ROWS;
+    s.rows = r.n * G.g - s.r0 < ROWS ? r.n * G.g - s.r0 : ROWS;
+    const BlockTiles t = block_tiles(p.window, p.n_first, r.before + s.r0 / G.g, r.before + (s.r0 + s.rows - 1) / G.g);
+    const long long left = x1 - x;
+    const int end = left < cnt - k ? k + (int)left : cnt;
+    s.k0 = k;
+    s.k1 = end < t.cnt ? end : t.cnt;
+    s.ns = t.ns, s.lo = t.lo;
+    s.x = x - k;
+    s.cnt = cnt;
+    x += end - k;
+    k = 0;
+    ++j;
+    return true;
+  }
+};
+
+__host__ __device__ inline int tile_of(const BlockSegment& s, int k) { return k < s.ns ? k : s.lo + (k - s.ns); }
+
+cudaError_t launch_block_plan(const BlockPlanParams& p, cudaStream_t st);
+cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st);
+cudaError_t launch_block_attn(const BlockAttnParams& p, int sms, int rows, cudaStream_t st);
+
+}  // namespace kvq

@@ -1,0 +1,267 @@
+// kvq_block_append.cu -- norm, rotation and 8-bit store of a step's keys and
+// values, and the queries made ready, in one launch.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w,  (y_i, y_{i+64}) turned by position * f_i
+//   e = least exponent with max |y| <= 448 2^e over the block's tokens of a head,
+//   code = e4m3(y 2^-e)
+//
+// Eight lanes hold a token's row of a head: lane l the channels 8l..8l+7 and
+// 64+8l..64+8l+7, so that both of a rotated pair are in one lane, loads are two
+// 16-byte words and the mean is three shuffles.  A CTA takes one block and head:
+// its keys, then its values, each read once into registers (one maximum over the
+// CTA between the read and the store).  Calls of few tokens per request run the
+// same with one warp per CTA, which walks a longer run of tokens twice.  The
+// queries go to CTAs of their own: a warp turns four tokens' rows head after
+// head with the same sines.
+//
+// Angles: position times a 64-bit fraction of a turn, whose top 32 bits are
+// the angle (exact to 2^-32 turns at any position), and the hardware sine and
+// cosine of it in [-pi, pi] (absolute error below 2^-20, where q_out's own
+// rounding is 2^-11 and a code's 2^-4).
+#include "kvq_block.cuh"
+
+namespace kvq {
+
+constexpr int kRowLanes = 8;
+constexpr int kWarpTokens = 32 / kRowLanes;
+
+__device__ __forceinline__ void halves_to_floats(const uint4& u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+// Channels 8l..8l+7 in v[0..7], 64+8l.. in v[8..15].
+__device__ __forceinline__ void load_row(const uint16_t* row, int l, float (&v)[16]) {
+  const uint4* at = reinterpret_cast<const uint4*>(row);
+  const uint4 a = __ldg(at + l), b = __ldg(at + kRowLanes + l);
+  halves_to_floats(a, v);
+  halves_to_floats(b, v + 8);
+}
+__device__ __forceinline__ void normalise(float (&v)[16], const float (&w)[16], float eps) {
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
+#pragma unroll
+  for (int o = 1; o < kRowLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  const float r = rsqrtf(ss * (1.0f / kHeadDim) + eps);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = v[i] * r * w[i];
+}
+__device__ __forceinline__ void angles(const unsigned long long* freq, int l, int pos, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int turn = (int)(unsigned)((freq[8 * l + i] * (unsigned long long)pos) >> 32);  // [-1/2, 1/2) turns
+    const float a = (float)turn * 1.4629180792671596e-9f;                                 // 2 pi / 2^32
+    c[i] = __cosf(a);
+    s[i] = __sinf(a);
+  }
+}
+__device__ __forceinline__ void rotate(float (&v)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = v[i], b = v[8 + i];
+    v[i] = a * c[i] - b * s[i];
+    v[8 + i] = b * c[i] + a * s[i];
+  }
+}
+// The least e in [kMinExp, kMaxExp] with amax <= 448 2^e (448 = 1.75 2^8).
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
+  return min(max(e, kMinExp), kMaxExp);
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
+
+// Two values as e4m3, nearest, ties to even, at most 448 (low byte: a).
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;\n" : "=h"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_floats(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)two));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The last b with at[b] <= v (v >= at[0] = 0), by a warp: 32 rows apart, then
+// between them.
+__device__ __forceinline__ int unit_request(const int* at, int B, int v, int lane) {
+  const int step = (B + 31) / 32;
+  const int far = lane * step;
+  const unsigned below = __ballot_sync(0xffffffffu, far < B && __ldg(at + far) <= v);
+  const int lo = (31 - __clz(below | 1u)) * step;
+  const int near = lo + lane;  // step <= 32
+  const unsigned in = __ballot_sync(0xffffffffu, lane < step && near < B && __ldg(at + near) <= v);
+  return lo + 31 - __clz(in | 1u);
+}
+
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) block_append_kernel(const __grid_constant__ BlockAppendParams p) {
+  __shared__ unsigned long long s_freq[kHeadDim / 2];
+  __shared__ uint32_t s_max[WARPS], s_bad[WARPS];
+  const BlockGeo& G = p.geo;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, l = lane & (kRowLanes - 1), sub = lane / kRowLanes;
+  if (p.rotate)
+    for (int i = tid; i < kHeadDim / 2; i += 32 * WARPS) s_freq[i] = p.freq[i];
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_trigger();
+  constexpr int kStep = kWarpTokens * WARPS;  // tokens of a CTA at a time
+  const int kv_ctas = p.units * G.Hkv;
+
+  if ((int)blockIdx.x >= kv_ctas) {  // queries: kStep token slots, heads_per_warp heads
+    const int x = blockIdx.x - kv_ctas, group = x / p.q_chunks, chunk = x - group * p.q_chunks;
+    const int i = group * kStep + w * kWarpTokens + sub;
+    const int used = min(max(__ldg(p.t.start + G.B), 0), G.N);
+    if (group * kStep + w * kWarpTokens >= used) return;
+    const bool live = i < used;
+    const int row = live ? i : group * kStep + w * kWarpTokens;
+    float c[8], s[8], wt[16];
+    if (p.q_weight) load_row(p.q_weight, l, wt);
+    if (p.rotate) angles(s_freq, l, __ldg(p.t.position + row), c, s);
+    const int h1 = min(G.Hq, (chunk + 1) * p.heads_per_warp);
+    const uint16_t* src = p.q + (long long)row * p.qs;
+    uint16_t* dst = p.q_out + (long long)row * G.Hq * kHeadDim;
+    for (int h = chunk * p.heads_per_warp; h < h1; ++h) {
+      float v[16];
+      load_row(src + h * kHeadDim, l, v);
+      if (p.q_weight) normalise(v, wt, p.eps);
+      if (p.rotate) rotate(v, c, s);
+      uint4 o[2];
+      uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const __half2 two = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        ow[k] = *reinterpret_cast<const uint32_t*>(&two);
+      }
+      __syncwarp();  // (q_out may be q: a row is read whole before it is written)
+      if (live) {
+        uint4* at = reinterpret_cast<uint4*>(dst + h * kHeadDim);
+        at[l] = o[0];
+        at[kRowLanes + l] = o[1];
+      }
+    }
+    return;
+  }
+
+  // keys and values: one touched block and head
+  const int unit = blockIdx.x / G.Hkv, h = blockIdx.x - unit * G.Hkv;
+  if (unit >= __ldg(p.t.unit0 + G.B)) return;
+  const int b = unit_request(p.t.unit0, G.B, unit, lane);
+  const BlockRequest r = block_request(G, __ldg(p.t.lens + b), __ldg(p.t.start + b), __ldg(p.t.start + b + 1));
+  if (r.n == 0) return;
+  const int j = r.before / kBlockTokens + (unit - __ldg(p.t.unit0 + b));
+  const int p0 = max(r.before, j * kBlockTokens), p1 = min(r.before + r.n, (j + 1) * kBlockTokens);
+  if (j < 0 || p0 >= p1) return;
+  const int id = __ldg(p.t.block_table + (size_t)b * G.max_blocks + j);
+  if (id < 0 || id >= G.n_blocks) return;
+  const int off = p0 - j * kBlockTokens, count = p1 - p0;
+  const long long slot0 = r.first + (p0 - r.before);
+  const size_t place = (size_t)id * G.Hkv + h;
+  const bool again = count > kStep;
+
+  for (int side = 0; side < 2; ++side) {
+    const uint16_t* src = (side ? p.v + slot0 * p.vs : p.k + slot0 * p.ks) + h * kHeadDim;
+    const long long stride = side ? p.vs : p.ks;
+    float v[16], wt[16];
+    const bool norm = side == 0 && p.k_weight;
+    if (norm) load_row(p.k_weight, l, wt);
+    const auto make = [&](int t) {  // token t of the run in v (past the end: the first one)
+      const int tt = t < count ? t : 0;
+      load_row(src + tt * stride, l, v);
+      if (norm) normalise(v, wt, p.eps);
+      if (side == 0 && p.rotate) {
+        float c[8], s[8];
+        angles(s_freq, l, p0 + tt, c, s);
+        rotate(v, c, s);
+      }
+    };
+    uint32_t top = 0, bad = 0;
+    for (int t0 = 0; t0 < count; t0 += kStep) {
+      make(t0 + w * kWarpTokens + sub);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
+        const bool finite = u < 0x7f800000u;
+        top = max(top, finite ? u : 0u);
+        bad |= !finite;
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    bad = __any_sync(0xffffffffu, bad);
+    const uint8_t was = off ? p.scales[place * 2 + side] : 0;
+    if constexpr (WARPS > 1) {
+      __syncthreads();  // the other side's maxima have been read
+      if (lane == 0) s_max[w] = top, s_bad[w] = bad;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) top = max(top, s_max[i]), bad |= s_bad[i];
+    }
+    int e = scale_exponent(__uint_as_float(top));
+    const bool spoilt = off && was == kScaleNaN;
+    uint8_t* block = p.codes + (place * 2 + side) * kBlockSide;
+    if (off && !spoilt) {
+      const int e_was = was - kScaleBias;
+      if (e_was >= e) {
+        e = e_was;
+      } else {  // earlier tokens move to the larger scale
+        const float f = exp2i(max(e_was - e, -126));
+        for (int x = tid; x < off * 32; x += 32 * WARPS) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(block) + x;
+          const uint32_t u = *at;
+          const float2 a = e4m3x2_floats(u & 0xffffu), c = e4m3x2_floats(u >> 16);
+          *at = e4m3x2(a.x * f, a.y * f) | e4m3x2(c.x * f, c.y * f) << 16;
+        }
+      }
+    }
+    const float f = e >= 127 ? 5.877471754111438e-39f : exp2i(-e);
+    for (int t0 = 0; t0 < count; t0 += kStep) {
+      const int t = t0 + w * kWarpTokens + sub;
+      if (again) make(t);
+      if (t < count) {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = fabsf(v[4 * i + k]) < INFINITY ? v[4 * i + k] * f : 0.0f;
+          c[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
+        }
+        const int tok = off + t;
+        uint8_t* at = block + tok * kHeadDim + (l & 1) * 8;
+        *reinterpret_cast<uint2*>(at + (((l >> 1) ^ (tok & 7)) << 4)) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(at + (((4 + (l >> 1)) ^ (tok & 7)) << 4)) = make_uint2(c[2], c[3]);
+      }
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (tid == 0) p.scales[place * 2 + side] = bad || spoilt ? kScaleNaN : (uint8_t)(e + kScaleBias);
+  }
+}
+
+cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st) {
+  const BlockGeo& G = p.geo;
+  // no more blocks are touched: each request's tokens start one and end one
+  const long long most = (long long)G.N / kBlockTokens + 2ll * G.B;
+  p.units = (int)(most < G.N ? most : G.N);
+  // eight warps hold a whole block's tokens; up to four tokens per request (drafted
+  // chains, single tokens) fill one warp
+  const bool few = (G.N + G.B - 1) / G.B <= kWarpTokens;
+  const int step = kWarpTokens * (few ? 1 : 8);
+  // heads of a query warp: more share a token's sines, fewer spread a small call
+  // over the SMs
+  const long long rows = (long long)G.N * G.Hq;
+  p.heads_per_warp = (int)(rows >= 8ll * 16384 ? 8 : rows >= 16384 ? rows / 16384 : 1);
+  p.q_chunks = (G.Hq + p.heads_per_warp - 1) / p.heads_per_warp;
+  const long long q_ctas = p.q ? (long long)((G.N + step - 1) / step) * p.q_chunks : 0;
+  const long long ctas = (long long)p.units * G.Hkv + q_ctas;
+  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  return few ? launch_dependent(block_append_kernel<1>, dim3((unsigned)ctas), dim3(32), 0, st, p)
+             : launch_dependent(block_append_kernel<8>, dim3((unsigned)ctas), dim3(256), 0, st, p);
+}
+
+}  // namespace kvq

@@ -1,0 +1,469 @@
+// kvq_block_attn.cu -- attention of a step's tokens over 8-bit blocks: causal,
+// with or without a sliding window and first tokens that stay visible.
+//
+// Row r = (token i, head j of the KV head's group), key t of a block with the
+// scales 2^ek, 2^ev:
+//   y_rt = scale log2(e) 2^ek (q_r . c_t) + ev,  w_rt = 2^(y_rt - ref_r),
+//   out_r = sum_t w_rt c'_t / l_r,  l_r = sum_t 2^-ev w_rt,
+//   lse_r = (ref_r + log2 l_r) ln 2:
+// the value scale is a power of two, so it rides in the exponent of the weight
+// and costs nothing per element.  The codes are fp16 numbers as they are (e4m3 is
+// a subset), so the products on the tensor cores are exact up to fp32 sums.
+//
+// Bound: the bytes of the visible blocks, each read once for up to 64 rows of a
+// KV head.  A 32-token tile of a head is two contiguous runs of 4 KB: one bulk
+// copy by one thread, stored in an order that both ldmatrix and the key loads
+// read without bank conflicts.  The visible tiles of all (request, head, row
+// block) lie end to end, cut into one equal range per SM; lengths come from the
+// GPU, so each CTA takes the prefix sums itself.  A CTA's eight warps form teams
+// of one warp per 16 rows; teams take a segment's tiles in turn, each with its
+// own ring of copies, which runs ahead across segments.  At a segment's end the
+// teams join their (ref, l, O) through shared memory, and a (request, head, row
+// block) that spans CTAs is joined by the CTA that comes last (nobody waits for
+// another CTA).  mma.sync rather than tcgen05: 1 to 64 rows fill an eighth to a
+// half of a 128-row tcgen05 tile, and its operands would have to be written back
+// to shared memory as fp16 first (4 times the tile's bytes); here the
+// conversion happens in the registers that feed the product.
+#include "kvq_block.cuh"
+#include "kvq_pipe.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kWarps = kBlockWarps;
+constexpr int kThreadsAttn = 32 * kWarps;
+constexpr int kStagesPerWarp = 3;
+constexpr int kPairBytes = 2 * kBlockSide;  // a tile: K then V
+constexpr int kStages = kWarps * kStagesPerWarp;
+constexpr float kRoom = 12.0f;       // weights up to 2^12 at a new reference,
+constexpr float kMoveAt = 15.0f;     // up to 2^15 before it moves (fp16 ends at 2^16)
+
+struct AttnSmem {
+  uint8_t stage[kStages][kPairBytes];
+  float4 join[4][16][32];      // 4 row tiles of accumulators, lane by lane
+  uint8_t scale16[kStages][16];
+  uint64_t full[kStages], empty[kStages];
+  float2 join_ml[4][16];
+  int meta[kStages];           // byte of scale16 where the tile's scales are; -1: no such block
+  long long warp_sum[kWarps];
+  long long first_x;           // the range's first request: where it begins
+  int first_b, gave_up, last;
+};
+static_assert(sizeof(AttnSmem) <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void e4m3_halves(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n" : "=r"(lo), "=r"(hi) : "r"(four));
+}
+__device__ __forceinline__ uint32_t pack_halves(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// RT: 16-row tiles that read a KV head's blocks together
+template <int RT>
+__global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __grid_constant__ BlockAttnParams p) {
+  constexpr int ROWS = 16 * RT, TEAMS = kWarps / RT, RING = kStagesPerWarp * RT;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  AttnSmem& sm = *reinterpret_cast<AttnSmem*>(smem_raw);
+  const BlockGeo& G = p.geo;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, team = w / RT, rt = w % RT;
+  const int gq = lane >> 2, tq = lane & 3;
+  volatile int* gave_up = &sm.gave_up;
+  if (tid < kStages) {
+    mbar_init(smem_u32(&sm.full[tid]), 1);
+    mbar_init(smem_u32(&sm.empty[tid]), RT);
+  }
+  if (tid == 0) sm.gave_up = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  grid_dep_wait();
+
+  // the schedule: tiles of four requests per thread, their sums, the CTA's range
+  long long mine[4], run = 0, total, x0, x1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = 4 * tid + i;
+    mine[i] = 0;
+    if (b < G.B) {
+      const BlockRequest r = request_at(p, b);
+      int nrb, streams, cnt;
+      BlockWalk<ROWS>::size(p, r, &nrb, &streams, &cnt);
+      mine[i] = (long long)streams * cnt;
+    }
+    run += mine[i];
+  }
+  long long upto = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) sm.warp_sum[w] = upto;
+  __syncthreads();
+  total = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) upto += sm.warp_sum[i];
+    total += sm.warp_sum[i];
+  }
+  const long long per = block_range(total, gridDim.x);
+  x0 = per * blockIdx.x;
+  x1 = min(total, x0 + per);
+  if (x0 >= x1) return;
+  long long at = upto - run;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (x0 >= at && x0 < at + mine[i]) sm.first_b = 4 * tid + i, sm.first_x = at;
+    at += mine[i];
+  }
+  __syncthreads();
+
+  BlockWalk<ROWS> walk, ahead;
+  walk.begin(p, x0, x1, sm.first_b, sm.first_x);
+  ahead = walk;
+  BlockSegment as;  // the segment that copies are asked for in, and the team's next tile of it
+  as.k0 = as.k1 = 0;
+  int ai = team, issued = 0, next_id = 0;
+  uint8_t* ring = sm.stage[team * RING];
+  // the team's next tile, if there is one; its block id is on the way when it was
+  // looked at the time before
+  const auto peek = [&]() {
+    while (as.k0 + ai >= as.k1) {
+      if (!ahead.next(p, as)) return false;
+      ai = team;
+    }
+    return true;
+  };
+  bool have = peek();
+  const auto fetch_id = [&]() {
+    if (have) next_id = __ldg(p.t.block_table + (size_t)as.b * G.max_blocks + tile_of(as, as.k0 + ai));
+  };
+  const auto issue = [&]() {  // by the team's first warp: copies of the next tile
+    if (!have) return;
+    const int slot = issued % RING, turn = issued / RING, st = team * RING + slot;
+    if (RT > 1 && turn && !mbar_wait(smem_u32(&sm.empty[st]), (turn - 1) & 1, gave_up)) {
+      have = false;
+      return;
+    }
+    if (lane == 0) {
+      const bool proper = (unsigned)next_id < (unsigned)G.n_blocks;
+      const size_t place = (size_t)(proper ? next_id : 0) * G.Hkv + as.h;
+      const uint32_t bar = smem_u32(&sm.full[st]);
+      sm.meta[st] = proper ? (int)(place * 2 & 15) : -1;
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(kPairBytes + 16) : "memory");
+      bulk_copy(smem_u32(ring + slot * kPairBytes), p.codes + place * kPairBytes, kPairBytes, bar);
+      bulk_copy(smem_u32(sm.scale16[st]), p.scales + (place * 2 & ~(size_t)15), 16, bar);
+    }
+    ++issued;
+    ai += TEAMS;
+    have = peek();
+    fetch_id();
+  };
+  if (rt == 0) {
+    fetch_id();
+    for (int i = 0; i < RING - 1; ++i) issue();
+  }
+
+  int used = 0;  // tiles that the team has consumed
+  BlockSegment s;
+  while (walk.next(p, s)) {
+    // ---- queries: channel 32 tq + 4 s' + {0, 1 | 2, 3} is the product's k = 2 tq + {0, 1 | 8, 9} of step s'
+    uint32_t qa[8][4];
+    float O[8][2][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int see[2];  // last position that the row sees (a row that is not there: q = 0, of no consequence)
+    const bool active = rt * 16 < s.rows;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = rt * 16 + gq + 8 * hf;
+      see[hf] = -1;
+      uint4 v[4] = {};
+      if (r < s.rows) {
+        const int i = (s.r0 + r) / G.g, j = (s.r0 + r) - i * G.g;
+        see[hf] = s.before + i;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)(s.first + i) * G.Hq + s.h * G.g + j) * kHeadDim + 32 * tq);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = __ldg(src + u);
+      }
+      const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        qa[k][hf] = vw[2 * k];
+        qa[k][2 + hf] = vw[2 * k + 1];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) O[c][e >> 2][e & 3] = 0.0f;
+    const int p_lo = s.before + s.r0 / G.g, p_hi = s.before + (s.r0 + s.rows - 1) / G.g;  // positions of the block's rows
+
+    for (int i = s.k0 + team; i < s.k1; i += TEAMS) {
+      if (rt == 0) issue();
+      const int slot = used % RING, st = team * RING + slot;
+      const bool ok = mbar_wait(smem_u32(&sm.full[st]), (used / RING) & 1, gave_up);
+      if (!ok) {  // the rows become NaN, and nothing more is asked for
+        l[0] = l[1] = NAN;
+        have = false;
+      }
+      if (ok && active) {
+        const uint8_t* K = ring + slot * kPairBytes;
+        const uint32_t V = smem_u32(K + kBlockSide);
+        const int meta = sm.meta[st], t0 = tile_of(s, i) * kBlockTokens;
+        const int kb = meta < 0 ? kScaleNaN : sm.scale16[st][meta & 15], vb = meta < 0 ? kScaleNaN : sm.scale16[st][(meta & 15) + 1];
+        const float f = kb == kScaleNaN ? NAN : p.q_scale * __uint_as_float((uint32_t)kb << 23);
+        const float ev = vb == kScaleNaN ? NAN : (float)(vb - kScaleBias);
+        const float inv_v = __uint_as_float((uint32_t)(254 - min(vb, 254)) << 23);
+        float S[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.0f;
+          const uint8_t* row = K + (8 * j + gq) * kHeadDim;
+          uint4 c[2];
+          c[0] = *reinterpret_cast<const uint4*>(row + (((2 * tq) ^ gq) << 4));
+          c[1] = *reinterpret_cast<const uint4*>(row + (((2 * tq + 1) ^ gq) << 4));
+          const uint32_t* cw = reinterpret_cast<const uint32_t*>(c);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t b0, b1;
+            e4m3_halves(cw[k], b0, b1);
+            mma16816(S[j], qa[k], b0, b1);
+          }
+        }
+        // ---- logits in log2 units, less the reference
+        float base[2] = {ev - ref[0], ev - ref[1]};
+        const bool masked = t0 + kBlockTokens - 1 > p_lo || (p.window < kNoWindow && t0 <= p_hi - p.window);
+        uint32_t hide = 0;
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = t0 + 8 * j + 2 * tq + (e & 1), pos = see[e >> 1];
+              const bool vis = t <= pos && (pos - t < p.window || t < p.n_first);
+              hide |= vis ? 0u : 1u << (4 * j + e);
+            }
+        }
+        float z[4][4];
+        bool move = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[j][e] = fmaf(S[j][e], f, base[e >> 1]);
+            if (hide >> (4 * j + e) & 1) z[j][e] = -INFINITY;
+            move |= z[j][e] > kMoveAt;
+          }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float top = -INFINITY, high = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 2 * hf; e < 2 * hf + 2; ++e) {
+                if (!(hide >> (4 * j + e) & 1)) top = fmaxf(top, fmaf(S[j][e], f, ev));
+                high = fmaxf(high, z[j][e]);
+              }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+            }
+            if (high > kMoveAt) {
+              const float to = top - kRoom, a = ex2(ref[hf] - to);
+              ref[hf] = to;
+              l[hf] *= a;
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  O[c][q][2 * hf] *= a;
+                  O[c][q][2 * hf + 1] *= a;
+                }
+            }
+            base[hf] = ev - ref[hf];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!(hide >> (4 * j + e) & 1)) z[j][e] = fmaf(S[j][e], f, base[e >> 1]);
+        }
+        float sum[2] = {0.0f, 0.0f};
+        uint32_t pa[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[j][e] = ex2(z[j][e]);
+            sum[e >> 1] += z[j][e];
+          }
+          pa[j >> 1][2 * (j & 1)] = pack_halves(z[j][0], z[j][1]);
+          pa[j >> 1][2 * (j & 1) + 1] = pack_halves(z[j][2], z[j][3]);
+        }
+        l[0] = fmaf(sum[0], inv_v, l[0]);
+        l[1] = fmaf(sum[1], inv_v, l[1]);
+        // ---- values: a pair of adjacent channels of two tokens per register, sorted by channel
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {
+            uint32_t v[4];
+            const int mt = lane >> 3, tok = 16 * kk + 8 * (mt & 1) + (lane & 7);
+            ldsm4t(v, V + tok * kHeadDim + (((c + (mt >> 1)) ^ (lane & 7)) << 4));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t e0, o0, e1, o1;
+              e4m3_halves(__byte_perm(v[2 * u], 0, 0x3120), e0, o0);
+              e4m3_halves(__byte_perm(v[2 * u + 1], 0, 0x3120), e1, o1);
+              mma16816(O[c + u][0], pa[kk], e0, e1);
+              mma16816(O[c + u][1], pa[kk], o0, o1);
+            }
+          }
+      }
+      ++used;
+      if constexpr (RT > 1) mbar_arrive_warp(smem_u32(&sm.empty[st]));
+      else __syncwarp();
+    }
+
+    // ---- the teams' parts, joined in a fixed order
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], o);
+#pragma unroll
+    for (int half = TEAMS / 2; half >= 1; half >>= 1) {
+      const int to = (team - half) * RT + rt;
+      if (team >= half && team < 2 * half) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            sm.join[to][2 * c + hf][lane] = make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]);
+        if (tq == 0) {
+          sm.join_ml[to][gq] = make_float2(ref[0], l[0]);
+          sm.join_ml[to][gq + 8] = make_float2(ref[1], l[1]);
+        }
+      }
+      __syncthreads();
+      if (team < half) {
+        const int from = team * RT + rt;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float2 o = sm.join_ml[from][gq + 8 * hf];
+          const float to_ref = fmaxf(ref[hf], o.x), zero = to_ref == -INFINITY ? 0.0f : to_ref;
+          const float a = ex2(ref[hf] - zero), b = ex2(o.x - zero);
+          ref[hf] = to_ref;
+          l[hf] = a * l[hf] + b * o.y;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float4 v = sm.join[from][2 * c + hf][lane];
+            O[c][0][2 * hf] = a * O[c][0][2 * hf] + b * v.x;
+            O[c][1][2 * hf] = a * O[c][1][2 * hf] + b * v.y;
+            O[c][0][2 * hf + 1] = a * O[c][0][2 * hf + 1] + b * v.z;
+            O[c][1][2 * hf + 1] = a * O[c][1][2 * hf + 1] + b * v.w;
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    const auto row_out = [&](int r) {  // where row r of the block goes: its row of out
+      const int i = (s.r0 + r) / G.g, j = (s.r0 + r) - i * G.g;
+      return (size_t)(s.first + i) * G.Hq + s.h * G.g + j;
+    };
+    const bool whole = s.x >= x0 && s.x + s.cnt <= x1;
+    const int my_slot = piece_slot(s.x, per, blockIdx.x);
+    if (team == 0) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = rt * 16 + gq + 8 * hf;
+        if (r >= s.rows) continue;
+        if (whole) {
+          const float inv = l[hf] == 0.0f ? 0.0f : 1.0f / l[hf];
+          const size_t row = row_out(r);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 16 * c + 4 * tq) =
+                make_uint2(pack_halves(O[c][0][2 * hf] * inv, O[c][1][2 * hf] * inv), pack_halves(O[c][0][2 * hf + 1] * inv, O[c][1][2 * hf + 1] * inv));
+          if (p.lse && tq == 0) p.lse[row] = l[hf] == 0.0f ? -INFINITY : (ref[hf] + log2f(l[hf])) * 0.6931471805599453f;
+        } else {
+          const size_t at_row = (size_t)my_slot * ROWS + r;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim + 16 * c + 4 * tq),
+                   make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]));
+          if (tq == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(ref[hf], l[hf]));
+        }
+      }
+      if (!whole) __threadfence();
+    }
+    if (!whole) {
+      // pieces of CTAs c0..c1; the last to come joins them
+      const int c0 = (int)(s.x / per), c1 = (int)((s.x + s.cnt - 1) / per);
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned before = atomicAdd(&p.counters[c0], 1u);
+        sm.last = before == (unsigned)(c1 - c0);
+        if (sm.last) p.counters[c0] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (sm.last) {
+        const auto piece = [&](int q, int r) { return (size_t)piece_slot(s.x, per, c0 + q) * ROWS + r; };
+        const int count = c1 - c0 + 1;
+        for (int r = w; r < s.rows; r += kWarps) {
+          float top = -INFINITY;
+          for (int q = lane; q < count; q += 32) top = fmaxf(top, __ldcg(p.part_ml + piece(q, r) * 2));
+          top = warp_max(top);
+          const float zero = top == -INFINITY ? 0.0f : top;
+          float L = 0.0f, acc[4] = {};
+          for (int q0 = 0; q0 < count; q0 += 32) {
+            float e = 0.0f;
+            if (q0 + lane < count) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + piece(q0 + lane, r) * 2));
+              e = ex2(ml.x - zero);
+              L = fmaf(e, ml.y, L);
+            }
+            const int n = min(32, count - q0);
+#pragma unroll 8
+            for (int q = 0; q < n; ++q) {
+              const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_acc + piece(q0 + q, r) * kHeadDim) + lane);
+              const float eq = __shfl_sync(0xffffffffu, e, q);
+              acc[0] = fmaf(eq, a.x, acc[0]);
+              acc[1] = fmaf(eq, a.y, acc[1]);
+              acc[2] = fmaf(eq, a.z, acc[2]);
+              acc[3] = fmaf(eq, a.w, acc[3]);
+            }
+          }
+          L = warp_sum(L);
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          const size_t row = row_out(r);
+          *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) =
+              make_uint2(pack_halves(acc[0] * inv, acc[1] * inv), pack_halves(acc[2] * inv, acc[3] * inv));
+          if (p.lse && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
+        }
+      }
+    }
+  }
+  // copies in flight end before the CTA does (all were waited for, unless a wait ran out)
+  if (rt == 0 && *gave_up)
+    for (int i = max(0, issued - RING); i < issued; ++i) mbar_wait(smem_u32(&sm.full[team * RING + i % RING]), (i / RING) & 1, nullptr);
+}
+
+template <int RT>
+cudaError_t launch_rows(const BlockAttnParams& p, int sms, cudaStream_t st) {
+  static std::atomic<long long> memo[kMemoDevices];
+  const cudaError_t e = ensure_smem_limit(block_attn_kernel<RT>, memo, (int)sizeof(AttnSmem));
+  if (e != cudaSuccess) return e;
+  return launch_dependent(block_attn_kernel<RT>, dim3(sms), dim3(kThreadsAttn), sizeof(AttnSmem), st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_block_attn(const BlockAttnParams& p, int sms, int rows, cudaStream_t st) {
+  return rows == 16 ? launch_rows<1>(p, sms, st) : rows == 32 ? launch_rows<2>(p, sms, st) : launch_rows<4>(p, sms, st);
+}
+
+}  // namespace kvq

@@ -639,14 +639,6 @@ static void spec_blocks(int64_t rows, int* rblk, int* sub, int* rstride) {
   *rstride = (int)(rows <= 16 ? 16 : rows < 128 ? (rows + 15) / 16 * 16 : 128);
 }
 
-// RoPE frequencies, turns per position as 64-bit fractions.
-static void spec_rope(float base, unsigned long long* freq) {
-  for (int i = 0; i < kHeadDim / 2; ++i) {
-    const double turns = std::pow((double)base, -2.0 * i / (double)kHeadDim) * 0.15915494309189533576888376337251;
-    freq[i] = (unsigned long long)std::ldexp(turns - std::floor(turns), 64);  // (1 - 2^-53) 2^64 at most
-  }
-}
-
 static kvq_status tree_rows(const kvq_config* cfg, const Geometry& g, const int32_t* tokens, const int32_t* nodes,
                             int32_t n_nodes) {
   if (n_nodes < 1) return KVQ_ERR_INVALID_ARG;
@@ -723,7 +715,7 @@ kvq_status kvq_tree_attn(const kvq_config* cfg, const void* layer_buf, const int
     p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
     p.v_lut_off[i] = cfg->v_lut[i] - cfg->v_lut[0];
   }
-  if (g.pre_rope) spec_rope(cfg->rope_theta, p.freq);
+  if (g.pre_rope) rope_turns(cfg->rope_theta, p.freq);
   int64_t total = 0, pairs = 0;
   bool any = false;
   for (int b = 0; b < g.B; ++b) {
@@ -777,7 +769,7 @@ kvq_status kvq_attn_mass(const kvq_config* cfg, const void* layer_buf, const int
   p.decay = decay;
   p.q_scale = cfg->softmax_scale > 0.0f ? cfg->softmax_scale : (float)(1.0 / std::sqrt((double)kHeadDim));
   for (int i = 0; i < 8; ++i) p.k_lut_off[i] = cfg->k_lut[i] - cfg->k_lut[0];
-  if (g.pre_rope) spec_rope(cfg->rope_theta, p.freq);
+  if (g.pre_rope) rope_turns(cfg->rope_theta, p.freq);
   int64_t total = 0;
   for (int b = 0; b < g.B; ++b) {
     if (tokens[b] < 0) return KVQ_ERR_INVALID_ARG;

@@ -495,6 +495,21 @@ __host__ __device__ inline float anchor_turns(const float4& v, float c0, int g) 
   return t - floorf(t);
 }
 
+// RoPE frequencies, turns per position as 64-bit fractions.  (The last base's
+// are remembered: 64 powers cost more than the rest of a short call's checks.)
+inline void rope_turns(float base, unsigned long long* freq) {
+  thread_local float of = 0.0f;
+  thread_local unsigned long long turns64[kHeadDim / 2];
+  if (of != base) {
+    for (int i = 0; i < kHeadDim / 2; ++i) {
+      const double turns = std::pow((double)base, -2.0 * i / (double)kHeadDim) * 0.15915494309189533576888376337251;
+      turns64[i] = (unsigned long long)std::ldexp(turns - std::floor(turns), 64);  // (1 - 2^-53) 2^64 at most
+    }
+    of = base;
+  }
+  for (int i = 0; i < kHeadDim / 2; ++i) freq[i] = turns64[i];
+}
+
 // ------------------------------------------------ dependent launch (PDL)
 // Kernels launched with launch_dependent() may start while the previous
 // kernel in the stream is still running (their CTAs set up shared memory and

@@ -594,6 +594,142 @@ KVQ_API kvq_status kvq_evict(const kvq_config *cfg, void *layer_buf, const int32
  * as kvq_evict. */
 KVQ_API kvq_status kvq_evict_workspace(const kvq_config *cfg, uint64_t *bytes);
 
+/* A cache in blocks: requests of a serving batch share one pool of blocks of 32
+ * tokens, and everything that a step depends on -- lengths, block tables, new
+ * tokens -- stays on the GPU, so that a captured step can be replayed while
+ * requests grow, end and start.  Per step: kvq_block_plan once, then
+ * kvq_block_append and kvq_block_attn in every layer (the layers share the
+ * tables; each has its own codes and scales).
+ *
+ * Keys (after norm and rotation) and values are held as e4m3 bytes with one
+ * power-of-two scale (E8M0) for each block of 32 tokens, KV head and side: a
+ * token costs 256 bytes per KV head.  Keys have channels that stand out; of the
+ * 8-bit forms that share one scale between 32 tokens and 128 channels e4m3 keeps
+ * four significant bits over 15 octaves below the block's maximum, where an
+ * integer code's step would be set by the largest channel.  A scale that is a
+ * power of two grows by moving exponents, so a block that gains a larger token
+ * keeps its earlier codes' values (but for those that fall below 2^-6 of the
+ * scale, which are rounded again).
+ *
+ *   codes   [n_blocks][n_kv_heads][2][32][128] u8: K then V of a block and head;
+ *           the 16-byte chunk c of token t's row lies at chunk c ^ (t % 8)
+ *   scales  [n_blocks][n_kv_heads][2] u8: byte s is the factor 2^(s - 127); 255
+ *           marks a block and side that holds a token with an infinity or a NaN
+ *           and reads as NaN as a whole.  The region is padded to 16 bytes.
+ * The caller zero-fills both once.  A block belongs to one request. */
+typedef struct kvq_block_config {
+    int32_t batch;            /* requests of a step, 1..1024 (slots of the tables) */
+    int32_t n_tokens;         /* token slots of a step: rows of q, k, v, q_out, out;
+                                 1..2^20                                       */
+    int32_t n_q_heads;        /* Hq, a multiple of n_kv_heads                  */
+    int32_t n_kv_heads;       /* Hkv, 1..1024                                  */
+    int32_t head_dim;         /* 128                                           */
+    int32_t n_blocks;         /* blocks of the pool, 1..2^26                   */
+    int32_t max_blocks;       /* blocks of one request at most: the row length of
+                                 block_table, 1..2^25                          */
+    int32_t window;           /* attention: a token sees the last `window` tokens
+                                 (itself among them); 0: all                   */
+    int32_t n_first;          /* attention with a window: the first n_first tokens
+                                 stay visible                                  */
+    float softmax_scale;      /* 0 selects 1/sqrt(d)                           */
+    float rope_theta;         /* append: rotation of the pairs (i, i + d/2) by
+                                 position * theta^(-2i/d); 0: not rotated      */
+    float norm_eps;           /* append: x / sqrt(mean(x^2) + norm_eps) * weight */
+} kvq_block_config;
+
+/* Device arrays that the layers of a model share.  int32, 4-byte aligned. */
+typedef struct kvq_block_tables {
+    int32_t *block_table;     /* [batch][max_blocks]: a request's blocks in order */
+    int32_t *free_list;       /* [n_blocks]: a stack of the free blocks' ids    */
+    int32_t *free_count;      /* [1]: entries of the stack                      */
+    int32_t *lens;            /* [batch]: tokens held, this step's included     */
+    int32_t *start;           /* [batch + 1]: first of a request's token slots;
+                                 the last: slots in use                        */
+    int32_t *unit0;           /* [batch + 1]: sums of the blocks that receive
+                                 tokens in this step                           */
+    int32_t *token_row;       /* [n_tokens]: request of a token slot, -1: unused */
+    int32_t *position;        /* [n_tokens]: position in its request (unused: 0) */
+    int32_t *slot;            /* [n_tokens]: block * 32 + position % 32 (unused: -1) */
+} kvq_block_tables;
+
+typedef struct kvq_block_layout {
+    uint64_t codes_bytes;     /* of one layer                                   */
+    uint64_t scales_bytes;    /* of one layer, padded                           */
+    uint64_t workspace_bytes; /* kvq_block_attn's scratch on any GPU of up to 256 SMs */
+} kvq_block_layout;
+
+/* kvq_block_layout_query -- host only.  Errors: KVQ_ERR_INVALID_ARG,
+ * KVQ_ERR_UNSUPPORTED (head_dim, sizes past those above). */
+KVQ_API kvq_status kvq_block_layout_query(const kvq_block_config *cfg, kvq_block_layout *out);
+
+/* kvq_block_plan -- a step's tables from the requests' lengths.
+ *   lens_before  device [batch]: tokens held before the step (tables->lens: in
+ *                place)
+ *   free_before  device [1]: entries of the free stack before the step
+ *                (tables->free_count: in place)
+ *   n_new        device [batch]: tokens that the request adds (0: none); negative:
+ *                the request ends, its length becomes 0 and its blocks go back to
+ *                the stack, requests in order, a request's blocks in order
+ * A request is served when its tokens fit its table row, when it needs no new
+ * block or the blocks needed by it and the requests before it that fit their
+ * rows are there (blocks that go back in this step count), and when their token
+ * slots are there; otherwise it keeps its length and gets no token
+ * (start[b + 1] == start[b]).  New blocks come from the top of the stack, in the
+ * order of requests and positions; what was popped stays in free_list above
+ * free_count.  Lengths outside [0, 32 max_blocks] are served nothing.  Entries of
+ * block_table behind a request's blocks are left as they are.  With lens_before
+ * and free_before apart from the tables the call can be repeated.
+ * One launch.  Errors: KVQ_ERR_INVALID_ARG (null, misaligned),
+ * KVQ_ERR_UNSUPPORTED, KVQ_ERR_CUDA. */
+KVQ_API kvq_status kvq_block_plan(const kvq_block_config *cfg, const kvq_block_tables *tables,
+                          const int32_t *lens_before, const int32_t *free_before, const int32_t *n_new,
+                          kvq_stream_t stream);
+
+/* kvq_block_append -- the planned step's keys and values into the blocks, and the
+ * queries made ready, in one pass: norm per head, rotation, 8-bit store.
+ *   k, v      device fp16, token slot i's rows at k + i * k_stride (elements):
+ *             [n_kv_heads][128]; a stride over more than the heads lets them lie
+ *             in one projection's rows.  Pointers 16-byte aligned, strides
+ *             multiples of 8
+ *   q, q_out  device fp16, q as k with n_q_heads; q_out [n_tokens][n_q_heads][128]
+ *             dense, q itself or apart from it; both NULL: keys and values alone
+ *   q_weight, k_weight  device fp16 [128], 16-byte aligned, or NULL: no norm
+ * A key or query x becomes x / sqrt(mean(x^2) + norm_eps) * weight (with a weight),
+ * then its pairs (i, i + 64) are rotated (with a rope_theta), in fp32; q_out is
+ * rounded once.  The scale of a block, head and side is the least 2^e, -40 <= e
+ * <= 40, with max |x| <= 448 2^e over its tokens, and no smaller than it was for
+ * the tokens held before; their codes are moved to it.  Codes are the e4m3 values nearest
+ * to x 2^-e, ties to even; they are always finite (see scales).  Token slots not in
+ * use are not read, and their q_out is left as it is.  Tables with ids or lengths
+ * out of range have those tokens left out.  One launch.
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_CUDA. */
+KVQ_API kvq_status kvq_block_append(const kvq_block_config *cfg, const kvq_block_tables *tables, uint8_t *codes,
+                            uint8_t *scales, const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                            const uint16_t *q, int64_t q_stride, uint16_t *q_out, const uint16_t *q_weight,
+                            const uint16_t *k_weight, kvq_stream_t stream);
+
+/* kvq_block_attn -- attention of the step's tokens over their requests' blocks.
+ * The token at position p sees position t when t <= p and (p - t < window, or
+ * t < n_first); without a window, every t <= p.
+ *   q          device fp16 [n_tokens][n_q_heads][128] (kvq_block_append's q_out)
+ *   out        device fp16, same shape; rows of token slots not in use stay as
+ *              they are
+ *   lse        device f32 [n_tokens][n_q_heads] natural-log log-sum-exp, or NULL
+ *   workspace  device scratch of >= workspace_bytes, 16-byte aligned, zero before
+ *              its first call; every call leaves its counters zero.  Calls that
+ *              share it must not overlap on the GPU.
+ * Any number of new tokens per request (with a chain of drafted tokens, all are
+ * appended first); made for few: 64 (token, query head) rows of a KV head
+ * read its blocks together, more rows read them again.  Logits, maxima and sums are fp32, weights enter the
+ * product as fp16 with 12 octaves of room above 1.  A block id that is not of the pool
+ * reads as NaN.  The result does not depend on timing.  One launch; its waits
+ * are bounded: should one run out (some 15 s), the rows it was for become NaN.
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_WORKSPACE,
+ * KVQ_ERR_CUDA. */
+KVQ_API kvq_status kvq_block_attn(const kvq_block_config *cfg, const kvq_block_tables *tables, const uint8_t *codes,
+                          const uint8_t *scales, const uint16_t *q, uint16_t *out, float *lse, void *workspace,
+                          uint64_t ws_bytes, kvq_stream_t stream);
+
 /* Static string naming a status code. */
 KVQ_API const char *kvq_status_string(kvq_status status);
 
