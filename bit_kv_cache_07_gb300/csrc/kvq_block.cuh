@@ -126,6 +126,8 @@ __host__ __device__ inline BlockRequest request_at(const BlockAttnParams& p, int
 #endif
 }
 
+constexpr int kSoloTiles = 2;
+
 // One segment: tiles k0..k1 of a (request, head, row block).
 struct BlockSegment {
   int b, h, first, before, n;  // request
@@ -133,6 +135,12 @@ struct BlockSegment {
   int k0, k1, ns, lo;          // its visible tiles in the CTA's range (k1 <= the block's own count)
   long long x;                 // where the (request, head, row block) begins
   int cnt;                     // and its tiles in the schedule
+
+  // Whether the range [x0, x1) holds all of it.
+  __host__ __device__ bool whole(long long x0, long long x1) const { return x >= x0 && x + cnt <= x1; }
+  // Whether one team takes it by itself (such segments go round the teams): what
+  // joining the teams' parts costs is worth a few tiles.
+  __host__ __device__ bool solo(long long x0, long long x1, int teams) const { return cnt <= kSoloTiles * teams && whole(x0, x1); }
 };
 
 template <int ROWS>

@@ -48,7 +48,9 @@ struct AttnSmem {
   int meta[kStages];           // byte of scale16 where the tile's scales are; -1: no such block
   long long warp_sum[kWarps];
   long long first_x;           // the range's first request: where it begins
-  int first_b, gave_up, last;
+  BlockSegment parted[2];
+  int last[2];
+  int first_b, gave_up;
 };
 static_assert(sizeof(AttnSmem) <= 227 * 1024, "shared memory");
 
@@ -60,6 +62,12 @@ __device__ __forceinline__ void e4m3_halves(uint32_t four, uint32_t& lo, uint32_
 __device__ __forceinline__ uint32_t pack_halves(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Row of q and out of row r of a segment's block.
+__device__ __forceinline__ size_t row_at(const BlockAttnParams& p, const BlockSegment& s, int r) {
+  const int i = (s.r0 + r) / p.geo.g, j = (s.r0 + r) - i * p.geo.g;
+  return (size_t)(s.first + i) * p.geo.Hq + s.h * p.geo.g + j;
 }
 
 // RT: 16-row tiles that read a KV head's blocks together
@@ -80,18 +88,19 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   grid_dep_wait();
 
-  // the schedule: tiles of four requests per thread, their sums, the CTA's range
-  long long mine[4], run = 0, total, x0, x1;
+  // the schedule: the requests' tiles, their sums, the CTA's range and the
+  // request that it begins in
+  const auto tiles_of = [&](int b) -> long long {
+    if (b >= G.B) return 0;
+    int nrb, streams, cnt;
+    BlockWalk<ROWS>::size(p, request_at(p, b), &nrb, &streams, &cnt);
+    return (long long)streams * cnt;
+  };
+  const int turns = (G.B + kThreadsAttn - 1) / kThreadsAttn;  // consecutive requests per thread
+  long long mine[kMaxBlockBatch / kThreadsAttn], run = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = 4 * tid + i;
-    mine[i] = 0;
-    if (b < G.B) {
-      const BlockRequest r = request_at(p, b);
-      int nrb, streams, cnt;
-      BlockWalk<ROWS>::size(p, r, &nrb, &streams, &cnt);
-      mine[i] = (long long)streams * cnt;
-    }
+  for (int i = 0; i < kMaxBlockBatch / kThreadsAttn; ++i) {
+    mine[i] = i < turns ? tiles_of(tid * turns + i) : 0;
     run += mine[i];
   }
   long long upto = run;
@@ -102,19 +111,18 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   }
   if (lane == 31) sm.warp_sum[w] = upto;
   __syncthreads();
-  total = 0;
+  long long total = 0;
+#pragma unroll
   for (int i = 0; i < kWarps; ++i) {
     if (i < w) upto += sm.warp_sum[i];
     total += sm.warp_sum[i];
   }
-  const long long per = block_range(total, gridDim.x);
-  x0 = per * blockIdx.x;
-  x1 = min(total, x0 + per);
+  const long long per = block_range(total, gridDim.x), x0 = per * blockIdx.x, x1 = min(total, x0 + per);
   if (x0 >= x1) return;
   long long at = upto - run;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (x0 >= at && x0 < at + mine[i]) sm.first_b = 4 * tid + i, sm.first_x = at;
+  for (int i = 0; i < kMaxBlockBatch / kThreadsAttn; ++i) {
+    if (x0 >= at && x0 < at + mine[i]) sm.first_b = tid * turns + i, sm.first_x = at;
     at += mine[i];
   }
   __syncthreads();
@@ -122,33 +130,39 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   BlockWalk<ROWS> walk, ahead;
   walk.begin(p, x0, x1, sm.first_b, sm.first_x);
   ahead = walk;
-  BlockSegment as;  // the segment that copies are asked for in, and the team's next tile of it
-  as.k0 = as.k1 = 0;
-  int ai = team, issued = 0, next_id = 0;
-  uint8_t* ring = sm.stage[team * RING];
-  // the team's next tile, if there is one; its block id is on the way when it was
-  // looked at the time before
-  const auto peek = [&]() {
-    while (as.k0 + ai >= as.k1) {
-      if (!ahead.next(p, as)) return false;
-      ai = team;
+  uint8_t* const ring = sm.stage[team * RING];
+  // The segment that copies are asked for in, the team's next tile of it, and the
+  // block ids of 32 of its tiles, one per lane.
+  BlockSegment as = {};
+  int ai = 0, step = TEAMS, solos_ahead = 0, issued = 0, id_at = 0, ids = 0;
+  bool have = rt == 0;
+  const auto look_up = [&]() {  // by the team's first warp
+    const int k = ai + lane * step;
+    ids = k < as.k1 ? __ldg(p.t.block_table + (size_t)as.b * G.max_blocks + tile_of(as, k)) : 0;
+    id_at = 0;
+  };
+  const auto find = [&]() {  // the team's next tile, if there is one
+    if (ai < as.k1 && id_at < 32) return;
+    while (ai >= as.k1) {
+      do {
+        if (!(have = ahead.next(p, as))) return;
+      } while (as.solo(x0, x1, TEAMS) && solos_ahead++ % TEAMS != team);
+      step = as.solo(x0, x1, TEAMS) ? 1 : TEAMS;
+      ai = as.k0 + (step == 1 ? 0 : team);
     }
-    return true;
+    look_up();
   };
-  bool have = peek();
-  const auto fetch_id = [&]() {
-    if (have) next_id = __ldg(p.t.block_table + (size_t)as.b * G.max_blocks + tile_of(as, as.k0 + ai));
-  };
-  const auto issue = [&]() {  // by the team's first warp: copies of the next tile
+  const auto issue = [&]() {  // copies of the next tile
     if (!have) return;
     const int slot = issued % RING, turn = issued / RING, st = team * RING + slot;
     if (RT > 1 && turn && !mbar_wait(smem_u32(&sm.empty[st]), (turn - 1) & 1, gave_up)) {
       have = false;
       return;
     }
+    const int id = __shfl_sync(0xffffffffu, ids, id_at);
     if (lane == 0) {
-      const bool proper = (unsigned)next_id < (unsigned)G.n_blocks;
-      const size_t place = (size_t)(proper ? next_id : 0) * G.Hkv + as.h;
+      const bool proper = (unsigned)id < (unsigned)G.n_blocks;
+      const size_t place = (size_t)(proper ? id : 0) * G.Hkv + as.h;
       const uint32_t bar = smem_u32(&sm.full[st]);
       sm.meta[st] = proper ? (int)(place * 2 & 15) : -1;
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(kPairBytes + 16) : "memory");
@@ -156,32 +170,27 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
       bulk_copy(smem_u32(sm.scale16[st]), p.scales + (place * 2 & ~(size_t)15), 16, bar);
     }
     ++issued;
-    ai += TEAMS;
-    have = peek();
-    fetch_id();
+    ++id_at;
+    ai += step;
+    find();
   };
   if (rt == 0) {
-    fetch_id();
+    find();
     for (int i = 0; i < RING - 1; ++i) issue();
   }
 
   int used = 0;  // tiles that the team has consumed
-  BlockSegment s;
-  while (walk.next(p, s)) {
-    // ---- queries: channel 32 tq + 4 s' + {0, 1 | 2, 3} is the product's k = 2 tq + {0, 1 | 8, 9} of step s'
-    uint32_t qa[8][4];
-    float O[8][2][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    int see[2];  // last position that the row sees (a row that is not there: q = 0, of no consequence)
-    const bool active = rt * 16 < s.rows;
+  int solos = 0;
+  // Queries of a segment: channel 32 tq + 4 k + {0, 1 | 2, 3} enters step k of the
+  // product as its row 2 tq + {0, 1 | 8, 9}.
+  uint32_t qa[8][4];
+  const auto load_q = [&](const BlockSegment& s) {
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       const int r = rt * 16 + gq + 8 * hf;
-      see[hf] = -1;
       uint4 v[4] = {};
       if (r < s.rows) {
-        const int i = (s.r0 + r) / G.g, j = (s.r0 + r) - i * G.g;
-        see[hf] = s.before + i;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)(s.first + i) * G.Hq + s.h * G.g + j) * kHeadDim + 32 * tq);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(p, s, r) * kHeadDim + 32 * tq);
 #pragma unroll
         for (int u = 0; u < 4; ++u) v[u] = __ldg(src + u);
       }
@@ -192,13 +201,33 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
         qa[k][2 + hf] = vw[2 * k + 1];
       }
     }
+  };
+  // the next segment that the team has a part in; its queries are on the way
+  const auto next_segment = [&](BlockSegment& s) {
+    do {
+      if (!walk.next(p, s)) return false;
+    } while (s.solo(x0, x1, TEAMS) && solos++ % TEAMS != team);
+    load_q(s);
+    return true;
+  };
+  BlockSegment s;
+  int parts = 0;  // 1: the range begins, 2: it ends within a (request, head, row block)
+  bool more = next_segment(s);
+  while (more) {
+    const bool solo = s.solo(x0, x1, TEAMS);
+    const int tile_step = solo ? 1 : TEAMS;
+    const int seg_rows = min(16, s.rows - rt * 16);  // of this warp; may be none
+    float O[8][2][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    // last position that a row sees (rows that are not there: q = 0, of no consequence)
+    const int see[2] = {s.before + (s.r0 + rt * 16 + gq) / G.g, s.before + (s.r0 + rt * 16 + gq + 8) / G.g};
+    const bool active = seg_rows > 0;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
 #pragma unroll
       for (int e = 0; e < 8; ++e) O[c][e >> 2][e & 3] = 0.0f;
     const int p_lo = s.before + s.r0 / G.g, p_hi = s.before + (s.r0 + s.rows - 1) / G.g;  // positions of the block's rows
 
-    for (int i = s.k0 + team; i < s.k1; i += TEAMS) {
+    for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
       if (rt == 0) issue();
       const int slot = used % RING, st = team * RING + slot;
       const bool ok = mbar_wait(smem_u32(&sm.full[st]), (used / RING) & 1, gave_up);
@@ -327,69 +356,68 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
       else __syncwarp();
     }
 
+    const BlockSegment done = s;
+    more = next_segment(s);
     // ---- the teams' parts, joined in a fixed order
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], o);
+    if (!solo) {
 #pragma unroll
-    for (int half = TEAMS / 2; half >= 1; half >>= 1) {
-      const int to = (team - half) * RT + rt;
-      if (team >= half && team < 2 * half) {
+      for (int half = TEAMS / 2; half >= 1; half >>= 1) {
+        const int to = (team - half) * RT + rt;
+        if (team >= half && team < 2 * half) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+          for (int hf = 0; hf < 2; ++hf) {
+            if (8 * hf >= seg_rows) break;
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            sm.join[to][2 * c + hf][lane] = make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]);
-        if (tq == 0) {
-          sm.join_ml[to][gq] = make_float2(ref[0], l[0]);
-          sm.join_ml[to][gq + 8] = make_float2(ref[1], l[1]);
-        }
-      }
-      __syncthreads();
-      if (team < half) {
-        const int from = team * RT + rt;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float2 o = sm.join_ml[from][gq + 8 * hf];
-          const float to_ref = fmaxf(ref[hf], o.x), zero = to_ref == -INFINITY ? 0.0f : to_ref;
-          const float a = ex2(ref[hf] - zero), b = ex2(o.x - zero);
-          ref[hf] = to_ref;
-          l[hf] = a * l[hf] + b * o.y;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float4 v = sm.join[from][2 * c + hf][lane];
-            O[c][0][2 * hf] = a * O[c][0][2 * hf] + b * v.x;
-            O[c][1][2 * hf] = a * O[c][1][2 * hf] + b * v.y;
-            O[c][0][2 * hf + 1] = a * O[c][0][2 * hf + 1] + b * v.z;
-            O[c][1][2 * hf + 1] = a * O[c][1][2 * hf + 1] + b * v.w;
+            for (int c = 0; c < 8; ++c)
+              sm.join[to][2 * c + hf][lane] = make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]);
+            if (tq == 0) sm.join_ml[to][gq + 8 * hf] = make_float2(ref[hf], l[hf]);
           }
         }
+        __syncthreads();
+        if (team < half) {
+          const int from = team * RT + rt;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            if (8 * hf >= seg_rows) break;
+            const float2 o = sm.join_ml[from][gq + 8 * hf];
+            const float to_ref = fmaxf(ref[hf], o.x), zero = to_ref == -INFINITY ? 0.0f : to_ref;
+            const float a = ex2(ref[hf] - zero), b = ex2(o.x - zero);
+            ref[hf] = to_ref;
+            l[hf] = a * l[hf] + b * o.y;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 v = sm.join[from][2 * c + hf][lane];
+              O[c][0][2 * hf] = a * O[c][0][2 * hf] + b * v.x;
+              O[c][1][2 * hf] = a * O[c][1][2 * hf] + b * v.y;
+              O[c][0][2 * hf + 1] = a * O[c][0][2 * hf + 1] + b * v.z;
+              O[c][1][2 * hf + 1] = a * O[c][1][2 * hf + 1] + b * v.w;
+            }
+          }
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
 
-    const auto row_out = [&](int r) {  // where row r of the block goes: its row of out
-      const int i = (s.r0 + r) / G.g, j = (s.r0 + r) - i * G.g;
-      return (size_t)(s.first + i) * G.Hq + s.h * G.g + j;
-    };
-    const bool whole = s.x >= x0 && s.x + s.cnt <= x1;
-    const int my_slot = piece_slot(s.x, per, blockIdx.x);
-    if (team == 0) {
+    const bool whole = done.whole(x0, x1);
+    if (solo || team == 0) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int r = rt * 16 + gq + 8 * hf;
-        if (r >= s.rows) continue;
+        if (r >= done.rows) continue;
         if (whole) {
           const float inv = l[hf] == 0.0f ? 0.0f : 1.0f / l[hf];
-          const size_t row = row_out(r);
+          const size_t row = row_at(p, done, r);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 16 * c + 4 * tq) =
                 make_uint2(pack_halves(O[c][0][2 * hf] * inv, O[c][1][2 * hf] * inv), pack_halves(O[c][0][2 * hf + 1] * inv, O[c][1][2 * hf + 1] * inv));
           if (p.lse && tq == 0) p.lse[row] = l[hf] == 0.0f ? -INFINITY : (ref[hf] + log2f(l[hf])) * 0.6931471805599453f;
         } else {
-          const size_t at_row = (size_t)my_slot * ROWS + r;
+          const size_t at_row = (size_t)piece_slot(done.x, per, blockIdx.x) * ROWS + r;
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim + 16 * c + 4 * tq),
@@ -397,53 +425,63 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
           if (tq == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(ref[hf], l[hf]));
         }
       }
-      if (!whole) __threadfence();
     }
-    if (!whole) {
-      // pieces of CTAs c0..c1; the last to come joins them
-      const int c0 = (int)(s.x / per), c1 = (int)((s.x + s.cnt - 1) / per);
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned before = atomicAdd(&p.counters[c0], 1u);
-        sm.last = before == (unsigned)(c1 - c0);
-        if (sm.last) p.counters[c0] = 0;
-        __threadfence();
-      }
-      __syncthreads();
-      if (sm.last) {
-        const auto piece = [&](int q, int r) { return (size_t)piece_slot(s.x, per, c0 + q) * ROWS + r; };
-        const int count = c1 - c0 + 1;
-        for (int r = w; r < s.rows; r += kWarps) {
-          float top = -INFINITY;
-          for (int q = lane; q < count; q += 32) top = fmaxf(top, __ldcg(p.part_ml + piece(q, r) * 2));
-          top = warp_max(top);
-          const float zero = top == -INFINITY ? 0.0f : top;
-          float L = 0.0f, acc[4] = {};
-          for (int q0 = 0; q0 < count; q0 += 32) {
-            float e = 0.0f;
-            if (q0 + lane < count) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + piece(q0 + lane, r) * 2));
-              e = ex2(ml.x - zero);
-              L = fmaf(e, ml.y, L);
-            }
-            const int n = min(32, count - q0);
-#pragma unroll 8
-            for (int q = 0; q < n; ++q) {
-              const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_acc + piece(q0 + q, r) * kHeadDim) + lane);
-              const float eq = __shfl_sync(0xffffffffu, e, q);
-              acc[0] = fmaf(eq, a.x, acc[0]);
-              acc[1] = fmaf(eq, a.y, acc[1]);
-              acc[2] = fmaf(eq, a.z, acc[2]);
-              acc[3] = fmaf(eq, a.w, acc[3]);
-            }
+    if (!whole) {  // its turn comes at the range's end
+      if (tid == 0) sm.parted[done.x >= x0 ? 1 : 0] = done;
+      parts |= done.x >= x0 ? 2 : 1;
+    }
+  }
+
+  // ---- what spans CTAs (the range's first and last segment): the last CTA to come joins the parts
+  if (parts) {
+    __threadfence();
+    __syncthreads();
+    if (tid < 2 && (parts >> tid & 1)) {
+      const BlockSegment& d = sm.parted[tid];
+      const int c0 = (int)(d.x / per), c1 = (int)((d.x + d.cnt - 1) / per);
+      __threadfence();
+      const unsigned before = atomicAdd(&p.counters[c0], 1u);
+      sm.last[tid] = before == (unsigned)(c1 - c0) ? c1 - c0 + 1 : 0;
+      if (sm.last[tid]) p.counters[c0] = 0;
+      __threadfence();
+    }
+    __syncthreads();
+    for (int side = 0; side < 2; ++side) {
+      const int count = parts >> side & 1 ? sm.last[side] : 0;
+      if (!count) continue;
+      const BlockSegment& d = sm.parted[side];
+      const int c0 = (int)(d.x / per);
+      const auto piece = [&](int q, int r) { return (size_t)piece_slot(d.x, per, c0 + q) * ROWS + r; };
+      for (int r = w; r < d.rows; r += kWarps) {
+        float top = -INFINITY;
+        for (int q = lane; q < count; q += 32) top = fmaxf(top, __ldcg(p.part_ml + piece(q, r) * 2));
+        top = warp_max(top);
+        const float zero = top == -INFINITY ? 0.0f : top;
+        float L = 0.0f, acc[4] = {};
+        for (int q0 = 0; q0 < count; q0 += 32) {
+          float e = 0.0f;
+          if (q0 + lane < count) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + piece(q0 + lane, r) * 2));
+            e = ex2(ml.x - zero);
+            L = fmaf(e, ml.y, L);
           }
-          L = warp_sum(L);
-          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          const size_t row = row_out(r);
-          *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) =
-              make_uint2(pack_halves(acc[0] * inv, acc[1] * inv), pack_halves(acc[2] * inv, acc[3] * inv));
-          if (p.lse && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
+          const int n = min(32, count - q0);
+#pragma unroll 8
+          for (int q = 0; q < n; ++q) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_acc + piece(q0 + q, r) * kHeadDim) + lane);
+            const float eq = __shfl_sync(0xffffffffu, e, q);
+            acc[0] = fmaf(eq, a.x, acc[0]);
+            acc[1] = fmaf(eq, a.y, acc[1]);
+            acc[2] = fmaf(eq, a.z, acc[2]);
+            acc[3] = fmaf(eq, a.w, acc[3]);
+          }
         }
+        L = warp_sum(L);
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const size_t row = row_at(p, d, r);
+        *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) =
+            make_uint2(pack_halves(acc[0] * inv, acc[1] * inv), pack_halves(acc[2] * inv, acc[3] * inv));
+        if (p.lse && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
       }
     }
   }
