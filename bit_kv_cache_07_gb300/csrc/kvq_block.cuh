@@ -66,6 +66,7 @@ struct BlockAttnParams {
   float* part_acc;     // [2 CTAs][rows][128]
   float q_scale;       // softmax_scale * log2(e)
   int window, n_first; // window: kNoWindow or 1..
+  unsigned g_inv;      // ceil(2^32 / g), g > 1
 };
 constexpr int kNoWindow = 1 << 30;
 constexpr int kMaxBlockCtas = 256;
@@ -110,7 +111,7 @@ __host__ __device__ inline int block_tiles_max(int window, int n_first, const Bl
 constexpr int kBlockWarps = 8;
 // A CTA's range: at least a tile for each of its warps.
 __host__ __device__ inline long long block_range(long long total, int ctas) {
-  const long long per = (total + ctas - 1) / ctas;
+  const long long per = udiv(total + ctas - 1, ctas);
   return per < kBlockWarps ? kBlockWarps : per;
 }
 // Where CTA c leaves its part of what begins at x and spans CTAs: a CTA has at
@@ -126,7 +127,11 @@ __host__ __device__ inline BlockRequest request_at(const BlockAttnParams& p, int
 #endif
 }
 
-constexpr int kSoloTiles = 2;
+// What a (request, head, row block) costs beyond its tiles, in tiles: the teams'
+// parts are joined (some 2 us, of 0.2 us a tile), or one team takes it alone and
+// the others go on.
+constexpr int kSoloTiles = 8;
+constexpr int kJoinTiles = 8;
 
 // One segment: tiles k0..k1 of a (request, head, row block).
 struct BlockSegment {
@@ -134,20 +139,22 @@ struct BlockSegment {
   int r0, rows;                // rows of the block
   int k0, k1, ns, lo;          // its visible tiles in the CTA's range (k1 <= the block's own count)
   long long x;                 // where the (request, head, row block) begins
-  int cnt;                     // and its tiles in the schedule
+  int cnt;                     // and its own count of tiles
 
   // Whether the range [x0, x1) holds all of it.
   __host__ __device__ bool whole(long long x0, long long x1) const { return x >= x0 && x + cnt <= x1; }
-  // Whether one team takes it by itself (such segments go round the teams): what
-  // joining the teams' parts costs is worth a few tiles.
-  __host__ __device__ bool solo(long long x0, long long x1, int teams) const { return cnt <= kSoloTiles * teams && whole(x0, x1); }
+  // Whether one of the CTA's teams takes it by itself, with nothing to join: it is
+  // short, and the range holds enough of its like for the other teams.
+  __host__ __device__ bool solo(long long x0, long long x1, long long per, int teams) const {
+    return cnt <= kSoloTiles && (long long)cnt * teams <= 2 * per && whole(x0, x1);
+  }
 };
 
 template <int ROWS>
 struct BlockWalk {
   long long x, x1;  // the range left
   int b, j, k;      // next: request, (head, row block) of it, tile
-  int streams, nrb, cnt;
+  int streams, nrb, cnt;  // cnt: tiles of a (head, row block) in the schedule, what it costs beyond them included
   BlockRequest r;
 
   __host__ __device__ inline void load(const BlockAttnParams& p) {
@@ -157,43 +164,52 @@ struct BlockWalk {
   __host__ __device__ static inline void size(const BlockAttnParams& p, const BlockRequest& r, int* nrb, int* streams, int* cnt) {
     *nrb = (int)(((long long)r.n * p.geo.g + ROWS - 1) / ROWS);
     *streams = *nrb * p.geo.Hkv;
-    *cnt = r.n ? block_tiles_max(p.window, p.n_first, r, p.geo.g, ROWS) : 0;
+    const int most = r.n ? block_tiles_max(p.window, p.n_first, r, p.geo.g, ROWS) : 0;
+    *cnt = most + (most > kSoloTiles ? kJoinTiles : 1);
   }
   // the range [x, x1), whose first tile is tile x - xb of request b
   __host__ __device__ inline void begin(const BlockAttnParams& p, long long x_, long long x1_, int b_, long long xb) {
     x = x_, x1 = x1_, b = b_;
     load(p);
     const long long at = x - xb;
-    j = cnt ? (int)(at / cnt) : 0;
-    k = cnt ? (int)(at - (long long)j * cnt) : 0;
+    j = (int)udiv(at, cnt);
+    k = (int)(at - (long long)j * cnt);
   }
   __host__ __device__ inline bool next(const BlockAttnParams& p, BlockSegment& s) {
     const BlockGeo& G = p.geo;
-    if (x >= x1) return false;
-    while (j >= streams) {
-      if (++b >= G.B) return false;
-      j = 0;
-      load(p);
+    while (x < x1) {
+      while (j >= streams) {
+        if (++b >= G.B) return false;
+        j = 0;
+        load(p);
+      }
+      const int M = r.n * G.g;
+      int p0 = r.before, p1 = r.before + r.n - 1;
+      s.h = j, s.r0 = 0, s.rows = M;
+      if (nrb > 1) {
+        s.h = j / nrb;
+        s.r0 = (j - s.h * nrb) * ROWS;
+        s.rows = M - s.r0 < ROWS ? M - s.r0 : ROWS;
+        p1 = p0 + (s.r0 + s.rows - 1) / G.g;
+        p0 += s.r0 / G.g;
+      }
+      const BlockTiles t = block_tiles(p.window, p.n_first, p0, p1);
+      const long long left = x1 - x;
+      const int end = left < cnt - k ? k + (int)left : cnt;
+      s.b = b, s.first = r.first, s.before = r.before, s.n = r.n;
+      s.k0 = k;
+      s.k1 = end < t.cnt ? end : t.cnt;
+      s.ns = t.ns, s.lo = t.lo;
+      s.x = x - k;
+      s.cnt = t.cnt;
+      x += end - k;
+      k = 0;
+      ++j;
+      if (s.k0 < s.k1) return true;  // (else the range begins behind its tiles)
     }
-    s.b = b, s.first = r.first, s.before = r.before, s.n = r.n;
-    s.h = j / nrb;
-    s.r0 = (j - s.h * nrb) * ROWS;
-    s.rows = r.n * G.g - s.r0 < ROWS ? r.n * G.g - s.r0 : ROWS;
-    const BlockTiles t = block_tiles(p.window, p.n_first, r.before + s.r0 / G.g, r.before + (s.r0 + s.rows - 1) / G.g);
-    const long long left = x1 - x;
-    const int end = left < cnt - k ? k + (int)left : cnt;
-    s.k0 = k;
-    s.k1 = end < t.cnt ? end : t.cnt;
-    s.ns = t.ns, s.lo = t.lo;
-    s.x = x - k;
-    s.cnt = cnt;
-    x += end - k;
-    k = 0;
-    ++j;
-    return true;
+    return false;
   }
 };
-
 __host__ __device__ inline int tile_of(const BlockSegment& s, int k) { return k < s.ns ? k : s.lo + (k - s.ns); }
 
 cudaError_t launch_block_plan(const BlockPlanParams& p, cudaStream_t st);

@@ -49,7 +49,7 @@ struct AttnSmem {
   long long warp_sum[kWarps];
   long long first_x;           // the range's first request: where it begins
   BlockSegment parted[2];
-  int last[2];
+  int last[2], from[2];
   int first_b, gave_up;
 };
 static_assert(sizeof(AttnSmem) <= 227 * 1024, "shared memory");
@@ -64,9 +64,15 @@ __device__ __forceinline__ uint32_t pack_halves(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Row of q and out of row r of a segment's block.
+// Token (of the request's new ones) of row r of a segment's block: a row below 64 and
+// what r0 lies into its token are below 2^11, so the product with ceil(2^32 / g) is exact.
+__device__ __forceinline__ int token_at(const BlockAttnParams& p, const BlockSegment& s, int r) {
+  const int i0 = s.r0 ? s.r0 / p.geo.g : 0, x = s.r0 - i0 * p.geo.g + r;
+  return i0 + (p.geo.g > 1 ? (int)__umulhi((unsigned)x, p.g_inv) : x);
+}
+// Row of q and out.
 __device__ __forceinline__ size_t row_at(const BlockAttnParams& p, const BlockSegment& s, int r) {
-  const int i = (s.r0 + r) / p.geo.g, j = (s.r0 + r) - i * p.geo.g;
+  const int i = token_at(p, s, r), j = s.r0 + r - i * p.geo.g;
   return (size_t)(s.first + i) * p.geo.Hq + s.h * p.geo.g + j;
 }
 
@@ -131,10 +137,18 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   walk.begin(p, x0, x1, sm.first_b, sm.first_x);
   ahead = walk;
   uint8_t* const ring = sm.stage[team * RING];
+  // A segment that one team takes goes to the team that has the fewest tiles of such
+  // so far, the first of them (lane t of `load`: team t's; every warp keeps the same).
+  const auto take = [&](int& load, const BlockSegment& s) {
+    const unsigned least = __reduce_min_sync(0xffffffffu, lane < TEAMS ? (unsigned)load << 3 | lane : 0xffffffffu);
+    const int t = least & 7;
+    if (lane == t) load += s.k1 - s.k0;
+    return t;
+  };
   // The segment that copies are asked for in, the team's next tile of it, and the
   // block ids of 32 of its tiles, one per lane.
   BlockSegment as = {};
-  int ai = 0, step = TEAMS, solos_ahead = 0, issued = 0, id_at = 0, ids = 0;
+  int ai = 0, step = TEAMS, load_ahead = 0, issued = 0, id_at = 0, ids = 0;
   bool have = rt == 0;
   const auto look_up = [&]() {  // by the team's first warp
     const int k = ai + lane * step;
@@ -144,11 +158,13 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   const auto find = [&]() {  // the team's next tile, if there is one
     if (ai < as.k1 && id_at < 32) return;
     while (ai >= as.k1) {
+      bool solo;
       do {
         if (!(have = ahead.next(p, as))) return;
-      } while (as.solo(x0, x1, TEAMS) && solos_ahead++ % TEAMS != team);
-      step = as.solo(x0, x1, TEAMS) ? 1 : TEAMS;
-      ai = as.k0 + (step == 1 ? 0 : team);
+        solo = as.solo(x0, x1, per, TEAMS);
+      } while (solo && take(load_ahead, as) != team);
+      step = solo ? 1 : TEAMS;
+      ai = as.k0 + (solo ? 0 : team);
     }
     look_up();
   };
@@ -180,20 +196,18 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   }
 
   int used = 0;  // tiles that the team has consumed
-  int solos = 0;
+  int load = 0;
   // Queries of a segment: channel 32 tq + 4 k + {0, 1 | 2, 3} enters step k of the
   // product as its row 2 tq + {0, 1 | 8, 9}.
   uint32_t qa[8][4];
   const auto load_q = [&](const BlockSegment& s) {
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int r = rt * 16 + gq + 8 * hf;
-      uint4 v[4] = {};
-      if (r < s.rows) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(p, s, r) * kHeadDim + 32 * tq);
+      const int r = min(rt * 16 + gq + 8 * hf, s.rows - 1);  // (rows that are not there: the last one again)
+      uint4 v[4];
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(p, s, r) * kHeadDim + 32 * tq);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = __ldg(src + u);
-      }
+      for (int u = 0; u < 4; ++u) v[u] = __ldg(src + u);
       const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -206,7 +220,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   const auto next_segment = [&](BlockSegment& s) {
     do {
       if (!walk.next(p, s)) return false;
-    } while (s.solo(x0, x1, TEAMS) && solos++ % TEAMS != team);
+    } while (s.solo(x0, x1, per, TEAMS) && take(load, s) != team);
     load_q(s);
     return true;
   };
@@ -214,18 +228,18 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   int parts = 0;  // 1: the range begins, 2: it ends within a (request, head, row block)
   bool more = next_segment(s);
   while (more) {
-    const bool solo = s.solo(x0, x1, TEAMS);
+    const bool solo = s.solo(x0, x1, per, TEAMS);
     const int tile_step = solo ? 1 : TEAMS;
     const int seg_rows = min(16, s.rows - rt * 16);  // of this warp; may be none
     float O[8][2][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    // last position that a row sees (rows that are not there: q = 0, of no consequence)
-    const int see[2] = {s.before + (s.r0 + rt * 16 + gq) / G.g, s.before + (s.r0 + rt * 16 + gq + 8) / G.g};
+    // last position that a row sees
+    const int see[2] = {s.before + token_at(p, s, min(rt * 16 + gq, s.rows - 1)), s.before + token_at(p, s, min(rt * 16 + gq + 8, s.rows - 1))};
     const bool active = seg_rows > 0;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
 #pragma unroll
       for (int e = 0; e < 8; ++e) O[c][e >> 2][e & 3] = 0.0f;
-    const int p_lo = s.before + s.r0 / G.g, p_hi = s.before + (s.r0 + s.rows - 1) / G.g;  // positions of the block's rows
+    const int p_lo = s.before + token_at(p, s, 0), p_hi = s.before + token_at(p, s, s.rows - 1);  // positions of the block's rows
 
     for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
       if (rt == 0) issue();
@@ -433,47 +447,59 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   }
 
   // ---- what spans CTAs (the range's first and last segment): the last CTA to come joins the parts
+  // (the barrier and the ticket's release order its writes before the ticket; the
+  // acquire and the barrier after it, the other CTAs' before the reads)
   if (parts) {
-    __threadfence();
     __syncthreads();
     if (tid < 2 && (parts >> tid & 1)) {
       const BlockSegment& d = sm.parted[tid];
-      const int c0 = (int)(d.x / per), c1 = (int)((d.x + d.cnt - 1) / per);
-      __threadfence();
-      const unsigned before = atomicAdd(&p.counters[c0], 1u);
+      const int c0 = (int)udiv(d.x, per), c1 = (int)udiv(d.x + d.cnt - 1, per);
+      unsigned before;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;\n" : "=r"(before) : "l"(p.counters + c0) : "memory");
       sm.last[tid] = before == (unsigned)(c1 - c0) ? c1 - c0 + 1 : 0;
+      sm.from[tid] = c0;
       if (sm.last[tid]) p.counters[c0] = 0;
-      __threadfence();
     }
     __syncthreads();
     for (int side = 0; side < 2; ++side) {
       const int count = parts >> side & 1 ? sm.last[side] : 0;
       if (!count) continue;
       const BlockSegment& d = sm.parted[side];
-      const int c0 = (int)(d.x / per);
+      const int c0 = sm.from[side];
       const auto piece = [&](int q, int r) { return (size_t)piece_slot(d.x, per, c0 + q) * ROWS + r; };
       for (int r = w; r < d.rows; r += kWarps) {
-        float top = -INFINITY;
-        for (int q = lane; q < count; q += 32) top = fmaxf(top, __ldcg(p.part_ml + piece(q, r) * 2));
+        const auto ml_at = [&](int q) {
+          return q < count ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + piece(q, r) * 2)) : make_float2(-INFINITY, 0.0f);
+        };
+        constexpr int kAhead = 16;  // accumulators in flight beside the maxima
+        const auto acc_at = [&](int q) {
+          return q < count ? __ldcg(reinterpret_cast<const float4*>(p.part_acc + piece(q, r) * kHeadDim) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float2 ml = ml_at(lane);
+        float4 a[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) a[u] = acc_at(u);
+        float top = ml.x;
+        for (int q = lane + 32; q < count; q += 32) top = fmaxf(top, ml_at(q).x);
         top = warp_max(top);
         const float zero = top == -INFINITY ? 0.0f : top;
         float L = 0.0f, acc[4] = {};
         for (int q0 = 0; q0 < count; q0 += 32) {
-          float e = 0.0f;
-          if (q0 + lane < count) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + piece(q0 + lane, r) * 2));
-            e = ex2(ml.x - zero);
-            L = fmaf(e, ml.y, L);
-          }
-          const int n = min(32, count - q0);
-#pragma unroll 8
-          for (int q = 0; q < n; ++q) {
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(p.part_acc + piece(q0 + q, r) * kHeadDim) + lane);
-            const float eq = __shfl_sync(0xffffffffu, e, q);
-            acc[0] = fmaf(eq, a.x, acc[0]);
-            acc[1] = fmaf(eq, a.y, acc[1]);
-            acc[2] = fmaf(eq, a.z, acc[2]);
-            acc[3] = fmaf(eq, a.w, acc[3]);
+          if (q0) ml = ml_at(q0 + lane);
+          const float e = ex2(ml.x - zero);
+          L = fmaf(e, ml.y, L);
+          for (int q = 0; q < min(32, count - q0); q += kAhead) {
+            if (q0 + q)
+#pragma unroll
+              for (int u = 0; u < kAhead; ++u) a[u] = acc_at(q0 + q + u);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+              const float eq = __shfl_sync(0xffffffffu, e, q + u);
+              acc[0] = fmaf(eq, a[u].x, acc[0]);
+              acc[1] = fmaf(eq, a[u].y, acc[1]);
+              acc[2] = fmaf(eq, a[u].z, acc[2]);
+              acc[3] = fmaf(eq, a[u].w, acc[3]);
+            }
           }
         }
         L = warp_sum(L);

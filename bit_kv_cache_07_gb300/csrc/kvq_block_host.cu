@@ -13,7 +13,7 @@ static kvq_status block_geometry(const kvq_block_config* c, BlockGeo* g) {
   if (!std::isfinite(c->softmax_scale) || c->softmax_scale < 0.0f || !std::isfinite(c->rope_theta) || c->rope_theta < 0.0f ||
       !std::isfinite(c->norm_eps) || c->norm_eps < 0.0f)
     return KVQ_ERR_INVALID_ARG;
-  if (c->head_dim != kHeadDim || c->batch > kMaxBlockBatch || c->n_tokens > (1 << 20) || c->n_kv_heads > 1024 || c->n_q_heads > 65536 ||
+  if (c->head_dim != kHeadDim || c->batch > kMaxBlockBatch || c->n_tokens > (1 << 20) || c->n_kv_heads > 1024 || c->n_q_heads > 1024 * c->n_kv_heads ||
       c->n_blocks > (1 << 26) || c->max_blocks > (1 << 25))
     return KVQ_ERR_UNSUPPORTED;
   *g = BlockGeo{c->batch, c->n_tokens, c->n_q_heads, c->n_kv_heads, c->n_q_heads / c->n_kv_heads, c->n_blocks, c->max_blocks};
@@ -128,6 +128,7 @@ kvq_status kvq_block_attn(const kvq_block_config* cfg, const kvq_block_tables* t
   p.q_scale = (float)(sm * 1.4426950408889634);
   p.window = cfg->window > 0 && cfg->window < kNoWindow ? cfg->window : kNoWindow;
   p.n_first = cfg->n_first;
+  p.g_inv = g.g > 1 ? (unsigned)(((1ull << 32) + g.g - 1) / g.g) : 0;
   int sms = 0;
   if (device_sm_count(&sms) != cudaSuccess) return KVQ_ERR_CUDA;
   if (sms > kMaxBlockCtas) sms = kMaxBlockCtas;

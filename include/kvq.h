@@ -621,7 +621,7 @@ typedef struct kvq_block_config {
     int32_t batch;            /* requests of a step, 1..1024 (slots of the tables) */
     int32_t n_tokens;         /* token slots of a step: rows of q, k, v, q_out, out;
                                  1..2^20                                       */
-    int32_t n_q_heads;        /* Hq, a multiple of n_kv_heads                  */
+    int32_t n_q_heads;        /* Hq, a multiple of n_kv_heads, up to 1024 times it */
     int32_t n_kv_heads;       /* Hkv, 1..1024                                  */
     int32_t head_dim;         /* 128                                           */
     int32_t n_blocks;         /* blocks of the pool, 1..2^26                   */

@@ -77,7 +77,7 @@ static int trial() {
       }
       const bool whole = s.x >= x0 && s.x + s.cnt <= x1;
       const int c0 = (int)(s.x / per), c1 = (int)((s.x + s.cnt - 1) / per);
-      if (whole != (c0 == c1)) ++bad;
+      if (whole != (c0 == c1) || s.k0 >= s.k1 || c < c0 || c > c1) ++bad;
       if (!whole) {
         ++parts[key];
         expect[key] = c1 - c0 + 1;

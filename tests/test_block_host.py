@@ -30,7 +30,7 @@ def test_layout():
 
 @pytest.mark.parametrize("field,value,status", [
     ("batch", 0, -1), ("batch", 1025, -2), ("n_tokens", 0, -1), ("n_tokens", (1 << 20) + 1, -2), ("n_q_heads", 7, -1),
-    ("n_q_heads", 0, -1), ("n_kv_heads", 0, -1), ("head_dim", 64, -2), ("n_blocks", 0, -1), ("n_blocks", (1 << 26) + 1, -2),
+    ("n_q_heads", 0, -1), ("n_q_heads", 4096, -2), ("n_kv_heads", 0, -1), ("head_dim", 64, -2), ("n_blocks", 0, -1), ("n_blocks", (1 << 26) + 1, -2),
     ("max_blocks", 0, -1), ("max_blocks", (1 << 25) + 1, -2), ("window", -1, -1), ("n_first", -1, -1),
     ("softmax_scale", -1.0, -1), ("softmax_scale", float("nan"), -1), ("rope_theta", float("inf"), -1),
     ("rope_theta", -1.0, -1), ("norm_eps", float("nan"), -1), ("norm_eps", -1.0, -1)])
