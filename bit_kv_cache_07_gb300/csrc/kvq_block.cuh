@@ -50,7 +50,7 @@ struct BlockAppendParams {
   long long ks, vs, qs;  // elements from a token slot to the next
   int rotate;
   float eps;
-  int units, heads_per_warp, q_chunks;
+  int units, heads_per_cta, kv_chunks, heads_per_warp, q_chunks;
   unsigned long long freq[kHeadDim / 2];  // turns per position, times 2^64
 };
 

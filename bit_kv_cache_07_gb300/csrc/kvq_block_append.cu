@@ -7,9 +7,10 @@
 //
 // Eight lanes hold a token's row of a head: lane l the channels 8l..8l+7 and
 // 64+8l..64+8l+7, so that both of a rotated pair are in one lane, loads are two
-// 16-byte words and the mean is three shuffles.  A CTA takes one block and head:
-// its keys, then its values, each read once into registers (one maximum over the
-// CTA between the read and the store).  Calls of few tokens per request run the
+// 16-byte words and the mean is three shuffles.  A CTA takes one block and several
+// heads: keys, then values of each, read once into registers (one maximum over the
+// CTA between the read and the store) while the next head's are on the way; the
+// sines are the block's.  Calls of few tokens per request run the
 // same with one warp per CTA, which walks a longer run of tokens twice.  The
 // queries go to CTAs of their own: a warp turns four tokens' rows head after
 // head with the same sines.
@@ -101,9 +102,9 @@ __device__ __forceinline__ int unit_request(const int* at, int B, int v, int lan
 }
 
 template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) block_append_kernel(const __grid_constant__ BlockAppendParams p) {
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_kernel(const __grid_constant__ BlockAppendParams p) {
   __shared__ unsigned long long s_freq[kHeadDim / 2];
-  __shared__ uint32_t s_max[WARPS], s_bad[WARPS];
+  __shared__ uint32_t s_top[2][WARPS];
   const BlockGeo& G = p.geo;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, l = lane & (kRowLanes - 1), sub = lane / kRowLanes;
   if (p.rotate)
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(32 * WARPS) block_append_kernel(const __grid_c
   grid_dep_wait();
   grid_dep_trigger();
   constexpr int kStep = kWarpTokens * WARPS;  // tokens of a CTA at a time
-  const int kv_ctas = p.units * G.Hkv;
+  const int kv_ctas = p.units * p.kv_chunks;
 
   if ((int)blockIdx.x >= kv_ctas) {  // queries: kStep token slots, heads_per_warp heads
     const int x = blockIdx.x - kv_ctas, group = x / p.q_chunks, chunk = x - group * p.q_chunks;
@@ -127,9 +128,20 @@ __global__ void __launch_bounds__(32 * WARPS) block_append_kernel(const __grid_c
     const int h1 = min(G.Hq, (chunk + 1) * p.heads_per_warp);
     const uint16_t* src = p.q + (long long)row * p.qs;
     uint16_t* dst = p.q_out + (long long)row * G.Hq * kHeadDim;
-    for (int h = chunk * p.heads_per_warp; h < h1; ++h) {
+    const int h0 = chunk * p.heads_per_warp;
+    uint4 raw[2], ahead[2];
+    const auto fetch = [&](int h) {
+      const uint4* at = reinterpret_cast<const uint4*>(src + h * kHeadDim);
+      ahead[0] = __ldg(at + l);
+      ahead[1] = __ldg(at + kRowLanes + l);
+    };
+    fetch(h0);
+    for (int h = h0; h < h1; ++h) {
       float v[16];
-      load_row(src + h * kHeadDim, l, v);
+      raw[0] = ahead[0], raw[1] = ahead[1];
+      if (h + 1 < h1) fetch(h + 1);
+      halves_to_floats(raw[0], v);
+      halves_to_floats(raw[1], v + 8);
       if (p.q_weight) normalise(v, wt, p.eps);
       if (p.rotate) rotate(v, c, s);
       uint4 o[2];
@@ -149,8 +161,8 @@ __global__ void __launch_bounds__(32 * WARPS) block_append_kernel(const __grid_c
     return;
   }
 
-  // keys and values: one touched block and head
-  const int unit = blockIdx.x / G.Hkv, h = blockIdx.x - unit * G.Hkv;
+  // keys and values: heads_per_cta heads of one touched block
+  const int unit = blockIdx.x / p.kv_chunks, chunk = blockIdx.x - unit * p.kv_chunks;
   if (unit >= __ldg(p.t.unit0 + G.B)) return;
   const int b = unit_request(p.t.unit0, G.B, unit, lane);
   const BlockRequest r = block_request(G, __ldg(p.t.lens + b), __ldg(p.t.start + b), __ldg(p.t.start + b + 1));
@@ -162,84 +174,120 @@ __global__ void __launch_bounds__(32 * WARPS) block_append_kernel(const __grid_c
   if (id < 0 || id >= G.n_blocks) return;
   const int off = p0 - j * kBlockTokens, count = p1 - p0;
   const long long slot0 = r.first + (p0 - r.before);
-  const size_t place = (size_t)id * G.Hkv + h;
-  const bool again = count > kStep;
+  const int h0 = chunk * p.heads_per_cta, h1 = min(G.Hkv, h0 + p.heads_per_cta);
+  constexpr bool kOnce = kStep >= kBlockTokens;  // no run is longer
+  const bool again = !kOnce && count > kStep;    // the run is walked twice
+  const int t_first = w * kWarpTokens + sub;
 
-  for (int side = 0; side < 2; ++side) {
-    const uint16_t* src = (side ? p.v + slot0 * p.vs : p.k + slot0 * p.ks) + h * kHeadDim;
-    const long long stride = side ? p.vs : p.ks;
-    float v[16], wt[16];
-    const bool norm = side == 0 && p.k_weight;
-    if (norm) load_row(p.k_weight, l, wt);
-    const auto make = [&](int t) {  // token t of the run in v (past the end: the first one)
-      const int tt = t < count ? t : 0;
-      load_row(src + tt * stride, l, v);
-      if (norm) normalise(v, wt, p.eps);
-      if (side == 0 && p.rotate) {
-        float c[8], s[8];
-        angles(s_freq, l, p0 + tt, c, s);
-        rotate(v, c, s);
-      }
-    };
-    uint32_t top = 0, bad = 0;
-    for (int t0 = 0; t0 < count; t0 += kStep) {
-      make(t0 + w * kWarpTokens + sub);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t u = __float_as_uint(v[i]) & 0x7fffffffu;
-        const bool finite = u < 0x7f800000u;
-        top = max(top, finite ? u : 0u);
-        bad |= !finite;
-      }
+  const uint16_t *k_row = p.k + slot0 * p.ks, *v_row = p.v + slot0 * p.vs;
+  const auto fetch = [&](int h, int side, int t, uint4 (&raw)[2]) {  // past the run's end: its first token
+    const uint4* at = reinterpret_cast<const uint4*>((side ? v_row + (t < count ? t : 0) * p.vs : k_row + (t < count ? t : 0) * p.ks) + h * kHeadDim);
+    raw[0] = __ldg(at + l);
+    raw[1] = __ldg(at + kRowLanes + l);
+  };
+  float c[8], s[8], v[16], wt[16];
+  if (p.k_weight) load_row(p.k_weight, l, wt);
+  const auto turn = [&](int t) {
+    if (p.rotate) angles(s_freq, l, p0 + (t < count ? t : 0), c, s);
+  };
+  const auto make = [&](int side, const uint4 (&raw)[2]) {
+    halves_to_floats(raw[0], v);
+    halves_to_floats(raw[1], v + 8);
+    if (side == 0) {
+      if (p.k_weight) normalise(v, wt, p.eps);
+      if (p.rotate) rotate(v, c, s);
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    bad = __any_sync(0xffffffffu, bad);
-    const uint8_t was = off ? p.scales[place * 2 + side] : 0;
-    if constexpr (WARPS > 1) {
-      __syncthreads();  // the other side's maxima have been read
-      if (lane == 0) s_max[w] = top, s_bad[w] = bad;
-      __syncthreads();
+  };
+  uint4 ahead[2][2];  // the next head's rows, on the way
+  fetch(h0, 0, t_first, ahead[0]);
+  fetch(h0, 1, t_first, ahead[1]);
+  turn(t_first);
+  int flip = 0;
+  for (int h = h0; h < h1; ++h) {
+    const size_t place = (size_t)id * G.Hkv + h;
+    for (int side = 0; side < 2; ++side) {
+      const uint8_t was = off ? p.scales[place * 2 + side] : 0;
+      uint4 raw[2] = {side ? ahead[1][0] : ahead[0][0], side ? ahead[1][1] : ahead[0][1]};
+      if (h + 1 < h1) {
+        if (side) fetch(h + 1, 1, t_first, ahead[1]);
+        else fetch(h + 1, 0, t_first, ahead[0]);
+      }
+      // the maximum, and a sum of zeros that an infinity or a NaN spoils
+      float amax = 0.0f, zeros = 0.0f, finite = 0.0f;
+      bool bad = false;
+      for (int t0 = 0; t0 < (kOnce ? 1 : count); t0 += kStep) {
+        if (t0) {
+          turn(t0 + t_first);
+          fetch(h, side, t0 + t_first, raw);
+        }
+        make(side, raw);
 #pragma unroll
-      for (int i = 0; i < WARPS; ++i) top = max(top, s_max[i]), bad |= s_bad[i];
-    }
-    int e = scale_exponent(__uint_as_float(top));
-    const bool spoilt = off && was == kScaleNaN;
-    uint8_t* block = p.codes + (place * 2 + side) * kBlockSide;
-    if (off && !spoilt) {
-      const int e_was = was - kScaleBias;
-      if (e_was >= e) {
-        e = e_was;
-      } else {  // earlier tokens move to the larger scale
-        const float f = exp2i(max(e_was - e, -126));
-        for (int x = tid; x < off * 32; x += 32 * WARPS) {
-          uint32_t* at = reinterpret_cast<uint32_t*>(block) + x;
-          const uint32_t u = *at;
-          const float2 a = e4m3x2_floats(u & 0xffffu), c = e4m3x2_floats(u >> 16);
-          *at = e4m3x2(a.x * f, a.y * f) | e4m3x2(c.x * f, c.y * f) << 16;
+        for (int i = 0; i < 16; ++i) {
+          amax = fmaxf(amax, fabsf(v[i]));
+          zeros = fmaf(v[i], 0.0f, zeros);
+        }
+        if (!(zeros == 0.0f)) {  // rare: without those that are not finite
+          bad = true;
+          amax = finite, zeros = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) amax = fabsf(v[i]) < INFINITY ? fmaxf(amax, fabsf(v[i])) : amax;
+        }
+        finite = amax;
+      }
+      uint32_t top = __float_as_uint(amax);
+      top = __reduce_max_sync(0xffffffffu, top);
+      bad = __any_sync(0xffffffffu, bad);
+      if constexpr (WARPS > 1) {
+        if (lane == 0) s_top[flip][w] = top | (bad ? 0x80000000u : 0u);
+        __syncthreads();  // (two sets of maxima: those of the time before are read by now)
+        const uint32_t x = lane < WARPS ? s_top[flip][lane] : 0u;
+        bad = __any_sync(0xffffffffu, x >> 31);
+        top = __reduce_max_sync(0xffffffffu, x & 0x7fffffffu);
+        flip ^= 1;
+      }
+      int e = scale_exponent(__uint_as_float(top));
+      const bool spoilt = off && was == kScaleNaN;
+      uint8_t* block = p.codes + (place * 2 + side) * kBlockSide;
+      if (off && !spoilt) {
+        const int e_was = was - kScaleBias;
+        if (e_was >= e) {
+          e = e_was;
+        } else {  // earlier tokens move to the larger scale
+          const float f = exp2i(max(e_was - e, -126));
+          for (int x = tid; x < off * 32; x += 32 * WARPS) {
+            uint32_t* at = reinterpret_cast<uint32_t*>(block) + x;
+            const uint32_t u = *at;
+            const float2 lo = e4m3x2_floats(u & 0xffffu), hi = e4m3x2_floats(u >> 16);
+            *at = e4m3x2(lo.x * f, lo.y * f) | e4m3x2(hi.x * f, hi.y * f) << 16;
+          }
         }
       }
-    }
-    const float f = e >= 127 ? 5.877471754111438e-39f : exp2i(-e);
-    for (int t0 = 0; t0 < count; t0 += kStep) {
-      const int t = t0 + w * kWarpTokens + sub;
-      if (again) make(t);
-      if (t < count) {
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = fabsf(v[4 * i + k]) < INFINITY ? v[4 * i + k] * f : 0.0f;
-          c[i] = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
+      const float f = e >= 127 ? 5.877471754111438e-39f : exp2i(-e);
+      for (int t0 = 0; t0 < (kOnce ? 1 : count); t0 += kStep) {
+        const int t = t0 + t_first;
+        if (again) {
+          turn(t);
+          fetch(h, side, t, raw);
+          make(side, raw);
         }
-        const int tok = off + t;
-        uint8_t* at = block + tok * kHeadDim + (l & 1) * 8;
-        *reinterpret_cast<uint2*>(at + (((l >> 1) ^ (tok & 7)) << 4)) = make_uint2(c[0], c[1]);
-        *reinterpret_cast<uint2*>(at + (((4 + (l >> 1)) ^ (tok & 7)) << 4)) = make_uint2(c[2], c[3]);
+        if (bad)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.0f;
+        if (t < count) {
+          uint32_t code[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            code[i] = e4m3x2(v[4 * i] * f, v[4 * i + 1] * f) | e4m3x2(v[4 * i + 2] * f, v[4 * i + 3] * f) << 16;
+          const int tok = off + t;
+          uint8_t* at = block + tok * kHeadDim + (l & 1) * 8;
+          *reinterpret_cast<uint2*>(at + (((l >> 1) ^ (tok & 7)) << 4)) = make_uint2(code[0], code[1]);
+          *reinterpret_cast<uint2*>(at + (((4 + (l >> 1)) ^ (tok & 7)) << 4)) = make_uint2(code[2], code[3]);
+        }
       }
+      if (again) turn(t_first);
+      __syncwarp();  // every lane has read the old scale
+      if (tid == 0) p.scales[place * 2 + side] = bad || spoilt ? kScaleNaN : (uint8_t)(e + kScaleBias);
     }
-    __syncwarp();  // every lane has read the old scale
-    if (tid == 0) p.scales[place * 2 + side] = bad || spoilt ? kScaleNaN : (uint8_t)(e + kScaleBias);
   }
 }
 
@@ -252,13 +300,19 @@ cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st) {
   // chains, single tokens) fill one warp
   const bool few = (G.N + G.B - 1) / G.B <= kWarpTokens;
   const int step = kWarpTokens * (few ? 1 : 8);
+  // heads of a block's CTA: as many as still leave several CTAs for each SM (a
+  // CTA's look-ups are paid once, and the next head's rows are read meanwhile)
+  const long long items = (long long)p.units * G.Hkv;
+  const long long share = few ? 1 : items / 1216;
+  p.heads_per_cta = (int)(share < 1 ? 1 : share > G.Hkv ? G.Hkv : share);
+  p.kv_chunks = (G.Hkv + p.heads_per_cta - 1) / p.heads_per_cta;
   // heads of a query warp: more share a token's sines, fewer spread a small call
   // over the SMs
   const long long rows = (long long)G.N * G.Hq;
   p.heads_per_warp = (int)(rows >= 8ll * 16384 ? 8 : rows >= 16384 ? rows / 16384 : 1);
   p.q_chunks = (G.Hq + p.heads_per_warp - 1) / p.heads_per_warp;
   const long long q_ctas = p.q ? (long long)((G.N + step - 1) / step) * p.q_chunks : 0;
-  const long long ctas = (long long)p.units * G.Hkv + q_ctas;
+  const long long ctas = (long long)p.units * p.kv_chunks + q_ctas;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   return few ? launch_dependent(block_append_kernel<1>, dim3((unsigned)ctas), dim3(32), 0, st, p)
              : launch_dependent(block_append_kernel<8>, dim3((unsigned)ctas), dim3(256), 0, st, p);

@@ -133,6 +133,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   }
   __syncthreads();
 
+  grid_dep_trigger();  // the next kernel may come as the CTAs leave
+
   BlockWalk<ROWS> walk, ahead;
   walk.begin(p, x0, x1, sm.first_b, sm.first_x);
   ahead = walk;
