@@ -129,33 +129,38 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
     const uint16_t* src = p.q + (long long)row * p.qs;
     uint16_t* dst = p.q_out + (long long)row * G.Hq * kHeadDim;
     const int h0 = chunk * p.heads_per_warp;
-    uint4 raw[2], ahead[2];
-    const auto fetch = [&](int h) {
-      const uint4* at = reinterpret_cast<const uint4*>(src + h * kHeadDim);
-      ahead[0] = __ldg(at + l);
-      ahead[1] = __ldg(at + kRowLanes + l);
+    uint4 ahead[2][2];  // the next two heads' rows, on the way
+    const auto fetch = [&](int h, uint4 (&raw)[2]) {
+      const uint4* at = reinterpret_cast<const uint4*>(src + min(h, h1 - 1) * kHeadDim);
+      raw[0] = __ldg(at + l);
+      raw[1] = __ldg(at + kRowLanes + l);
     };
-    fetch(h0);
-    for (int h = h0; h < h1; ++h) {
-      float v[16];
-      raw[0] = ahead[0], raw[1] = ahead[1];
-      if (h + 1 < h1) fetch(h + 1);
-      halves_to_floats(raw[0], v);
-      halves_to_floats(raw[1], v + 8);
-      if (p.q_weight) normalise(v, wt, p.eps);
-      if (p.rotate) rotate(v, c, s);
-      uint4 o[2];
-      uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+    fetch(h0, ahead[0]);
+    fetch(h0 + 1, ahead[1]);
+    for (int hh = h0; hh < h1; hh += 2) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const __half2 two = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
-        ow[k] = *reinterpret_cast<const uint32_t*>(&two);
-      }
-      __syncwarp();  // (q_out may be q: a row is read whole before it is written)
-      if (live) {
-        uint4* at = reinterpret_cast<uint4*>(dst + h * kHeadDim);
-        at[l] = o[0];
-        at[kRowLanes + l] = o[1];
+      for (int u = 0; u < 2; ++u) {
+        const int h = hh + u;
+        if (h >= h1) break;
+        float v[16];
+        halves_to_floats(ahead[u][0], v);
+        halves_to_floats(ahead[u][1], v + 8);
+        if (h + 2 < h1) fetch(h + 2, ahead[u]);
+        if (p.q_weight) normalise(v, wt, p.eps);
+        if (p.rotate) rotate(v, c, s);
+        uint4 o[2];
+        uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const __half2 two = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+          ow[k] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        __syncwarp();  // (q_out may be q: a row is read whole before it is written)
+        if (live) {
+          uint4* at = reinterpret_cast<uint4*>(dst + h * kHeadDim);
+          at[l] = o[0];
+          at[kRowLanes + l] = o[1];
+        }
       }
     }
     return;
