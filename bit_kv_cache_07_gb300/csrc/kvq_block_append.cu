@@ -42,32 +42,63 @@ __device__ __forceinline__ void load_row(const uint16_t* row, int l, float (&v)[
   halves_to_floats(a, v);
   halves_to_floats(b, v + 8);
 }
-__device__ __forceinline__ void normalise(float (&v)[16], const float (&w)[16], float eps) {
+// What turns a row x into y / r (r: the row's own factor of the norm), weights and
+// sines of the token together:
+//   y_i = a_i x_i - b_i x_{i+64},  y_{i+64} = c_i x_{i+64} + d_i x_i.
+struct Turn {
+  float a[8], b[8], c[8], d[8];
+};
+__device__ __forceinline__ void make_turn(Turn& t, const uint16_t* weight, const unsigned long long* freq, bool rotate, int l, int pos) {
+  float w[16];
+  if (weight) load_row(weight, l, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t.a[i] = weight ? w[i] : 1.0f;
+    t.c[i] = weight ? w[8 + i] : 1.0f;
+    if (rotate) {
+      const int turns = (int)(unsigned)((freq[8 * l + i] * (unsigned long long)pos) >> 32);  // [-1/2, 1/2) turns
+      const float x = (float)turns * 1.4629180792671596e-9f;                                 // 2 pi / 2^32
+      const float cs = __cosf(x), sn = __sinf(x);
+      t.b[i] = t.c[i] * sn;
+      t.d[i] = t.a[i] * sn;
+      t.a[i] *= cs;
+      t.c[i] *= cs;
+    }
+  }
+}
+__device__ __forceinline__ void apply_turn(const Turn& t, bool weight, bool rotate, float (&v)[16]) {
+  if (rotate) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = v[i], y = v[8 + i];
+      v[i] = t.a[i] * x - t.b[i] * y;
+      v[8 + i] = t.c[i] * y + t.d[i] * x;
+    }
+  } else if (weight) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] *= t.a[i];
+      v[8 + i] *= t.c[i];
+    }
+  }
+}
+// 1 / sqrt(mean x^2 + eps) of the row
+__device__ __forceinline__ float norm_factor(const float (&v)[16], float eps) {
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
 #pragma unroll
   for (int o = 1; o < kRowLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float r = rsqrtf(ss * (1.0f / kHeadDim) + eps);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = v[i] * r * w[i];
+  return rsqrtf(ss * (1.0f / kHeadDim) + eps);
 }
-__device__ __forceinline__ void angles(const unsigned long long* freq, int l, int pos, float (&c)[8], float (&s)[8]) {
+// The largest magnitude of the lane's halves; not below infinity where one is not finite.
+__device__ __forceinline__ float halves_max(const uint4 (&raw)[2]) {
+  const __half2* h = reinterpret_cast<const __half2*>(raw);
+  __half2 m = __habs2(h[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int turn = (int)(unsigned)((freq[8 * l + i] * (unsigned long long)pos) >> 32);  // [-1/2, 1/2) turns
-    const float a = (float)turn * 1.4629180792671596e-9f;                                 // 2 pi / 2^32
-    c[i] = __cosf(a);
-    s[i] = __sinf(a);
-  }
-}
-__device__ __forceinline__ void rotate(float (&v)[16], const float (&c)[8], const float (&s)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = v[i], b = v[8 + i];
-    v[i] = a * c[i] - b * s[i];
-    v[8 + i] = b * c[i] + a * s[i];
-  }
+  for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(h[i]));
+  const float x = __low2float(m), y = __high2float(m);
+  return x <= y || isnan(y) ? y : x;  // (a NaN stays one)
 }
 // The least e in [kMinExp, kMaxExp] with amax <= 448 2^e (448 = 1.75 2^8).
 __device__ __forceinline__ int scale_exponent(float amax) {
@@ -122,9 +153,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
     if (group * kStep + w * kWarpTokens >= used) return;
     const bool live = i < used;
     const int row = live ? i : group * kStep + w * kWarpTokens;
-    float c[8], s[8], wt[16];
-    if (p.q_weight) load_row(p.q_weight, l, wt);
-    if (p.rotate) angles(s_freq, l, __ldg(p.t.position + row), c, s);
+    Turn turn;
+    make_turn(turn, p.q_weight, s_freq, p.rotate, l, p.rotate ? __ldg(p.t.position + row) : 0);
     const int h1 = min(G.Hq, (chunk + 1) * p.heads_per_warp);
     const uint16_t* src = p.q + (long long)row * p.qs;
     uint16_t* dst = p.q_out + (long long)row * G.Hq * kHeadDim;
@@ -146,13 +176,13 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
         halves_to_floats(ahead[u][0], v);
         halves_to_floats(ahead[u][1], v + 8);
         if (h + 2 < h1) fetch(h + 2, ahead[u]);
-        if (p.q_weight) normalise(v, wt, p.eps);
-        if (p.rotate) rotate(v, c, s);
+        const float r = p.q_weight ? norm_factor(v, p.eps) : 1.0f;
+        apply_turn(turn, p.q_weight, p.rotate, v);
         uint4 o[2];
         uint32_t* ow = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const __half2 two = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+          const __half2 two = __floats2half2_rn(v[2 * k] * r, v[2 * k + 1] * r);
           ow[k] = *reinterpret_cast<const uint32_t*>(&two);
         }
         __syncwarp();  // (q_out may be q: a row is read whole before it is written)
@@ -190,23 +220,31 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
     raw[0] = __ldg(at + l);
     raw[1] = __ldg(at + kRowLanes + l);
   };
-  float c[8], s[8], v[16], wt[16];
-  if (p.k_weight) load_row(p.k_weight, l, wt);
-  const auto turn = [&](int t) {
-    if (p.rotate) angles(s_freq, l, p0 + (t < count ? t : 0), c, s);
+  Turn turn;
+  float v[16], r_row = 1.0f;
+  bool odd_weight = false;
+  const auto turn_to = [&](int t) {
+    make_turn(turn, p.k_weight, s_freq, p.rotate, l, p0 + (t < count ? t : 0));
+    if (p.k_weight) {
+      float zeros = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) zeros += turn.a[i] * 0.0f + turn.c[i] * 0.0f;
+      odd_weight = !(zeros == 0.0f);
+    }
   };
-  const auto make = [&](int side, const uint4 (&raw)[2]) {
+  const auto make = [&](int side, const uint4 (&raw)[2]) {  // y / r_row in v
     halves_to_floats(raw[0], v);
     halves_to_floats(raw[1], v + 8);
+    r_row = 1.0f;
     if (side == 0) {
-      if (p.k_weight) normalise(v, wt, p.eps);
-      if (p.rotate) rotate(v, c, s);
+      if (p.k_weight) r_row = norm_factor(v, p.eps);
+      apply_turn(turn, p.k_weight, p.rotate, v);
     }
   };
   uint4 ahead[2][2];  // the next head's rows, on the way
   fetch(h0, 0, t_first, ahead[0]);
   fetch(h0, 1, t_first, ahead[1]);
-  turn(t_first);
+  turn_to(t_first);
   int flip = 0;
   for (int h = h0; h < h1; ++h) {
     const size_t place = (size_t)id * G.Hkv + h;
@@ -217,27 +255,30 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
         if (side) fetch(h + 1, 1, t_first, ahead[1]);
         else fetch(h + 1, 0, t_first, ahead[0]);
       }
-      // the maximum, and a sum of zeros that an infinity or a NaN spoils
-      float amax = 0.0f, zeros = 0.0f, finite = 0.0f;
+      float amax = 0.0f;
       bool bad = false;
       for (int t0 = 0; t0 < (kOnce ? 1 : count); t0 += kStep) {
         if (t0) {
-          turn(t0 + t_first);
+          turn_to(t0 + t_first);
           fetch(h, side, t0 + t_first, raw);
         }
         make(side, raw);
+        float m = halves_max(raw);
+        bool odd = !(m < INFINITY);
+        if (side == 0) {
+          m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          amax = fmaxf(amax, fabsf(v[i]));
-          zeros = fmaf(v[i], 0.0f, zeros);
+          for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i]));
+          m *= r_row;
+          odd = odd || odd_weight || !(m < INFINITY);
         }
-        if (!(zeros == 0.0f)) {  // rare: without those that are not finite
+        if (odd) {  // rare: the largest of the others
           bad = true;
-          amax = finite, zeros = 0.0f;
+          m = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) amax = fabsf(v[i]) < INFINITY ? fmaxf(amax, fabsf(v[i])) : amax;
+          for (int i = 0; i < 16; ++i) m = fabsf(v[i] * r_row) < INFINITY ? fmaxf(m, fabsf(v[i] * r_row)) : m;
         }
-        finite = amax;
+        amax = fmaxf(amax, m);
       }
       uint32_t top = __float_as_uint(amax);
       top = __reduce_max_sync(0xffffffffu, top);
@@ -271,25 +312,26 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
       for (int t0 = 0; t0 < (kOnce ? 1 : count); t0 += kStep) {
         const int t = t0 + t_first;
         if (again) {
-          turn(t);
+          turn_to(t);
           fetch(h, side, t, raw);
           make(side, raw);
         }
         if (bad)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.0f;
+          for (int i = 0; i < 16; ++i) v[i] = fabsf(v[i] * r_row) < INFINITY ? v[i] : 0.0f;
         if (t < count) {
+          const float fr = f * r_row;
           uint32_t code[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            code[i] = e4m3x2(v[4 * i] * f, v[4 * i + 1] * f) | e4m3x2(v[4 * i + 2] * f, v[4 * i + 3] * f) << 16;
+            code[i] = e4m3x2(v[4 * i] * fr, v[4 * i + 1] * fr) | e4m3x2(v[4 * i + 2] * fr, v[4 * i + 3] * fr) << 16;
           const int tok = off + t;
           uint8_t* at = block + tok * kHeadDim + (l & 1) * 8;
           *reinterpret_cast<uint2*>(at + (((l >> 1) ^ (tok & 7)) << 4)) = make_uint2(code[0], code[1]);
           *reinterpret_cast<uint2*>(at + (((4 + (l >> 1)) ^ (tok & 7)) << 4)) = make_uint2(code[2], code[3]);
         }
       }
-      if (again) turn(t_first);
+      if (again) turn_to(t_first);
       __syncwarp();  // every lane has read the old scale
       if (tid == 0) p.scales[place * 2 + side] = bad || spoilt ? kScaleNaN : (uint8_t)(e + kScaleBias);
     }
