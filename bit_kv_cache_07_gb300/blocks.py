@@ -16,8 +16,9 @@ from __future__ import annotations
 
 import ctypes as C
 
-from .binding import (BLOCK_TABLES, KvqError, _arg, _check, _on_device, _stream_of, kvq_block_config, kvq_block_layout,
-                      kvq_block_tables, lib)
+import torch
+
+from .binding import (BLOCK_TABLES, KvqError, _check, kvq_block_config, kvq_block_layout, kvq_block_tables, lib)
 
 BLOCK_TOKENS = 32
 _SHARED = ("batch", "n_tokens", "n_blocks", "max_blocks")  # what tables and layers agree in
@@ -47,15 +48,43 @@ def layout(cfg) -> kvq_block_layout:
 
 def new_workspace(cfg, device="cuda"):
     """Zeroed scratch for ``Layer.attn``."""
-    import torch
     return torch.zeros(layout(cfg).workspace_bytes, dtype=torch.uint8, device=device)
 
 
-def _ints(t, what: str, shape):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{what}: expected a contiguous int32 CUDA tensor of shape {shape}")
-    return t.data_ptr()
+def _here() -> int:
+    """The device that the calls launch on: the current one; their tensors live there."""
+    return torch._C._cuda_getDevice()
+
+
+def _stream_on(stream, device: int):
+    """A stream's handle; None: the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse(t, what: str, dtype, shape, device):
+    """The error for a tensor that is not of this type and shape on this device."""
+    want = f"{what}: expected a {dtype} tensor of shape {tuple(shape)} on cuda:{device}"
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{want}, got {type(t).__name__}")
+    raise ValueError(f"{want}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _dense(t, what: str, dtype, shape, device) -> int:
+    """The address of a contiguous tensor."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        raise ValueError(f"{what} must be contiguous")
+    _refuse(t, what, dtype, shape, device)
+
+
+def _ints(t, what: str, shape, device) -> int:
+    return _dense(t, what, torch.int32, shape, device)
 
 
 class Tables:
@@ -64,7 +93,6 @@ class Tables:
     unless tensors of the layout of kvq_block_tables are given by name."""
 
     def __init__(self, cfg, device="cuda", **arrays):
-        import torch
         self.cfg = make_config(cfg)
         layout(self.cfg)  # its refusals
         c = self.cfg
@@ -85,42 +113,43 @@ class Tables:
                 else:
                     t = torch.zeros(shapes[name], dtype=torch.int32, device=device)
             setattr(self, name, t)
-        self.arrays = kvq_block_tables(*[_ints(getattr(self, n), n, shapes[n]) for n in BLOCK_TABLES])
+        self.device = self.lens.get_device() if isinstance(self.lens, torch.Tensor) else None
+        self.arrays = kvq_block_tables(*[_ints(getattr(self, n), n, shapes[n], self.device) for n in BLOCK_TABLES])
+        if self.device < 0:
+            raise ValueError("the tables must be on a GPU")
         self._refs = C.byref(self.cfg), C.byref(self.arrays)
-        if len({getattr(self, n).device for n in BLOCK_TABLES}) != 1:
-            raise ValueError("the tables must be on one device")
+        self._call = lib().kvq_block_plan
+        self._rows = (c.batch,)
 
     def plan(self, n_new, lens=None, free_count=None, stream=None):
         """The step's tables: request b adds n_new[b] tokens, or ends (negative).
         lens, free_count: lengths and free blocks before the step, the tables' own
         (updated in place) unless given."""
-        rows = (self.cfg.batch,)
-        np_ = _ints(n_new, "n_new", rows)
-        lp = self.arrays.lens if lens is None else _ints(lens, "lens", rows)
-        fp = self.arrays.free_count if free_count is None else _ints(free_count, "free_count", (1,))
-        _on_device(self.lens, n_new, lens, free_count)
-        _check("kvq_block_plan", lib().kvq_block_plan(*self._refs, lp, fp, np_, _stream_of(stream, self.lens)))
+        d = _here()
+        if d != self.device:
+            raise ValueError(f"the tables are on cuda:{self.device}, the current device is cuda:{d}")
+        np_ = _ints(n_new, "n_new", self._rows, d)
+        lp = self.arrays.lens if lens is None else _ints(lens, "lens", self._rows, d)
+        fp = self.arrays.free_count if free_count is None else _ints(free_count, "free_count", (1,), d)
+        st = self._call(*self._refs, lp, fp, np_, _stream_on(stream, d))
+        if st:
+            _check("kvq_block_plan", st)
 
 
-def _rows(t, what: str, tokens: int, heads: int):
+def _strided(t, what: str, shape, dense, device):
     """(address, elements from a token to the next) of fp16 rows [tokens, heads, 128]
-    whose heads lie one after the other."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float16 or not t.is_cuda or tuple(t.shape) != (tokens, heads, 128):
-        raise ValueError(f"{what}: expected a float16 CUDA tensor of shape {(tokens, heads, 128)}")
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != 128):
-        raise ValueError(f"{what}: a token's heads must lie one after the other")
-    return t.data_ptr(), s[0] if tokens > 1 else heads * 128
-
-
-def _weight(t, what: str):
-    import torch
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != (128,):
-        raise ValueError(f"{what}: expected a tensor of shape (128,)")
-    return _arg(t, what, torch.float16, 256)
+    whose heads lie one after the other; dense: the strides of contiguous ones."""
+    try:
+        if t.dtype is torch.float16 and t.shape == shape and t.get_device() == device:
+            s = t.stride()
+            if s == dense:
+                return t.data_ptr(), dense[0]
+            if s[2] == 1 and (s[1] == 128 or shape[1] == 1):
+                return t.data_ptr(), s[0] if shape[0] > 1 else dense[0]
+            raise ValueError(f"{what}: a token's heads must lie one after the other")
+    except AttributeError:
+        pass
+    _refuse(t, what, torch.float16, shape, device)
 
 
 class Layer:
@@ -128,7 +157,6 @@ class Layer:
     uint8 [n_blocks, Hkv, 2], or tensors of that layout."""
 
     def __init__(self, cfg, codes=None, scales=None, device="cuda"):
-        import torch
         self.cfg = make_config(cfg)
         self.layout = layout(self.cfg)
         c = self.cfg
@@ -139,63 +167,62 @@ class Layer:
         if scales is None:
             room = torch.zeros(self.layout.scales_bytes, dtype=torch.uint8, device=device)
             scales = room[:c.n_blocks * c.n_kv_heads * 2].view(shape)
-        self._codes = _arg(codes, "codes", torch.uint8, self.layout.codes_bytes)
-        self._scales = _arg(scales, "scales", torch.uint8, c.n_blocks * c.n_kv_heads * 2)
-        if tuple(codes.shape) != shape + (BLOCK_TOKENS, 128) or tuple(scales.shape) != shape:
-            raise ValueError(f"codes, scales: expected shapes {shape + (BLOCK_TOKENS, 128)} and {shape}")
+        self.device = codes.get_device() if isinstance(codes, torch.Tensor) else None
+        self._codes = _dense(codes, "codes", torch.uint8, shape + (BLOCK_TOKENS, 128), self.device)
+        self._scales = _dense(scales, "scales", torch.uint8, shape, self.device)
+        if self.device < 0:
+            raise ValueError("codes and scales must be on a GPU")
         if scales.untyped_storage().nbytes() - scales.storage_offset() < self.layout.scales_bytes:
             raise ValueError(f"scales: its storage must reach {self.layout.scales_bytes} bytes (padded to 16)")
-        if codes.device != scales.device:
-            raise ValueError("codes and scales must be on one device")
         self.codes, self.scales = codes, scales
         self._ref = C.byref(self.cfg)
+        self._append, self._attn = lib().kvq_block_append, lib().kvq_block_attn
+        self._kv = (c.n_tokens, c.n_kv_heads, 128), (c.n_kv_heads * 128, 128, 1)
+        self._q = (c.n_tokens, c.n_q_heads, 128), (c.n_q_heads * 128, 128, 1)
+        self._lse = (c.n_tokens, c.n_q_heads)
 
-    def _tables(self, tables):
+    def _ready(self, tables):
+        """The current device, which the layer and the tables must be on."""
         if tables.shared != self.shared:
             raise ValueError(f"tables and layer differ in {', '.join(_SHARED)}: {tables.shared}, {self.shared}")
-        return tables._refs[1]
+        d = _here()
+        if d != self.device or d != tables.device:
+            raise ValueError(f"the layer is on cuda:{self.device}, the tables on cuda:{tables.device}, the current device is cuda:{d}")
+        return d
 
     def append(self, tables: Tables, k, v, q=None, q_out=None, q_weight=None, k_weight=None, stream=None):
         """The planned tokens' keys and values [n_tokens, Hkv, 128] into the blocks,
         and the queries [n_tokens, Hq, 128] normed and rotated into q_out (q itself,
         or apart from it).  k, v, q may be parts of one projection's rows."""
-        c = self.cfg
-        tp = self._tables(tables)
-        kp, ks = _rows(k, "k", c.n_tokens, c.n_kv_heads)
-        vp, vs = _rows(v, "v", c.n_tokens, c.n_kv_heads)
-        qp = op = None
+        d = self._ready(tables)
+        kp, ks = _strided(k, "k", *self._kv, d)
+        vp, vs = _strided(v, "v", *self._kv, d)
+        qp = op = wq = wk = None
         qs = 0
         if q is not None or q_out is not None:
             if q is None or q_out is None:
                 raise ValueError("q and q_out go together")
-            qp, qs = _rows(q, "q", c.n_tokens, c.n_q_heads)
-            op, os_ = _rows(q_out, "q_out", c.n_tokens, c.n_q_heads)
-            if os_ != c.n_q_heads * 128:
-                raise ValueError("q_out must be contiguous")
-        _on_device(tables.lens, self.codes, k, v, q, q_out, q_weight, k_weight)
-        _check("kvq_block_append", lib().kvq_block_append(
-            self._ref, tp, self._codes, self._scales, kp, ks, vp, vs, qp, qs, op, _weight(q_weight, "q_weight"),
-            _weight(k_weight, "k_weight"), _stream_of(stream, k)))
+            qp, qs = _strided(q, "q", *self._q, d)
+            op = _dense(q_out, "q_out", torch.float16, self._q[0], d)
+        if q_weight is not None:
+            wq = _dense(q_weight, "q_weight", torch.float16, (128,), d)
+        if k_weight is not None:
+            wk = _dense(k_weight, "k_weight", torch.float16, (128,), d)
+        st = self._append(self._ref, tables._refs[1], self._codes, self._scales, kp, ks, vp, vs, qp, qs, op, wq, wk, _stream_on(stream, d))
+        if st:
+            _check("kvq_block_append", st)
 
     def attn(self, tables: Tables, q, out, lse=None, workspace=None, stream=None):
         """Attention of the planned tokens' queries [n_tokens, Hq, 128] (as append
         leaves them) over their requests' blocks into out, and the log-sum-exp
         [n_tokens, Hq] into lse."""
-        import torch
-        c = self.cfg
-        tp = self._tables(tables)
-        qp, qs = _rows(q, "q", c.n_tokens, c.n_q_heads)
-        op, os_ = _rows(out, "out", c.n_tokens, c.n_q_heads)
-        if qs != c.n_q_heads * 128 or os_ != qs:
-            raise ValueError("q and out must be contiguous")
-        lp = None
-        if lse is not None:
-            lp = _arg(lse, "lse", torch.float32, 4 * c.n_tokens * c.n_q_heads)
-            if tuple(lse.shape) != (c.n_tokens, c.n_q_heads):
-                raise ValueError(f"lse: expected shape {(c.n_tokens, c.n_q_heads)}, got {tuple(lse.shape)}")
+        d = self._ready(tables)
+        qp = _dense(q, "q", torch.float16, self._q[0], d)
+        op = _dense(out, "out", torch.float16, self._q[0], d)
+        lp = None if lse is None else _dense(lse, "lse", torch.float32, self._lse, d)
         if workspace is None:
             raise KvqError("kvq_block_attn", -4)
-        wp = _arg(workspace, "workspace", torch.uint8, 0)
-        _on_device(tables.lens, self.codes, q, out, lse, workspace)
-        _check("kvq_block_attn", lib().kvq_block_attn(self._ref, tp, self._codes, self._scales, qp, op, lp, wp,
-                                                     workspace.nbytes, _stream_of(stream, q)))
+        wp = _dense(workspace, "workspace", torch.uint8, workspace.shape, d)
+        st = self._attn(self._ref, tables._refs[1], self._codes, self._scales, qp, op, lp, wp, workspace.nbytes, _stream_on(stream, d))
+        if st:
+            _check("kvq_block_attn", st)
