@@ -23,7 +23,7 @@ namespace kvq {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;  // at most
 constexpr int kPlanCtas = 8;
 
 // Inclusive sums over the CTA of up to three values per thread.
@@ -105,7 +105,9 @@ __global__ void __launch_bounds__(kPlanThreads) block_plan_kernel(const __grid_c
       s_start[G.B] = (int)u[1];
     }
   }
-  cg::this_cluster().sync();  // (a barrier of the CTA too) every old length and count is read
+  // every old length and count is read
+  if (gridDim.x > 1) cg::this_cluster().sync();
+  else __syncthreads();
   grid_dep_trigger();
 
   if (rank == 0 && mine) {
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) block_plan_kernel(const __grid_c
     }
     if (b == G.B - 1) p.t.free_count[0] = all - s_new0[G.B];
   }
-  const int tid = rank * kPlanThreads + b, threads = gridDim.x * kPlanThreads;
+  const int tid = rank * blockDim.x + b, threads = gridDim.x * blockDim.x;
   const auto came_back = [&](int i) {  // the i-th block that comes back
     const int r = range_of(s_back0, G.B, i);
     return p.t.block_table[(size_t)r * G.max_blocks + (i - s_back0[r])];
@@ -151,10 +153,11 @@ __global__ void __launch_bounds__(kPlanThreads) block_plan_kernel(const __grid_c
 
 cudaError_t launch_block_plan(const BlockPlanParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  // one CTA where its threads cover the token slots
+  // a thread per request; one CTA where a thread per token slot fits it, too
   const int ctas = p.geo.N <= kPlanThreads ? 1 : kPlanCtas;
+  const int want = ctas == 1 ? p.geo.N : 512, threads = ((p.geo.B > want ? p.geo.B : want) + 31) / 32 * 32;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -163,7 +166,7 @@ cudaError_t launch_block_plan(const BlockPlanParams& p, cudaStream_t st) {
   attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = ctas == 1 ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, block_plan_kernel, p);
 }
 
