@@ -128,10 +128,23 @@ __host__ __device__ inline BlockRequest request_at(const BlockAttnParams& p, int
 }
 
 // What a (request, head, row block) costs beyond its tiles, in tiles: the teams'
-// parts are joined (some 2 us, of 0.2 us a tile), or one team takes it alone and
-// the others go on.
+// parts are joined (of 8 to 20 tiles' time, 16 measured best: 64 ragged requests
+// to 8k tokens 62 us with 8, 57 with 16, 58 with 20), or one team takes it alone
+// and the others go on (up to 8 tiles: 256 requests of 200 tokens 62 us with 4,
+// 32 with 8; with 16, the ragged batch loses 4 us).
 constexpr int kSoloTiles = 8;
-constexpr int kJoinTiles = 8;
+constexpr int kJoinTiles = 16;
+// Short ones are not cut between CTAs, which would have to join them: up to
+// kUncutTiles, where ranges that end with whole ones are at most kUncutExtra tiles
+// longer (64 requests of 100 tokens 20.6 us cut, 10.8 whole; 16 of 1000, 16.7 and
+// 11.6; one of 1024 tokens, one head: 8.9 cut, 10.5 whole).
+constexpr int kUncutTiles = 48;
+constexpr int kUncutExtra = 16;
+__host__ __device__ inline bool block_uncut(int cnt, long long per) {
+  if (cnt > kUncutTiles) return false;
+  const int range = per < (1 << 30) ? (int)per : 1 << 30;
+  return (range / cnt + 1) * (long long)cnt - range <= kUncutExtra;  // (as many begin in a range, at most)
+}
 
 // One segment: tiles k0..k1 of a (request, head, row block).
 struct BlockSegment {
@@ -140,26 +153,28 @@ struct BlockSegment {
   int k0, k1, ns, lo;          // its visible tiles in the CTA's range (k1 <= the block's own count)
   long long x;                 // where the (request, head, row block) begins
   int cnt;                     // and its own count of tiles
+  bool whole;                  // the CTA has all of it
 
-  // Whether the range [x0, x1) holds all of it.
-  __host__ __device__ bool whole(long long x0, long long x1) const { return x >= x0 && x + cnt <= x1; }
   // Whether one of the CTA's teams takes it by itself, with nothing to join: it is
   // short, and the range holds enough of its like for the other teams.
-  __host__ __device__ bool solo(long long x0, long long x1, long long per, int teams) const {
-    return cnt <= kSoloTiles && (long long)cnt * teams <= 2 * per && whole(x0, x1);
+  __host__ __device__ bool solo(long long per, int teams) const {
+    return whole && cnt <= kSoloTiles && (long long)cnt * teams <= 2 * per;
   }
 };
 
 template <int ROWS>
 struct BlockWalk {
-  long long x, x1;  // the range left
+  long long x, x0, x1;  // where it is, and the range
   int b, j, k;      // next: request, (head, row block) of it, tile
   int streams, nrb, cnt;  // cnt: tiles of a (head, row block) in the schedule, what it costs beyond them included
+  long long per;
+  bool uncut;
   BlockRequest r;
 
   __host__ __device__ inline void load(const BlockAttnParams& p) {
     r = request_at(p, b);
     size(p, r, &nrb, &streams, &cnt);
+    uncut = block_uncut(cnt, per);
   }
   __host__ __device__ static inline void size(const BlockAttnParams& p, const BlockRequest& r, int* nrb, int* streams, int* cnt) {
     *nrb = (int)(((long long)r.n * p.geo.g + ROWS - 1) / ROWS);
@@ -167,9 +182,9 @@ struct BlockWalk {
     const int most = r.n ? block_tiles_max(p.window, p.n_first, r, p.geo.g, ROWS) : 0;
     *cnt = most + (most > kSoloTiles ? kJoinTiles : 1);
   }
-  // the range [x, x1), whose first tile is tile x - xb of request b
-  __host__ __device__ inline void begin(const BlockAttnParams& p, long long x_, long long x1_, int b_, long long xb) {
-    x = x_, x1 = x1_, b = b_;
+  // the range [x, x1), of ranges of `per`, whose first tile is tile x - xb of request b
+  __host__ __device__ inline void begin(const BlockAttnParams& p, long long x_, long long x1_, long long per_, int b_, long long xb) {
+    x = x0 = x_, x1 = x1_, per = per_, b = b_;
     load(p);
     const long long at = x - xb;
     j = (int)udiv(at, cnt);
@@ -194,18 +209,21 @@ struct BlockWalk {
         p0 += s.r0 / G.g;
       }
       const BlockTiles t = block_tiles(p.window, p.n_first, p0, p1);
+      // (one that is not cut belongs to the range that it begins in)
       const long long left = x1 - x;
-      const int end = left < cnt - k ? k + (int)left : cnt;
+      const int end = uncut || left >= cnt - k ? cnt : k + (int)left;
       s.b = b, s.first = r.first, s.before = r.before, s.n = r.n;
       s.k0 = k;
       s.k1 = end < t.cnt ? end : t.cnt;
       s.ns = t.ns, s.lo = t.lo;
       s.x = x - k;
       s.cnt = t.cnt;
+      s.whole = uncut || (s.x >= x0 && s.x + t.cnt <= x1);
+      const bool here = uncut ? k == 0 : s.k0 < s.k1;  // (or the range begins behind its tiles)
       x += end - k;
       k = 0;
       ++j;
-      if (s.k0 < s.k1) return true;  // (else the range begins behind its tiles)
+      if (here) return true;
     }
     return false;
   }

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   grid_dep_trigger();  // the next kernel may come as the CTAs leave
 
   BlockWalk<ROWS> walk, ahead;
-  walk.begin(p, x0, x1, sm.first_b, sm.first_x);
+  walk.begin(p, x0, x1, per, sm.first_b, sm.first_x);
   ahead = walk;
   uint8_t* const ring = sm.stage[team * RING];
   // A segment that one team takes goes to the team that has the fewest tiles of such
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
       bool solo;
       do {
         if (!(have = ahead.next(p, as))) return;
-        solo = as.solo(x0, x1, per, TEAMS);
+        solo = as.solo(per, TEAMS);
       } while (solo && take(load_ahead, as) != team);
       step = solo ? 1 : TEAMS;
       ai = as.k0 + (solo ? 0 : team);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   const auto next_segment = [&](BlockSegment& s) {
     do {
       if (!walk.next(p, s)) return false;
-    } while (s.solo(x0, x1, per, TEAMS) && take(load, s) != team);
+    } while (s.solo(per, TEAMS) && take(load, s) != team);
     load_q(s);
     return true;
   };
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   int parts = 0;  // 1: the range begins, 2: it ends within a (request, head, row block)
   bool more = next_segment(s);
   while (more) {
-    const bool solo = s.solo(x0, x1, per, TEAMS);
+    const bool solo = s.solo(per, TEAMS);
     const int tile_step = solo ? 1 : TEAMS;
     const int seg_rows = min(16, s.rows - rt * 16);  // of this warp; may be none
     float O[8][2][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
       }
     }
 
-    const bool whole = done.whole(x0, x1);
+    const bool whole = done.whole;
     if (solo || team == 0) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {

@@ -66,7 +66,7 @@ static int trial() {
     int b0 = 0;
     while (!(x0 >= first[b0] && x0 < first[b0 + 1])) ++b0;
     BlockWalk<ROWS> w;
-    w.begin(p, x0, x1, b0, first[b0]);
+    w.begin(p, x0, x1, per, b0, first[b0]);
     BlockSegment s;
     while (w.next(p, s)) {
       const auto key = std::make_tuple(s.b, s.h, s.r0 / ROWS);
@@ -75,9 +75,9 @@ static int trial() {
         const int tile = tile_of(s, k);
         if (tile < 0 || tile >= G.max_blocks || !got[key].insert(tile).second) ++bad;
       }
-      const bool whole = s.x >= x0 && s.x + s.cnt <= x1;
+      const bool whole = s.whole;
       const int c0 = (int)(s.x / per), c1 = (int)((s.x + s.cnt - 1) / per);
-      if (whole != (c0 == c1) || s.k0 >= s.k1 || c < c0 || c > c1) ++bad;
+      if (s.k0 >= s.k1 || c < c0 || c > c1 || (whole ? s.k0 != 0 || s.k1 != s.cnt : c0 == c1)) ++bad;
       if (!whole) {
         ++parts[key];
         expect[key] = c1 - c0 + 1;
