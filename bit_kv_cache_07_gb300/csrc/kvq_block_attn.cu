@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   // The segment that copies are asked for in, the team's next tile of it, and the
   // block ids of 32 of its tiles, one per lane.
   BlockSegment as = {};
-  int ai = 0, step = TEAMS, load_ahead = 0, issued = 0, id_at = 0, ids = 0;
+  int ai = 0, step = TEAMS, load_ahead = 0, issued = 0, in_slot = 0, id_at = 0, ids = 0;
+  uint32_t in_turn = 0;
   bool have = rt == 0;
   const auto look_up = [&]() {  // by the team's first warp
     const int k = ai + lane * step;
@@ -172,8 +173,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   };
   const auto issue = [&]() {  // copies of the next tile
     if (!have) return;
-    const int slot = issued % RING, turn = issued / RING, st = team * RING + slot;
-    if (RT > 1 && turn && !mbar_wait(smem_u32(&sm.empty[st]), (turn - 1) & 1, gave_up)) {
+    const int slot = in_slot, st = team * RING + slot;
+    if (RT > 1 && in_turn && !mbar_wait(smem_u32(&sm.empty[st]), (in_turn - 1) & 1, gave_up)) {
       have = false;
       return;
     }
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
       bulk_copy(smem_u32(sm.scale16[st]), p.scales + (place * 2 & ~(size_t)15), 16, bar);
     }
     ++issued;
+    if (++in_slot == RING) in_slot = 0, ++in_turn;
     ++id_at;
     ai += step;
     find();
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     for (int i = 0; i < RING - 1; ++i) issue();
   }
 
-  int used = 0;  // tiles that the team has consumed
+  int out_slot = 0;  // of the tile that the team is at
+  uint32_t out_phase = 0;
   int load = 0;
   // Queries of a segment: channel 32 tq + 4 k + {0, 1 | 2, 3} enters step k of the
   // product as its row 2 tq + {0, 1 | 8, 9}.
@@ -245,8 +248,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
 
     for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
       if (rt == 0) issue();
-      const int slot = used % RING, st = team * RING + slot;
-      const bool ok = mbar_wait(smem_u32(&sm.full[st]), (used / RING) & 1, gave_up);
+      const int slot = out_slot, st = team * RING + slot;
+      const bool ok = mbar_wait(smem_u32(&sm.full[st]), out_phase, gave_up);
       if (!ok) {  // the rows become NaN, and nothing more is asked for
         l[0] = l[1] = NAN;
         have = false;
@@ -275,48 +278,48 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
             mma16816(S[j], qa[k], b0, b1);
           }
         }
-        // ---- logits in log2 units, less the reference
-        float base[2] = {ev - ref[0], ev - ref[1]};
+        // ---- logits in log2 units, less the reference (hidden keys: -infinity), weights
         const bool masked = t0 + kBlockTokens - 1 > p_lo || (p.window < kNoWindow && t0 <= p_hi - p.window);
-        uint32_t hide = 0;
-        if (masked) {
+        uint32_t pa[2][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int t = t0 + 8 * j + 2 * tq + (e & 1), pos = see[e >> 1];
-              const bool vis = t <= pos && (pos - t < p.window || t < p.n_first);
-              hide |= vis ? 0u : 1u << (4 * j + e);
-            }
-        }
-        float z[4][4];
-        bool move = false;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            z[j][e] = fmaf(S[j][e], f, base[e >> 1]);
-            if (hide >> (4 * j + e) & 1) z[j][e] = -INFINITY;
-            move |= z[j][e] > kMoveAt;
+        for (int hf = 0; hf < 2; ++hf) {
+          if (hf && seg_rows <= 8) {
+            pa[0][1] = pa[0][3] = pa[1][1] = pa[1][3] = 0;
+            break;
           }
-        if (__any_sync(0xffffffffu, move)) {
+          float z[4][2];
+          const float base = ev - ref[hf];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float top = -INFINITY, high = -INFINITY;
+          for (int j = 0; j < 4; ++j) {
+            z[j][0] = fmaf(S[j][2 * hf], f, base);
+            z[j][1] = fmaf(S[j][2 * hf + 1], f, base);
+          }
+          if (masked) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-              for (int e = 2 * hf; e < 2 * hf + 2; ++e) {
-                if (!(hide >> (4 * j + e) & 1)) top = fmaxf(top, fmaf(S[j][e], f, ev));
-                high = fmaxf(high, z[j][e]);
+              for (int e = 0; e < 2; ++e) {
+                const int t = t0 + 8 * j + 2 * tq + e;
+                if (!(t <= see[hf] && (see[hf] - t < p.window || t < p.n_first))) z[j][e] = -INFINITY;
               }
+          }
+          float high = fmaxf(z[0][0], z[0][1]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) high = fmaxf(high, fmaxf(z[j][0], z[j][1]));
+          if (__any_sync(0xffffffffu, high > kMoveAt)) {  // a row's reference moves
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (z[j][e] != -INFINITY) top = fmaxf(top, fmaf(S[j][2 * hf + e], f, ev));
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
               high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
             }
             if (high > kMoveAt) {
-              const float to = top - kRoom, a = ex2(ref[hf] - to);
+              const float to = top - kRoom, a = ex2(ref[hf] - to), base_to = ev - to;
               ref[hf] = to;
               l[hf] *= a;
 #pragma unroll
@@ -326,29 +329,23 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
                   O[c][q][2 * hf] *= a;
                   O[c][q][2 * hf + 1] *= a;
                 }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (z[j][e] != -INFINITY) z[j][e] = fmaf(S[j][2 * hf + e], f, base_to);
             }
-            base[hf] = ev - ref[hf];
           }
+          float sum = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!(hide >> (4 * j + e) & 1)) z[j][e] = fmaf(S[j][e], f, base[e >> 1]);
-        }
-        float sum[2] = {0.0f, 0.0f};
-        uint32_t pa[2][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            z[j][e] = ex2(z[j][e]);
-            sum[e >> 1] += z[j][e];
+          for (int j = 0; j < 4; ++j) {
+            z[j][0] = ex2(z[j][0]);
+            z[j][1] = ex2(z[j][1]);
+            sum += z[j][0] + z[j][1];
+            pa[j >> 1][2 * (j & 1) + hf] = pack_halves(z[j][0], z[j][1]);
           }
-          pa[j >> 1][2 * (j & 1)] = pack_halves(z[j][0], z[j][1]);
-          pa[j >> 1][2 * (j & 1) + 1] = pack_halves(z[j][2], z[j][3]);
+          l[hf] = fmaf(sum, inv_v, l[hf]);
         }
-        l[0] = fmaf(sum[0], inv_v, l[0]);
-        l[1] = fmaf(sum[1], inv_v, l[1]);
         // ---- values: a pair of adjacent channels of two tokens per register, sorted by channel
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
@@ -367,7 +364,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
             }
           }
       }
-      ++used;
+      if (++out_slot == RING) out_slot = 0, out_phase ^= 1;
       if constexpr (RT > 1) mbar_arrive_warp(smem_u32(&sm.empty[st]));
       else __syncwarp();
     }
