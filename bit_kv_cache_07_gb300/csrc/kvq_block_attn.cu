@@ -40,20 +40,21 @@ constexpr int kStages = kWarps * kStagesPerWarp;
 constexpr float kRoom = 12.0f;       // weights up to 2^12 at a new reference,
 constexpr float kMoveAt = 15.0f;     // up to 2^15 before it moves (fp16 ends at 2^16)
 
+template <typename Walk>
 struct AttnSmem {
   uint8_t stage[kStages][kPairBytes];
-  float4 join[4][16][32];      // 4 row tiles of accumulators, lane by lane
+  float4 join[kWarps][16][32];  // the warps' accumulators, row by row
   uint8_t scale16[kStages][16];
   uint64_t full[kStages], empty[kStages];
-  float2 join_ml[4][16];
+  float2 join_ml[kWarps][16];
   int meta[kStages];           // byte of scale16 where the tile's scales are; -1: no such block
   long long warp_sum[kWarps];
-  long long first_x;           // the range's first request: where it begins
   BlockSegment parted[2];
   int last[2], from[2];
-  int first_b, gave_up;
+  int gave_up;
+  Walk first;                  // at the range's begin
 };
-static_assert(sizeof(AttnSmem) <= 227 * 1024, "shared memory");
+static_assert(sizeof(AttnSmem<BlockWalk<16>>) <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -84,12 +85,20 @@ __device__ __forceinline__ size_t row_at(const BlockAttnParams& p, const BlockSe
   return (size_t)(s.first + i) * p.geo.Hq + s.h * p.geo.g + j;
 }
 
+// A finished row: lane's four channels of sum w v, the weights' sum, their reference.
+__device__ __forceinline__ void put_row(const BlockAttnParams& p, const BlockSegment& s, int r, int lane, float ref, float l, const float (&acc)[4]) {
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const size_t row = row_at(p, s, r);
+  *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) = make_uint2(pack_halves(acc[0] * inv, acc[1] * inv), pack_halves(acc[2] * inv, acc[3] * inv));
+  if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+}
+
 // RT: 16-row tiles that read a KV head's blocks together
 template <int RT>
 __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __grid_constant__ BlockAttnParams p) {
   constexpr int ROWS = 16 * RT, TEAMS = kWarps / RT, RING = kStagesPerWarp * RT;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  AttnSmem& sm = *reinterpret_cast<AttnSmem*>(smem_raw);
+  AttnSmem<BlockWalk<ROWS>>& sm = *reinterpret_cast<AttnSmem<BlockWalk<ROWS>>*>(smem_raw);
   const BlockGeo& G = p.geo;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, team = w / RT, rt = w % RT;
   const int gq = lane >> 2, tq = lane & 3;
@@ -136,16 +145,14 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   long long at = upto - run;
 #pragma unroll
   for (int i = 0; i < kMaxBlockBatch / kThreadsAttn; ++i) {
-    if (x0 >= at && x0 < at + mine[i]) sm.first_b = tid * turns + i, sm.first_x = at;
+    if (x0 >= at && x0 < at + mine[i]) sm.first.begin(p, x0, x1, per, tid * turns + i, at);
     at += mine[i];
   }
   __syncthreads();
 
   grid_dep_trigger();  // the next kernel may come as the CTAs leave
 
-  BlockWalk<ROWS> walk, ahead;
-  walk.begin(p, x0, x1, per, sm.first_b, sm.first_x);
-  ahead = walk;
+  BlockWalk<ROWS> walk = sm.first, ahead = walk;
   uint8_t* const ring = sm.stage[team * RING];
   // A segment that one team takes goes to the team that has the fewest tiles of such
   // so far, the first of them (lane t of `load`: team t's; every warp keeps the same).
@@ -241,6 +248,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     return true;
   };
   BlockSegment s;
+  bool joined = false;
   int parts = 0;  // 1: the range begins, 2: it ends within a (request, head, row block)
   bool more = next_segment(s);
   while (more) {
@@ -387,67 +395,59 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], o);
-    if (!solo) {
-#pragma unroll
-      for (int half = TEAMS / 2; half >= 1; half >>= 1) {
-        const int to = (team - half) * RT + rt;
-        if (team >= half && team < 2 * half) {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            if (8 * hf >= seg_rows) break;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              sm.join[to][2 * c + hf][lane] = make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]);
-            if (tq == 0) sm.join_ml[to][gq + 8 * hf] = make_float2(ref[hf], l[hf]);
-          }
-        }
-        __syncthreads();
-        if (team < half) {
-          const int from = team * RT + rt;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            if (8 * hf >= seg_rows) break;
-            const float2 o = sm.join_ml[from][gq + 8 * hf];
-            const float to_ref = fmaxf(ref[hf], o.x), zero = to_ref == -INFINITY ? 0.0f : to_ref;
-            const float a = ex2(ref[hf] - zero), b = ex2(o.x - zero);
-            ref[hf] = to_ref;
-            l[hf] = a * l[hf] + b * o.y;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float4 v = sm.join[from][2 * c + hf][lane];
-              O[c][0][2 * hf] = a * O[c][0][2 * hf] + b * v.x;
-              O[c][1][2 * hf] = a * O[c][1][2 * hf] + b * v.y;
-              O[c][0][2 * hf + 1] = a * O[c][0][2 * hf + 1] + b * v.z;
-              O[c][1][2 * hf + 1] = a * O[c][1][2 * hf + 1] + b * v.w;
-            }
-          }
-        }
-        __syncthreads();
-      }
-    }
-
-    const bool whole = done.whole;
-    if (solo || team == 0) {
+    if (solo) {  // (whole)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const int r = rt * 16 + gq + 8 * hf;
         if (r >= done.rows) continue;
-        if (whole) {
-          const float inv = l[hf] == 0.0f ? 0.0f : 1.0f / l[hf];
-          const size_t row = row_at(p, done, r);
+        const float inv = l[hf] == 0.0f ? 0.0f : 1.0f / l[hf];
+        const size_t row = row_at(p, done, r);
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 16 * c + 4 * tq) =
-                make_uint2(pack_halves(O[c][0][2 * hf] * inv, O[c][1][2 * hf] * inv), pack_halves(O[c][0][2 * hf + 1] * inv, O[c][1][2 * hf + 1] * inv));
-          if (p.lse && tq == 0) p.lse[row] = l[hf] == 0.0f ? -INFINITY : (ref[hf] + log2f(l[hf])) * 0.6931471805599453f;
-        } else {
-          const size_t at_row = (size_t)piece_slot(done.x, per, blockIdx.x) * ROWS + r;
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 16 * c + 4 * tq) =
+              make_uint2(pack_halves(O[c][0][2 * hf] * inv, O[c][1][2 * hf] * inv), pack_halves(O[c][0][2 * hf + 1] * inv, O[c][1][2 * hf + 1] * inv));
+        if (p.lse && tq == 0) p.lse[row] = l[hf] == 0.0f ? -INFINITY : (ref[hf] + log2f(l[hf])) * 0.6931471805599453f;
+      }
+      continue;
+    }
+    if (joined) __syncthreads();  // the parts of the segment before have been read
+    joined = true;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim + 16 * c + 4 * tq),
-                   make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]));
-          if (tq == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(ref[hf], l[hf]));
-        }
+    for (int hf = 0; hf < 2; ++hf) {
+      if (8 * hf >= seg_rows) break;
+      const int r = gq + 8 * hf;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)  // (odd rows four places on: no two rows of a store in one bank)
+        sm.join[w][r][(4 * c + tq) ^ (r & 1) << 2] = make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]);
+      if (tq == 0) sm.join_ml[w][r] = make_float2(ref[hf], l[hf]);
+    }
+    __syncthreads();
+    const bool whole = done.whole;
+    for (int r = w; r < done.rows; r += kWarps) {
+      float2 ml[TEAMS];
+      float top = -INFINITY, L = 0.0f, acc[4] = {};
+#pragma unroll
+      for (int t = 0; t < TEAMS; ++t) {
+        ml[t] = sm.join_ml[t * RT + (r >> 4)][r & 15];
+        top = fmaxf(top, ml[t].x);
+      }
+      const float zero = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int t = 0; t < TEAMS; ++t) {
+        const float e = ex2(ml[t].x - zero);
+        const float4 v = sm.join[t * RT + (r >> 4)][r & 15][lane ^ (r & 1) << 2];
+        L = fmaf(e, ml[t].y, L);
+        acc[0] = fmaf(e, v.x, acc[0]);
+        acc[1] = fmaf(e, v.y, acc[1]);
+        acc[2] = fmaf(e, v.z, acc[2]);
+        acc[3] = fmaf(e, v.w, acc[3]);
+      }
+      if (whole) {
+        put_row(p, done, r, lane, top, L, acc);
+      } else {
+        const size_t at_row = (size_t)piece_slot(done.x, per, blockIdx.x) * ROWS + r;
+        __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim) + lane, make_float4(acc[0], acc[1], acc[2], acc[3]));
+        if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(top, L));
       }
     }
     if (!whole) {  // its turn comes at the range's end
@@ -513,11 +513,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
           }
         }
         L = warp_sum(L);
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const size_t row = row_at(p, d, r);
-        *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) =
-            make_uint2(pack_halves(acc[0] * inv, acc[1] * inv), pack_halves(acc[2] * inv, acc[3] * inv));
-        if (p.lse && lane == 0) p.lse[row] = L == 0.0f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
+        put_row(p, d, r, lane, top, L, acc);
       }
     }
   }
@@ -529,9 +525,9 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
 template <int RT>
 cudaError_t launch_rows(const BlockAttnParams& p, int sms, cudaStream_t st) {
   static std::atomic<long long> memo[kMemoDevices];
-  const cudaError_t e = ensure_smem_limit(block_attn_kernel<RT>, memo, (int)sizeof(AttnSmem));
+  const cudaError_t e = ensure_smem_limit(block_attn_kernel<RT>, memo, (int)sizeof(AttnSmem<BlockWalk<16 * RT>>));
   if (e != cudaSuccess) return e;
-  return launch_dependent(block_attn_kernel<RT>, dim3(sms), dim3(kThreadsAttn), sizeof(AttnSmem), st, p);
+  return launch_dependent(block_attn_kernel<RT>, dim3(sms), dim3(kThreadsAttn), sizeof(AttnSmem<BlockWalk<16 * RT>>), st, p);
 }
 
 }  // namespace
