@@ -14,7 +14,7 @@ static kvq_status block_geometry(const kvq_block_config* c, BlockGeo* g) {
       !std::isfinite(c->norm_eps) || c->norm_eps < 0.0f)
     return KVQ_ERR_INVALID_ARG;
   if (c->head_dim != kHeadDim || c->batch > kMaxBlockBatch || c->n_tokens > (1 << 20) || c->n_kv_heads > 1024 || c->n_q_heads > 1024 * c->n_kv_heads ||
-      c->n_blocks > (1 << 26) || c->max_blocks > (1 << 25))
+      c->n_blocks > (1 << 26) || c->max_blocks > (1 << 25) || (int64_t)c->n_tokens * c->n_q_heads > (1 << 30))
     return KVQ_ERR_UNSUPPORTED;
   *g = BlockGeo{c->batch, c->n_tokens, c->n_q_heads, c->n_kv_heads, c->n_q_heads / c->n_kv_heads, c->n_blocks, c->max_blocks};
   return KVQ_OK;

@@ -620,7 +620,7 @@ KVQ_API kvq_status kvq_evict_workspace(const kvq_config *cfg, uint64_t *bytes);
 typedef struct kvq_block_config {
     int32_t batch;            /* requests of a step, 1..1024 (slots of the tables) */
     int32_t n_tokens;         /* token slots of a step: rows of q, k, v, q_out, out;
-                                 1..2^20                                       */
+                                 1..2^20, and n_tokens * n_q_heads <= 2^30     */
     int32_t n_q_heads;        /* Hq, a multiple of n_kv_heads, up to 1024 times it */
     int32_t n_kv_heads;       /* Hkv, 1..1024                                  */
     int32_t head_dim;         /* 128                                           */

@@ -40,6 +40,12 @@ def test_config_refusals(field, value, status):
     assert e.value.status == status
 
 
+def test_too_many_rows():
+    with pytest.raises(binding.KvqError) as e:
+        blocks.layout(config(n_tokens=1 << 20, n_q_heads=2048, n_kv_heads=16))
+    assert e.value.status == -2
+
+
 def test_unknown_names():
     with pytest.raises(ValueError):
         blocks.make_config(dict(batch=1, heads=3))
