@@ -93,19 +93,20 @@ __device__ __forceinline__ void put_row(const BlockAttnParams& p, const BlockSeg
   if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
 }
 
-// RT: 16-row tiles that read a KV head's blocks together
-template <int RT>
+// RT: 16-row tiles that read a KV head's blocks together, MT of them by one warp (one
+// conversion of keys and values for both; its queries then lie in shared memory)
+template <int RT, int MT>
 __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __grid_constant__ BlockAttnParams p) {
-  constexpr int ROWS = 16 * RT, TEAMS = kWarps / RT, RING = kStagesPerWarp * RT;
+  constexpr int ROWS = 16 * RT, WT = RT / MT, TEAMS = kWarps / WT, RING = kStagesPerWarp * WT;  // WT: warps of a team
   extern __shared__ __align__(128) unsigned char smem_raw[];
   AttnSmem<BlockWalk<ROWS>>& sm = *reinterpret_cast<AttnSmem<BlockWalk<ROWS>>*>(smem_raw);
   const BlockGeo& G = p.geo;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, team = w / RT, rt = w % RT;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, team = w / WT, wt = w % WT;
   const int gq = lane >> 2, tq = lane & 3;
   volatile int* gave_up = &sm.gave_up;
   if (tid < kStages) {
     mbar_init(smem_u32(&sm.full[tid]), 1);
-    mbar_init(smem_u32(&sm.empty[tid]), RT);
+    mbar_init(smem_u32(&sm.empty[tid]), WT);
   }
   if (tid == 0) sm.gave_up = 0;
   asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   BlockSegment as = {};
   int ai = 0, step = TEAMS, load_ahead = 0, issued = 0, in_slot = 0, id_at = 0, ids = 0;
   uint32_t in_turn = 0;
-  bool have = rt == 0;
+  bool have = wt == 0;
   const auto look_up = [&]() {  // by the team's first warp
     const int k = ai + lane * step;
     ids = k < as.k1 ? __ldg(p.t.block_table + (size_t)as.b * G.max_blocks + tile_of(as, k)) : 0;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   const auto issue = [&]() {  // copies of the next tile
     if (!have) return;
     const int slot = in_slot, st = team * RING + slot;
-    if (RT > 1 && in_turn && !mbar_wait(smem_u32(&sm.empty[st]), (in_turn - 1) & 1, gave_up)) {
+    if (WT > 1 && in_turn && !mbar_wait(smem_u32(&sm.empty[st]), (in_turn - 1) & 1, gave_up)) {
       have = false;
       return;
     }
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     ai += step;
     find();
   };
-  if (rt == 0) {
+  if (wt == 0) {
     find();
     for (int i = 0; i < RING - 1; ++i) issue();
   }
@@ -222,55 +223,72 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   int load = 0;
   // Queries of a segment: channel 32 tq + 4 k + {0, 1 | 2, 3} enters step k of the
   // product as its row 2 tq + {0, 1 | 8, 9}.
-  uint32_t qa[8][4];
+  uint32_t qa[MT == 1 ? 8 : 1][4];
+  uint4* const q_mine = reinterpret_cast<uint4*>(sm.join[w]);  // MT 2: [tile][step][lane], the lane's own words
   const auto load_q = [&](const BlockSegment& s) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = min(rt * 16 + gq + 8 * hf, s.rows - 1);  // (rows that are not there: the last one again)
-      uint4 v[4];
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(p, s, r) * kHeadDim + 32 * tq);
+    for (int m = 0; m < MT; ++m) {
+      uint4 v[2][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = __ldg(src + u);
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(v);
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = min((wt * MT + m) * 16 + gq + 8 * hf, s.rows - 1);  // (rows that are not there: the last one again)
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(p, s, r) * kHeadDim + 32 * tq);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[hf][u] = __ldg(src + u);
+      }
+      const uint32_t *lo = reinterpret_cast<const uint32_t*>(v[0]), *hi = reinterpret_cast<const uint32_t*>(v[1]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        qa[k][hf] = vw[2 * k];
-        qa[k][2 + hf] = vw[2 * k + 1];
+        if constexpr (MT == 1) {
+          qa[k][0] = lo[2 * k], qa[k][1] = hi[2 * k], qa[k][2] = lo[2 * k + 1], qa[k][3] = hi[2 * k + 1];
+        } else {
+          q_mine[(m * 8 + k) * 32 + lane] = make_uint4(lo[2 * k], hi[2 * k], lo[2 * k + 1], hi[2 * k + 1]);
+        }
       }
     }
   };
-  // the next segment that the team has a part in; its queries are on the way
+  // the next segment that the team has a part in (MT 1: its queries are on the way)
   const auto next_segment = [&](BlockSegment& s) {
     do {
       if (!walk.next(p, s)) return false;
     } while (s.solo(per, TEAMS) && take(load, s) != team);
-    load_q(s);
+    if (MT == 1) load_q(s);
     return true;
   };
   BlockSegment s;
   bool joined = false;
   int parts = 0;  // 1: the range begins, 2: it ends within a (request, head, row block)
   bool more = next_segment(s);
+  if (MT > 1 && more) load_q(s);
   while (more) {
     const bool solo = s.solo(per, TEAMS);
     const int tile_step = solo ? 1 : TEAMS;
-    const int seg_rows = min(16, s.rows - rt * 16);  // of this warp; may be none
-    float O[8][2][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    // last position that a row sees
-    const int see[2] = {s.before + token_at(p, s, min(rt * 16 + gq, s.rows - 1)), s.before + token_at(p, s, min(rt * 16 + gq + 8, s.rows - 1))};
+    const int row0 = wt * MT * 16, seg_rows = s.rows - row0;  // rows from this warp's first on; may be none
+    float O[MT][8][2][4], ref[MT][2], l[MT][2];
+    int see[MT][2];  // last position that a row sees
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        ref[m][hf] = -INFINITY;
+        l[m][hf] = 0.0f;
+        see[m][hf] = s.before + token_at(p, s, min(row0 + 16 * m + gq + 8 * hf, s.rows - 1));
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) O[m][c][e >> 2][e & 3] = 0.0f;
+    }
     const bool active = seg_rows > 0;
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) O[c][e >> 2][e & 3] = 0.0f;
     const int p_lo = s.before + token_at(p, s, 0), p_hi = s.before + token_at(p, s, s.rows - 1);  // positions of the block's rows
 
     for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
-      if (rt == 0) issue();
+      if (wt == 0) issue();
       const int slot = out_slot, st = team * RING + slot;
-      const bool ok = mbar_wait(smem_u32(&sm.full[st]), out_phase, gave_up);
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), out_phase, gave_up));
       if (!ok) {  // the rows become NaN, and nothing more is asked for
-        l[0] = l[1] = NAN;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) l[m][0] = l[m][1] = NAN;
         have = false;
       }
       if (ok && active) {
@@ -281,37 +299,55 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
         const float f = kb == kScaleNaN ? NAN : p.q_scale * __uint_as_float((uint32_t)kb << 23);
         const float ev = vb == kScaleNaN ? NAN : (float)(vb - kScaleBias);
         const float inv_v = __uint_as_float((uint32_t)(254 - min(vb, 254)) << 23);
-        float S[4][4];
+        float S[MT][4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.0f;
-          const uint8_t* row = K + (8 * j + gq) * kHeadDim;
-          uint4 c[2];
-          c[0] = *reinterpret_cast<const uint4*>(row + (((2 * tq) ^ gq) << 4));
-          c[1] = *reinterpret_cast<const uint4*>(row + (((2 * tq + 1) ^ gq) << 4));
-          const uint32_t* cw = reinterpret_cast<const uint32_t*>(c);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t b0, b1;
-            e4m3_halves(cw[k], b0, b1);
-            mma16816(S[j], qa[k], b0, b1);
+          for (int j = 0; j < 4; ++j) S[m][j][0] = S[m][j][1] = S[m][j][2] = S[m][j][3] = 0.0f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // of the channels
+          uint4 kc[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            kc[j] = *reinterpret_cast<const uint4*>(K + (8 * j + gq) * kHeadDim + (((2 * tq + half) ^ gq) << 4));
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k) {
+            uint32_t a[MT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              if constexpr (MT == 1) {
+                a[m][0] = qa[k][0], a[m][1] = qa[k][1], a[m][2] = qa[k][2], a[m][3] = qa[k][3];
+              } else {
+                const uint4 q = q_mine[(m * 8 + k) * 32 + lane];
+                a[m][0] = q.x, a[m][1] = q.y, a[m][2] = q.z, a[m][3] = q.w;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t b0, b1;
+              e4m3_halves(reinterpret_cast<const uint32_t*>(&kc[j])[k & 3], b0, b1);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) mma16816(S[m][j], a[m], b0, b1);
+            }
           }
         }
         // ---- logits in log2 units, less the reference (hidden keys: -infinity), weights
         const bool masked = t0 + kBlockTokens - 1 > p_lo || (p.window < kNoWindow && t0 <= p_hi - p.window);
-        uint32_t pa[2][4];
+        uint32_t pa[MT][2][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          if (hf && seg_rows <= 8) {
-            pa[0][1] = pa[0][3] = pa[1][1] = pa[1][3] = 0;
-            break;
+          if (16 * m + 8 * hf >= seg_rows) {  // no such rows
+            pa[m][0][hf] = pa[m][0][2 + hf] = pa[m][1][hf] = pa[m][1][2 + hf] = 0;
+            continue;
           }
           float z[4][2];
-          const float base = ev - ref[hf];
+          const float base = ev - ref[m][hf];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            z[j][0] = fmaf(S[j][2 * hf], f, base);
-            z[j][1] = fmaf(S[j][2 * hf + 1], f, base);
+            z[j][0] = fmaf(S[m][j][2 * hf], f, base);
+            z[j][1] = fmaf(S[m][j][2 * hf + 1], f, base);
           }
           if (masked) {
 #pragma unroll
@@ -319,7 +355,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int t = t0 + 8 * j + 2 * tq + e;
-                if (!(t <= see[hf] && (see[hf] - t < p.window || t < p.n_first))) z[j][e] = -INFINITY;
+                if (!(t <= see[m][hf] && (see[m][hf] - t < p.window || t < p.n_first))) z[j][e] = -INFINITY;
               }
           }
           float high = fmaxf(z[0][0], z[0][1]);
@@ -331,28 +367,28 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
             for (int j = 0; j < 4; ++j)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (z[j][e] != -INFINITY) top = fmaxf(top, fmaf(S[j][2 * hf + e], f, ev));
+                if (z[j][e] != -INFINITY) top = fmaxf(top, fmaf(S[m][j][2 * hf + e], f, ev));
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
               high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
             }
             if (high > kMoveAt) {
-              const float to = top - kRoom, a = ex2(ref[hf] - to), base_to = ev - to;
-              ref[hf] = to;
-              l[hf] *= a;
+              const float to = top - kRoom, a = ex2(ref[m][hf] - to), base_to = ev - to;
+              ref[m][hf] = to;
+              l[m][hf] *= a;
 #pragma unroll
               for (int c = 0; c < 8; ++c)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                  O[c][q][2 * hf] *= a;
-                  O[c][q][2 * hf + 1] *= a;
+                  O[m][c][q][2 * hf] *= a;
+                  O[m][c][q][2 * hf + 1] *= a;
                 }
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  if (z[j][e] != -INFINITY) z[j][e] = fmaf(S[j][2 * hf + e], f, base_to);
+                  if (z[j][e] != -INFINITY) z[j][e] = fmaf(S[m][j][2 * hf + e], f, base_to);
             }
           }
           float sum = 0.0f;
@@ -361,9 +397,9 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
             z[j][0] = ex2(z[j][0]);
             z[j][1] = ex2(z[j][1]);
             sum += z[j][0] + z[j][1];
-            pa[j >> 1][2 * (j & 1) + hf] = pack_halves(z[j][0], z[j][1]);
+            pa[m][j >> 1][2 * (j & 1) + hf] = pack_halves(z[j][0], z[j][1]);
           }
-          l[hf] = fmaf(sum, inv_v, l[hf]);
+          l[m][hf] = fmaf(sum, inv_v, l[m][hf]);
         }
         // ---- values: a pair of adjacent channels of two tokens per register, sorted by channel
 #pragma unroll
@@ -378,13 +414,16 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
               uint32_t e0, o0, e1, o1;
               e4m3_halves(__byte_perm(v[2 * u], 0, 0x3120), e0, o0);
               e4m3_halves(__byte_perm(v[2 * u + 1], 0, 0x3120), e1, o1);
-              mma16816(O[c + u][0], pa[kk], e0, e1);
-              mma16816(O[c + u][1], pa[kk], o0, o1);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816(O[m][c + u][0], pa[m][kk], e0, e1);
+                mma16816(O[m][c + u][1], pa[m][kk], o0, o1);
+              }
             }
           }
       }
       if (++out_slot == RING) out_slot = 0, out_phase ^= 1;
-      if constexpr (RT > 1) mbar_arrive_warp(smem_u32(&sm.empty[st]));
+      if constexpr (WT > 1) mbar_arrive_warp(smem_u32(&sm.empty[st]));
       else __syncwarp();
     }
 
@@ -392,63 +431,83 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     more = next_segment(s);
     // ---- the teams' parts, joined in a fixed order
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], o);
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) l[m][hf] += __shfl_xor_sync(0xffffffffu, l[m][hf], o);
     if (solo) {  // (whole)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = rt * 16 + gq + 8 * hf;
-        if (r >= done.rows) continue;
-        const float inv = l[hf] == 0.0f ? 0.0f : 1.0f / l[hf];
-        const size_t row = row_at(p, done, r);
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 16 * c + 4 * tq) =
-              make_uint2(pack_halves(O[c][0][2 * hf] * inv, O[c][1][2 * hf] * inv), pack_halves(O[c][0][2 * hf + 1] * inv, O[c][1][2 * hf + 1] * inv));
-        if (p.lse && tq == 0) p.lse[row] = l[hf] == 0.0f ? -INFINITY : (ref[hf] + log2f(l[hf])) * 0.6931471805599453f;
-      }
+        for (int hf = 0; hf < 2; ++hf) {
+          const int r = row0 + 16 * m + gq + 8 * hf;
+          if (r >= done.rows) continue;
+          const float inv = l[m][hf] == 0.0f ? 0.0f : 1.0f / l[m][hf];
+          const size_t row = row_at(p, done, r);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const float(&o)[2][4] = O[m][c];
+            *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 16 * c + 4 * tq) =
+                make_uint2(pack_halves(o[0][2 * hf] * inv, o[1][2 * hf] * inv), pack_halves(o[0][2 * hf + 1] * inv, o[1][2 * hf + 1] * inv));
+          }
+          if (p.lse && tq == 0) p.lse[row] = l[m][hf] == 0.0f ? -INFINITY : (ref[m][hf] + log2f(l[m][hf])) * 0.6931471805599453f;
+        }
+      if (MT > 1 && more) load_q(s);
       continue;
     }
-    if (joined) __syncthreads();  // the parts of the segment before have been read
-    joined = true;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      if (8 * hf >= seg_rows) break;
-      const int r = gq + 8 * hf;
-#pragma unroll
-      for (int c = 0; c < 8; ++c)  // (odd rows four places on: no two rows of a store in one bank)
-        sm.join[w][r][(4 * c + tq) ^ (r & 1) << 2] = make_float4(O[c][0][2 * hf], O[c][1][2 * hf], O[c][0][2 * hf + 1], O[c][1][2 * hf + 1]);
-      if (tq == 0) sm.join_ml[w][r] = make_float2(ref[hf], l[hf]);
-    }
-    __syncthreads();
     const bool whole = done.whole;
-    for (int r = w; r < done.rows; r += kWarps) {
-      float2 ml[TEAMS];
-      float top = -INFINITY, L = 0.0f, acc[4] = {};
 #pragma unroll
-      for (int t = 0; t < TEAMS; ++t) {
-        ml[t] = sm.join_ml[t * RT + (r >> 4)][r & 15];
-        top = fmaxf(top, ml[t].x);
-      }
-      const float zero = top == -INFINITY ? 0.0f : top;
+    for (int m = 0; m < MT; ++m) {
+      if (MT > 1 && 16 * m >= done.rows) break;  // (no team has such rows)
+      if (joined) __syncthreads();  // the parts of the time before have been read
+      joined = true;
 #pragma unroll
-      for (int t = 0; t < TEAMS; ++t) {
-        const float e = ex2(ml[t].x - zero);
-        const float4 v = sm.join[t * RT + (r >> 4)][r & 15][lane ^ (r & 1) << 2];
-        L = fmaf(e, ml[t].y, L);
-        acc[0] = fmaf(e, v.x, acc[0]);
-        acc[1] = fmaf(e, v.y, acc[1]);
-        acc[2] = fmaf(e, v.z, acc[2]);
-        acc[3] = fmaf(e, v.w, acc[3]);
+      for (int hf = 0; hf < 2; ++hf) {
+        if (16 * m + 8 * hf >= seg_rows) break;
+        const int r = gq + 8 * hf;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // (odd rows four places on: no two rows of a store in one bank)
+          const float(&o)[2][4] = O[m][c];
+          sm.join[w][r][(4 * c + tq) ^ (r & 1) << 2] = make_float4(o[0][2 * hf], o[1][2 * hf], o[0][2 * hf + 1], o[1][2 * hf + 1]);
+        }
+        if (tq == 0) sm.join_ml[w][r] = make_float2(ref[m][hf], l[m][hf]);
       }
-      if (whole) {
-        put_row(p, done, r, lane, top, L, acc);
-      } else {
-        const size_t at_row = (size_t)piece_slot(done.x, per, blockIdx.x) * ROWS + r;
-        __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim) + lane, make_float4(acc[0], acc[1], acc[2], acc[3]));
-        if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(top, L));
+      __syncthreads();
+      for (int r = w; r < done.rows; r += kWarps) {
+        if (MT > 1 && (r >> 4) % MT != m) continue;
+        const int from = (r >> 4) / MT;  // warp of each team
+        float2 ml[TEAMS];
+        float top = -INFINITY, L = 0.0f, acc[4] = {};
+#pragma unroll
+        for (int t = 0; t < TEAMS; ++t) {
+          ml[t] = sm.join_ml[t * WT + from][r & 15];
+          top = fmaxf(top, ml[t].x);
+        }
+        const float zero = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int t = 0; t < TEAMS; ++t) {
+          const float e = ex2(ml[t].x - zero);
+          const float4 v = sm.join[t * WT + from][r & 15][lane ^ (r & 1) << 2];
+          L = fmaf(e, ml[t].y, L);
+          acc[0] = fmaf(e, v.x, acc[0]);
+          acc[1] = fmaf(e, v.y, acc[1]);
+          acc[2] = fmaf(e, v.z, acc[2]);
+          acc[3] = fmaf(e, v.w, acc[3]);
+        }
+        if (whole) {
+          put_row(p, done, r, lane, top, L, acc);
+        } else {
+          const size_t at_row = (size_t)piece_slot(done.x, per, blockIdx.x) * ROWS + r;
+          __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim) + lane, make_float4(acc[0], acc[1], acc[2], acc[3]));
+          if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(top, L));
+        }
       }
+    }
+    if constexpr (MT > 1) {
+      __syncthreads();
+      joined = false;
+      if (more) load_q(s);
     }
     if (!whole) {  // its turn comes at the range's end
       if (tid == 0) sm.parted[done.x >= x0 ? 1 : 0] = done;
@@ -518,22 +577,22 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     }
   }
   // copies in flight end before the CTA does (all were waited for, unless a wait ran out)
-  if (rt == 0 && *gave_up)
+  if (wt == 0 && *gave_up)
     for (int i = max(0, issued - RING); i < issued; ++i) mbar_wait(smem_u32(&sm.full[team * RING + i % RING]), (i / RING) & 1, nullptr);
 }
 
-template <int RT>
+template <int RT, int MT>
 cudaError_t launch_rows(const BlockAttnParams& p, int sms, cudaStream_t st) {
   static std::atomic<long long> memo[kMemoDevices];
-  const cudaError_t e = ensure_smem_limit(block_attn_kernel<RT>, memo, (int)sizeof(AttnSmem<BlockWalk<16 * RT>>));
+  const cudaError_t e = ensure_smem_limit(block_attn_kernel<RT, MT>, memo, (int)sizeof(AttnSmem<BlockWalk<16 * RT>>));
   if (e != cudaSuccess) return e;
-  return launch_dependent(block_attn_kernel<RT>, dim3(sms), dim3(kThreadsAttn), sizeof(AttnSmem<BlockWalk<16 * RT>>), st, p);
+  return launch_dependent(block_attn_kernel<RT, MT>, dim3(sms), dim3(kThreadsAttn), sizeof(AttnSmem<BlockWalk<16 * RT>>), st, p);
 }
 
 }  // namespace
 
 cudaError_t launch_block_attn(const BlockAttnParams& p, int sms, int rows, cudaStream_t st) {
-  return rows == 16 ? launch_rows<1>(p, sms, st) : rows == 32 ? launch_rows<2>(p, sms, st) : launch_rows<4>(p, sms, st);
+  return rows == 16 ? launch_rows<1, 1>(p, sms, st) : rows == 32 ? launch_rows<2, 2>(p, sms, st) : launch_rows<4, 2>(p, sms, st);
 }
 
 }  // namespace kvq
