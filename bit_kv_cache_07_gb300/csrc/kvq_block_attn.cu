@@ -24,12 +24,13 @@
 // half of a 128-row tcgen05 tile, and its operands would have to be written back
 // to shared memory as fp16 first (4 times the tile's bytes); here the
 // conversion happens in the registers that feed the product.
-#include "kvq_block.cuh"
-#include "kvq_pipe.cuh"
+#include "kvq_block_tile.cuh"
 
 namespace kvq {
 
 namespace {
+
+using namespace kvq::tile;
 
 constexpr int kWarps = kBlockWarps;
 constexpr int kThreadsAttn = 32 * kWarps;
@@ -37,8 +38,6 @@ constexpr int kStagesPerWarp = 2;    // a tile at work, one on the way: with two
                                      // flight) 16 x 32k tokens take 171 us, with one 160
 constexpr int kPairBytes = 2 * kBlockSide;  // a tile: K then V
 constexpr int kStages = kWarps * kStagesPerWarp;
-constexpr float kRoom = 12.0f;       // weights up to 2^12 at a new reference,
-constexpr float kMoveAt = 15.0f;     // up to 2^15 before it moves (fp16 ends at 2^16)
 
 template <typename Walk>
 struct AttnSmem {
@@ -58,9 +57,6 @@ static_assert(sizeof(AttnSmem<BlockWalk<16>>) <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void e4m3_halves(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n" : "=r"(lo), "=r"(hi) : "r"(four));
-}
 // bulk_copy with an L2 policy: blocks that one (head, row block) reads leave L2 first
 // (16 x 32k tokens 160.6 to 158.5 us, 256k 84.6 to 82.7), those that several read stay.
 __device__ __forceinline__ void stream_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
@@ -68,41 +64,22 @@ __device__ __forceinline__ void stream_copy(uint32_t dst, const void* src, uint3
                "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar), "l"(policy)
                : "memory");
 }
-__device__ __forceinline__ uint32_t pack_halves(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Token (of the request's new ones) of row r of a segment's block: a row below 64 and
-// what r0 lies into its token are below 2^11, so the product with ceil(2^32 / g) is exact.
-__device__ __forceinline__ int token_at(const BlockAttnParams& p, const BlockSegment& s, int r) {
-  const int i0 = s.r0 ? s.r0 / p.geo.g : 0, x = s.r0 - i0 * p.geo.g + r;
-  return i0 + (p.geo.g > 1 ? (int)__umulhi((unsigned)x, p.g_inv) : x);
-}
-// Row of q and out.
-__device__ __forceinline__ size_t row_at(const BlockAttnParams& p, const BlockSegment& s, int r) {
-  const int i = token_at(p, s, r), j = s.r0 + r - i * p.geo.g;
-  return (size_t)(s.first + i) * p.geo.Hq + s.h * p.geo.g + j;
-}
-
 // A finished row: lane's four channels of sum w v, the weights' sum, their reference.
 __device__ __forceinline__ void put_row(const BlockAttnParams& p, const BlockSegment& s, int r, int lane, float ref, float l, const float (&acc)[4]) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t row = row_at(p, s, r);
   *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 4 * lane) = make_uint2(pack_halves(acc[0] * inv, acc[1] * inv), pack_halves(acc[2] * inv, acc[3] * inv));
-  if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+  if (p.lse && lane == 0) p.lse[row] = log_sum(ref, l);
 }
 
-// RT: 16-row tiles that read a KV head's blocks together, MT of them by one warp (one
-// conversion of keys and values for both; its queries then lie in shared memory)
-template <int RT, int MT>
+// Math: a warp's arithmetic; WT: warps of a team, each with rows of its own
+template <typename Math, int WT>
 __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __grid_constant__ BlockAttnParams p) {
-  constexpr int ROWS = 16 * RT, WT = RT / MT, TEAMS = kWarps / WT, RING = kStagesPerWarp * WT;  // WT: warps of a team
+  constexpr int ROWS = Math::kRows * WT, TEAMS = kWarps / WT, RING = kStagesPerWarp * WT;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   AttnSmem<BlockWalk<ROWS>>& sm = *reinterpret_cast<AttnSmem<BlockWalk<ROWS>>*>(smem_raw);
   const BlockGeo& G = p.geo;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, team = w / WT, wt = w % WT;
-  const int gq = lane >> 2, tq = lane & 3;
   volatile int* gave_up = &sm.gave_up;
   if (tid < kStages) {
     mbar_init(smem_u32(&sm.full[tid]), 1);
@@ -221,65 +198,29 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   int out_slot = 0;  // of the tile that the team is at
   uint32_t out_phase = 0;
   int load = 0;
-  // Queries of a segment: channel 32 tq + 4 k + {0, 1 | 2, 3} enters step k of the
-  // product as its row 2 tq + {0, 1 | 8, 9}.
-  uint32_t qa[MT == 1 ? 8 : 1][4];
-  uint4* const q_mine = reinterpret_cast<uint4*>(sm.join[w]);  // MT 2: [tile][step][lane], the lane's own words
-  const auto load_q = [&](const BlockSegment& s) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      uint4 v[2][4];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = min((wt * MT + m) * 16 + gq + 8 * hf, s.rows - 1);  // (rows that are not there: the last one again)
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_at(p, s, r) * kHeadDim + 32 * tq);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[hf][u] = __ldg(src + u);
-      }
-      const uint32_t *lo = reinterpret_cast<const uint32_t*>(v[0]), *hi = reinterpret_cast<const uint32_t*>(v[1]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if constexpr (MT == 1) {
-          qa[k][0] = lo[2 * k], qa[k][1] = hi[2 * k], qa[k][2] = lo[2 * k + 1], qa[k][3] = hi[2 * k + 1];
-        } else {
-          q_mine[(m * 8 + k) * 32 + lane] = make_uint4(lo[2 * k], hi[2 * k], lo[2 * k + 1], hi[2 * k + 1]);
-        }
-      }
-    }
-  };
-  // the next segment that the team has a part in (MT 1: its queries are on the way)
+  Math math;
+  const int row0 = wt * Math::kRows;                            // of a block's rows
+  uint4* const q_mine = reinterpret_cast<uint4*>(sm.join[w]);  // queries that do not fit the registers lie where the join will be
+  // the next segment that the team has a part in; its queries are on the way where
+  // the registers hold them
   const auto next_segment = [&](BlockSegment& s) {
     do {
       if (!walk.next(p, s)) return false;
     } while (s.solo(per, TEAMS) && take(load, s) != team);
-    if (MT == 1) load_q(s);
+    if constexpr (Math::kQueriesAhead) math.load_q(p, s, row0, lane, q_mine);
     return true;
   };
   BlockSegment s;
   bool joined = false;
   int parts = 0;  // 1: the range begins, 2: it ends within a (request, head, row block)
   bool more = next_segment(s);
-  if (MT > 1 && more) load_q(s);
+  if (!Math::kQueriesAhead && more) math.load_q(p, s, row0, lane, q_mine);
   while (more) {
     const bool solo = s.solo(per, TEAMS);
     const int tile_step = solo ? 1 : TEAMS;
-    const int row0 = wt * MT * 16, seg_rows = s.rows - row0;  // rows from this warp's first on; may be none
-    float O[MT][8][2][4], ref[MT][2], l[MT][2];
-    int see[MT][2];  // last position that a row sees
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        ref[m][hf] = -INFINITY;
-        l[m][hf] = 0.0f;
-        see[m][hf] = s.before + token_at(p, s, min(row0 + 16 * m + gq + 8 * hf, s.rows - 1));
-      }
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) O[m][c][e >> 2][e & 3] = 0.0f;
-    }
+    const int seg_rows = s.rows - row0;  // from this warp's first one on; may be none
     const bool active = seg_rows > 0;
+    math.begin(p, s, row0, lane);
     const int p_lo = s.before + token_at(p, s, 0), p_hi = s.before + token_at(p, s, s.rows - 1);  // positions of the block's rows
 
     for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
@@ -287,140 +228,23 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
       const int slot = out_slot, st = team * RING + slot;
       const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), out_phase, gave_up));
       if (!ok) {  // the rows become NaN, and nothing more is asked for
-#pragma unroll
-        for (int m = 0; m < MT; ++m) l[m][0] = l[m][1] = NAN;
+        math.spoil();
         have = false;
       }
       if (ok && active) {
-        const uint8_t* K = ring + slot * kPairBytes;
-        const uint32_t V = smem_u32(K + kBlockSide);
-        const int meta = sm.meta[st], t0 = tile_of(s, i) * kBlockTokens;
+        const int meta = sm.meta[st];
         const int kb = meta < 0 ? kScaleNaN : sm.scale16[st][meta & 15], vb = meta < 0 ? kScaleNaN : sm.scale16[st][(meta & 15) + 1];
-        const float f = kb == kScaleNaN ? NAN : p.q_scale * __uint_as_float((uint32_t)kb << 23);
-        const float ev = vb == kScaleNaN ? NAN : (float)(vb - kScaleBias);
-        const float inv_v = __uint_as_float((uint32_t)(254 - min(vb, 254)) << 23);
-        float S[MT][4][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) S[m][j][0] = S[m][j][1] = S[m][j][2] = S[m][j][3] = 0.0f;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // of the channels
-          uint4 kc[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            kc[j] = *reinterpret_cast<const uint4*>(K + (8 * j + gq) * kHeadDim + (((2 * tq + half) ^ gq) << 4));
-#pragma unroll
-          for (int k = 4 * half; k < 4 * half + 4; ++k) {
-            uint32_t a[MT][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              if constexpr (MT == 1) {
-                a[m][0] = qa[k][0], a[m][1] = qa[k][1], a[m][2] = qa[k][2], a[m][3] = qa[k][3];
-              } else {
-                const uint4 q = q_mine[(m * 8 + k) * 32 + lane];
-                a[m][0] = q.x, a[m][1] = q.y, a[m][2] = q.z, a[m][3] = q.w;
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t b0, b1;
-              e4m3_halves(reinterpret_cast<const uint32_t*>(&kc[j])[k & 3], b0, b1);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) mma16816(S[m][j], a[m], b0, b1);
-            }
-          }
-        }
-        // ---- logits in log2 units, less the reference (hidden keys: -infinity), weights
-        const bool masked = t0 + kBlockTokens - 1 > p_lo || (p.window < kNoWindow && t0 <= p_hi - p.window);
-        uint32_t pa[MT][2][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (16 * m + 8 * hf >= seg_rows) {  // no such rows
-            pa[m][0][hf] = pa[m][0][2 + hf] = pa[m][1][hf] = pa[m][1][2 + hf] = 0;
-            continue;
-          }
-          float z[4][2];
-          const float base = ev - ref[m][hf];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z[j][0] = fmaf(S[m][j][2 * hf], f, base);
-            z[j][1] = fmaf(S[m][j][2 * hf + 1], f, base);
-          }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int t = t0 + 8 * j + 2 * tq + e;
-                if (!(t <= see[m][hf] && (see[m][hf] - t < p.window || t < p.n_first))) z[j][e] = -INFINITY;
-              }
-          }
-          float high = fmaxf(z[0][0], z[0][1]);
-#pragma unroll
-          for (int j = 1; j < 4; ++j) high = fmaxf(high, fmaxf(z[j][0], z[j][1]));
-          if (__any_sync(0xffffffffu, high > kMoveAt)) {  // a row's reference moves
-            float top = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (z[j][e] != -INFINITY) top = fmaxf(top, fmaf(S[m][j][2 * hf + e], f, ev));
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-            }
-            if (high > kMoveAt) {
-              const float to = top - kRoom, a = ex2(ref[m][hf] - to), base_to = ev - to;
-              ref[m][hf] = to;
-              l[m][hf] *= a;
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  O[m][c][q][2 * hf] *= a;
-                  O[m][c][q][2 * hf + 1] *= a;
-                }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (z[j][e] != -INFINITY) z[j][e] = fmaf(S[m][j][2 * hf + e], f, base_to);
-            }
-          }
-          float sum = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z[j][0] = ex2(z[j][0]);
-            z[j][1] = ex2(z[j][1]);
-            sum += z[j][0] + z[j][1];
-            pa[m][j >> 1][2 * (j & 1) + hf] = pack_halves(z[j][0], z[j][1]);
-          }
-          l[m][hf] = fmaf(sum, inv_v, l[m][hf]);
-        }
-        // ---- values: a pair of adjacent channels of two tokens per register, sorted by channel
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-          for (int c = 0; c < 8; c += 2) {
-            uint32_t v[4];
-            const int mt = lane >> 3, tok = 16 * kk + 8 * (mt & 1) + (lane & 7);
-            ldsm4t(v, V + tok * kHeadDim + (((c + (mt >> 1)) ^ (lane & 7)) << 4));
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t e0, o0, e1, o1;
-              e4m3_halves(__byte_perm(v[2 * u], 0, 0x3120), e0, o0);
-              e4m3_halves(__byte_perm(v[2 * u + 1], 0, 0x3120), e1, o1);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma16816(O[m][c + u][0], pa[m][kk], e0, e1);
-                mma16816(O[m][c + u][1], pa[m][kk], o0, o1);
-              }
-            }
-          }
+        Tile t;
+        t.K = ring + slot * kPairBytes;
+        t.V = smem_u32(t.K + kBlockSide);
+        t.f = kb == kScaleNaN ? NAN : p.q_scale * __uint_as_float((uint32_t)kb << 23);
+        t.ev = vb == kScaleNaN ? NAN : (float)(vb - kScaleBias);
+        t.inv_v = __uint_as_float((uint32_t)(254 - min(vb, 254)) << 23);
+        t.t0 = tile_of(s, i) * kBlockTokens;
+        t.masked = t.t0 + kBlockTokens - 1 > p_lo || (p.window < kNoWindow && t.t0 <= p_hi - p.window);
+        t.window = p.window;
+        t.n_first = p.n_first;
+        math.tile(t, lane, seg_rows, q_mine);
       }
       if (++out_slot == RING) out_slot = 0, out_phase ^= 1;
       if constexpr (WT > 1) mbar_arrive_warp(smem_u32(&sm.empty[st]));
@@ -430,65 +254,37 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     const BlockSegment done = s;
     more = next_segment(s);
     // ---- the teams' parts, joined in a fixed order
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) l[m][hf] += __shfl_xor_sync(0xffffffffu, l[m][hf], o);
+    math.close();
     if (solo) {  // (whole)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int r = row0 + 16 * m + gq + 8 * hf;
-          if (r >= done.rows) continue;
-          const float inv = l[m][hf] == 0.0f ? 0.0f : 1.0f / l[m][hf];
-          const size_t row = row_at(p, done, r);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float(&o)[2][4] = O[m][c];
-            *reinterpret_cast<uint2*>(p.out + row * kHeadDim + 16 * c + 4 * tq) =
-                make_uint2(pack_halves(o[0][2 * hf] * inv, o[1][2 * hf] * inv), pack_halves(o[0][2 * hf + 1] * inv, o[1][2 * hf + 1] * inv));
-          }
-          if (p.lse && tq == 0) p.lse[row] = l[m][hf] == 0.0f ? -INFINITY : (ref[m][hf] + log2f(l[m][hf])) * 0.6931471805599453f;
-        }
-      if (MT > 1 && more) load_q(s);
+      if (active) math.put(p, done, row0, lane);
+      if (!Math::kQueriesAhead && more) math.load_q(p, s, row0, lane, q_mine);
       continue;
     }
     const bool whole = done.whole;
+    constexpr int kPhaseRows = Math::kRows / Math::kPhases;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (MT > 1 && 16 * m >= done.rows) break;  // (no team has such rows)
+    for (int phase = 0; phase < Math::kPhases; ++phase) {
+      if (phase && kPhaseRows * phase >= done.rows) break;  // (no team has such rows)
       if (joined) __syncthreads();  // the parts of the time before have been read
       joined = true;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (16 * m + 8 * hf >= seg_rows) break;
-        const int r = gq + 8 * hf;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {  // (odd rows four places on: no two rows of a store in one bank)
-          const float(&o)[2][4] = O[m][c];
-          sm.join[w][r][(4 * c + tq) ^ (r & 1) << 2] = make_float4(o[0][2 * hf], o[1][2 * hf], o[0][2 * hf + 1], o[1][2 * hf + 1]);
-        }
-        if (tq == 0) sm.join_ml[w][r] = make_float2(ref[m][hf], l[m][hf]);
-      }
+      math.dump(phase, sm.join[w], sm.join_ml[w], lane, seg_rows);
       __syncthreads();
       for (int r = w; r < done.rows; r += kWarps) {
-        if (MT > 1 && (r >> 4) % MT != m) continue;
-        const int from = (r >> 4) / MT;  // warp of each team
+        const int part = r / kPhaseRows, in = r % kPhaseRows;
+        if (Math::kPhases > 1 && part % Math::kPhases != phase) continue;
+        const int from = part / Math::kPhases;  // warp of each team
         float2 ml[TEAMS];
         float top = -INFINITY, L = 0.0f, acc[4] = {};
 #pragma unroll
         for (int t = 0; t < TEAMS; ++t) {
-          ml[t] = sm.join_ml[t * WT + from][r & 15];
+          ml[t] = sm.join_ml[t * WT + from][in];
           top = fmaxf(top, ml[t].x);
         }
         const float zero = top == -INFINITY ? 0.0f : top;
 #pragma unroll
         for (int t = 0; t < TEAMS; ++t) {
           const float e = ex2(ml[t].x - zero);
-          const float4 v = sm.join[t * WT + from][r & 15][lane ^ (r & 1) << 2];
+          const float4 v = sm.join[t * WT + from][in][Math::place(in, lane)];
           L = fmaf(e, ml[t].y, L);
           acc[0] = fmaf(e, v.x, acc[0]);
           acc[1] = fmaf(e, v.y, acc[1]);
@@ -504,10 +300,10 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
         }
       }
     }
-    if constexpr (MT > 1) {
+    if constexpr (!Math::kQueriesAhead) {
       __syncthreads();
       joined = false;
-      if (more) load_q(s);
+      if (more) math.load_q(p, s, row0, lane, q_mine);
     }
     if (!whole) {  // its turn comes at the range's end
       if (tid == 0) sm.parted[done.x >= x0 ? 1 : 0] = done;
@@ -581,18 +377,24 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     for (int i = max(0, issued - RING); i < issued; ++i) mbar_wait(smem_u32(&sm.full[team * RING + i % RING]), (i / RING) & 1, nullptr);
 }
 
-template <int RT, int MT>
+template <typename Math, int WT>
 cudaError_t launch_rows(const BlockAttnParams& p, int sms, cudaStream_t st) {
+  constexpr int smem = (int)sizeof(AttnSmem<BlockWalk<Math::kRows * WT>>);
   static std::atomic<long long> memo[kMemoDevices];
-  const cudaError_t e = ensure_smem_limit(block_attn_kernel<RT, MT>, memo, (int)sizeof(AttnSmem<BlockWalk<16 * RT>>));
+  const cudaError_t e = ensure_smem_limit(block_attn_kernel<Math, WT>, memo, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(block_attn_kernel<RT, MT>, dim3(sms), dim3(kThreadsAttn), sizeof(AttnSmem<BlockWalk<16 * RT>>), st, p);
+  return launch_dependent(block_attn_kernel<Math, WT>, dim3(sms), dim3(kThreadsAttn), smem, st, p);
 }
 
 }  // namespace
 
 cudaError_t launch_block_attn(const BlockAttnParams& p, int sms, int rows, cudaStream_t st) {
-  return rows == 16 ? launch_rows<1, 1>(p, sms, st) : rows == 32 ? launch_rows<2, 2>(p, sms, st) : launch_rows<4, 2>(p, sms, st);
+  switch (rows) {
+    case 8: return launch_rows<Rows8, 1>(p, sms, st);
+    case 16: return launch_rows<RowsWide<1>, 1>(p, sms, st);
+    case 32: return launch_rows<RowsWide<2>, 1>(p, sms, st);
+    default: return launch_rows<RowsWide<2>, 2>(p, sms, st);
+  }
 }
 
 }  // namespace kvq

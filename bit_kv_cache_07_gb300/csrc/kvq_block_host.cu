@@ -135,7 +135,7 @@ kvq_status kvq_block_attn(const kvq_block_config* cfg, const kvq_block_tables* t
   // rows that read a KV head's blocks together: those of an even share of the
   // token slots (a request of more takes several passes)
   const long long rows = (long long)((g.N + g.B - 1) / g.B) * g.g;
-  return launch_block_attn(p, sms, rows <= 16 ? 16 : rows <= 32 ? 32 : 64, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_block_attn(p, sms, rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }

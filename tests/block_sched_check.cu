@@ -103,7 +103,7 @@ static int trial() {
 
 int main() {
   int bad = 0;
-  for (int i = 0; i < 400; ++i) bad += trial<16>() + trial<32>() + trial<64>();
+  for (int i = 0; i < 400; ++i) bad += trial<8>() + trial<16>() + trial<32>() + trial<64>();
   printf("bad %d\n", bad);
   return bad != 0;
 }
