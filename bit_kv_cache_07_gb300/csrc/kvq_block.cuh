@@ -162,19 +162,23 @@ struct BlockSegment {
   }
 };
 
+// A CTA's range of tiles, of ranges of `per`.
+struct BlockRange {
+  long long x0, x1, per;
+};
+
 template <int ROWS>
 struct BlockWalk {
-  long long x, x0, x1;  // where it is, and the range
+  long long x;      // where it is
   int b, j, k;      // next: request, (head, row block) of it, tile
   int streams, nrb, cnt;  // cnt: tiles of a (head, row block) in the schedule, what it costs beyond them included
-  long long per;
   bool uncut;
   BlockRequest r;
 
-  __host__ __device__ inline void load(const BlockAttnParams& p) {
+  __host__ __device__ inline void load(const BlockAttnParams& p, const BlockRange& g) {
     r = request_at(p, b);
     size(p, r, &nrb, &streams, &cnt);
-    uncut = block_uncut(cnt, per);
+    uncut = block_uncut(cnt, g.per);
   }
   __host__ __device__ static inline void size(const BlockAttnParams& p, const BlockRequest& r, int* nrb, int* streams, int* cnt) {
     *nrb = (int)(((long long)r.n * p.geo.g + ROWS - 1) / ROWS);
@@ -182,21 +186,21 @@ struct BlockWalk {
     const int most = r.n ? block_tiles_max(p.window, p.n_first, r, p.geo.g, ROWS) : 0;
     *cnt = most + (most > kSoloTiles ? kJoinTiles : 1);
   }
-  // the range [x, x1), of ranges of `per`, whose first tile is tile x - xb of request b
-  __host__ __device__ inline void begin(const BlockAttnParams& p, long long x_, long long x1_, long long per_, int b_, long long xb) {
-    x = x0 = x_, x1 = x1_, per = per_, b = b_;
-    load(p);
+  // the range g, whose first tile is tile x0 - xb of request b
+  __host__ __device__ inline void begin(const BlockAttnParams& p, const BlockRange& g, int b_, long long xb) {
+    x = g.x0, b = b_;
+    load(p, g);
     const long long at = x - xb;
     j = (int)udiv(at, cnt);
     k = (int)(at - (long long)j * cnt);
   }
-  __host__ __device__ inline bool next(const BlockAttnParams& p, BlockSegment& s) {
+  __host__ __device__ inline bool next(const BlockAttnParams& p, const BlockRange& g, BlockSegment& s) {
     const BlockGeo& G = p.geo;
-    while (x < x1) {
+    while (x < g.x1) {
       while (j >= streams) {
         if (++b >= G.B) return false;
         j = 0;
-        load(p);
+        load(p, g);
       }
       const int M = r.n * G.g;
       int p0 = r.before, p1 = r.before + r.n - 1;
@@ -210,7 +214,7 @@ struct BlockWalk {
       }
       const BlockTiles t = block_tiles(p.window, p.n_first, p0, p1);
       // (one that is not cut belongs to the range that it begins in)
-      const long long left = x1 - x;
+      const long long left = g.x1 - x;
       const int end = uncut || left >= cnt - k ? cnt : k + (int)left;
       s.b = b, s.first = r.first, s.before = r.before, s.n = r.n;
       s.k0 = k;
@@ -218,7 +222,7 @@ struct BlockWalk {
       s.ns = t.ns, s.lo = t.lo;
       s.x = x - k;
       s.cnt = t.cnt;
-      s.whole = uncut || (s.x >= x0 && s.x + t.cnt <= x1);
+      s.whole = uncut || (s.x >= g.x0 && s.x + t.cnt <= g.x1);
       const bool here = uncut ? k == 0 : s.k0 < s.k1;  // (or the range begins behind its tiles)
       x += end - k;
       k = 0;

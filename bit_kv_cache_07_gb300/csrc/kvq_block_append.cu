@@ -42,6 +42,8 @@ __device__ __forceinline__ void load_row(const uint16_t* row, int l, float (&v)[
   halves_to_floats(a, v);
   halves_to_floats(b, v + 8);
 }
+// Where pair i's frequency lies: the eight lanes of a row read side by side.
+__device__ __forceinline__ int freq_place(int i) { return (i & 7) * 8 + (i >> 3); }
 // What turns a row x into y / r (r: the row's own factor of the norm), weights and
 // sines of the token together:
 //   y_i = a_i x_i - b_i x_{i+64},  y_{i+64} = c_i x_{i+64} + d_i x_i.
@@ -56,7 +58,7 @@ __device__ __forceinline__ void make_turn(Turn& t, const uint16_t* weight, const
     t.a[i] = weight ? w[i] : 1.0f;
     t.c[i] = weight ? w[8 + i] : 1.0f;
     if (rotate) {
-      const int turns = (int)(unsigned)((freq[8 * l + i] * (unsigned long long)pos) >> 32);  // [-1/2, 1/2) turns
+      const int turns = (int)(unsigned)((freq[freq_place(8 * l + i)] * (unsigned long long)pos) >> 32);  // [-1/2, 1/2) turns
       const float x = (float)turns * 1.4629180792671596e-9f;                                 // 2 pi / 2^32
       const float cs = __cosf(x), sn = __sinf(x);
       t.b[i] = t.c[i] * sn;
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
   const BlockGeo& G = p.geo;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, l = lane & (kRowLanes - 1), sub = lane / kRowLanes;
   if (p.rotate)
-    for (int i = tid; i < kHeadDim / 2; i += 32 * WARPS) s_freq[i] = p.freq[i];
+    for (int i = tid; i < kHeadDim / 2; i += 32 * WARPS) s_freq[freq_place(i)] = p.freq[i];
   __syncthreads();
   grid_dep_wait();
   grid_dep_trigger();

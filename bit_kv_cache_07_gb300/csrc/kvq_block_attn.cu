@@ -11,19 +11,21 @@
 // a subset), so the products on the tensor cores are exact up to fp32 sums.
 //
 // Bound: the bytes of the visible blocks, each read once for up to 64 rows of a
-// KV head.  A 32-token tile of a head is two contiguous runs of 4 KB: one bulk
-// copy by one thread, stored in an order that both ldmatrix and the key loads
-// read without bank conflicts.  The visible tiles of all (request, head, row
-// block) lie end to end, cut into one equal range per SM; lengths come from the
-// GPU, so each CTA takes the prefix sums itself.  A CTA's eight warps form teams
-// of one warp per 16 rows; teams take a segment's tiles in turn, each with its
-// own ring of copies, which runs ahead across segments.  At a segment's end the
-// teams join their (ref, l, O) through shared memory, and a (request, head, row
-// block) that spans CTAs is joined by the CTA that comes last (nobody waits for
-// another CTA).  mma.sync rather than tcgen05: 1 to 64 rows fill an eighth to a
-// half of a 128-row tcgen05 tile, and its operands would have to be written back
-// to shared memory as fp16 first (4 times the tile's bytes); here the
-// conversion happens in the registers that feed the product.
+// KV head (16 x 32k tokens of 32 on 8 heads: 157 us, 6.8 TB/s).  A 32-token tile of a
+// head is one contiguous run of 8 KB: one bulk copy by one thread, stored in an order
+// that both ldmatrix and the key loads read without bank conflicts.  The visible
+// tiles of all (request, head, row block) lie end to end, cut into one equal range per
+// SM; lengths come from the GPU, so each CTA takes the prefix sums itself.  A CTA's
+// eight warps form teams of one warp per 16 rows (or 8); teams take a segment's tiles
+// in turn, each with its own ring of copies, which runs ahead across segments.  At a
+// segment's end the teams join their (ref, l, O) through shared memory, and a
+// (request, head, row block) that spans CTAs is joined by the CTA that comes last
+// (nobody waits for another CTA).  mma.sync rather than tcgen05: 1 to 64 rows fill an
+// eighth to a half of a 128-row tcgen05 tile, and its operands would have to be
+// written back to shared memory as fp16 first (4 times the tile's bytes); here the
+// conversion happens in the registers that feed the product.  Past 16 rows the tiles'
+// conversions, done again by every warp of a team, bound it (two warps a scheduler:
+// latency; 16 x 8k tokens of 32 on 8 heads: 45 us for 4 rows, 52 for 16, 96 for 32).
 #include "kvq_block_tile.cuh"
 
 namespace kvq {
@@ -120,10 +122,11 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   }
   const long long per = block_range(total, gridDim.x), x0 = per * blockIdx.x, x1 = min(total, x0 + per);
   if (x0 >= x1) return;
+  const BlockRange range{x0, x1, per};
   long long at = upto - run;
 #pragma unroll
   for (int i = 0; i < kMaxBlockBatch / kThreadsAttn; ++i) {
-    if (x0 >= at && x0 < at + mine[i]) sm.first.begin(p, x0, x1, per, tid * turns + i, at);
+    if (x0 >= at && x0 < at + mine[i]) sm.first.begin(p, range, tid * turns + i, at);
     at += mine[i];
   }
   __syncthreads();
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     while (ai >= as.k1) {
       bool solo;
       do {
-        if (!(have = ahead.next(p, as))) return;
+        if (!(have = ahead.next(p, range, as))) return;
         solo = as.solo(per, TEAMS);
       } while (solo && take(load_ahead, as) != team);
       step = solo ? 1 : TEAMS;
@@ -199,28 +202,25 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   uint32_t out_phase = 0;
   int load = 0;
   Math math;
-  const int row0 = wt * Math::kRows;                            // of a block's rows
-  uint4* const q_mine = reinterpret_cast<uint4*>(sm.join[w]);  // queries that do not fit the registers lie where the join will be
-  // the next segment that the team has a part in; its queries are on the way where
-  // the registers hold them
+  const int row0 = wt * Math::kRows;  // of a block's rows
+  // the next segment that the team has a part in; its queries are on the way
   const auto next_segment = [&](BlockSegment& s) {
     do {
-      if (!walk.next(p, s)) return false;
+      if (!walk.next(p, range, s)) return false;
     } while (s.solo(per, TEAMS) && take(load, s) != team);
-    if constexpr (Math::kQueriesAhead) math.load_q(p, s, row0, lane, q_mine);
+    math.load_q(p, s, row0, lane);
     return true;
   };
   BlockSegment s;
   bool joined = false;
   int parts = 0;  // 1: the range begins, 2: it ends within a (request, head, row block)
   bool more = next_segment(s);
-  if (!Math::kQueriesAhead && more) math.load_q(p, s, row0, lane, q_mine);
   while (more) {
     const bool solo = s.solo(per, TEAMS);
     const int tile_step = solo ? 1 : TEAMS;
     const int seg_rows = s.rows - row0;  // from this warp's first one on; may be none
     const bool active = seg_rows > 0;
-    math.begin(p, s, row0, lane);
+    math.begin();
     const int p_lo = s.before + token_at(p, s, 0), p_hi = s.before + token_at(p, s, s.rows - 1);  // positions of the block's rows
 
     for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
@@ -242,9 +242,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
         t.inv_v = __uint_as_float((uint32_t)(254 - min(vb, 254)) << 23);
         t.t0 = tile_of(s, i) * kBlockTokens;
         t.masked = t.t0 + kBlockTokens - 1 > p_lo || (p.window < kNoWindow && t.t0 <= p_hi - p.window);
-        t.window = p.window;
-        t.n_first = p.n_first;
-        math.tile(t, lane, seg_rows, q_mine);
+        math.tile(p, s, t, lane, row0);
       }
       if (++out_slot == RING) out_slot = 0, out_phase ^= 1;
       if constexpr (WT > 1) mbar_arrive_warp(smem_u32(&sm.empty[st]));
@@ -257,53 +255,40 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     math.close();
     if (solo) {  // (whole)
       if (active) math.put(p, done, row0, lane);
-      if (!Math::kQueriesAhead && more) math.load_q(p, s, row0, lane, q_mine);
       continue;
     }
     const bool whole = done.whole;
-    constexpr int kPhaseRows = Math::kRows / Math::kPhases;
+    if (joined) __syncthreads();  // the parts of the segment before have been read
+    joined = true;
+    math.dump(sm.join[w], sm.join_ml[w], lane);
+    __syncthreads();
+    for (int r = w; r < done.rows; r += kWarps) {
+      const int from = r / Math::kRows, in = r % Math::kRows;  // warp of each team, its row
+      float2 ml[TEAMS];
+      float top = -INFINITY, L = 0.0f, acc[4] = {};
 #pragma unroll
-    for (int phase = 0; phase < Math::kPhases; ++phase) {
-      if (phase && kPhaseRows * phase >= done.rows) break;  // (no team has such rows)
-      if (joined) __syncthreads();  // the parts of the time before have been read
-      joined = true;
-      math.dump(phase, sm.join[w], sm.join_ml[w], lane, seg_rows);
-      __syncthreads();
-      for (int r = w; r < done.rows; r += kWarps) {
-        const int part = r / kPhaseRows, in = r % kPhaseRows;
-        if (Math::kPhases > 1 && part % Math::kPhases != phase) continue;
-        const int from = part / Math::kPhases;  // warp of each team
-        float2 ml[TEAMS];
-        float top = -INFINITY, L = 0.0f, acc[4] = {};
-#pragma unroll
-        for (int t = 0; t < TEAMS; ++t) {
-          ml[t] = sm.join_ml[t * WT + from][in];
-          top = fmaxf(top, ml[t].x);
-        }
-        const float zero = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-        for (int t = 0; t < TEAMS; ++t) {
-          const float e = ex2(ml[t].x - zero);
-          const float4 v = sm.join[t * WT + from][in][Math::place(in, lane)];
-          L = fmaf(e, ml[t].y, L);
-          acc[0] = fmaf(e, v.x, acc[0]);
-          acc[1] = fmaf(e, v.y, acc[1]);
-          acc[2] = fmaf(e, v.z, acc[2]);
-          acc[3] = fmaf(e, v.w, acc[3]);
-        }
-        if (whole) {
-          put_row(p, done, r, lane, top, L, acc);
-        } else {
-          const size_t at_row = (size_t)piece_slot(done.x, per, blockIdx.x) * ROWS + r;
-          __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim) + lane, make_float4(acc[0], acc[1], acc[2], acc[3]));
-          if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(top, L));
-        }
+      for (int t = 0; t < TEAMS; ++t) {
+        ml[t] = sm.join_ml[t * WT + from][in];
+        top = fmaxf(top, ml[t].x);
       }
-    }
-    if constexpr (!Math::kQueriesAhead) {
-      __syncthreads();
-      joined = false;
-      if (more) math.load_q(p, s, row0, lane, q_mine);
+      const float zero = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int t = 0; t < TEAMS; ++t) {
+        const float e = ex2(ml[t].x - zero);
+        const float4 v = sm.join[t * WT + from][in][Math::place(in, lane)];
+        L = fmaf(e, ml[t].y, L);
+        acc[0] = fmaf(e, v.x, acc[0]);
+        acc[1] = fmaf(e, v.y, acc[1]);
+        acc[2] = fmaf(e, v.z, acc[2]);
+        acc[3] = fmaf(e, v.w, acc[3]);
+      }
+      if (whole) {
+        put_row(p, done, r, lane, top, L, acc);
+      } else {
+        const size_t at_row = (size_t)piece_slot(done.x, per, blockIdx.x) * ROWS + r;
+        __stcg(reinterpret_cast<float4*>(p.part_acc + at_row * kHeadDim) + lane, make_float4(acc[0], acc[1], acc[2], acc[3]));
+        if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + at_row * 2), make_float2(top, L));
+      }
     }
     if (!whole) {  // its turn comes at the range's end
       if (tid == 0) sm.parted[done.x >= x0 ? 1 : 0] = done;
@@ -390,10 +375,10 @@ cudaError_t launch_rows(const BlockAttnParams& p, int sms, cudaStream_t st) {
 
 cudaError_t launch_block_attn(const BlockAttnParams& p, int sms, int rows, cudaStream_t st) {
   switch (rows) {
-    case 8: return launch_rows<Rows8, 1>(p, sms, st);
-    case 16: return launch_rows<RowsWide<1>, 1>(p, sms, st);
-    case 32: return launch_rows<RowsWide<2>, 1>(p, sms, st);
-    default: return launch_rows<RowsWide<2>, 2>(p, sms, st);
+    case 8: return launch_rows<Rows<1>, 1>(p, sms, st);
+    case 16: return launch_rows<Rows<2>, 1>(p, sms, st);
+    case 32: return launch_rows<Rows<2>, 2>(p, sms, st);
+    default: return launch_rows<Rows<2>, 4>(p, sms, st);
   }
 }
 

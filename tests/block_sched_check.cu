@@ -66,9 +66,10 @@ static int trial() {
     int b0 = 0;
     while (!(x0 >= first[b0] && x0 < first[b0 + 1])) ++b0;
     BlockWalk<ROWS> w;
-    w.begin(p, x0, x1, per, b0, first[b0]);
+    const BlockRange range{x0, x1, per};
+    w.begin(p, range, b0, first[b0]);
     BlockSegment s;
-    while (w.next(p, s)) {
+    while (w.next(p, range, s)) {
       const auto key = std::make_tuple(s.b, s.h, s.r0 / ROWS);
       if (s.rows < 1 || s.rows > ROWS || s.first < 0 || s.first + (s.r0 + s.rows - 1) / G.g >= G.N || s.h < 0 || s.h >= G.Hkv) ++bad;
       for (int k = s.k0; k < s.k1; ++k) {
