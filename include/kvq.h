@@ -718,12 +718,15 @@ KVQ_API kvq_status kvq_block_append(const kvq_block_config *cfg, const kvq_block
  *   workspace  device scratch of >= workspace_bytes, 16-byte aligned, zero before
  *              its first call; every call leaves its counters zero.  Calls that
  *              share it must not overlap on the GPU.
- * Any number of new tokens per request (with a chain of drafted tokens, all are
- * appended first); made for few: 64 (token, query head) rows of a KV head
- * read its blocks together, more rows read them again.  Logits, maxima and sums are fp32, weights enter the
- * product as fp16 with 12 octaves of room above 1.  A block id that is not of the pool
- * reads as NaN.  The result does not depend on timing.  One launch; its waits
- * are bounded: should one run out (some 15 s), the rows it was for become NaN.
+ * Any number of new tokens per request (of a chain of drafted tokens all are
+ * appended first); made for few: up to 64 (token, query head) rows of a KV head
+ * read its blocks together, more rows read them again.  Logits, maxima and sums are
+ * fp32.  Weights enter the product with the values in two fp16 parts (22 bits) where a
+ * request's even share of the token slots makes no more than 8 rows of a KV head, in
+ * one beyond that, with 12 octaves of room above 1.  A block id that is not of the pool
+ * reads as NaN, and so does a block marked so (see scales): rows that see a token of it
+ * become NaN, the others do not.  The result does not depend on timing.  One launch;
+ * its waits are bounded: should one run out (some 15 s), the rows it was for become NaN.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_WORKSPACE,
  * KVQ_ERR_CUDA. */
 KVQ_API kvq_status kvq_block_attn(const kvq_block_config *cfg, const kvq_block_tables *tables, const uint8_t *codes,
