@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
     uint16_t* dst = p.q_out + (long long)row * G.Hq * kHeadDim;
     const int h0 = chunk * p.heads_per_warp;
     uint4 ahead[2][2];  // the next two heads' rows, on the way
-    const auto fetch = [&](int h, uint4 (&raw)[2]) {
+    const auto fetch = [&](int h, uint4 (&raw)[2]) {  // (plain loads: q_out may be q)
       const uint4* at = reinterpret_cast<const uint4*>(src + min(h, h1 - 1) * kHeadDim);
-      raw[0] = __ldg(at + l);
-      raw[1] = __ldg(at + kRowLanes + l);
+      raw[0] = at[l];
+      raw[1] = at[kRowLanes + l];
     };
     fetch(h0, ahead[0]);
     fetch(h0 + 1, ahead[1]);
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
           const __half2 two = __floats2half2_rn(v[2 * k] * r, v[2 * k + 1] * r);
           ow[k] = *reinterpret_cast<const uint32_t*>(&two);
         }
-        __syncwarp();  // (q_out may be q: a row is read whole before it is written)
+        __syncwarp();  // (a row is read whole before it is written)
         if (live) {
           uint4* at = reinterpret_cast<uint4*>(dst + h * kHeadDim);
           at[l] = o[0];
@@ -205,8 +205,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
   const BlockRequest r = block_request(G, __ldg(p.t.lens + b), __ldg(p.t.start + b), __ldg(p.t.start + b + 1));
   if (r.n == 0) return;
   const int j = r.before / kBlockTokens + (unit - __ldg(p.t.unit0 + b));
+  if (j < 0 || j >= G.max_blocks) return;
   const int p0 = max(r.before, j * kBlockTokens), p1 = min(r.before + r.n, (j + 1) * kBlockTokens);
-  if (j < 0 || p0 >= p1) return;
+  if (p0 >= p1) return;
   const int id = __ldg(p.t.block_table + (size_t)b * G.max_blocks + j);
   if (id < 0 || id >= G.n_blocks) return;
   const int off = p0 - j * kBlockTokens, count = p1 - p0;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = fabsf(v[i] * r_row) < INFINITY ? v[i] : 0.0f;
         if (t < count) {
-          const float fr = f * r_row;
+          const float fr = bad && !(fabsf(f * r_row) < INFINITY) ? 0.0f : f * r_row;
           uint32_t code[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)

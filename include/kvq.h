@@ -672,8 +672,8 @@ KVQ_API kvq_status kvq_block_layout_query(const kvq_block_config *cfg, kvq_block
  *                the stack, requests in order, a request's blocks in order
  * A request is served when its tokens fit its table row, when it needs no new
  * block or the blocks needed by it and the requests before it that fit their
- * rows are there (blocks that go back in this step count), and when their token
- * slots are there; otherwise it keeps its length and gets no token
+ * rows are there (blocks that go back in this step count), and when the token
+ * slots for it and those requests are there; otherwise it keeps its length and gets no token
  * (start[b + 1] == start[b]).  New blocks come from the top of the stack, in the
  * order of requests and positions; what was popped stays in free_list above
  * free_count.  Lengths outside [0, 32 max_blocks] are served nothing.  Entries of

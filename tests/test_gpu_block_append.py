@@ -232,6 +232,45 @@ def test_not_finite(bad, few):
     assert (c.layer.scales.cpu().numpy()[blk] != 255).all()
 
 
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("what", ["key", "weight", "zero row"])
+def test_not_finite_after_the_norm(what, few):
+    """A norm that is not finite (a key, a weight, a row of zeros with eps 0) marks the
+    block's keys; codes stay numbers, values as they are."""
+    n_tokens = 8 if few else 80
+    c = Cache(2, n_tokens, 2, 2, 6, 3, seed=4, norm_eps=0.0)
+    x = c.inputs()
+    wq, wk = c.weights()
+    if what == "key":
+        x[1, 2, 5] = np.inf
+    elif what == "weight":
+        wk[70] = np.nan
+    else:
+        x[1, 2] = 0
+    g, gw = torch.from_numpy(x).cuda(), torch.from_numpy(wk).cuda()
+    c.t.plan(torch.tensor([4, 3], dtype=torch.int32, device="cuda"))
+    c.layer.append(c.t, g[:, 2:4], g[:, 4:], k_weight=gw)
+    s, codes = c.layer.scales.cpu().numpy(), c.layer.codes.cpu().numpy()
+    assert ((codes & 127) != 127).all()
+    a, b = int(c.t.block_table[0, 0]), int(c.t.block_table[1, 0])
+    assert s[a, 0, 0] == 255 and (s[[a, b], :, 1] != 255).all()
+    assert (s[b, :, 0] == 255).all() if what == "weight" else (s[b, :, 0] != 255).all() and s[a, 1, 0] != 255
+
+
+def test_tables_that_no_plan_writes_are_left_out():
+    """Sums of touched blocks far out of range: nothing is written anywhere."""
+    c = Cache(3, 40, 2, 2, 6, 3, seed=9)
+    g = torch.from_numpy(c.inputs()).cuda()
+    c.t.plan(torch.tensor([10, 10, 10], dtype=torch.int32, device="cuda"))
+    before = c.layer.codes.clone()
+    for unit0 in ([-(2**31), 1, 2, 3], [-(2**27), -(2**27) + 1, 2**30, 2**31 - 1], [0, 0, 0, 2**31 - 1], [5, 5, 5, 9], [7, 3, 1, 0]):
+        c.t.unit0.copy_(torch.tensor(unit0, dtype=torch.int32))
+        c.layer.append(c.t, g[:, 2:4], g[:, 4:])
+    torch.cuda.synchronize()
+    changed = (c.layer.codes != before).reshape(6, -1).any(1).nonzero().reshape(-1).tolist()
+    assert set(changed) <= {int(c.t.block_table[b, 0]) for b in range(3)}
+
+
 def test_values_at_the_ends_of_the_range():
     """Zeros, the smallest and largest fp16 numbers, one of each sign."""
     c = Cache(3, 6, 1, 1, 5, 2, seed=6, rope_theta=0.0)
