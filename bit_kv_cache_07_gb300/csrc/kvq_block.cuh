@@ -128,16 +128,17 @@ __host__ __device__ inline BlockRequest request_at(const BlockAttnParams& p, int
 }
 
 // What a (request, head, row block) costs beyond its tiles, in tiles: the teams'
-// parts are joined (of 8 to 20 tiles' time, 16 measured best: 64 ragged requests
-// to 8k tokens 62 us with 8, 57 with 16, 58 with 20), or one team takes it alone
-// and the others go on (up to 8 tiles: 256 requests of 200 tokens 62 us with 4,
-// 32 with 8; with 16, the ragged batch loses 4 us).
+// parts are joined (64 ragged requests to 8k tokens: 51.7 us where that weighs 8
+// tiles, 49.4 with 12, 49.2 with 16, 49.9 with 20; one request of 8k: 12.7, 12.7, 10.4,
+// 10.5), or one team takes it alone and the others go on (256 requests of 200 tokens:
+// 44.7 us where that ends at 4 tiles, 27.5 at 8 and at 12; the ragged batch 48.2, 49.2,
+// 49.1).
 constexpr int kSoloTiles = 8;
 constexpr int kJoinTiles = 16;
 // Short ones are not cut between CTAs, which would have to join them: up to
 // kUncutTiles, where ranges that end with whole ones are at most kUncutExtra tiles
-// longer (64 requests of 100 tokens 20.6 us cut, 10.8 whole; 16 of 1000, 16.7 and
-// 11.6; one of 1024 tokens, one head: 8.9 cut, 10.5 whole).
+// longer (16 requests of 1000 tokens: 15.0 us where that ends at 24 tiles, 10.2 at 48;
+// one of 1024 tokens, one head: 8.3 us cut, 9.0 whole, as with an extra of 64).
 constexpr int kUncutTiles = 48;
 constexpr int kUncutExtra = 16;
 __host__ __device__ inline bool block_uncut(int cnt, long long per) {
