@@ -122,16 +122,27 @@ __device__ __forceinline__ float2 e4m3x2_floats(uint32_t two) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The last b with at[b] <= v (v >= at[0] = 0), by a warp: 32 rows apart, then
-// between them.
-__device__ __forceinline__ int unit_request(const int* at, int B, int v, int lane) {
+// A unit's request: the last one whose first unit is not behind it.  By a warp: 32
+// requests apart where there are more than 32, then between them, with what the
+// request's tokens need read beside (each further read would be a latency that
+// nothing hides at a CTA's begin).
+struct UnitRequest {
+  int b, unit0, len, start, end;
+};
+__device__ __forceinline__ UnitRequest unit_request(const kvq_block_tables& t, int B, int unit, int lane) {
   const int step = (B + 31) / 32;
-  const int far = lane * step;
-  const unsigned below = __ballot_sync(0xffffffffu, far < B && __ldg(at + far) <= v);
-  const int lo = (31 - __clz(below | 1u)) * step;
-  const int near = lo + lane;  // step <= 32
-  const unsigned in = __ballot_sync(0xffffffffu, lane < step && near < B && __ldg(at + near) <= v);
-  return lo + 31 - __clz(in | 1u);
+  int lo = 0;
+  if (step > 1) {
+    const int far = lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, far < B && __ldg(t.unit0 + far) <= unit);
+    lo = (31 - __clz(below | 1u)) * step;
+  }
+  const int near = lo + lane, at = min(near, B - 1);  // step <= 32
+  const int unit0 = __ldg(t.unit0 + at), len = __ldg(t.lens + at), start = __ldg(t.start + at), end = __ldg(t.start + at + 1);
+  const unsigned in = __ballot_sync(0xffffffffu, (step == 1 || lane < step) && near < B && unit0 <= unit);
+  const int from = 31 - __clz(in | 1u);
+  return {lo + from, __shfl_sync(0xffffffffu, unit0, from), __shfl_sync(0xffffffffu, len, from), __shfl_sync(0xffffffffu, start, from),
+          __shfl_sync(0xffffffffu, end, from)};
 }
 
 template <int WARPS>
@@ -151,12 +162,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
   if ((int)blockIdx.x >= kv_ctas) {  // queries: kStep token slots, heads_per_warp heads
     const int x = blockIdx.x - kv_ctas, group = x / p.q_chunks, chunk = x - group * p.q_chunks;
     const int i = group * kStep + w * kWarpTokens + sub;
+    const int pos = p.rotate ? __ldg(p.t.position + min(i, G.N - 1)) : 0;  // (of a row behind the last: unused)
     const int used = min(max(__ldg(p.t.start + G.B), 0), G.N);
     if (group * kStep + w * kWarpTokens >= used) return;
     const bool live = i < used;
     const int row = live ? i : group * kStep + w * kWarpTokens;
-    Turn turn;
-    make_turn(turn, p.q_weight, s_freq, p.rotate, l, p.rotate ? __ldg(p.t.position + row) : 0);
     const int h1 = min(G.Hq, (chunk + 1) * p.heads_per_warp);
     const uint16_t* src = p.q + (long long)row * p.qs;
     uint16_t* dst = p.q_out + (long long)row * G.Hq * kHeadDim;
@@ -169,6 +179,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
     };
     fetch(h0, ahead[0]);
     fetch(h0 + 1, ahead[1]);
+    Turn turn;  // (made while they come)
+    make_turn(turn, p.q_weight, s_freq, p.rotate, l, pos);
     for (int hh = h0; hh < h1; hh += 2) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -200,16 +212,16 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
 
   // keys and values: heads_per_cta heads of one touched block
   const int unit = blockIdx.x / p.kv_chunks, chunk = blockIdx.x - unit * p.kv_chunks;
-  if (unit >= __ldg(p.t.unit0 + G.B)) return;
-  const int b = unit_request(p.t.unit0, G.B, unit, lane);
-  const BlockRequest r = block_request(G, __ldg(p.t.lens + b), __ldg(p.t.start + b), __ldg(p.t.start + b + 1));
+  const int units = __ldg(p.t.unit0 + G.B);
+  const UnitRequest u = unit_request(p.t, G.B, unit, lane);
+  if (unit >= units) return;
+  const BlockRequest r = block_request(G, u.len, u.start, u.end);
   if (r.n == 0) return;
-  const int j = r.before / kBlockTokens + (unit - __ldg(p.t.unit0 + b));
+  const int j = r.before / kBlockTokens + (unit - u.unit0);
   if (j < 0 || j >= G.max_blocks) return;
   const int p0 = max(r.before, j * kBlockTokens), p1 = min(r.before + r.n, (j + 1) * kBlockTokens);
   if (p0 >= p1) return;
-  const int id = __ldg(p.t.block_table + (size_t)b * G.max_blocks + j);
-  if (id < 0 || id >= G.n_blocks) return;
+  const int id = __ldg(p.t.block_table + (size_t)u.b * G.max_blocks + j);
   const int off = p0 - j * kBlockTokens, count = p1 - p0;
   const long long slot0 = r.first + (p0 - r.before);
   const int h0 = chunk * p.heads_per_cta, h1 = min(G.Hkv, h0 + p.heads_per_cta);
@@ -247,6 +259,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
   uint4 ahead[2][2];  // the next head's rows, on the way
   fetch(h0, 0, t_first, ahead[0]);
   fetch(h0, 1, t_first, ahead[1]);
+  if (id < 0 || id >= G.n_blocks) return;  // (after the rows are asked for: its read is on the way with them)
   turn_to(t_first);
   int flip = 0;
   for (int h = h0; h < h1; ++h) {
