@@ -363,12 +363,16 @@ cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st) {
   // chains, single tokens) fill one warp
   const bool few = (G.N + G.B - 1) / G.B <= kWarpTokens;
   const int step = kWarpTokens * (few ? 1 : 8);
-  // heads of a block's CTA: as many as still leave several CTAs for each SM (a
-  // CTA's look-ups are paid once, and the next head's rows are read meanwhile)
-  const long long items = (long long)p.units * G.Hkv;
-  const long long share = few ? 1 : items / 1216;
+  // heads of a block's CTA: many, since its look-ups and sines are paid once and the
+  // next head's rows are read meanwhile, but no more than an eighth of an SM's share
+  // of the call's rows (the last CTAs to start are then short beside the call: prompts
+  // of 32 on 8 heads 64.4 us with all heads in a CTA, 66.1 in two, 70.3 in four; of
+  // 32 heads 126.1 us in two, 149.7 in one, 129.4 in four)
+  const long long all_rows = (long long)G.N * (2 * G.Hkv + (p.q ? G.Hq : 0));
+  const long long share = few ? 1 : all_rows / (2 * kBlockTokens * 8 * 152);
   p.heads_per_cta = (int)(share < 1 ? 1 : share > G.Hkv ? G.Hkv : share);
   p.kv_chunks = (G.Hkv + p.heads_per_cta - 1) / p.heads_per_cta;
+  p.heads_per_cta = (G.Hkv + p.kv_chunks - 1) / p.kv_chunks;  // (evenly)
   // heads of a query warp: more share a token's sines, fewer spread a small call
   // over the SMs
   const long long rows = (long long)G.N * G.Hq;
