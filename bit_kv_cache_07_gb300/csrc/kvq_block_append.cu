@@ -8,9 +8,9 @@
 // Eight lanes hold a token's row of a head: lane l the channels 8l..8l+7 and
 // 64+8l..64+8l+7, so that both of a rotated pair are in one lane, loads are two
 // 16-byte words and the mean is three shuffles.  A CTA takes one block and several
-// heads: keys, then values of each, read once into registers (one maximum over the
-// CTA between the read and the store) while the next head's are on the way; the
-// sines are the block's.  Calls of few tokens per request run the
+// heads: keys, then values of each, read once (in registers between the one maximum
+// over the CTA and the store) while the next two heads' are on the way to shared
+// memory; the sines are the block's.  Calls of few tokens per request run the
 // same with one warp per CTA, which walks a longer run of tokens twice.  The
 // queries go to CTAs of their own: a warp turns four tokens' rows head after
 // head with the same sines.
@@ -145,10 +145,28 @@ __device__ __forceinline__ UnitRequest unit_request(const kvq_block_tables& t, i
           __shfl_sync(0xffffffffu, end, from)};
 }
 
+// Rows on the way: each thread copies its own 32 bytes of a row into its own slots of
+// shared memory (so that no barrier is needed), kRowsAhead rows ahead, and in flight
+// they take no registers (prompts of 32 on 8 heads 64.4 to 57.4 us, of 32 heads 126.1
+// to 105.5 us against rows on the way in registers; six rows ahead 58.5 and 106.5; four
+// CTAs per SM in place of three, in 64 registers, 57.4 and 110.5).
+constexpr int kRowsAhead = 4;
+template <int WARPS>
+struct RowRing {
+  uint4 at[kRowsAhead][2][32 * WARPS];
+};
+__device__ __forceinline__ void copy_chunk(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
+
 template <int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_kernel(const __grid_constant__ BlockAppendParams p) {
   __shared__ unsigned long long s_freq[kHeadDim / 2];
   __shared__ uint32_t s_top[2][WARPS];
+  __shared__ RowRing<WARPS> ring;
   const BlockGeo& G = p.geo;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, l = lane & (kRowLanes - 1), sub = lane / kRowLanes;
   if (p.rotate)
@@ -156,6 +174,22 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
   __syncthreads();
   grid_dep_wait();
   grid_dep_trigger();
+  int slot = 0;
+  // One group of copies per row, empty past the last: after wait<kRowsAhead - 1> the oldest is there.
+  const auto ask = [&](const uint16_t* row, bool any) {
+    if (any) {
+      copy_chunk(&ring.at[slot][0][tid], row + 8 * l);
+      copy_chunk(&ring.at[slot][1][tid], row + kHeadDim / 2 + 8 * l);
+    }
+    copy_commit();
+    slot = (slot + 1) % kRowsAhead;
+  };
+  const auto take = [&](uint4 (&raw)[2]) {  // the oldest row; its slot is the next to ask for
+    copy_wait<kRowsAhead - 1>();
+    raw[0] = ring.at[slot][0][tid];
+    raw[1] = ring.at[slot][1][tid];
+    __syncwarp();
+  };
   constexpr int kStep = kWarpTokens * WARPS;  // tokens of a CTA at a time
   const int kv_ctas = p.units * p.kv_chunks;
 
@@ -171,40 +205,30 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
     const uint16_t* src = p.q + (long long)row * p.qs;
     uint16_t* dst = p.q_out + (long long)row * G.Hq * kHeadDim;
     const int h0 = chunk * p.heads_per_warp;
-    uint4 ahead[2][2];  // the next two heads' rows, on the way
-    const auto fetch = [&](int h, uint4 (&raw)[2]) {  // (plain loads: q_out may be q)
-      const uint4* at = reinterpret_cast<const uint4*>(src + min(h, h1 - 1) * kHeadDim);
-      raw[0] = at[l];
-      raw[1] = at[kRowLanes + l];
-    };
-    fetch(h0, ahead[0]);
-    fetch(h0 + 1, ahead[1]);
+    // (q_out may be q: a row is read by its own warp only, and whole before it is written)
+    for (int u = 0; u < kRowsAhead; ++u) ask(src + (h0 + u) * kHeadDim, h0 + u < h1);
     Turn turn;  // (made while they come)
     make_turn(turn, p.q_weight, s_freq, p.rotate, l, pos);
-    for (int hh = h0; hh < h1; hh += 2) {
+    for (int h = h0; h < h1; ++h) {
+      uint4 raw[2];
+      take(raw);
+      ask(src + (h + kRowsAhead) * kHeadDim, h + kRowsAhead < h1);
+      float v[16];
+      halves_to_floats(raw[0], v);
+      halves_to_floats(raw[1], v + 8);
+      const float r = p.q_weight ? norm_factor(v, p.eps) : 1.0f;
+      apply_turn(turn, p.q_weight, p.rotate, v);
+      uint4 o[2];
+      uint32_t* ow = reinterpret_cast<uint32_t*>(o);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int h = hh + u;
-        if (h >= h1) break;
-        float v[16];
-        halves_to_floats(ahead[u][0], v);
-        halves_to_floats(ahead[u][1], v + 8);
-        if (h + 2 < h1) fetch(h + 2, ahead[u]);
-        const float r = p.q_weight ? norm_factor(v, p.eps) : 1.0f;
-        apply_turn(turn, p.q_weight, p.rotate, v);
-        uint4 o[2];
-        uint32_t* ow = reinterpret_cast<uint32_t*>(o);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const __half2 two = __floats2half2_rn(v[2 * k] * r, v[2 * k + 1] * r);
-          ow[k] = *reinterpret_cast<const uint32_t*>(&two);
-        }
-        __syncwarp();  // (a row is read whole before it is written)
-        if (live) {
-          uint4* at = reinterpret_cast<uint4*>(dst + h * kHeadDim);
-          at[l] = o[0];
-          at[kRowLanes + l] = o[1];
-        }
+      for (int k = 0; k < 8; ++k) {
+        const __half2 two = __floats2half2_rn(v[2 * k] * r, v[2 * k + 1] * r);
+        ow[k] = *reinterpret_cast<const uint32_t*>(&two);
+      }
+      if (live) {
+        uint4* at = reinterpret_cast<uint4*>(dst + h * kHeadDim);
+        at[l] = o[0];
+        at[kRowLanes + l] = o[1];
       }
     }
     return;
@@ -256,21 +280,24 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
       apply_turn(turn, p.k_weight, p.rotate, v);
     }
   };
-  uint4 ahead[2][2];  // the next head's rows, on the way
-  fetch(h0, 0, t_first, ahead[0]);
-  fetch(h0, 1, t_first, ahead[1]);
-  if (id < 0 || id >= G.n_blocks) return;  // (after the rows are asked for: its read is on the way with them)
+  const uint16_t *k_at = k_row + (t_first < count ? t_first : 0) * p.ks, *v_at = v_row + (t_first < count ? t_first : 0) * p.vs;
+  for (int u = 0; u < kRowsAhead / 2; ++u) {
+    ask(k_at + (h0 + u) * kHeadDim, h0 + u < h1);
+    ask(v_at + (h0 + u) * kHeadDim, h0 + u < h1);
+  }
+  if (id < 0 || id >= G.n_blocks) {  // (its read was on the way with the rows)
+    copy_wait<0>();
+    return;
+  }
   turn_to(t_first);
   int flip = 0;
   for (int h = h0; h < h1; ++h) {
     const size_t place = (size_t)id * G.Hkv + h;
     for (int side = 0; side < 2; ++side) {
       const uint8_t was = off ? p.scales[place * 2 + side] : 0;
-      uint4 raw[2] = {side ? ahead[1][0] : ahead[0][0], side ? ahead[1][1] : ahead[0][1]};
-      if (h + 1 < h1) {
-        if (side) fetch(h + 1, 1, t_first, ahead[1]);
-        else fetch(h + 1, 0, t_first, ahead[0]);
-      }
+      uint4 raw[2];
+      take(raw);
+      ask((side ? v_at : k_at) + (h + kRowsAhead / 2) * kHeadDim, h + kRowsAhead / 2 < h1);
       float amax = 0.0f;
       bool bad = false;
       for (int t0 = 0; t0 < (kOnce ? 1 : count); t0 += kStep) {
@@ -366,8 +393,8 @@ cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st) {
   // heads of a block's CTA: many, since its look-ups and sines are paid once and the
   // next head's rows are read meanwhile, but no more than an eighth of an SM's share
   // of the call's rows (the last CTAs to start are then short beside the call: prompts
-  // of 32 on 8 heads 64.4 us with all heads in a CTA, 66.1 in two, 70.3 in four; of
-  // 32 heads 126.1 us in two, 149.7 in one, 129.4 in four)
+  // of 32 on 8 heads 57.4 us with all heads in a CTA, 59.8 in two, 64.2 in four; of
+  // 32 heads 105.9 us in two, 109.4 in one, 110.3 in four)
   const long long all_rows = (long long)G.N * (2 * G.Hkv + (p.q ? G.Hq : 0));
   const long long share = few ? 1 : all_rows / (2 * kBlockTokens * 8 * 152);
   p.heads_per_cta = (int)(share < 1 ? 1 : share > G.Hkv ? G.Hkv : share);
