@@ -186,6 +186,55 @@ def test_far_positions():
     assert (np.abs(got - k) <= half_step(np.abs(k) / unit) * unit + 2.0**-17 * np.abs(k).max()).all()
 
 
+def test_large_calls_give_the_bytes_of_small_ones():
+    """Several heads per CTA and per warp (rows asked for more than the ring's depth
+    ahead) against the same tokens request by request: no sum or maximum reaches over a
+    head's block, so the bytes are the same.  The large call's queries lie in place."""
+    sizes, hq, hkv = [2731, 3000, 3269], 24, 12
+    N = sum(sizes)
+    x = torch.from_numpy(np.random.default_rng(11).standard_normal((N, hq + 2 * hkv, D)).astype(np.float16)).cuda()
+    w = torch.from_numpy((1 + 0.3 * np.random.default_rng(12).standard_normal((2, D))).astype(np.float16)).cuda()
+    k, v = x[:, hq:hq + hkv], x[:, hq + hkv:]
+
+    def cache(batch, n):
+        cfg = dict(batch=batch, n_tokens=n, n_q_heads=hq, n_kv_heads=hkv, head_dim=128, n_blocks=300, max_blocks=110,
+                   rope_theta=10000.0, norm_eps=EPS)
+        return blocks.Tables(cfg), blocks.Layer(cfg)
+
+    t, layer = cache(3, N)
+    t.plan(torch.tensor(sizes, dtype=torch.int32, device="cuda"))
+    q = x[:, :hq].contiguous()
+    layer.append(t, k, v, q, q, w[0], w[1])
+    at = 0
+    for b, n in enumerate(sizes):
+        t1, one = cache(1, n)
+        t1.plan(torch.tensor([n], dtype=torch.int32, device="cuda"))
+        out = torch.zeros((n, hq, D), dtype=torch.float16, device="cuda")
+        rows = slice(at, at + n)
+        one.append(t1, k[rows], v[rows], x[rows, :hq], out, w[0], w[1])
+        assert torch.equal(out, q[rows])
+        used = -(-n // BLOCK)
+        ids, ids1 = t.block_table[b, :used].long(), t1.block_table[0, :used].long()
+        assert torch.equal(layer.scales[ids], one.scales[ids1])
+        tail = n % BLOCK or BLOCK
+        assert torch.equal(layer.codes[ids[:-1]], one.codes[ids1[:-1]])
+        assert torch.equal(layer.codes[ids[-1], :, :, :tail], one.codes[ids1[-1], :, :, :tail])
+        at += n
+
+
+@pytest.mark.parametrize("batch", [31, 32, 33, 65])
+def test_requests_around_a_warp(batch):
+    """The search for a block's request takes one step up to 32 requests and two beyond."""
+    rng = random.Random(batch)
+    new = [rng.choice([0, 1, 5, 40]) for _ in range(batch)]
+    new[0], new[-1] = 0, 33
+    c = Cache(batch, sum(new) + 3, 2, 1, 3 * batch, 4, seed=batch)
+    for step in (new, [1] * batch):
+        if sum(step) <= c.cfg["n_tokens"]:
+            c.append(step, c.inputs(), *c.weights())
+            c.check()
+
+
 def test_queries_in_place():
     c = Cache(2, 8, 4, 2, 8, 4, seed=3)
     x = c.inputs()
