@@ -19,6 +19,8 @@
 // the angle (exact to 2^-32 turns at any position), and the hardware sine and
 // cosine of it in [-pi, pi] (absolute error below 2^-20, where q_out's own
 // rounding is 2^-11 and a code's 2^-4).
+#include <algorithm>
+
 #include "kvq_block.cuh"
 
 namespace kvq {
@@ -391,12 +393,16 @@ cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st) {
   const bool few = (G.N + G.B - 1) / G.B <= kWarpTokens;
   const int step = kWarpTokens * (few ? 1 : 8);
   // heads of a block's CTA: many, since its look-ups and sines are paid once and the
-  // next head's rows are read meanwhile, but no more than an eighth of an SM's share
-  // of the call's rows (the last CTAs to start are then short beside the call: prompts
-  // of 32 on 8 heads 57.4 us with all heads in a CTA, 59.8 in two, 64.2 in four; of
-  // 32 heads 105.9 us in two, 109.4 in one, 110.3 in four)
+  // next head's rows are read meanwhile.  Up to four as long as the call's rows give
+  // each SM its three CTAs (43 prompts of 255 tokens of 4 heads 11.9 us in one CTA, 15.5
+  // in four; 51 of 80 tokens of 16 on 8 heads 14.0 in two, 18.5 in eight), more only
+  // while a CTA has no more than an eighth of an SM's share (the last CTAs to start are
+  // then short beside the call: prompts of 32 on 8 heads 57.4 us with all heads in a
+  // CTA, 59.8 in two, 64.2 in four; of 32 heads 105.9 in two, 109.4 in one, 110.3 in
+  // four)
   const long long all_rows = (long long)G.N * (2 * G.Hkv + (p.q ? G.Hq : 0));
-  const long long share = few ? 1 : all_rows / (2 * kBlockTokens * 8 * 152);
+  const long long per_sm = all_rows / (2 * kBlockTokens * 152);  // CTAs of one head
+  const long long share = few ? 1 : std::max(per_sm / 8, std::min(per_sm / 3, 4ll));
   p.heads_per_cta = (int)(share < 1 ? 1 : share > G.Hkv ? G.Hkv : share);
   p.kv_chunks = (G.Hkv + p.heads_per_cta - 1) / p.heads_per_cta;
   p.heads_per_cta = (G.Hkv + p.kv_chunks - 1) / p.kv_chunks;  // (evenly)
