@@ -83,6 +83,9 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   const BlockGeo& G = p.geo;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, team = w / WT, wt = w % WT;
   volatile int* gave_up = &sm.gave_up;
+  const auto wait = [&](const uint64_t* bar, uint32_t phase) {  // by a warp: all of its lanes get the same answer
+    return (bool)__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase, gave_up));
+  };
   if (tid < kStages) {
     mbar_init(smem_u32(&sm.full[tid]), 1);
     mbar_init(smem_u32(&sm.empty[tid]), WT);
@@ -173,7 +176,8 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   const auto issue = [&]() {  // copies of the next tile
     if (!have) return;
     const int slot = in_slot, st = team * RING + slot;
-    if (WT > 1 && in_turn && !mbar_wait(smem_u32(&sm.empty[st]), (in_turn - 1) & 1, gave_up)) {
+    // (agreed, as every wait here: lanes whose limits end beside the phase would part ways before the shuffles)
+    if (WT > 1 && in_turn && !wait(&sm.empty[st], (in_turn - 1) & 1)) {
       have = false;
       return;
     }
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
       if (wt == 0) issue();
       const int slot = out_slot, st = team * RING + slot;
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[st]), out_phase, gave_up));
+      const bool ok = wait(&sm.full[st], out_phase);
       if (!ok) {  // the rows become NaN, and nothing more is asked for
         math.spoil();
         have = false;
