@@ -202,7 +202,11 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     for (int i = 0; i < RING - 1; ++i) issue();
   }
 
-  int out_slot = 0;  // of the tile that the team is at
+  // Slot of the tile that the team is at.  -1: a wait ran out; the warp reads and empties no
+  // slot any more, and its rows of every further segment become NaN.  (A later tile's phase
+  // would look complete where the slot was last filled two turns before, and an arrival
+  // without a tile read would let a slot be filled that another warp of the team still reads.)
+  int out_slot = 0;
   uint32_t out_phase = 0;
   int load = 0;
   Math math;
@@ -226,15 +230,15 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
     math.begin();
     const int p_lo = s.before + token_at(p, s, 0), p_hi = s.before + token_at(p, s, s.rows - 1);  // positions of the block's rows
 
-    for (int i = s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
+    for (int i = out_slot < 0 ? s.k1 : s.k0 + (solo ? 0 : team); i < s.k1; i += tile_step) {
       if (wt == 0) issue();
       const int slot = out_slot, st = team * RING + slot;
-      const bool ok = wait(&sm.full[st], out_phase);
-      if (!ok) {  // the rows become NaN, and nothing more is asked for
-        math.spoil();
-        have = false;
+      if (!wait(&sm.full[st], out_phase)) {
+        out_slot = -1;
+        have = false;  // (nothing more is asked for)
+        break;
       }
-      if (ok && active) {
+      if (active) {
         const int meta = sm.meta[st];
         const int kb = meta < 0 ? kScaleNaN : sm.scale16[st][meta & 15], vb = meta < 0 ? kScaleNaN : sm.scale16[st][(meta & 15) + 1];
         Tile t;
@@ -252,6 +256,7 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
       else __syncwarp();
     }
 
+    if (out_slot < 0) math.spoil();
     const BlockSegment done = s;
     more = next_segment(s);
     // ---- the teams' parts, joined in a fixed order

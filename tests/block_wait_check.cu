@@ -117,6 +117,7 @@ int main(int argc, char** argv) {
     if (!run(width, none, out, lse)) return printf("%s, bad 1\n", cudaGetErrorString(cudaGetLastError())), 1;
     bad += out != want || std::memcmp(lse.data(), want_lse.data(), rows * 4);
   }
+  bad += spoilt == 0;
   printf("%s, %d runs, %d rows spoilt, bad %d\n", cudaGetErrorString(cudaGetLastError()), runs, spoilt, bad);
   return bad != 0;
 }

@@ -27,3 +27,8 @@ def check(tmp_path_factory):
 
 def test_every_wait_runs_out(check):
     check()
+
+
+def test_one_wait_runs_out(check):
+    """A chosen wait of one warp, or of one lane of it, at a range's begin and later."""
+    check("later")
