@@ -25,9 +25,11 @@ _SHARED = ("batch", "n_tokens", "n_blocks", "max_blocks")  # what tables and lay
 
 
 def make_config(d) -> kvq_block_config:
-    """kvq_block_config from a dict with the same field names (missing -> 0)."""
+    """kvq_block_config from a dict with the same field names (missing -> 0), or a
+    copy of one: what tables and layers hold agrees with their arrays, whatever the
+    caller writes into the configuration afterwards."""
     if isinstance(d, kvq_block_config):
-        return d
+        return kvq_block_config.from_buffer_copy(d)
     known = {n: t for n, t in kvq_block_config._fields_}
     for name in d:
         if name not in known:

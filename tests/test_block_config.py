@@ -1,0 +1,44 @@
+"""The block cache's Python objects keep what their arrays were made for, whatever
+the caller does with the configuration and the attributes afterwards."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from bit_kv_cache_07_gb300 import blocks  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from bit_kv_cache_07_gb300 import build
+    build.build_library()
+
+
+CFG = dict(batch=2, n_tokens=4, n_q_heads=4, n_kv_heads=2, head_dim=128, n_blocks=6, max_blocks=3, window=0)
+
+
+def test_a_configuration_is_copied():
+    c = blocks.make_config(CFG)
+    d = blocks.make_config(c)
+    c.n_tokens, c.window = 1 << 20, 5
+    assert (d.n_tokens, d.window) == (4, 0)
+
+
+@pytest.mark.gpu
+def test_a_configuration_written_to_afterwards():
+    """One configuration object for several layers: the first keeps its window, the
+    tables their sizes (a plan of more token slots would be written behind them)."""
+    c = blocks.make_config(CFG)
+    t, wide = blocks.Tables(c), blocks.Layer(c)
+    c.window = 1
+    narrow = blocks.Layer(c)
+    t.plan(torch.tensor([3, 1], dtype=torch.int32, device="cuda"))
+    k, q = torch.randn((4, 2, 128), device="cuda").half(), torch.randn((4, 4, 128), device="cuda").half()
+    ws, out = blocks.new_workspace(c), {}
+    for name, layer in (("wide", wide), ("narrow", narrow)):
+        layer.append(t, k, k.clone())
+        out[name] = torch.zeros_like(q)
+        layer.attn(t, q, out[name], None, ws)
+    assert torch.equal(out["wide"][0], out["narrow"][0]) and not torch.equal(out["wide"][2], out["narrow"][2])
+    c.n_tokens, c.batch, c.max_blocks = 4096, 64, 100
+    t.plan(torch.tensor([-1, 1], dtype=torch.int32, device="cuda"))
+    assert t.lens.tolist() == [0, 2] and t.start.tolist() == [0, 0, 1] and t.token_row.tolist() == [1, -1, -1, -1]
