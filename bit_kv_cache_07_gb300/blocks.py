@@ -89,15 +89,28 @@ def _ints(t, what: str, shape, device) -> int:
     return _dense(t, what, torch.int32, shape, device)
 
 
+def _kept(name):
+    """An attribute whose tensor's address the kernels hold: written in place, never
+    exchanged (the calls would go on with the old one's memory)."""
+    def put(self, value):
+        if value is not self._tensors[name]:  # (`x.lens += 1` assigns the tensor itself)
+            raise AttributeError(f"{name}: the calls hold the address of its tensor; write into it in place")
+    return property(lambda self: self._tensors[name], put)
+
+
 class Tables:
     """Block tables, the free stack, lengths and the step's offsets and slot maps,
     shared by the layers of a model; every block is free and every request empty
-    unless tensors of the layout of kvq_block_tables are given by name."""
+    unless tensors of the layout of kvq_block_tables are given by name.  They are
+    attributes of these names and are written in place."""
+
+    cfg = property(lambda self: make_config(self._cfg), doc="a copy of the configuration")
+    block_table, free_list, free_count, lens, start, unit0, token_row, position, slot = map(_kept, BLOCK_TABLES)
 
     def __init__(self, cfg, device="cuda", **arrays):
-        self.cfg = make_config(cfg)
-        layout(self.cfg)  # its refusals
-        c = self.cfg
+        self._cfg = make_config(cfg)
+        layout(self._cfg)  # its refusals
+        c = self._cfg
         self.shared = tuple(getattr(c, n) for n in _SHARED)
         shapes = dict(block_table=(c.batch, c.max_blocks), free_list=(c.n_blocks,), free_count=(1,), lens=(c.batch,),
                       start=(c.batch + 1,), unit0=(c.batch + 1,), token_row=(c.n_tokens,), position=(c.n_tokens,),
@@ -105,6 +118,7 @@ class Tables:
         for name in arrays:
             if name not in shapes:
                 raise ValueError(f"no array {name!r} in a block cache's tables")
+        self._tensors = {}
         for name in BLOCK_TABLES:
             t = arrays.get(name)
             if t is None:
@@ -114,12 +128,12 @@ class Tables:
                     t = torch.full((1,), c.n_blocks, dtype=torch.int32, device=device)
                 else:
                     t = torch.zeros(shapes[name], dtype=torch.int32, device=device)
-            setattr(self, name, t)
+            self._tensors[name] = t
         self.device = self.lens.get_device() if isinstance(self.lens, torch.Tensor) else None
-        self.arrays = kvq_block_tables(*[_ints(getattr(self, n), n, shapes[n], self.device) for n in BLOCK_TABLES])
+        self.arrays = kvq_block_tables(*[_ints(t, n, shapes[n], self.device) for n, t in self._tensors.items()])
         if self.device < 0:
             raise ValueError("the tables must be on a GPU")
-        self._refs = C.byref(self.cfg), C.byref(self.arrays)
+        self._refs = C.byref(self._cfg), C.byref(self.arrays)
         self._call = lib().kvq_block_plan
         self._rows = (c.batch,)
 
@@ -158,10 +172,13 @@ class Layer:
     """One layer's cache: zeroed codes uint8 [n_blocks, Hkv, 2, 32, 128] and scales
     uint8 [n_blocks, Hkv, 2], or tensors of that layout."""
 
+    cfg = property(lambda self: make_config(self._cfg), doc="a copy of the configuration")
+    codes, scales = map(_kept, ("codes", "scales"))
+
     def __init__(self, cfg, codes=None, scales=None, device="cuda"):
-        self.cfg = make_config(cfg)
-        self.layout = layout(self.cfg)
-        c = self.cfg
+        self._cfg = make_config(cfg)
+        self.layout = layout(self._cfg)
+        c = self._cfg
         self.shared = tuple(getattr(c, n) for n in _SHARED)
         shape = (c.n_blocks, c.n_kv_heads, 2)
         if codes is None:
@@ -176,8 +193,8 @@ class Layer:
             raise ValueError("codes and scales must be on a GPU")
         if scales.untyped_storage().nbytes() - scales.storage_offset() < self.layout.scales_bytes:
             raise ValueError(f"scales: its storage must reach {self.layout.scales_bytes} bytes (padded to 16)")
-        self.codes, self.scales = codes, scales
-        self._ref = C.byref(self.cfg)
+        self._tensors = dict(codes=codes, scales=scales)
+        self._ref = C.byref(self._cfg)
         self._append, self._attn = lib().kvq_block_append, lib().kvq_block_attn
         self._kv = (c.n_tokens, c.n_kv_heads, 128), (c.n_kv_heads * 128, 128, 1)
         self._q = (c.n_tokens, c.n_q_heads, 128), (c.n_q_heads * 128, 128, 1)

@@ -42,3 +42,22 @@ def test_a_configuration_written_to_afterwards():
     c.n_tokens, c.batch, c.max_blocks = 4096, 64, 100
     t.plan(torch.tensor([-1, 1], dtype=torch.int32, device="cuda"))
     assert t.lens.tolist() == [0, 2] and t.start.tolist() == [0, 0, 1] and t.token_row.tolist() == [1, -1, -1, -1]
+
+
+@pytest.mark.gpu
+def test_tensors_are_not_exchanged():
+    """The calls hold the tensors' addresses: an assignment is refused, writing in place works."""
+    t, layer = blocks.Tables(CFG), blocks.Layer(CFG)
+    for obj, names in ((t, ("block_table", "free_list", "free_count", "lens", "start", "unit0", "token_row", "position", "slot")),
+                       (layer, ("codes", "scales"))):
+        for name in names:
+            old = getattr(obj, name)
+            with pytest.raises(AttributeError):
+                setattr(obj, name, old.clone())
+            assert getattr(obj, name) is old
+        obj.cfg.batch = 1000  # of a copy
+        assert obj.cfg.batch == 2
+    t.lens += 5
+    t.free_count -= 1
+    t.plan(torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
+    assert t.lens.tolist() == [6, 5] and int(t.free_count) == 5
