@@ -241,6 +241,8 @@ class Layer:
         lp = None if lse is None else _dense(lse, "lse", torch.float32, self._lse, d)
         if workspace is None:
             raise KvqError("kvq_block_attn", -4)
+        if not isinstance(workspace, torch.Tensor):
+            raise ValueError(f"workspace: expected a uint8 tensor on cuda:{d}, got {type(workspace).__name__}")
         wp = _dense(workspace, "workspace", torch.uint8, workspace.shape, d)
         st = self._attn(self._ref, tables._refs[1], self._codes, self._scales, qp, op, lp, wp, workspace.nbytes, _stream_on(stream, d))
         if st:

@@ -61,3 +61,14 @@ def test_tensors_are_not_exchanged():
     t.free_count -= 1
     t.plan(torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
     assert t.lens.tolist() == [6, 5] and int(t.free_count) == 5
+
+
+@pytest.mark.gpu
+def test_a_workspace_of_another_type_is_refused():
+    t, layer = blocks.Tables(CFG), blocks.Layer(CFG)
+    q = torch.zeros((4, 4, 128), dtype=torch.float16, device="cuda")
+    ws = blocks.new_workspace(CFG)
+    for bad in (ws.data_ptr(), [0] * 16, ws.cpu(), ws.int(), ws[::2]):
+        with pytest.raises(ValueError):
+            layer.attn(t, q, torch.zeros_like(q), None, bad)
+    layer.attn(t, q, torch.zeros_like(q), None, ws)
