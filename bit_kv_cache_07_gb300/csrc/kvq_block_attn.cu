@@ -247,8 +247,12 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
         t.K = ring + slot * kPairBytes;
         t.V = smem_u32(t.K + kBlockSide);
         t.f = kb == kScaleNaN ? NAN : p.q_scale * __uint_as_float((uint32_t)kb << 23);
-        t.ev = vb == kScaleNaN ? NAN : (float)(vb - kScaleBias);
-        t.inv_v = __uint_as_float((uint32_t)(254 - min(vb, 254)) << 23);
+        // The weights hold 2^ev and the sum 2^-ev: over 80 octaves of it neither leaves fp32 (a
+        // weight that a larger one flushes is below 2^-46 of it).  Smaller scales are as good as
+        // the least one, whose values end below 2^-31 (out's least step is 2^-24).
+        const int ev = max(vb - kScaleBias, kMinExp);
+        t.ev = ev > kMaxExp ? NAN : (float)ev;
+        t.inv_v = __uint_as_float((uint32_t)(127 - min(ev, kMaxExp)) << 23);
         t.t0 = tile_of(s, i) * kBlockTokens;
         t.masked = t.t0 + kBlockTokens - 1 > p_lo || (p.window < kNoWindow && t.t0 <= p_hi - p.window);
         math.tile(p, s, t, lane, row0);

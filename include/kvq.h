@@ -615,7 +615,10 @@ KVQ_API kvq_status kvq_evict_workspace(const kvq_config *cfg, uint64_t *bytes);
  *           the 16-byte chunk c of token t's row lies at chunk c ^ (t % 8)
  *   scales  [n_blocks][n_kv_heads][2] u8: byte s is the factor 2^(s - 127); 255
  *           marks a block and side that holds a token with an infinity or a NaN
- *           and reads as NaN as a whole.  The region is padded to 16 bytes.
+ *           and reads as NaN as a whole.  The append gives 2^-40 to 2^40; where
+ *           the caller writes others, values past 2^40 read as NaN, too, and
+ *           scales of values below 2^-40 as 2^-40 (nothing that fp16 could tell).
+ *           The region is padded to 16 bytes.
  * The caller zero-fills both once.  A block belongs to one request. */
 typedef struct kvq_block_config {
     int32_t batch;            /* requests of a step, 1..1024 (slots of the tables) */
