@@ -81,7 +81,7 @@ EXPORTS = ["kvq_layout_query", "kvq_append", "kvq_decode_attn", "kvq_decode_plan
            "kvq_merge_attn", "kvq_fit_nuq_lut", "kvq_measure_distortion", "kvq_rate_allocate",
            "kvq_append_ragged", "kvq_decode_attn_ragged", "kvq_tree_attn", "kvq_tree_workspace",
            "kvq_attn_mass", "kvq_evict", "kvq_evict_workspace", "kvq_block_layout_query", "kvq_block_plan",
-           "kvq_block_append", "kvq_block_attn"]
+           "kvq_block_plan_back", "kvq_block_append", "kvq_block_attn"]
 NUQ_FIT_WORKSPACE_BYTES = 3 * 65538 * 8
 
 _lib = None
@@ -150,6 +150,8 @@ def lib():
         L.kvq_block_layout_query.restype = C.c_int
         L.kvq_block_plan.argtypes = [bcp, btp, vp, vp, vp, vp]
         L.kvq_block_plan.restype = C.c_int
+        L.kvq_block_plan_back.argtypes = [bcp, btp, vp, vp, vp, vp, vp]
+        L.kvq_block_plan_back.restype = C.c_int
         L.kvq_block_append.argtypes = [bcp, btp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
         L.kvq_block_append.restype = C.c_int
         L.kvq_block_attn.argtypes = [bcp, btp, vp, vp, vp, vp, vp, vp, C.c_uint64, vp]

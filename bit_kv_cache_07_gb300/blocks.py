@@ -134,20 +134,25 @@ class Tables:
         if self.device < 0:
             raise ValueError("the tables must be on a GPU")
         self._refs = C.byref(self._cfg), C.byref(self.arrays)
-        self._call = lib().kvq_block_plan
+        self._call, self._call_back = lib().kvq_block_plan, lib().kvq_block_plan_back
         self._rows = (c.batch,)
 
-    def plan(self, n_new, lens=None, free_count=None, stream=None):
+    def plan(self, n_new, lens=None, free_count=None, stream=None, n_back=None):
         """The step's tables: request b adds n_new[b] tokens, or ends (negative).
         lens, free_count: lengths and free blocks before the step, the tables' own
-        (updated in place) unless given."""
+        (updated in place) unless given.  n_back: tokens that a request takes back
+        first (drafted ones that were not accepted); lengths are lowered in no other
+        way, or the blocks behind them are lost."""
         d = _here()
         if d != self.device:
             raise ValueError(f"the tables are on cuda:{self.device}, the current device is cuda:{d}")
         np_ = _ints(n_new, "n_new", self._rows, d)
         lp = self.arrays.lens if lens is None else _ints(lens, "lens", self._rows, d)
         fp = self.arrays.free_count if free_count is None else _ints(free_count, "free_count", (1,), d)
-        st = self._call(*self._refs, lp, fp, np_, _stream_on(stream, d))
+        if n_back is None:
+            st = self._call(*self._refs, lp, fp, np_, _stream_on(stream, d))
+        else:
+            st = self._call_back(*self._refs, lp, fp, np_, _ints(n_back, "n_back", self._rows, d), _stream_on(stream, d))
         if st:
             _check("kvq_block_plan", st)
 

@@ -39,6 +39,7 @@ struct BlockPlanParams {
   BlockGeo geo;
   kvq_block_tables t;
   const int *lens_before, *free_before, *n_new;
+  const int* n_back;  // or null
 };
 
 struct BlockAppendParams {

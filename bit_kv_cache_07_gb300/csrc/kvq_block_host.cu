@@ -47,16 +47,23 @@ kvq_status kvq_block_layout_query(const kvq_block_config* cfg, kvq_block_layout*
 
 kvq_status kvq_block_plan(const kvq_block_config* cfg, const kvq_block_tables* tables, const int32_t* lens_before,
                           const int32_t* free_before, const int32_t* n_new, kvq_stream_t stream) {
+  return kvq_block_plan_back(cfg, tables, lens_before, free_before, n_new, nullptr, stream);
+}
+
+kvq_status kvq_block_plan_back(const kvq_block_config* cfg, const kvq_block_tables* tables, const int32_t* lens_before,
+                               const int32_t* free_before, const int32_t* n_new, const int32_t* n_back, kvq_stream_t stream) {
   BlockPlanParams p;
   kvq_status st = block_geometry(cfg, &p.geo);
   if (st != KVQ_OK) return st;
   if ((st = block_arrays(tables)) != KVQ_OK) return st;
-  if (!lens_before || !free_before || !n_new || ((uintptr_t)lens_before | (uintptr_t)free_before | (uintptr_t)n_new) % 4)
+  if (!lens_before || !free_before || !n_new ||
+      ((uintptr_t)lens_before | (uintptr_t)free_before | (uintptr_t)n_new | (uintptr_t)n_back) % 4)
     return KVQ_ERR_INVALID_ARG;
   p.t = *tables;
   p.lens_before = lens_before;
   p.free_before = free_before;
   p.n_new = n_new;
+  p.n_back = n_back;
   return launch_block_plan(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 

@@ -688,6 +688,23 @@ KVQ_API kvq_status kvq_block_plan(const kvq_block_config *cfg, const kvq_block_t
                           const int32_t *lens_before, const int32_t *free_before, const int32_t *n_new,
                           kvq_stream_t stream);
 
+/* kvq_block_plan_back -- kvq_block_plan for requests that first take tokens back, as
+ * after the verification of drafted tokens, which were all appended:
+ *   n_back       device [batch]: tokens that leave the request's end before the step's
+ *                own come (0: none), or NULL: none anywhere
+ * The request holds lens_before - n_back tokens then, whether or not it is served, and
+ * the blocks behind them go back to the stack like those of requests that end (in one
+ * order with theirs), before any is given out.  Outside [0, lens_before] the request is
+ * served nothing and keeps its length; of a request that ends n_back means nothing.
+ * Lengths are lowered in no other way: a plan takes the blocks of a request from its
+ * length, so that one that the caller lowers leaves the blocks behind it to nobody.
+ * A block keeps the scale that its largest token needed, and, where that was not finite,
+ * its mark, when the token is taken back, until its first token is.
+ * Errors: those of kvq_block_plan. */
+KVQ_API kvq_status kvq_block_plan_back(const kvq_block_config *cfg, const kvq_block_tables *tables,
+                               const int32_t *lens_before, const int32_t *free_before, const int32_t *n_new,
+                               const int32_t *n_back, kvq_stream_t stream);
+
 /* kvq_block_append -- the planned step's keys and values into the blocks, and the
  * queries made ready, in one pass: norm per head, rotation, 8-bit store.
  *   k, v      device fp16, token slot i's rows at k + i * k_stride (elements):
@@ -722,7 +739,8 @@ KVQ_API kvq_status kvq_block_append(const kvq_block_config *cfg, const kvq_block
  *              its first call; every call leaves its counters zero.  Calls that
  *              share it must not overlap on the GPU.
  * Any number of new tokens per request (of a chain of drafted tokens all are
- * appended first); made for few: up to 64 (token, query head) rows of a KV head
+ * appended first, and those that are not accepted taken back with the next plan);
+ * made for few: up to 64 (token, query head) rows of a KV head
  * read its blocks together, more rows read them again.  Logits, maxima and sums are
  * fp32.  Weights enter the product with the values in two fp16 parts (22 bits) where a
  * request's even share of the token slots makes no more than 8 rows of a KV head, in
