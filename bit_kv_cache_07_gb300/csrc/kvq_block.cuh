@@ -106,6 +106,48 @@ __host__ __device__ inline int block_tiles_max(int window, int n_first, const Bl
   return most < all ? (int)most : all;
 }
 
+// ------------------------------------------------- the append's split
+constexpr int kRowLanes = 8;  // lanes that hold a token's row of a head
+constexpr int kWarpTokens = 32 / kRowLanes;
+struct AppendSplit {
+  bool few;                     // one warp per CTA, else eight
+  int units;                    // touched blocks, at most
+  int heads_per_cta, kv_chunks; // heads of a block's CTA, CTAs of a block
+  int heads_per_warp, q_chunks; // heads of a query warp, CTAs of its token slots
+  long long ctas;
+};
+inline AppendSplit append_split(const BlockGeo& G, bool queries, int sms) {
+  AppendSplit s;
+  // no more blocks are touched: each request's tokens start one and end one
+  const long long most = (long long)G.N / kBlockTokens + 2ll * G.B;
+  s.units = (int)(most < G.N ? most : G.N);
+  // eight warps hold a whole block's tokens; up to four tokens per request (drafted
+  // chains, single tokens) fill one warp
+  s.few = (G.N + G.B - 1) / G.B <= kWarpTokens;
+  const int step = kWarpTokens * (s.few ? 1 : 8);
+  // heads of a block's CTA: many, since its look-ups and sines are paid once and the
+  // next head's rows are read meanwhile.  Up to four as long as the call's rows give
+  // each SM its three CTAs (43 prompts of 255 tokens of 4 heads 11.9 us in one CTA, 15.5
+  // in four; 51 of 80 tokens of 16 on 8 heads 14.0 in two, 18.5 in eight), more only
+  // while a CTA has no more than an eighth of an SM's share (the last CTAs to start are
+  // then short beside the call: prompts of 32 on 8 heads 57.4 us with all heads in a
+  // CTA, 59.8 in two, 64.2 in four; of 32 heads 105.9 in two, 109.4 in one, 110.3 in
+  // four)
+  const long long all_rows = (long long)G.N * (2 * G.Hkv + (queries ? G.Hq : 0));
+  const long long per_sm = all_rows / (2ll * kBlockTokens * sms);  // CTAs of one head
+  const long long up_to_four = per_sm / 3 < 4 ? per_sm / 3 : 4, share = s.few ? 1 : per_sm / 8 > up_to_four ? per_sm / 8 : up_to_four;
+  s.heads_per_cta = (int)(share < 1 ? 1 : share > G.Hkv ? G.Hkv : share);
+  s.kv_chunks = (G.Hkv + s.heads_per_cta - 1) / s.heads_per_cta;
+  s.heads_per_cta = (G.Hkv + s.kv_chunks - 1) / s.kv_chunks;  // (evenly)
+  // heads of a query warp: more share a token's sines, fewer spread a small call
+  // over the SMs
+  const long long rows = (long long)G.N * G.Hq;
+  s.heads_per_warp = (int)(rows >= 8ll * 16384 ? 8 : rows >= 16384 ? rows / 16384 : 1);
+  s.q_chunks = (G.Hq + s.heads_per_warp - 1) / s.heads_per_warp;
+  s.ctas = (long long)s.units * s.kv_chunks + (queries ? (long long)((G.N + step - 1) / step) * s.q_chunks : 0);
+  return s;
+}
+
 // ------------------------------------------------- the attention's schedule
 // The tiles of all (request, head, row block) lie end to end; CTA c takes
 // [c per, (c + 1) per).  (Shared with a host check.)
@@ -237,7 +279,7 @@ struct BlockWalk {
 __host__ __device__ inline int tile_of(const BlockSegment& s, int k) { return k < s.ns ? k : s.lo + (k - s.ns); }
 
 cudaError_t launch_block_plan(const BlockPlanParams& p, cudaStream_t st);
-cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st);
+cudaError_t launch_block_append(BlockAppendParams& p, int sms, cudaStream_t st);
 cudaError_t launch_block_attn(const BlockAttnParams& p, int sms, int rows, cudaStream_t st);
 
 }  // namespace kvq

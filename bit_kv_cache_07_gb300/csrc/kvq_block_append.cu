@@ -19,14 +19,9 @@
 // the angle (exact to 2^-32 turns at any position), and the hardware sine and
 // cosine of it in [-pi, pi] (absolute error below 2^-20, where q_out's own
 // rounding is 2^-11 and a code's 2^-4).
-#include <algorithm>
-
 #include "kvq_block.cuh"
 
 namespace kvq {
-
-constexpr int kRowLanes = 8;
-constexpr int kWarpTokens = 32 / kRowLanes;
 
 __device__ __forceinline__ void halves_to_floats(const uint4& u, float* v) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -383,39 +378,14 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 16) block_append_
   }
 }
 
-cudaError_t launch_block_append(BlockAppendParams& p, cudaStream_t st) {
-  const BlockGeo& G = p.geo;
-  // no more blocks are touched: each request's tokens start one and end one
-  const long long most = (long long)G.N / kBlockTokens + 2ll * G.B;
-  p.units = (int)(most < G.N ? most : G.N);
-  // eight warps hold a whole block's tokens; up to four tokens per request (drafted
-  // chains, single tokens) fill one warp
-  const bool few = (G.N + G.B - 1) / G.B <= kWarpTokens;
-  const int step = kWarpTokens * (few ? 1 : 8);
-  // heads of a block's CTA: many, since its look-ups and sines are paid once and the
-  // next head's rows are read meanwhile.  Up to four as long as the call's rows give
-  // each SM its three CTAs (43 prompts of 255 tokens of 4 heads 11.9 us in one CTA, 15.5
-  // in four; 51 of 80 tokens of 16 on 8 heads 14.0 in two, 18.5 in eight), more only
-  // while a CTA has no more than an eighth of an SM's share (the last CTAs to start are
-  // then short beside the call: prompts of 32 on 8 heads 57.4 us with all heads in a
-  // CTA, 59.8 in two, 64.2 in four; of 32 heads 105.9 in two, 109.4 in one, 110.3 in
-  // four)
-  const long long all_rows = (long long)G.N * (2 * G.Hkv + (p.q ? G.Hq : 0));
-  const long long per_sm = all_rows / (2 * kBlockTokens * 152);  // CTAs of one head
-  const long long share = few ? 1 : std::max(per_sm / 8, std::min(per_sm / 3, 4ll));
-  p.heads_per_cta = (int)(share < 1 ? 1 : share > G.Hkv ? G.Hkv : share);
-  p.kv_chunks = (G.Hkv + p.heads_per_cta - 1) / p.heads_per_cta;
-  p.heads_per_cta = (G.Hkv + p.kv_chunks - 1) / p.kv_chunks;  // (evenly)
-  // heads of a query warp: more share a token's sines, fewer spread a small call
-  // over the SMs
-  const long long rows = (long long)G.N * G.Hq;
-  p.heads_per_warp = (int)(rows >= 8ll * 16384 ? 8 : rows >= 16384 ? rows / 16384 : 1);
-  p.q_chunks = (G.Hq + p.heads_per_warp - 1) / p.heads_per_warp;
-  const long long q_ctas = p.q ? (long long)((G.N + step - 1) / step) * p.q_chunks : 0;
-  const long long ctas = (long long)p.units * p.kv_chunks + q_ctas;
-  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-  return few ? launch_dependent(block_append_kernel<1>, dim3((unsigned)ctas), dim3(32), 0, st, p)
-             : launch_dependent(block_append_kernel<8>, dim3((unsigned)ctas), dim3(256), 0, st, p);
+cudaError_t launch_block_append(BlockAppendParams& p, int sms, cudaStream_t st) {
+  const AppendSplit s = append_split(p.geo, p.q != nullptr, sms);
+  p.units = s.units;
+  p.heads_per_cta = s.heads_per_cta, p.kv_chunks = s.kv_chunks;
+  p.heads_per_warp = s.heads_per_warp, p.q_chunks = s.q_chunks;
+  if (s.ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  return s.few ? launch_dependent(block_append_kernel<1>, dim3((unsigned)s.ctas), dim3(32), 0, st, p)
+               : launch_dependent(block_append_kernel<8>, dim3((unsigned)s.ctas), dim3(256), 0, st, p);
 }
 
 }  // namespace kvq

@@ -105,7 +105,9 @@ kvq_status kvq_block_append(const kvq_block_config* cfg, const kvq_block_tables*
   p.eps = cfg->norm_eps;
   p.rotate = cfg->rope_theta > 0.0f;
   if (p.rotate) rope_turns(cfg->rope_theta, p.freq);
-  return launch_block_append(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  int sms = 0;
+  if (device_sm_count(&sms) != cudaSuccess) return KVQ_ERR_CUDA;
+  return launch_block_append(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 kvq_status kvq_block_attn(const kvq_block_config* cfg, const kvq_block_tables* tables, const uint8_t* codes, const uint8_t* scales,
