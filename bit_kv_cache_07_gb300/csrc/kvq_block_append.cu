@@ -15,10 +15,13 @@
 // queries go to CTAs of their own: a warp turns four tokens' rows head after
 // head with the same sines.
 //
-// Angles: position times a 64-bit fraction of a turn, whose top 32 bits are
-// the angle (exact to 2^-32 turns at any position), and the hardware sine and
-// cosine of it in [-pi, pi] (absolute error below 2^-20, where q_out's own
-// rounding is 2^-11 and a code's 2^-4).
+// Angles: position times a 64-bit fraction of a turn, whose top 32 bits are the
+// angle.  The fraction is off by less than 2^-54 of a turn (a power in doubles, for a
+// base of 1 or more), the angle by position 2^-54 turns, its fp32 radians by 5e-7 at
+// most; the hardware sine and cosine in [-pi, pi] add 4.2e-7.  Together the
+// absolute error stays below 2^-20 up to position 2^25 and below 2^-19 up to 2^30,
+// where q_out's own rounding is 2^-11 and a code's 2^-4: the hardware's functions are
+// taken for their speed, and show in neither.
 #include "kvq_block.cuh"
 
 namespace kvq {
