@@ -176,14 +176,12 @@ __global__ void __launch_bounds__(kThreadsAttn, 1) block_attn_kernel(const __gri
   const auto issue = [&]() {  // copies of the next tile
     if (!have) return;
     const int slot = in_slot, st = team * RING + slot;
-    bool emptied = true;
-    if (WT > 1 && in_turn) emptied = mbar_wait(smem_u32(&sm.empty[st]), (in_turn - 1) & 1, gave_up);
-    const int id = __shfl_sync(0xffffffffu, ids, id_at);
-    // (agreed, as every wait here: lanes whose limits end beside the phase would part ways before the next shuffle)
-    if (WT > 1 && !__all_sync(0xffffffffu, emptied)) {
+    // (agreed, as every wait here: lanes whose limits end beside the phase would part ways before the shuffles)
+    if (WT > 1 && in_turn && !wait(&sm.empty[st], (in_turn - 1) & 1)) {
       have = false;
       return;
     }
+    const int id = __shfl_sync(0xffffffffu, ids, id_at);
     if (lane == 0) {
       const bool proper = (unsigned)id < (unsigned)G.n_blocks;
       const size_t place = (size_t)(proper ? id : 0) * G.Hkv + as.h;
