@@ -11,7 +11,7 @@
 // a subset), so the products on the tensor cores are exact up to fp32 sums.
 //
 // Bound: the bytes of the visible blocks, each read once for up to 64 rows of a
-// KV head (16 x 32k tokens of 32 on 8 heads: 157 us, 6.8 TB/s).  A 32-token tile of a
+// KV head (16 x 32k tokens of 32 on 8 heads: 157 to 162 us, 6.6 to 6.8 TB/s).  A 32-token tile of a
 // head is one contiguous run of 8 KB: one bulk copy by one thread, stored in an order
 // that both ldmatrix and the key loads read without bank conflicts.  The visible
 // tiles of all (request, head, row block) lie end to end, cut into one equal range per
@@ -25,7 +25,7 @@
 // written back to shared memory as fp16 first (4 times the tile's bytes); here the
 // conversion happens in the registers that feed the product.  Past 16 rows the tiles'
 // conversions, done again by every warp of a team, bound it (two warps a scheduler:
-// latency; 16 x 8k tokens of 32 on 8 heads: 45 us for 4 rows, 52 for 16, 96 for 32).
+// latency; 16 x 8k tokens of 32 on 8 heads: 45 us for 4 rows, 51 for 16, 95 for 32).
 #include "kvq_block_tile.cuh"
 
 namespace kvq {

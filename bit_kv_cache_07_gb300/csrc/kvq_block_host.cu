@@ -141,8 +141,10 @@ kvq_status kvq_block_attn(const kvq_block_config* cfg, const kvq_block_tables* t
   int sms = 0;
   if (device_sm_count(&sms) != cudaSuccess) return KVQ_ERR_CUDA;
   if (sms > kMaxBlockCtas) sms = kMaxBlockCtas;
-  // rows that read a KV head's blocks together: those of an even share of the
-  // token slots (a request of more takes several passes)
+  // rows that read a KV head's blocks together: those of an even share of the token
+  // slots (the step's own numbers are on the GPU).  A request of more takes several
+  // passes, one of fewer leaves warps without rows: 64 requests of a token each, 100 to 8k
+  // tokens, 32 on 8 heads: 84 us with 64 slots, 87 with 256, 330 with 1,024.
   const long long rows = (long long)((g.N + g.B - 1) / g.B) * g.g;
   return launch_block_attn(p, sms, rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVQ_OK

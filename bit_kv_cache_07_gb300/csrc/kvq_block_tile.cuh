@@ -13,11 +13,13 @@
 // 53.5 us that way, 48.3 this way).  A tile's conversions (128 instructions, the larger
 // part) serve all NT column tiles.  With NT 1 the weights enter in two fp16 parts (22
 // bits, 16 matrix instructions more), which leaves the output its own rounding's
-// error (2.1e-4 normwise against 64 bits; in one part, as with NT 2: 2.6e-4).
+// error (2.1e-4 normwise against 64 bits).  With NT 2 they enter in one (2.6e-4): its
+// 255 registers are full, and two take 56.5 us in place of 50.8 at 16 rows, 114 in place
+// of 95 at 32 (16 x 8k tokens of 32 on 8 heads).
 //
 // More rows are more warps on a tile, 16 rows each, which convert it again: 32 rows by
-// one warp spill their accumulators (and take 98 us where two warps take 96, 16 x 8k
-// tokens, 8 new ones of 32 on 8 heads).
+// one warp spill their accumulators (and took 98 us where two warps took 94, 16 x 8k
+// tokens, 8 new ones of 32 on 8 heads; 16 rows spill 16 to 44 bytes themselves).
 #pragma once
 
 #include "kvq_block.cuh"

@@ -740,8 +740,11 @@ KVQ_API kvq_status kvq_block_append(const kvq_block_config *cfg, const kvq_block
  *              share it must not overlap on the GPU.
  * Any number of new tokens per request (of a chain of drafted tokens all are
  * appended first, and those that are not accepted taken back with the next plan);
- * made for few: up to 64 (token, query head) rows of a KV head
- * read its blocks together, more rows read them again.  Logits, maxima and sums are
+ * made for few.  8, 16, 32 or 64 (token, query head) rows of a KV head read its blocks
+ * together: the least of these that holds ceil(n_tokens / batch) * Hq / Hkv, a request's
+ * even share of the token slots, whatever the step brings.  A request of more rows reads
+ * its blocks again for them, one of fewer leaves part of the kernel idle: steps of single
+ * tokens are served best with about a slot for each request.  Logits, maxima and sums are
  * fp32.  Weights enter the product with the values in two fp16 parts (22 bits) where a
  * request's even share of the token slots makes no more than 8 rows of a KV head, in
  * one beyond that, with 12 octaves of room above 1.  A block id that is not of the pool
