@@ -11,10 +11,10 @@
 // a subset), so the products on the tensor cores are exact up to fp32 sums.
 //
 // Bound: the bytes of the visible blocks, each read once for up to 64 rows of a
-// KV head (16 x 32k tokens of 32 on 8 heads: 157 to 162 us, 6.6 to 6.8 TB/s).  A 32-token tile of a
-// head is one contiguous run of 8 KB: one bulk copy by one thread, stored in an order
-// that both ldmatrix and the key loads read without bank conflicts.  The visible
-// tiles of all (request, head, row block) lie end to end, cut into one equal range per
+// KV head (16 x 32k tokens of 32 on 8 heads: 157 to 162 us, 6.6 to 6.8 TB/s).  A
+// 32-token tile of a head is one contiguous run of 8 KB: one bulk copy by one thread,
+// stored in an order that both ldmatrix and the key loads read without bank conflicts.
+// The visible tiles of all (request, head, row block) lie end to end, cut into one equal range per
 // SM; lengths come from the GPU, so each CTA takes the prefix sums itself.  A CTA's
 // eight warps form teams of one warp per 16 rows (or 8); teams take a segment's tiles
 // in turn, each with its own ring of copies, which runs ahead across segments.  At a
